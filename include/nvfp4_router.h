@@ -283,6 +283,148 @@ int grouped_gemm(const uint8_t* x_codes, const uint8_t* x_scales, const float* g
                  int64_t max_rows, int64_t N, int64_t D, float* out, void* stream);
 
 /*
+ * The routed experts between the router's top-k and the next layer, on rows
+ * sorted by expert: grouped_plan, then grouped_swiglu (gate and up
+ * projections with the gated activation), router_quantize over its output,
+ * and grouped_combine (down projection and the weighted sum per token). The
+ * experts' sizes are ragged and stay on the device; every expert may have any
+ * number of rows, none included. T tokens of k choices give R = T * k slots,
+ * slot t * k + j being token t's j-th choice. An expert-parallel rank holds
+ * the G experts first_expert .. first_expert + G - 1: slots of other experts
+ * are left out, and the ranks' outputs add up to the layer's.
+ *
+ * Bytes of workspace for grouped_plan and grouped_combine with these sizes
+ * (D: hidden size, the combined output's columns; F: the experts' inner
+ * size); 0 for invalid sizes. The workspace's state prefix is the router
+ * calls' (see router_workspace_bytes); neither call touches it.
+ */
+size_t grouped_workspace_bytes(int64_t T, int64_t k, int64_t G, int64_t D, int64_t F);
+
+/*
+ * Sorts the slots by expert, slots of one expert in slot order.
+ *   topk_idx      [T, k] int32: router_gate_topk's choices (values outside
+ *                 first_expert .. first_expert + G - 1, -1 for example, are
+ *                 slots of no expert held here; a token may name an expert
+ *                 twice).
+ *   offsets       [G + 1] int32 out: expert first_expert + g owns rows
+ *                 offsets[g] .. offsets[g + 1] - 1.
+ *   rows          [T * k] int32 out: the slot of each row; -1 from offsets[G]
+ *                 on.
+ *   pos           [T * k] int32 out: the row of each slot; -1 for slots of no
+ *                 expert held here.
+ *   T, k, G       T >= 0, 1 <= k <= 32, 1 <= G <= 512, T * k < 2^30
+ *                 (ROUTER_EUNSUPPORTED beyond the upper bounds);
+ *                 first_expert >= 0.
+ * Pointers 4-byte aligned, the workspace 256-byte aligned (needed for more
+ * than 4096 slots). One launch up to 4096 slots, two beyond.
+ */
+int grouped_plan(const int32_t* topk_idx, int64_t T, int64_t k, int64_t first_expert, int64_t G, int32_t* offsets,
+                 int32_t* rows, int32_t* pos, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gate and up projections of the sorted rows with the SwiGLU activation: for
+ * row p of expert g, with t = rows[p] / k,
+ *   y[n] = gsa * gsw[g] * sum_d xhat[t, d] * what_g[n, d] + bias[g, n],  n < 2F
+ *   out[p, f] = bf16(silu(y[f]) * y[F + f]),  silu(v) = v / (1 + e^-v)
+ * with exact products and fp32 sums; rows from offsets[G] on are set to zero,
+ * so that router_quantize over all T * k rows sees no stale values.
+ *   x_codes, x_scales, gsa   router_quantize outputs for x [T, D] (not
+ *                            gathered: the rows are read through `rows`).
+ *   w_codes, w_scales, gsw   [G, 2F, D/2], [G, 2F, D/16], [G] fp32: each
+ *                            expert's F gate rows, then its F up rows.
+ *   bias                     NULL or [G, 2F] fp32.
+ *   offsets, rows            grouped_plan's. Values that no plan gives are
+ *                            clamped (their rows are not defined).
+ *   F, D                     F >= 16, F % 16 == 0; D % 32 == 0; D and 2F at
+ *                            most ROUTER_MAX_GATE_D; T * D / 2 and F * D
+ *                            below 2^31 - 65536 (ROUTER_EUNSUPPORTED
+ *                            otherwise).
+ *   out                      [T * k, F] bf16.
+ * Code pointers and out 16-byte, scale pointers 2-byte, the rest 4-byte
+ * aligned. One launch, no workspace.
+ */
+int grouped_swiglu(const uint8_t* x_codes, const uint8_t* x_scales, const float* gsa, const uint8_t* w_codes,
+                   const uint8_t* w_scales, const float* gsw, const float* bias, const int32_t* offsets,
+                   const int32_t* rows, int64_t T, int64_t k, int64_t G, int64_t F, int64_t D, void* out,
+                   void* stream);
+
+/*
+ * Down projection of the sorted rows and the weighted sum of each token's
+ * rows, in slot order:
+ *   y[p, n] = gsh * gsw[g] * sum_f hhat[p, f] * what_g[n, f] + bias[g, n]
+ *   out[t, n] = bf16(residual[t, n] + sum_j topk_w[t, j] * y[pos[t, j], n])
+ * over the j with pos[t, j] >= 0 (weights of other slots are not read); a
+ * token without any gets its residual, or zeros. fp32 until the one rounding.
+ *   h_codes, h_scales, gsh   router_quantize outputs for grouped_swiglu's
+ *                            output [T * k, F].
+ *   w_codes, w_scales, gsw   [G, D, F/2], [G, D, F/16], [G] fp32.
+ *   bias                     NULL or [G, D] fp32.
+ *   offsets, pos             grouped_plan's.
+ *   topk_w                   [T, k] fp32: router_gate_topk's weights.
+ *   residual                 NULL or [T, D] bf16; may be `out` itself.
+ *   out                      [T, D] bf16.
+ *   D, F                     D >= 16, D % 16 == 0; F % 32 == 0; both at most
+ *                            ROUTER_MAX_GATE_D, D * F / 2 below 2^31 - 65536
+ *                            (ROUTER_EUNSUPPORTED otherwise).
+ *   workspace                grouped_workspace_bytes(T, k, G, D, F) bytes.
+ * Code pointers, residual and out 16-byte, scale pointers 2-byte, workspace
+ * 256-byte, the rest 4-byte aligned.
+ */
+int grouped_combine(const uint8_t* h_codes, const uint8_t* h_scales, const float* gsh, const uint8_t* w_codes,
+                    const uint8_t* w_scales, const float* gsw, const float* bias, const int32_t* offsets,
+                    const int32_t* pos, const float* topk_w, const void* residual, int64_t T, int64_t k, int64_t G,
+                    int64_t D, int64_t F, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+#define ROUTER_F32 0  /* dtype of lmhead_penalize's logits */
+#define ROUTER_BF16 1
+
+/*
+ * Repetition, frequency and presence penalties, token biases and a grammar
+ * mask on logits, and the greedy token: the constrained form of
+ * lmhead_argmax's choice, on its logits_out or any others. For row t, in
+ * fp32, each operation rounded by itself and in this order:
+ *   tokens in history[t, :lengths[t]]:     x = x > 0 ? x / r : x * r
+ *   tokens that occur c > 0 times in
+ *   history[t, prompt[t]:lengths[t]]:      x = (x - f * c) - p
+ *   tokens listed in the row's biases:     x = x + value
+ *   tokens whose mask bit is clear:        x = -inf, whatever x is
+ * The token with the largest x (a tie going to the lower one, -inf and NaN
+ * never chosen) is the row's choice, made before the logits are rounded to
+ * their type.
+ *   logits, out    [T, N] of `dtype`, `ld` >= N elements between rows; out
+ *                  may be logits itself, and must not overlap it otherwise.
+ *   history        NULL or [T, L] int32 with ld_history >= L elements
+ *                  between rows; tokens outside [0, N) are ignored.
+ *   lengths        NULL (every row has L) or [T] int32, clamped to [0, L].
+ *   prompt         NULL (0) or [T] int32: tokens before it count as seen
+ *                  only, from it on also as made.
+ *   repetition, frequency, presence   NULL (1, 0, 0) or [T] fp32: r, f, p.
+ *   bias_start     NULL or [T + 1] int32: row t's biases are entries
+ *                  bias_start[t] .. bias_start[t + 1] - 1 of bias_token
+ *                  (int32) and bias_value (fp32), nbias entries in all. A
+ *                  token listed twice in a row takes its last value.
+ *   mask           NULL or [T, ld_mask] 32-bit words, ld_mask >= N / 32
+ *                  rounded up: bit n % 32 of word n / 32 is set where token n
+ *                  is allowed.
+ *   out_idx, out_logit   [T] int32 / fp32 out: the choice and its x; -1 and
+ *                  -inf when nothing can be chosen.
+ *   T, N           T >= 0, 1 <= N <= 2^30.
+ *   workspace      lmhead_penalize_workspace_bytes(T, N) bytes, 256-byte
+ *                  aligned, with the router calls' state prefix (not needed
+ *                  for N <= 4096).
+ * The other pointers are aligned to their element; 16-byte aligned rows of
+ * logits and out are read and written 16 bytes at a time. One launch for each
+ * 1024 rows. ROUTER_EINVAL for bad sizes, pointers or workspace.
+ */
+size_t lmhead_penalize_workspace_bytes(int64_t T, int64_t N);
+int lmhead_penalize(const void* logits, int dtype, int64_t T, int64_t N, int64_t ld, const int32_t* history,
+                    int64_t L, int64_t ld_history, const int32_t* lengths, const int32_t* prompt,
+                    const float* repetition, const float* frequency, const float* presence,
+                    const int32_t* bias_start, const int32_t* bias_token, const float* bias_value, int64_t nbias,
+                    const uint32_t* mask, int64_t ld_mask, void* out, int32_t* out_idx, float* out_logit,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Measurement aid, not part of the router path: reads `bytes` of `buf`
  * (device, 16-byte aligned, bytes % 16 == 0) once with 16-byte loads in one
  * launch of min(bytes / 4096 rounded up, sink_words, 8192) workgroups of 256

@@ -17,7 +17,9 @@ LIB_PATH = os.path.join(_HERE, "libnvfp4_router.so")
 ROUTER_OK = 0
 EXPORTS = ("router_workspace_bytes", "router_workspace_init", "router_quantize", "router_gate_topk",
            "router_forward", "router_forward_noalloc", "router_status_string", "router_probe_read",
-           "router_probe_mfma", "lmhead_workspace_bytes", "lmhead_argmax", "grouped_offsets", "grouped_gemm")
+           "router_probe_mfma", "lmhead_workspace_bytes", "lmhead_argmax", "grouped_offsets", "grouped_gemm",
+           "grouped_workspace_bytes", "grouped_plan", "grouped_swiglu", "grouped_combine",
+           "lmhead_penalize_workspace_bytes", "lmhead_penalize")
 ROUTER_ESCRATCH = -4
 STATIC_SCRATCH_BYTES = 16 << 20
 
@@ -66,6 +68,19 @@ def load_library(path=LIB_PATH):
     L.grouped_offsets.restype = ctypes.c_int
     L.grouped_gemm.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp]
     L.grouped_gemm.restype = ctypes.c_int
+    L.grouped_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    L.grouped_workspace_bytes.restype = sz
+    L.grouped_plan.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+    L.grouped_plan.restype = ctypes.c_int
+    L.grouped_swiglu.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp]
+    L.grouped_swiglu.restype = ctypes.c_int
+    L.grouped_combine.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, sz, vp]
+    L.grouped_combine.restype = ctypes.c_int
+    L.lmhead_penalize_workspace_bytes.argtypes = [i64, i64]
+    L.lmhead_penalize_workspace_bytes.restype = sz
+    L.lmhead_penalize.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64,
+                                  vp, i64, vp, vp, vp, vp, sz, vp]
+    L.lmhead_penalize.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -325,6 +340,198 @@ def grouped_gemm(xq, wg, offsets, max_rows, out=None):
                                        _ptr(wg.scales), _ptr(wg.gscale), _ptr(offsets), wg.G, R, int(max_rows),
                                        wg.N, D, _ptr(out), _stream()))
     return out
+
+
+def grouped_workspace_bytes(T, k, G, D, F):
+    n = load_library().grouped_workspace_bytes(T, k, G, D, F)
+    if n == 0:
+        raise RouterError(f"invalid expert sizes T={T} k={k} G={G} D={D} F={F}")
+    return int(n)
+
+
+def _tensor(t, name, dtype, shape, device, contiguous=True):
+    """A GPU tensor of this dtype, shape and device, or RouterError."""
+    _device_tensor(t, name, (dtype,)) if contiguous else None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape):
+        raise RouterError(f"{name} must be {dtype} {tuple(shape)} on {device}")
+    return t
+
+
+def _on(device):
+    """The library launches on the current device: make it the tensors' own."""
+    return torch.cuda.device(device)
+
+
+class GroupedPlan:
+    """Slots sorted by expert: offsets [G + 1], rows [T * k] (the slot of each row) and pos [T * k] (the row of each
+    slot), all int32, for T tokens of k choices."""
+
+    def __init__(self, offsets, rows, pos, T, k):
+        self.offsets, self.rows, self.pos, self.T, self.k = offsets, rows, pos, T, k
+
+    @property
+    def G(self):
+        return self.offsets.numel() - 1
+
+
+def empty_plan(T, k, G, device="cuda"):
+    i32 = dict(dtype=torch.int32, device=device)
+    return GroupedPlan(torch.empty(G + 1, **i32), torch.empty(T * k, **i32), torch.empty(T * k, **i32), T, k)
+
+
+def _check_plan(plan, dev, G):
+    R = plan.T * plan.k
+    _tensor(plan.offsets, "plan offsets", torch.int32, (G + 1,), dev)
+    _tensor(plan.rows, "plan rows", torch.int32, (R,), dev)
+    _tensor(plan.pos, "plan pos", torch.int32, (R,), dev)
+
+
+def _check_workspace(workspace, dev):
+    if workspace.buf.device != dev:
+        raise RouterError(f"the workspace is on {workspace.buf.device}, not on {dev}")
+
+
+def _check_grouped(xq, wg, rows):
+    """NVFP4 operands of a grouped product: x [rows, D] and weights [G, N, D], on one device."""
+    dev, D = xq.codes.device, xq.D
+    _tensor(xq.codes, "x codes", torch.uint8, (rows, D // 2), dev)
+    _tensor(xq.scales, "x scales", torch.uint8, (rows, D // 16), dev)
+    _tensor(xq.gscale, "x global scale", torch.float32, (1,), dev)
+    if wg.D != D:
+        raise RouterError("grouped weights do not match x")
+    _tensor(wg.codes, "w codes", torch.uint8, (wg.G, wg.N, D // 2), dev)
+    _tensor(wg.scales, "w scales", torch.uint8, (wg.G, wg.N, D // 16), dev)
+    _tensor(wg.gscale, "w global scales", torch.float32, (wg.G,), dev)
+    return dev
+
+
+def grouped_plan(topk_idx, G, workspace, first_expert=0, out=None):
+    """grouped_plan: the slots of topk_idx [T, k] int32 sorted by expert -> GroupedPlan over the G experts from
+    first_expert on (slots of other experts are left out)."""
+    _device_tensor(topk_idx, "topk_idx", (torch.int32,), ndim=2)
+    T, k = topk_idx.shape
+    dev = topk_idx.device
+    _check_workspace(workspace, dev)
+    with _on(dev):
+        if out is None:
+            out = empty_plan(T, k, G, dev)
+        elif (out.T, out.k) != (T, k):
+            raise RouterError("the plan does not match topk_idx")
+        _check_plan(out, dev, G)
+        _check(load_library().grouped_plan(_ptr(topk_idx), T, k, int(first_expert), G, _ptr(out.offsets),
+                                           _ptr(out.rows), _ptr(out.pos), _ptr(workspace.buf), workspace.nbytes,
+                                           _stream()))
+    return out
+
+
+def grouped_swiglu(xq, wg, plan, bias=None, out=None):
+    """grouped_swiglu: out [T * k, F] bf16, row p being silu(gate) * up of its token's row of xq [T, D] under its
+    expert's weights wg [G, 2F, D] (F gate rows, then F up rows) and bias [G, 2F] fp32; rows of no expert are zeros."""
+    dev = _check_grouped(xq, wg, plan.T)
+    _check_plan(plan, dev, wg.G)
+    if wg.N % 2:
+        raise RouterError("gate and up weights need an even number of rows")
+    R, F = plan.T * plan.k, wg.N // 2
+    if bias is not None:
+        _tensor(bias, "bias", torch.float32, (wg.G, wg.N), dev)
+    with _on(dev):
+        if out is None:
+            out = torch.empty((R, F), dtype=torch.bfloat16, device=dev)
+        _tensor(out, "out", torch.bfloat16, (R, F), dev)
+        _check(load_library().grouped_swiglu(_ptr(xq.codes), _ptr(xq.scales), _ptr(xq.gscale), _ptr(wg.codes),
+                                             _ptr(wg.scales), _ptr(wg.gscale), _ptr(bias), _ptr(plan.offsets),
+                                             _ptr(plan.rows), plan.T, plan.k, wg.G, F, xq.D, _ptr(out), _stream()))
+    return out
+
+
+def grouped_combine(hq, wg, plan, topk_w, workspace, bias=None, residual=None, out=None):
+    """grouped_combine: out [T, D] bf16 = residual + the topk_w-weighted sum of each token's rows of hq [T * k, F]
+    times its expert's weights wg [G, D, F] plus bias [G, D] fp32; residual may be out itself."""
+    T, k, D = plan.T, plan.k, wg.N
+    dev = _check_grouped(hq, wg, T * k)
+    _check_plan(plan, dev, wg.G)
+    _check_workspace(workspace, dev)
+    _tensor(topk_w, "topk_w", torch.float32, (T, k), dev)
+    if bias is not None:
+        _tensor(bias, "bias", torch.float32, (wg.G, D), dev)
+    if residual is not None:
+        _tensor(residual, "residual", torch.bfloat16, (T, D), dev)
+    with _on(dev):
+        if out is None:
+            out = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+        _tensor(out, "out", torch.bfloat16, (T, D), dev)
+        _check(load_library().grouped_combine(_ptr(hq.codes), _ptr(hq.scales), _ptr(hq.gscale), _ptr(wg.codes),
+                                              _ptr(wg.scales), _ptr(wg.gscale), _ptr(bias), _ptr(plan.offsets),
+                                              _ptr(plan.pos), _ptr(topk_w), _ptr(residual), T, k, wg.G, D, hq.D,
+                                              _ptr(out), _ptr(workspace.buf), workspace.nbytes, _stream()))
+    return out
+
+
+def lmhead_penalize_workspace_bytes(T, N):
+    n = load_library().lmhead_penalize_workspace_bytes(T, N)
+    if n == 0:
+        raise RouterError(f"invalid logits sizes T={T} N={N}")
+    return int(n)
+
+
+def _rows_tensor(t, name, dtypes, T):
+    """A GPU matrix of T rows whose elements are adjacent inside a row; returns its row stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() != 2 or t.shape[0] != T:
+        raise RouterError(f"{name} must be a GPU matrix of {T} rows of {' or '.join(map(str, dtypes))}")
+    if t.shape[1] > 1 and t.stride(1) != 1 or T > 1 and t.stride(0) < t.shape[1]:
+        raise RouterError(f"{name} must hold its rows contiguously")
+    return max(t.stride(0), t.shape[1]) if T > 1 else t.shape[1]
+
+
+def lmhead_penalize(logits, workspace, history=None, prompt=None, lengths=None, repetition=None, frequency=None,
+                    presence=None, bias=None, mask=None, out=None):
+    """lmhead_penalize: penalties, biases and a grammar mask on logits [T, N] (fp32 or bf16) and the greedy token.
+
+    history [T, L] int32 with lengths and prompt [T] int32; repetition, frequency and presence [T] fp32; bias =
+    (start [T + 1] int32, token int32, value fp32); mask [T, >= N / 32] int32 words, a bit set where a token is
+    allowed. Returns ``(idx [T] int32, logit [T] fp32, out)``; out may be logits itself."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise RouterError("logits must be a GPU matrix")
+    T, N = logits.shape
+    ld = _rows_tensor(logits, "logits", (torch.float32, torch.bfloat16), T)
+    dev = logits.device
+    _check_workspace(workspace, dev)
+    if out is None:
+        out = torch.empty_strided((T, N), (ld, 1), dtype=logits.dtype, device=dev)
+    if out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev or \
+            _rows_tensor(out, "out", (logits.dtype,), T) != ld:
+        raise RouterError("out must have the dtype, shape, device and row stride of logits")
+    L = ldh = ldm = nbias = 0
+    if history is not None:
+        L, ldh = history.shape[-1], _rows_tensor(history, "history", (torch.int32,), T)
+    for name, t, dtype in (("lengths", lengths, torch.int32), ("prompt", prompt, torch.int32),
+                           ("repetition", repetition, torch.float32), ("frequency", frequency, torch.float32),
+                           ("presence", presence, torch.float32)):
+        if t is not None:
+            _tensor(t, name, dtype, (T,), dev)
+    start = token = value = None
+    if bias is not None:
+        start, token, value = bias
+        nbias = token.numel()
+        _tensor(start, "bias start", torch.int32, (T + 1,), dev)
+        _tensor(token, "bias token", torch.int32, (nbias,), dev)
+        _tensor(value, "bias value", torch.float32, (nbias,), dev)
+    if mask is not None:
+        ldm = _rows_tensor(mask, "mask", (torch.int32, torch.uint32), T)
+        if mask.shape[1] * 32 < N:
+            raise RouterError("mask has too few words")
+    for name, t in (("history", history), ("mask", mask)):
+        if t is not None and t.device != dev:
+            raise RouterError(f"{name} must be on {dev}")
+    with _on(dev):
+        idx = torch.empty(T, dtype=torch.int32, device=dev)
+        logit = torch.empty(T, dtype=torch.float32, device=dev)
+        _check(load_library().lmhead_penalize(
+            _ptr(logits), 0 if logits.dtype == torch.float32 else 1, T, N, ld, _ptr(history), L, ldh, _ptr(lengths),
+            _ptr(prompt), _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(start), _ptr(token), _ptr(value),
+            nbias, _ptr(mask), ldm, _ptr(out), _ptr(idx), _ptr(logit), _ptr(workspace.buf), workspace.nbytes,
+            _stream()))
+    return idx, logit, out
 
 
 MFMA_PROBE_SINK = 1024 * 256
