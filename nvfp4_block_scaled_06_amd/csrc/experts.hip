@@ -9,6 +9,8 @@
 #include "../../include/nvfp4_router.h"
 #include "experts_common.hpp"
 
+#include <algorithm>
+
 namespace nvr {
 
 size_t plan_scratch_bytes(int64_t R, int64_t G);  // experts_plan.hip
@@ -26,6 +28,8 @@ struct ExpertArgs {
   void* out;               // swiglu: bf16 [R, N/2]; combine: fp32 [R, N] products
   int T, k, R, G, N, D;
   int col_tiles, nsteps;
+  Take take;      // which experts this launch takes
+  int tile_cols;  // column tiles of the 128-row tile kernel
 };
 
 // Token of row p, or -1.
@@ -37,13 +41,38 @@ __device__ __forceinline__ int row_token(const ExpertArgs& a, int p) {
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return g * sigmoid_fast(g) * u; }
 
+// Work item b -> (row tile, column tile). The products of the experts' rows
+// come first, numbered so that consecutive items (the row tiles of one column
+// tile of an expert, then its next column tile) run on one XCD and share its
+// L2; then, if `others` (grouped_swiglu), one item per row tile of no expert.
+// False behind the last item.
+struct ExpertTile {
+  RowTile rt;
+  int ct;
+};
+__device__ __forceinline__ bool expert_tile(const ExpertArgs& a, const TileScan& scan, bool others, int b,
+                                            ExpertTile& t) {
+  const int products = scan.experts * a.col_tiles;
+  if (b < products) {
+    t.rt = scan.at(xcd_order(b, products), a.col_tiles, t.ct);
+    return true;
+  }
+  if (others && b - products < scan.others()) {
+    t.ct = 0;
+    t.rt = scan.none(b - products);
+    return true;
+  }
+  return false;
+}
+
 // Zeros for the rows of no expert: router_quantize runs over all R rows, and
-// stale values there would set its global scale.
-__device__ __forceinline__ void zero_rows(const ExpertArgs& a, const RowTile& t, int col0, int cols, int nthreads) {
-  uint16_t* out = static_cast<uint16_t*>(a.out);
-  const int F = a.N >> 1, nc = min(cols, F - col0);
-  for (int i = threadIdx.x; i < t.nr * nc; i += nthreads)
-    out[(int64_t)(t.row0 + i / nc) * F + col0 + i % nc] = 0;
+// stale values there would set its global scale. F is a multiple of 16, so
+// whole rows are whole 16-byte pieces (a 2-byte store per element and column
+// tile took 1.1 ms for the 28672 rows of an eighth of 4096 tokens' experts).
+__device__ __forceinline__ void zero_rows(const ExpertArgs& a, const RowTile& t, int nthreads) {
+  const int64_t per_row = a.N >> 4;  // F / 8 pieces
+  u32x4_t* out = static_cast<u32x4_t*>(a.out) + t.row0 * per_row;
+  for (int64_t i = threadIdx.x; i < t.nr * per_row; i += nthreads) out[i] = u32x4_t{0u, 0u, 0u, 0u};
 }
 
 // Scale row offsets of a tile of gathered rows (A) and paired weight rows
@@ -54,36 +83,29 @@ struct TableRows {
   __device__ __forceinline__ uint32_t operator()(bool isA, int rr) const { return tab[isA ? rr : bm + rr]; }
 };
 
-// One tile of BM rows of an expert times 128 NTW weight rows on the shared
-// MFMA tile. GLU: the rows are gathered, and each 32-column tile holds 16
-// gate rows and the 16 up rows of the same outputs, so that one lane swap
+// LDS of one tile: the A tiles, the scale windows and the row table.
+template <bool GLU, int BM, int NTW, int KS, bool STAGED>
+struct ExpertLds {
+  alignas(16) _Float16 abuf[KS][2][BM * kMmaARow];
+  alignas(16) uint8_t swin[STAGED ? mma_win_bytes<BM, NTW>() : 16];
+  uint32_t srow[GLU ? BM + 128 * NTW : 1];
+};
+
+// One tile of up to BM rows of an expert times 128 NTW weight rows on the
+// shared MFMA tile. GLU: the rows are gathered, and each 32-column tile holds
+// 16 gate rows and the 16 up rows of the same outputs, so that one lane swap
 // brings the two halves of an output together.
 template <bool GLU, int BM, int NTW, int KS, bool STAGED>
-__global__ __launch_bounds__(kMmaThreads * KS) __attribute__((amdgpu_waves_per_eu(KS, KS))) void experts_mfma_kernel(
-    ExpertArgs a) {
+__device__ __forceinline__ void experts_tile(const ExpertArgs& a, const RowTile& rt, int ct,
+                                             ExpertLds<GLU, BM, NTW, KS, STAGED>& lds) {
   static_assert(KS == mma_ksplit<BM, NTW>(), "K groups as the main loop has them");
   constexpr int BN = 128 * NTW;
-  constexpr int SH = BM == 32 ? 5 : (BM == 64 ? 6 : 7);
-  static_assert(BM == 1 << SH, "rows per tile");
   static_assert(KS == 1 || BM * BN * sizeof(float) <= sizeof(_Float16) * KS * 2 * BM * kMmaARow,
                 "the epilogue's partial sums fit in the A tiles' LDS");
-  __shared__ __attribute__((aligned(16))) _Float16 abuf[KS][2][BM * kMmaARow];
-  __shared__ __attribute__((aligned(16))) uint8_t swin[STAGED ? mma_win_bytes<BM, NTW>() : 16];
-  __shared__ uint32_t srow[GLU ? BM + BN : 1];
+  _Float16* abuf = &lds.abuf[0][0][0];
+  uint32_t* srow = lds.srow;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wt = wave & 3, grp = wave >> 2;
-  const TileScan scan(a.offsets, a.G, a.R, SH);
-  const int total = GLU ? scan.total : scan.experts;
-  if ((int)blockIdx.x >= total * a.col_tiles) return;
-  // Consecutive tiles (the column tiles of one row tile first) run on one
-  // XCD, so a row tile's activations are fetched into one L2.
-  const int n = xcd_order(blockIdx.x, total * a.col_tiles);
-  const int ct = n % a.col_tiles;
-  const RowTile rt = scan.at(n / a.col_tiles);
   const int row0 = rt.row0, nr = rt.nr;
-  if (GLU && rt.g == a.G) {
-    zero_rows(a, rt, ct * (BN / 2), BN / 2, kMmaThreads * KS);
-    return;
-  }
   const float gsa = load_early(a.gsa), gsw = load_early(a.gsw + rt.g);
   const int64_t rowc = a.D / 2, rows = a.D / 16;
   const int r = lane & 31, h = lane >> 5, F = a.N >> 1;
@@ -131,13 +153,13 @@ __global__ __launch_bounds__(kMmaThreads * KS) __attribute__((amdgpu_waves_per_e
   constexpr int NS = mma_sets<BM, NTW>();
   f32x16_t acc[NS][BM / 32][NTW];
   if constexpr (GLU)
-    mma_mainloop<BM, NTW, KS, STAGED>(P, a.D, a.nsteps, &abuf[0][0][0], swin, lane, acc, TableRows{srow, BM});
+    mma_mainloop<BM, NTW, KS, STAGED>(P, a.D, a.nsteps, abuf, lds.swin, lane, acc, TableRows{srow, BM});
   else
-    mma_mainloop<BM, NTW, KS, STAGED>(P, a.D, a.nsteps, &abuf[0][0][0], swin, lane, acc);
+    mma_mainloop<BM, NTW, KS, STAGED>(P, a.D, a.nsteps, abuf, lds.swin, lane, acc);
 
   // 32x32 accumulator layout: value v of lane (r, h) is row 8(v/4) + 4h +
   // v%4, column r of its tile; wavefront wt holds the column tiles wt + 4t.
-  float* part = reinterpret_cast<float*>(&abuf[0][0][0]);  // [BM][BN], K group 1's sums
+  float* part = reinterpret_cast<float*>(abuf);  // [BM][BN], K group 1's sums
   if (KS == 2 && grp == 1) {
 #pragma unroll
     for (int rt2 = 0; rt2 < BM / 32; ++rt2)
@@ -197,130 +219,303 @@ __global__ __launch_bounds__(kMmaThreads * KS) __attribute__((amdgpu_waves_per_e
   }
 }
 
-// Few rows per expert: a stream of the hit experts' weights. Workgroup (row
-// tile of up to 4 rows of an expert, column tile) = 64 weight rows, four
-// wavefronts of 16 rows with the loads of 2 in flight, as in the lm_head
-// GEMV. GLU: a wavefront's rows are the gate and up rows of 8 outputs in
-// turn.
-constexpr int kEvWaves = 4;
-constexpr int kEvThreads = 64 * kEvWaves;
-constexpr int kEvRowsPerWave = 16;
-constexpr int kEvCols = kEvWaves * kEvRowsPerWave;
-constexpr int kEvInFlight = 2;
-constexpr int kEvMaxRows = 4;
-constexpr int kEvMaxXHalves = 32768;  // rows x D of the fp16 x copy in LDS (64 KB)
-
-template <bool GLU, int CPL, int NR>
-__global__ __launch_bounds__(kEvThreads) void experts_gemv_kernel(ExpertArgs a) {
-  extern __shared__ half8_t xg[];  // [nr][D / 8]
-  constexpr int SH = NR == 1 ? 0 : (NR == 2 ? 1 : 2);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const TileScan scan(a.offsets, a.G, a.R, SH);
-  const int total = GLU ? scan.total : scan.experts;
-  if ((int)blockIdx.x >= total * a.col_tiles) return;
-  const int n = xcd_order(blockIdx.x, total * a.col_tiles);
-  const int ct = n % a.col_tiles;
-  const RowTile rt = scan.at(n / a.col_tiles);
-  if (GLU && rt.g == a.G) {
-    zero_rows(a, rt, ct * (kEvCols / 2), kEvCols / 2, kEvThreads);
-    return;
-  }
-  const int nr = rt.nr, F = a.N >> 1, nch = a.D >> 5;
-  const int64_t rowc = a.D / 2, rows = a.D / 16;
-  const float gsa = load_early(a.gsa), gsw = load_early(a.gsw + rt.g);
-  for (int i = threadIdx.x; i < nr * nch; i += kEvThreads) {
-    const int t = i / nch, c = i - t * nch;
-    const int64_t xr = GLU ? row_token(a, rt.row0 + t) : rt.row0 + t;
-    u32x4_t v{0u, 0u, 0u, 0u};
-    uint32_t sb = 0u;
-    if (!GLU || xr >= 0) {
-      v = *reinterpret_cast<const u32x4_t*>(a.xc + xr * rowc + 16 * c);
-      sb = *reinterpret_cast<const uint16_t*>(a.xs + xr * rows + 2 * c);
+// Workgroup (row tile of up to BM rows of an expert, column tile). A ragged
+// last tile with at most half the rows takes the 64-row tile instead of the
+// 128-row one, which costs it little more than half as much.
+template <bool GLU, int BM, int NTW, int KS, bool STAGED>
+__global__ __launch_bounds__(kMmaThreads * KS) __attribute__((amdgpu_waves_per_eu(KS, KS))) void experts_mfma_kernel(
+    ExpertArgs a) {
+  constexpr int SH = BM == 32 ? 5 : (BM == 64 ? 6 : 7);
+  static_assert(BM == 1 << SH, "rows per tile");
+  constexpr bool kHalf = BM == 128 && mma_ksplit<64, NTW>() == KS;
+  __shared__ union {
+    ExpertLds<GLU, BM, NTW, KS, STAGED> full;
+    ExpertLds<GLU, kHalf ? 64 : BM, NTW, KS, STAGED> half;
+  } lds;
+  const TileScan scan(a.offsets, a.G, a.R, SH, a.take, a.tile_cols);
+  ExpertTile tile;
+  if (!expert_tile(a, scan, false, blockIdx.x, tile)) return;
+  const RowTile& rt = tile.rt;
+  const int ct = tile.ct;
+  if constexpr (kHalf) {
+    if (rt.nr <= 64) {
+      experts_tile<GLU, 64, NTW, KS, STAGED>(a, rt, ct, lds.half);
+      return;
     }
-    const _Float16 s0 = e4m3_f16(sb & 0xFFu), s1 = e4m3_f16(sb >> 8);
-    half8_t* d = xg + (int64_t)t * (nch * 4) + 4 * c;
-    d[0] = fp4x8_to_f16(v[0], s0);
-    d[1] = fp4x8_to_f16(v[1], s0);
-    d[2] = fp4x8_to_f16(v[2], s1);
-    d[3] = fp4x8_to_f16(v[3], s1);
   }
-  __syncthreads();
+  experts_tile<GLU, BM, NTW, KS, STAGED>(a, rt, ct, lds.full);
+}
 
-  const float scale = gsa * gsw;
-  const int64_t we = (int64_t)rt.g * a.N;
+// Few rows per expert (up to MR per tile): a stream of the hit experts'
+// weights through MFMA. Wavefront = 32 weight rows (GLU: 16 gate rows and the
+// 16 up rows of the same outputs) times MR rows on 16x16x32 MFMAs, weights as
+// the row operand, so a lane ends up with 4 adjacent outputs of one row (and
+// with gate and up of the same output).
+//  * Weights: 256 K values (one 128-byte line of codes) per row and step,
+//    loaded 8 whole lines per instruction: the address unit takes a pass per
+//    line that an instruction touches, and a load in MFMA layout (16 bytes of
+//    each of 32 rows) touches four times as many. Two steps are in flight per
+//    wavefront; a step's codes pass through 4 KB of LDS private to the
+//    wavefront (16-byte pieces XOR-swizzled by row) into MFMA layout: lane
+//    (r, q) takes the 32 K values from 32 q of every 128 of row r.
+//  * Scales: windows of 512 K (32 bytes per row), likewise.
+//  * x: KB K values of the tile's rows, converted to fp16 q S once per
+//    workgroup into one of two LDS tiles (one barrier per KB).
+//  * Past D the x tile holds zeros, so whatever finite weights a padded step
+//    reads there add nothing.
+constexpr int kEsWaves = 4;
+constexpr int kEsThreads = 64 * kEsWaves;
+constexpr int kEsRows = 32;       // weight rows per wavefront
+constexpr int kEsSmallGrid = 256 * 6;  // workgroups that share a launch's items: two rounds of three per CU
+constexpr int kEsScaleLd = 36;    // LDS bytes per row of a scale window (32 + 4)
+
+template <int MR, int KB>
+struct StreamLds {
+  alignas(16) _Float16 x[2][MR * KB];
+  alignas(16) uint8_t codes[kEsWaves][kEsRows * 128];
+  alignas(16) uint8_t scales[kEsWaves][kEsRows * kEsScaleLd];
+};
+
+// Halves offset of 16-byte piece c of row r of an x tile.
+template <int KB>
+__device__ __forceinline__ int stream_x_at(int r, int c) {
+  return r * KB + 8 * (c ^ (r & 7));
+}
+
+// One tile. ALIGNED: D % 256 == 0, so scale rows can be read 16 bytes at a
+// time.
+template <bool GLU, int MR, int KB, bool ALIGNED>
+__device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTile& tile, StreamLds<MR, KB>& lds) {
+  constexpr int NT = MR / 16, NTHREADS = kEsThreads;
+  static_assert(KB == 256 || KB == 512, "whole steps");
+  constexpr int XP = MR * (KB / 32) / NTHREADS;  // 32-value pieces of x per thread and block
+  static_assert(XP * NTHREADS == MR * (KB / 32), "whole pieces per thread");
+  constexpr int SPB = KB / 256;  // steps per x block
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const RowTile& rt = tile.rt;
+  const float gsa = load_early(a.gsa), gsw = load_early(a.gsw + rt.g);
+  const int nr = rt.nr, F = a.N >> 1;
+  const int64_t rowc = a.D / 2, rows = a.D / 16, we = (int64_t)rt.g * a.N;
+  // This wavefront's first output (GLU) or weight row, and its two 16-row tiles.
+  const int o0 = (tile.ct * kEsWaves + wave) * (GLU ? 16 : 32);
+  const bool live0 = o0 < (GLU ? F : a.N), live1 = GLU ? live0 : o0 + 16 < a.N;
+  auto wrow = [&](int m) { return GLU ? (m ? F + o0 : o0) : o0 + 16 * m; };
+
   const __amdgpu_buffer_rsrc_t wcr = make_rsrc(a.wc + we * rowc, a.N * rowc);
   const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.ws + we * rows, a.N * rows);
-  // Weight row of this wavefront's u-th row (-1: behind the last one).
-  auto wrow = [&](int u) {
-    const int i = wave * kEvRowsPerWave + u;
-    if constexpr (GLU) {
-      const int f = ct * (kEvCols / 2) + (i >> 1);
-      return f < F ? (i & 1 ? F + f : f) : -1;
-    } else {
-      const int c = ct * kEvCols + i;
-      return c < a.N ? c : -1;
-    }
-  };
-  uint32_t oc[CPL], os[CPL];
+  uint32_t wo[4];
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) {
-    const int c = lane + 64 * i;
-    oc[i] = c < nch ? (uint32_t)(16 * c) : kMmaOob;
-    os[i] = c < nch ? (uint32_t)(2 * c) : kMmaOob;
+  for (int i = 0; i < 4; ++i)
+    wo[i] = ((i >> 1) ? live1 : live0) ? (uint32_t)((wrow(i >> 1) + 8 * (i & 1) + (lane >> 3)) * rowc + 16 * (lane & 7))
+                                       : kMmaOob;
+  u32x4_t wv[2][4];
+  auto load_w = [&](int slot, int step) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      wv[slot][i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wcr, wo[i] + 128 * step, 0, kNtAux));
+  };
+  // Scale window: lane = (row lane / 2, 16 bytes) of the 32 rows, or 2 bytes
+  // of 4 rows in each of 8 loads.
+  constexpr int SL = ALIGNED ? 1 : 8;
+  uint32_t so[SL];
+  if constexpr (ALIGNED) {
+    const int m = lane >> 5;
+    so[0] = (m ? live1 : live0) ? (uint32_t)((wrow(m) + ((lane >> 1) & 15)) * rows + 16 * (lane & 1)) : kMmaOob;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int m = i >> 2;
+      so[i] = (m ? live1 : live0) ? (uint32_t)((wrow(m) + 4 * (i & 3) + (lane >> 4)) * rows + 2 * (lane & 15)) : kMmaOob;
+    }
   }
-  u32x4_t wv[kEvInFlight][CPL];
-  uint32_t wsv[kEvInFlight][CPL];
-  auto load_row = [&](int slot, int u) {
-    // A row behind the last one re-reads row 0 (not used), so every offset
-    // stays in range or at kMmaOob plus less than 2^31.
-    const int w = max(wrow(u), 0);
-    const uint32_t rc = (uint32_t)w * (uint32_t)rowc, rs = (uint32_t)w * (uint32_t)rows;
+  u32x4_t sv16;
+  uint32_t sv2[SL];
+  auto load_s = [&](int win) {
+    if constexpr (ALIGNED) sv16 = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wsr, so[0] + 32 * win, 0, 0));
+    else {
 #pragma unroll
-    for (int i = 0; i < CPL; ++i) {
-      wv[slot][i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wcr, oc[i] + rc, 0, kNtAux));
-      wsv[slot][i] = __builtin_amdgcn_raw_buffer_load_b16(wsr, os[i] + rs, 0, kNtAux);
+      for (int i = 0; i < 8; ++i) sv2[i] = __builtin_amdgcn_raw_buffer_load_b16(wsr, so[i] + 32 * win, 0, 0);
     }
   };
+  uint8_t* my_codes = lds.codes[wave];
+  uint8_t* my_scales = lds.scales[wave];
+  auto store_s = [&]() {
+    if constexpr (ALIGNED) {
+      uint32_t* d = reinterpret_cast<uint32_t*>(my_scales + (lane >> 1) * kEsScaleLd + 16 * (lane & 1));
 #pragma unroll
-  for (int u = 0; u < kEvInFlight; ++u) load_row(u, u);
-  float gate[NR];
+      for (int i = 0; i < 4; ++i) d[i] = sv16[i];
+    } else {
 #pragma unroll
-  for (int u = 0; u < kEvRowsPerWave; ++u) {
-    const int slot = u % kEvInFlight, w = wrow(u);
-    float acc[NR];
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint16_t*>(my_scales + (4 * i + (lane >> 4)) * kEsScaleLd + 2 * (lane & 15)) = (uint16_t)sv2[i];
+    }
+  };
+
+  // x pieces of this thread: (row, 32-value piece of the block).
+  const uint8_t* xcp[XP];
+  const uint8_t* xsp[XP];
+  int xk[XP];
 #pragma unroll
-    for (int t = 0; t < NR; ++t) acc[t] = 0.0f;
+  for (int i = 0; i < XP; ++i) {
+    const int p = threadIdx.x + NTHREADS * i, r = p / (KB / 32);
+    xk[i] = 32 * (p % (KB / 32));
+    int t = -1;
+    if (r < nr) t = GLU ? row_token(a, rt.row0 + r) : rt.row0 + r;
+    if (t < 0) xk[i] = a.D;  // no such row: zeros
+    xcp[i] = a.xc + (int64_t)max(t, 0) * rowc;
+    xsp[i] = a.xs + (int64_t)max(t, 0) * rows;
+  }
+  u32x4_t xv[XP];
+  uint32_t xsv[XP];
+  auto load_x = [&](int k0) {
 #pragma unroll
-    for (int i = 0; i < CPL; ++i) {
-      const int c = min(lane + 64 * i, nch - 1);  // chunks past D hold zero weights
-      const _Float16 s0 = e4m3_f16(wsv[slot][i] & 0xFFu), s1 = e4m3_f16(wsv[slot][i] >> 8);
-      const half8_t w0 = fp4x8_to_f16(wv[slot][i][0], s0), w1 = fp4x8_to_f16(wv[slot][i][1], s0);
-      const half8_t w2 = fp4x8_to_f16(wv[slot][i][2], s1), w3 = fp4x8_to_f16(wv[slot][i][3], s1);
+    for (int i = 0; i < XP; ++i) {
+      // Clamped to the row's first piece past D; those values are zeroed below.
+      const int k = k0 + xk[i] < a.D ? k0 + xk[i] : 0;
+      xv[i] = *reinterpret_cast<const u32x4_t*>(xcp[i] + k / 2);
+      xsv[i] = *reinterpret_cast<const uint16_t*>(xsp[i] + k / 16);
+    }
+  };
+  auto store_x = [&](int k0, int buf) {
 #pragma unroll
-      for (int t = 0; t < NR; ++t) {
-        if (t < nr) {
-          const half8_t* xp = xg + (int64_t)t * (nch * 4) + 4 * c;
-          acc[t] += dot8(xp[1], w1, dot8(xp[0], w0, 0.0f));
-          acc[t] += dot8(xp[3], w3, dot8(xp[2], w2, 0.0f));
+    for (int i = 0; i < XP; ++i) {
+      const int p = threadIdx.x + NTHREADS * i, r = p / (KB / 32), c = p % (KB / 32);
+      const half2_t s = e4m3x2_f16(k0 + xk[i] < a.D ? xsv[i] : 0u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<half8_t*>(&lds.x[buf][stream_x_at<KB>(r, 4 * c + j)]) = fp4x8_scaled(xv[i][j], s, j >> 1);
+    }
+  };
+
+  const int nsteps = (a.D + 255) / 256;
+  load_x(0);
+  load_s(0);
+  load_w(0, 0);
+  load_w(1, 1);
+  store_x(0, 0);
+  __syncthreads();
+  f32x4_t acc[2][NT];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[m][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int r = lane & 15, q = lane >> 4;
+  for (int s0 = 0; s0 < nsteps; s0 += 2) {
+    // The window's scales; the next one's loads.
+    store_s();
+    load_s((s0 >> 1) + 1);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int step = s0 + u;
+      const int block = step / SPB, in = u % SPB, buf = block & 1;
+      // Before the weight loads: loads complete in order, and the wait for x
+      // at the end of the block must not wait for weights two steps ahead.
+      if (in == 0) load_x((block + 1) * KB);
+      // Codes through LDS into MFMA layout.
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 8 * i + (lane >> 3);
+        *reinterpret_cast<u32x4_t*>(my_codes + row * 128 + 16 * ((lane & 7) ^ (row & 7))) = wv[u][i];
+      }
+      load_w(u, step + 2);
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      if (step < nsteps) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          u32x4_t c[2];
+          half2_t s[2];
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            c[m] = *reinterpret_cast<const u32x4_t*>(my_codes + (16 * m + r) * 128 + 16 * ((4 * g + q) ^ (r & 7)));
+            s[m] = e4m3x2_f16(lds_u16(my_scales + (16 * m + r) * kEsScaleLd + 16 * u + 8 * g + 2 * q));
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            half8_t w[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) w[m] = fp4x8_scaled(c[m][j], s[m], j >> 1);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const half8_t xf = *reinterpret_cast<const half8_t*>(
+                  &lds.x[buf][stream_x_at<KB>(16 * t + r, 32 * in + 16 * g + 4 * q + j)]);
+#pragma unroll
+              for (int m = 0; m < 2; ++m) acc[m][t] = mfma16(w[m], xf, acc[m][t]);
+            }
+          }
         }
       }
-    }
-    if (u + kEvInFlight < kEvRowsPerWave) load_row(slot, u + kEvInFlight);
-    const float b = a.bias && w >= 0 ? a.bias[we + w] : 0.0f;
-#pragma unroll
-    for (int t = 0; t < NR; ++t) {
-      if (t < nr) {
-        const float y = wave_sum(acc[t]) * scale + b;
-        const int64_t p = rt.row0 + t;
-        if constexpr (GLU) {
-          if ((u & 1) == 0) gate[t] = y;
-          else if (lane == 0 && w >= 0)
-            static_cast<uint16_t*>(a.out)[p * F + (w - F)] = bf16_round(silu_mul(gate[t], y));
-        } else if (lane == 0 && w >= 0) {
-          static_cast<float*>(a.out)[p * a.N + w] = y;
-        }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      if (in == SPB - 1) {
+        store_x((block + 1) * KB, buf ^ 1);
+        __syncthreads();
       }
     }
+  }
+
+  // Lane (r, q), value v of tile m: row r (+ 16 t), weight row 4 q + v of the tile.
+  const float scale = gsa * gsw;
+  if constexpr (GLU) {
+    if (!live0) return;
+    const int f = o0 + 4 * q;
+    float bg[4] = {0.0f, 0.0f, 0.0f, 0.0f}, bu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.bias) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        bg[v] = a.bias[we + f + v];
+        bu[v] = a.bias[we + F + f + v];
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float y[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) y[v] = silu_mul(acc[0][t][v] * scale + bg[v], acc[1][t][v] * scale + bu[v]);
+      if (16 * t + r < nr) {
+        uint2* d = reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (int64_t)(rt.row0 + 16 * t + r) * F + f);
+        *d = make_uint2(bf16_round2(y[0], y[1]), bf16_round2(y[2], y[3]));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if (!(m ? live1 : live0)) continue;
+      const int n = o0 + 16 * m + 4 * q;
+      f32x4_t b = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (a.bias) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) b[v] = a.bias[we + n + v];
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        f32x4_t y;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) y[v] = acc[m][t][v] * scale + b[v];
+        if (16 * t + r < nr)
+          *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + (int64_t)(rt.row0 + 16 * t + r) * a.N + n) = y;
+      }
+    }
+  }
+}
+
+// SHARED: workgroups take items in turn; else one item each (the loop around
+// the tile costs some 50 registers, and with them one of the three workgroups
+// per CU that the LDS allows).
+template <bool GLU, int MR, int KB, bool ALIGNED, bool SHARED>
+__global__ __launch_bounds__(kEsThreads) void experts_stream_kernel(ExpertArgs a) {
+  constexpr int SH = MR == 16 ? 4 : 5;
+  static_assert(MR == 1 << SH, "rows per tile");
+  __shared__ StreamLds<MR, KB> lds;
+  const TileScan scan(a.offsets, a.G, a.R, SH, a.take, a.tile_cols);
+  ExpertTile tile;
+  for (int b = blockIdx.x; expert_tile(a, scan, GLU, b, tile); b += gridDim.x) {
+    if (GLU && tile.rt.g == a.G) zero_rows(a, tile.rt, kEsThreads);
+    else stream_tile<GLU, MR, KB, ALIGNED>(a, tile, lds);
+    if (!SHARED) return;
+    __syncthreads();  // the next item writes the LDS tiles
   }
 }
 
@@ -384,46 +579,40 @@ static hipError_t launch_mfma(ExpertArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool GLU, int CPL, int NR>
-static hipError_t launch_gemv_t(ExpertArgs a, hipStream_t stream) {
-  a.col_tiles = (a.N + kEvCols - 1) / kEvCols;
-  const int64_t nwg = max_row_tiles(a.R, a.G, NR == 1 ? 0 : (NR == 2 ? 1 : 2)) * a.col_tiles;
-  if (nwg >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-  experts_gemv_kernel<GLU, CPL, NR><<<(int)nwg, kEvThreads, (size_t)NR * a.D * sizeof(_Float16), stream>>>(a);
+template <bool GLU, int MR, int KB, bool SHARED>
+static hipError_t launch_stream(ExpertArgs a, hipStream_t stream) {
+  a.col_tiles = (a.N + kEsRows * kEsWaves - 1) / (kEsRows * kEsWaves);
+  const int64_t items = max_row_tiles(a.R, a.G, MR == 16 ? 4 : 5) * a.col_tiles;
+  if (items >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
+  // A launch of small experts beside the large ones is mostly empty: there
+  // each workgroup takes several items (129 thousand workgroups that had
+  // nothing to do took 140 us at T = 8192).
+  const int nwg = (int)(SHARED ? std::min<int64_t>(items, kEsSmallGrid) : items);
+  if (a.D % 256 == 0) experts_stream_kernel<GLU, MR, KB, true, SHARED><<<nwg, kEsThreads, 0, stream>>>(a);
+  else experts_stream_kernel<GLU, MR, KB, false, SHARED><<<nwg, kEsThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-template <bool GLU, int CPL>
-static hipError_t launch_gemv_n(const ExpertArgs& a, int nr, hipStream_t stream) {
-  if (nr == 1) return launch_gemv_t<GLU, CPL, 1>(a, stream);
-  if (nr == 2) return launch_gemv_t<GLU, CPL, 2>(a, stream);
-  return launch_gemv_t<GLU, CPL, 4>(a, stream);
-}
-
+// By the mean number of rows per expert, were every slot's expert held here:
+// up to 8 (T = 64 of 256 experts, k = 8: 433 us with 16-row tiles, 478 with
+// 32, 650 with the 128-row ones), up to 32 (T = 1024: 1211 us with 32-row
+// tiles, 1484 with 16, 1229 with 128); beyond that two launches share the
+// experts by their sizes, which only the device knows (an expert-parallel
+// rank's experts have a fraction of the mean, and a layer's popular experts
+// several times its others' rows).
 template <bool GLU>
-static hipError_t launch_gemv(const ExpertArgs& a, int nr, hipStream_t stream) {
-  const int cpl = ((a.D >> 5) + 63) / 64;
-  if (cpl <= 1) return launch_gemv_n<GLU, 1>(a, nr, stream);
-  if (cpl <= 2) return launch_gemv_n<GLU, 2>(a, nr, stream);
-  if (cpl <= 4) return launch_gemv_n<GLU, 4>(a, nr, stream);
-  return launch_gemv_n<GLU, 8>(a, nr, stream);
-}
-
-// Rows per GEMV tile, or 0 for the MFMA tiles.
-static int gemv_rows(int64_t T, int64_t R, int64_t G, int64_t D) {
-  if (D > 16384 || R > 4 * G) return 0;
-  const int nr = T == 1 ? 1 : (T == 2 ? 2 : 4);
-  return nr * D <= kEvMaxXHalves ? nr : (2 * D <= kEvMaxXHalves ? 2 : 1);
-}
-
-template <bool GLU>
-static hipError_t launch_products(const ExpertArgs& a, hipStream_t stream) {
-  const int nr = gemv_rows(a.T, a.R, a.G, a.D);
-  if (nr > 0) return launch_gemv<GLU>(a, nr, stream);
+static hipError_t launch_products(ExpertArgs a, hipStream_t stream) {
   const int64_t mean = a.R / a.G;
-  if (mean <= 32) return launch_mfma<GLU, 32, 1>(a, stream);
-  if (mean <= 64) return launch_mfma<GLU, 64, 1>(a, stream);
-  return launch_mfma<GLU, 128, 2>(a, stream);
+  a.take = Take::kAll;
+  if (mean <= 8) return launch_stream<GLU, 16, 512, false>(a, stream);
+  if (mean <= 32) return launch_stream<GLU, 32, 256, false>(a, stream);
+  constexpr int NTW = 2;
+  a.tile_cols = (a.N + 128 * NTW - 1) / (128 * NTW);
+  a.take = Take::kSmall;
+  const hipError_t e = launch_stream<GLU, 32, 256, true>(a, stream);
+  if (e != hipSuccess) return e;
+  a.take = Take::kLarge;
+  return launch_mfma<GLU, 128, NTW>(a, stream);
 }
 
 }  // namespace nvr
@@ -479,7 +668,7 @@ int grouped_swiglu(const uint8_t* x_codes, const uint8_t* x_scales, const float*
     return ROUTER_EINVAL;
   if (T == 0) return ROUTER_OK;
   const nvr::ExpertArgs a{x_codes, x_scales, gsa, w_codes, w_scales, gsw, bias, offsets, rows, out,
-                          (int)T, (int)k, (int)(T * k), (int)G, (int)(2 * F), (int)D, 0, 0};
+                          (int)T, (int)k, (int)(T * k), (int)G, (int)(2 * F), (int)D, 0, 0, nvr::Take::kAll, 0};
   return status_from(nvr::launch_products<true>(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -500,7 +689,7 @@ int grouped_combine(const uint8_t* h_codes, const uint8_t* h_scales, const float
   if (workspace_bytes < nvr::kScratchOffset + combine_scratch(T, k, D)) return ROUTER_EINVAL;
   float* y = reinterpret_cast<float*>(static_cast<char*>(workspace) + nvr::kScratchOffset);
   const nvr::ExpertArgs a{h_codes, h_scales, gsh, w_codes, w_scales, gsw, bias, offsets, nullptr, y,
-                          (int)T, (int)k, (int)(T * k), (int)G, (int)D, (int)F, 0, 0};
+                          (int)T, (int)k, (int)(T * k), (int)G, (int)D, (int)F, 0, 0, nvr::Take::kAll, 0};
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t cwg = (T * (D / 8) + 255) / 256;
   if (cwg >= (int64_t(1) << 31)) return ROUTER_EUNSUPPORTED;

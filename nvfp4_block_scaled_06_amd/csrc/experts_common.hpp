@@ -7,7 +7,7 @@
 // expert, the rows of no expert last. The host knows neither the sizes nor
 // the number of tiles, only that there are at most
 //   sum_g ceil(n_g / B) <= R / B + (experts with rows) <= R / B + min(R, G + 1)
-// of them, so it launches that many and the others exit.
+// of them.
 #pragma once
 
 #include "mma_tile.hpp"
@@ -31,65 +31,99 @@ __device__ __forceinline__ int wave_prefix_sum(int v) {
 struct RowTile {
   int g;     // expert; G: rows of no expert
   int row0;  // first row
-  int nr;    // rows (0: no such tile)
+  int nr;    // rows
 };
+
+// Experts by size: those with more rows than kSmallExpert are large when
+// there are enough of them to fill the GPU with 128-row tiles, i.e. when
+// `tile_cols` column tiles of their 128-row tiles give kMinTileItems work
+// items; otherwise every expert is small.
+constexpr int kSmallExpert = 32;
+constexpr int kMinTileItems = 512;
+enum class Take { kAll, kSmall, kLarge };
 
 // Every wavefront scans the offsets by itself: lane l holds experts 8l ..
 // 8l + 7. Offsets are clamped to [0, R] and a decreasing pair counts as no
 // rows (a precondition violation then stays inside the caller's buffers).
 struct TileScan {
   int off[kGroupsPerLane + 1];
-  int before;  // tiles of the experts of lower lanes
-  int experts, total;  // tiles of every expert; and of the rows of no expert too
-  int G, R, sh;
+  int before;   // tiles of the experts of lower lanes
+  int experts;  // tiles of every expert taken
+  int G, R, sh, above, upto;
 
-  __device__ __forceinline__ TileScan(const int32_t* offsets, int G_, int R_, int sh_) : G(G_), R(R_), sh(sh_) {
+  __device__ __forceinline__ TileScan(const int32_t* offsets, int G_, int R_, int sh_, Take take, int tile_cols)
+      : G(G_), R(R_), sh(sh_), above(0), upto(0x7FFFFFFF) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int i = 0; i <= kGroupsPerLane; ++i)
-      off[i] = offsets[min(kGroupsPerLane * lane + i, G)];
+    for (int i = 0; i <= kGroupsPerLane; ++i) off[i] = offsets[min(kGroupsPerLane * lane + i, G)];
 #pragma unroll
     for (int i = 0; i <= kGroupsPerLane; ++i) off[i] = min(max(off[i], 0), R);
+    if (take != Take::kAll) {
+      int big = 0;
+#pragma unroll
+      for (int i = 0; i < kGroupsPerLane; ++i) {
+        const int n = off[i + 1] - off[i];
+        big += n > kSmallExpert ? (n + 127) >> 7 : 0;
+      }
+      big = __builtin_amdgcn_readlane(wave_prefix_sum(big), 63);
+      const bool split = (int64_t)big * tile_cols >= kMinTileItems;
+      if (take == Take::kSmall) upto = split ? kSmallExpert : upto;
+      else above = split ? kSmallExpert : upto;
+    }
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < kGroupsPerLane; ++i) mine += tiles(i);
-    const int upto = wave_prefix_sum(mine);
-    before = upto - mine;
-    experts = __builtin_amdgcn_readlane(upto, 63);
-    total = experts + ((R - end() + (1 << sh) - 1) >> sh);
+    const int incl = wave_prefix_sum(mine);
+    before = incl - mine;
+    experts = __builtin_amdgcn_readlane(incl, 63);
   }
-  __device__ __forceinline__ int tiles(int i) const { return (max(off[i + 1] - off[i], 0) + (1 << sh) - 1) >> sh; }
+  __device__ __forceinline__ int tiles(int i) const {
+    const int n = off[i + 1] - off[i];
+    return n > above && n <= upto ? (n + (1 << sh) - 1) >> sh : 0;
+  }
+  // Tiles of the rows of no expert.
+  __device__ __forceinline__ int others() const { return (R - end() + (1 << sh) - 1) >> sh; }
   // First row of no expert.
   __device__ __forceinline__ int end() const { return __builtin_amdgcn_readlane(off[kGroupsPerLane], 63); }
 
-  __device__ __forceinline__ RowTile at(int n) const {
-    RowTile t;
-    if (n >= experts) {
-      t.g = G;
-      t.row0 = end() + ((n - experts) << sh);
-      t.nr = min(1 << sh, R - t.row0);
-      return t;
-    }
-    int g = 0, row0 = 0, nr = 0, c = before;
+  // Tile n of the rows of no expert.
+  __device__ __forceinline__ RowTile none(int n) const {
+    const int row0 = end() + (n << sh);
+    return {G, row0, min(1 << sh, R - row0)};
+  }
+
+  // Work item n < experts * cols: an expert's row tiles times `cols` column
+  // tiles, the row tiles of one column tile first, so that workgroups that
+  // read the same weights run side by side.
+  __device__ __forceinline__ RowTile at(int n, int cols, int& ct) const {
+    const int q = n / cols;  // a tile of the same expert
+    int g = 0, first = 0, rows = 0, base = 0, m = 0, c = before;
 #pragma unroll
     for (int i = 0; i < kGroupsPerLane; ++i) {
-      const int m = tiles(i);
-      if (n >= c && n < c + m) {
+      const int k = tiles(i);
+      if (q >= c && q < c + k) {
         g = kGroupsPerLane * (int)(threadIdx.x & 63) + i;
-        row0 = off[i] + ((n - c) << sh);
-        nr = min(1 << sh, off[i + 1] - row0);
+        first = off[i];
+        rows = off[i + 1] - off[i];
+        base = c;
+        m = k;
       }
-      c += m;
+      c += k;
     }
-    const int lane = (int)__builtin_ctzll(__ballot(nr > 0));  // one lane holds tile n
-    t.g = __builtin_amdgcn_readlane(g, lane);
-    t.row0 = __builtin_amdgcn_readlane(row0, lane);
-    t.nr = __builtin_amdgcn_readlane(nr, lane);
-    return t;
+    const int lane = (int)__builtin_ctzll(__ballot(m > 0));  // one lane holds the expert
+    g = __builtin_amdgcn_readlane(g, lane);
+    first = __builtin_amdgcn_readlane(first, lane);
+    rows = __builtin_amdgcn_readlane(rows, lane);
+    base = __builtin_amdgcn_readlane(base, lane);
+    m = __builtin_amdgcn_readlane(m, lane);
+    const int i = n - base * cols;  // of m * cols
+    ct = i / m;
+    const int r0 = (i - ct * m) << sh;
+    return {g, first + r0, min(1 << sh, rows - r0)};
   }
 };
 
-// Upper bound on TileScan::total.
+// Upper bound on the tiles of the experts and of the rows of no expert.
 inline int64_t max_row_tiles(int64_t R, int64_t G, int sh) { return (R >> sh) + (R < G + 1 ? R : G + 1); }
 
 // Workgroup b's number among `total` when the 8 XCDs (workgroups go to them

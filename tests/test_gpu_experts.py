@@ -116,22 +116,30 @@ def f64(t):
 
 # T, k, E, first, G, F, D, routing, bias: one line per path and edge.
 SWIGLU = [
-    (1, 8, 64, 0, 64, 64, 1024, "skewed", False),     # one token: one row per tile
+    # Up to 8 slots per expert: 16-row tiles.
+    (1, 8, 64, 0, 64, 64, 1024, "skewed", False),
     (1, 2, 4, 0, 4, 16, 32, "repeat", True),          # the smallest sizes
-    (2, 4, 32, 0, 32, 48, 2080, "skewed", True),      # two rows per tile, two chunks a lane
-    (3, 8, 40, 0, 40, 80, 7168, "skewed", False),     # four rows per tile, four chunks a lane
-    (2, 3, 16, 0, 16, 32, 16384, "skewed", True),     # eight chunks a lane
-    (33, 4, 64, 10, 40, 112, 512, "holes", True),     # few rows per expert, some of no expert
+    (2, 4, 32, 0, 32, 48, 2080, "skewed", True),      # D % 256 != 0
+    (3, 8, 40, 0, 40, 80, 7168, "skewed", False),
+    (2, 3, 16, 0, 16, 32, 16384, "skewed", True),
+    (2, 8, 2, 0, 2, 64, 16416, "repeat", False),
+    (33, 4, 64, 10, 40, 112, 512, "holes", True),     # some slots of no expert
     (4, 8, 256, 0, 256, 32, 256, "one", False),       # all rows in one of many experts
-    (64, 4, 16, 0, 16, 144, 512, "skewed", True),     # 32-row tiles, staged scales
-    (50, 4, 16, 0, 16, 64, 1056, "skewed", False),    # 32-row tiles, D not a multiple of 128
-    (2, 8, 2, 0, 2, 64, 16416, "repeat", False),      # D past the few-row path's limit
-    (100, 4, 12, 2, 8, 80, 768, "holes", True),       # 64-row tiles
-    (200, 2, 8, 0, 8, 208, 2080, "skewed", False),    # 64-row tiles, unstaged
-    (300, 4, 8, 0, 8, 320, 1024, "skewed", True),     # 128-row tiles, staged, two windows of it
-    (257, 6, 10, 0, 10, 96, 992, "holes", True),      # 128-row tiles, unstaged
+    (200, 8, 200, 0, 200, 144, 768, "one", True),     # 1600 rows of it, 100 tiles
+    (9, 3, 512, 5, 500, 48, 288, "skewed", False),    # many experts
+    # Up to 32: 32-row tiles.
+    (64, 4, 16, 0, 16, 144, 512, "skewed", True),
+    (50, 4, 16, 0, 16, 64, 1056, "skewed", False),
+    (16, 16, 16, 0, 16, 16, 32, "repeat", True),
+    (300, 3, 32, 1, 30, 176, 992, "holes", True),
+    # More: shared by size, all small here (too few rows for 128-row tiles) ...
+    (100, 4, 12, 2, 8, 80, 768, "holes", True),
+    (200, 2, 8, 0, 8, 208, 2080, "skewed", False),
     (129, 1, 3, 0, 1, 128, 256, "one", False),        # an expert without rows
     (40, 8, 4, 0, 4, 32, 256, "none", True),          # no rows at all
+    # ... and with 512 of those tiles and small experts beside them, scales staged and not.
+    (1400, 8, 40, 0, 40, 704, 512, "skewed", True),
+    (1300, 8, 44, 3, 38, 1408, 416, "holes", True),
 ]
 
 
@@ -154,7 +162,8 @@ def test_swiglu(dev, ws, T, k, E, first, G, F, D, kind, with_bias):
 
 
 COMBINE = [(T, k, E, first, G, max(16, F), 32 * max(1, D // 64), kind, b, i % 2 == 0)
-           for i, (T, k, E, first, G, F, D, kind, b) in enumerate(SWIGLU)]
+           for i, (T, k, E, first, G, F, D, kind, b) in enumerate(SWIGLU[:-2])]
+COMBINE += [(1400, 8, 40, 0, 40, 1360, 512, "skewed", True, True), (1300, 8, 44, 3, 38, 2816, 352, "holes", True, False)]
 
 
 @pytest.mark.parametrize("T,k,E,first,G,N,F,kind,with_bias,with_residual", COMBINE)
