@@ -15,7 +15,6 @@
 namespace nvr {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kPlanBins = kMaxGroups + 1;
 constexpr int kPlanChunk = 4096;     // slots per workgroup, at least
 constexpr int kPlanMaxChunks = 256;  // every workgroup reads every chunk's histogram
@@ -39,90 +38,134 @@ __device__ __forceinline__ int plan_bin(const PlanArgs& a, int s) {
 // One histogram per chunk of slots.
 __global__ __launch_bounds__(kPlanThreads) void plan_hist_kernel(PlanArgs a) {
   __shared__ int h[kPlanBins];
+  const int s0 = blockIdx.x * a.chunk, s1 = min(s0 + a.chunk, a.R);
   for (int i = threadIdx.x; i <= a.G; i += kPlanThreads) h[i] = 0;
   __syncthreads();
-  const int s0 = blockIdx.x * a.chunk, s1 = min(s0 + a.chunk, a.R);
   for (int s = s0 + threadIdx.x; s < s1; s += kPlanThreads) atomicAdd(&h[plan_bin(a, s)], 1);
   __syncthreads();
   for (int i = threadIdx.x; i <= a.G; i += kPlanThreads) a.hist[(int64_t)blockIdx.x * (a.G + 1) + i] = h[i];
 }
 
-// Places one chunk's slots. Each wavefront owns a contiguous segment of the
-// chunk: it counts its slots per bin, the workgroup turns the counts into
-// first rows (bins in order, chunks in order inside a bin, wavefronts in
-// order inside a chunk), and the wavefront places 64 slots at a time, a
-// slot's rank among the 64 being the number of lower lanes with its bin (one
-// ballot per bit of the bin).
-__global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(PlanArgs a) {
-  __shared__ int h[kPlanWaves][kPlanBins];
-  __shared__ int wsum[kPlanWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nb = a.G + 1;
-  for (int i = threadIdx.x; i < kPlanWaves * kPlanBins; i += kPlanThreads) (&h[0][0])[i] = 0;
-  __syncthreads();
-  const int s0 = blockIdx.x * a.chunk, s1 = min(s0 + a.chunk, a.R);
-  const int seg = ((s1 - s0 + kPlanWaves - 1) / kPlanWaves + 63) & ~63;
-  const int b0 = min(s0 + wave * seg, s1), b1 = min(b0 + seg, s1);
-  for (int s = b0 + lane; s < b1; s += 64) atomicAdd(&h[wave][plan_bin(a, s)], 1);
-  __syncthreads();
+// Places one chunk's slots. Each of WAVES wavefronts owns a contiguous segment
+// of the chunk: it counts its slots per bin, the workgroup turns the counts
+// into first rows (bins in order, chunks in order inside a bin, wavefronts in
+// order inside a chunk), and the wavefront places 64 slots at a time, a slot's
+// rank among the 64 being the number of lower lanes with its bin (one ballot
+// per bit of the bin). A thread's first kPlanHeld slots stay in registers
+// between the two. With several chunks the threads share the chunks'
+// histograms of each bin, all loads of a share in flight at once.
+constexpr int kPlanHeld = 4;
 
-  // Totals of every bin over all chunks, and over the lower chunks only.
-  const int i = threadIdx.x;
-  int total = 0, low = 0;
-  if (i < nb) {
-    if (gridDim.x > 1) {
-      for (int c = 0; c < (int)gridDim.x; ++c) {
-        const int v = a.hist[(int64_t)c * nb + i];
-        total += v;
-        low += c < (int)blockIdx.x ? v : 0;
-      }
-    } else {
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void plan_place_kernel(PlanArgs a) {
+  constexpr int NT = 64 * WAVES;
+  __shared__ int h[WAVES][kPlanBins];
+  __shared__ int total[kPlanBins], low[kPlanBins];  // a bin's slots in all chunks, and in lower ones
+  __shared__ int wsum[WAVES];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nb = a.G + 1;
+  const int s0 = blockIdx.x * a.chunk, s1 = min(s0 + a.chunk, a.R);
+  const int seg = ((s1 - s0 + WAVES - 1) / WAVES + 63) & ~63;
+  const int b0 = min(s0 + wave * seg, s1), b1 = min(b0 + seg, s1);
+  int held[kPlanHeld];
 #pragma unroll
-      for (int w = 0; w < kPlanWaves; ++w) total += h[w][i];
+  for (int j = 0; j < kPlanHeld; ++j) held[j] = b0 + 64 * j + lane < b1 ? plan_bin(a, b0 + 64 * j + lane) : -1;
+  for (int w = 0; w < WAVES; ++w)
+    for (int i = threadIdx.x; i < nb; i += NT) h[w][i] = 0;
+  for (int i = threadIdx.x; i < nb; i += NT) total[i] = low[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kPlanHeld; ++j)
+    if (held[j] >= 0) atomicAdd(&h[wave][held[j]], 1);
+  for (int s = b0 + 64 * kPlanHeld + lane; s < b1; s += 64) atomicAdd(&h[wave][plan_bin(a, s)], 1);
+  if (gridDim.x > 1) {
+    const int chunks = gridDim.x, shares = max(NT / nb, 1), each = (chunks + shares - 1) / shares;
+    for (int i = threadIdx.x; i < shares * nb; i += NT) {
+      const int bin = i % nb, c0 = (i / nb) * each, c1 = min(c0 + each, chunks);
+      int t = 0, l = 0;
+      for (int c = c0; c < c1; c += 16) {
+        int v[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) v[u] = a.hist[(int64_t)min(c + u, c1 - 1) * nb + bin];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const int n = c + u < c1 ? v[u] : 0;
+          t += n;
+          l += c + u < (int)blockIdx.x ? n : 0;
+        }
+      }
+      atomicAdd(&total[bin], t);
+      atomicAdd(&low[bin], l);
     }
   }
-  // Exclusive scan over the bins (kPlanBins <= kPlanThreads).
-  const int incl = wave_prefix_sum(total);
+  __syncthreads();
+
+  // Exclusive scan over the bins, kPerThread adjacent ones per thread.
+  constexpr int kPerThread = (kPlanBins + NT - 1) / NT;
+  const int i0 = threadIdx.x * kPerThread;
+  int sum = 0, mine[kPerThread];
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const int i = i0 + j;
+    int n = 0;
+    if (i < nb) {
+      if (gridDim.x > 1) n = total[i];
+      else {
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) n += h[w][i];
+      }
+    }
+    mine[j] = n;
+    sum += n;
+  }
+  const int incl = wave_prefix_sum(sum);
   if (lane == 63) wsum[wave] = incl;
   __syncthreads();
-  int base = 0;
+  int at = incl - sum;
 #pragma unroll
-  for (int w = 0; w < kPlanWaves; ++w) base += w < wave ? wsum[w] : 0;
-  if (i < nb) {
-    const int r = base + incl - total;
-    if (blockIdx.x == 0) a.offsets[i] = r;  // offsets[G]: the rows of bins below G
-    int at = r + low;
+  for (int w = 0; w < WAVES; ++w) at += w < wave ? wsum[w] : 0;
 #pragma unroll
-    for (int w = 0; w < kPlanWaves; ++w) {
-      const int n = h[w][i];
-      h[w][i] = at;
-      at += n;
+  for (int j = 0; j < kPerThread; ++j) {
+    const int i = i0 + j;
+    if (i < nb) {
+      if (blockIdx.x == 0) a.offsets[i] = at;  // offsets[G]: the rows of bins below G
+      int p = at + low[i];
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        const int n = h[w][i];
+        h[w][i] = p;
+        p += n;
+      }
+      at += mine[j];
     }
   }
   __syncthreads();
 
   const int bits = 32 - __builtin_clz((unsigned)a.G);
-  for (int s = b0 + lane; __any(s < b1); s += 64) {
-    const bool ok = s < b1;
-    const int e = ok ? plan_bin(a, s) : a.G;
+  auto place = [&](int s, int e) {  // 64 slots, e < 0: none
+    const bool ok = e >= 0;
     uint64_t peers = __ballot(ok);
     for (int b = 0; b < bits; ++b) {
       const uint64_t m = __ballot((e >> b) & 1);
       peers &= ((e >> b) & 1) ? m : ~m;
     }
-    const int rank = (int)__popcll(peers & ((1ull << lane) - 1ull));
     if (ok) {
-      const int p = h[wave][e] + rank;
+      const int p = h[wave][e] + (int)__popcll(peers & ((1ull << lane) - 1ull));
       a.rows[p] = e < a.G ? s : -1;
       a.pos[s] = e < a.G ? p : -1;
     }
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
     // The last peer moves the bin's next row on (LDS accesses of one
     // wavefront are processed in order).
     if (ok && (peers >> lane) == 1ull) h[wave][e] += (int)__popcll(peers);
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  }
+  };
+#pragma unroll
+  for (int j = 0; j < kPlanHeld; ++j)
+    if (b0 + 64 * j < b1) place(b0 + 64 * j + lane, held[j]);
+  for (int s = b0 + 64 * kPlanHeld; s < b1; s += 64) place(s + lane, s + lane < b1 ? plan_bin(a, s + lane) : -1);
 }
 
 static int plan_chunk(int64_t R) {
@@ -160,6 +203,8 @@ extern "C" int grouped_plan(const int32_t* topk_idx, int64_t T, int64_t k, int64
     nvr::plan_hist_kernel<<<chunks, nvr::kPlanThreads, 0, s>>>(a);
     if (hipGetLastError() != hipSuccess) return ROUTER_EHIP;
   }
-  nvr::plan_place_kernel<<<chunks, nvr::kPlanThreads, 0, s>>>(a);
+  // Few slots: fewer wavefronts, whose counts are quicker to scan.
+  if (R <= 256) nvr::plan_place_kernel<4><<<1, 256, 0, s>>>(a);
+  else nvr::plan_place_kernel<16><<<chunks, 1024, 0, s>>>(a);
   return hipGetLastError() == hipSuccess ? ROUTER_OK : ROUTER_EHIP;
 }

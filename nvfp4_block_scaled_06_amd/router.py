@@ -349,17 +349,30 @@ def grouped_workspace_bytes(T, k, G, D, F):
     return int(n)
 
 
-def _tensor(t, name, dtype, shape, device, contiguous=True):
-    """A GPU tensor of this dtype, shape and device, or RouterError."""
-    _device_tensor(t, name, (dtype,)) if contiguous else None
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape):
-        raise RouterError(f"{name} must be {dtype} {tuple(shape)} on {device}")
-    return t
+def _tensor(t, name, dtype, shape, device):
+    """A contiguous GPU tensor of this dtype, shape and device, or RouterError."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != device or \
+            not t.is_contiguous():
+        raise RouterError(f"{name} must be a contiguous {dtype} {tuple(shape)} on {device}")
 
 
-def _on(device):
-    """The library launches on the current device: make it the tensors' own."""
-    return torch.cuda.device(device)
+def _gpu(device):
+    if device.type != "cuda":
+        raise RouterError("GPU tensors are required")
+    return device
+
+
+def _call(fn, device, *args):
+    """One library call on the tensors' device and its current stream (tensors as pointers, None and empty ones as
+    NULL); raises on a non-zero status."""
+    i = device.index
+    if torch.cuda.current_device() != i:
+        with torch.cuda.device(i):
+            return _call(fn, device, *args)
+    a = [(x.data_ptr() or None) if isinstance(x, torch.Tensor) else x for x in args]
+    status = fn(*a, torch.cuda.current_stream(i).cuda_stream)
+    if status != ROUTER_OK:
+        _check(status)
 
 
 class GroupedPlan:
@@ -375,34 +388,37 @@ class GroupedPlan:
 
 
 def empty_plan(T, k, G, device="cuda"):
-    i32 = dict(dtype=torch.int32, device=device)
-    return GroupedPlan(torch.empty(G + 1, **i32), torch.empty(T * k, **i32), torch.empty(T * k, **i32), T, k)
+    buf = torch.empty(G + 1 + 2 * T * k, dtype=torch.int32, device=device)
+    offsets, rows, pos = buf.split((G + 1, T * k, T * k))
+    return GroupedPlan(offsets, rows, pos, T, k)
 
 
 def _check_plan(plan, dev, G):
-    R = plan.T * plan.k
+    R = (plan.T * plan.k,)
     _tensor(plan.offsets, "plan offsets", torch.int32, (G + 1,), dev)
-    _tensor(plan.rows, "plan rows", torch.int32, (R,), dev)
-    _tensor(plan.pos, "plan pos", torch.int32, (R,), dev)
+    _tensor(plan.rows, "plan rows", torch.int32, R, dev)
+    _tensor(plan.pos, "plan pos", torch.int32, R, dev)
 
 
 def _check_workspace(workspace, dev):
-    if workspace.buf.device != dev:
-        raise RouterError(f"the workspace is on {workspace.buf.device}, not on {dev}")
+    if not isinstance(workspace, Workspace) or workspace.buf.device != dev:
+        raise RouterError(f"a workspace on {dev} is required")
 
 
 def _check_grouped(xq, wg, rows):
     """NVFP4 operands of a grouped product: x [rows, D] and weights [G, N, D], on one device."""
-    dev, D = xq.codes.device, xq.D
-    _tensor(xq.codes, "x codes", torch.uint8, (rows, D // 2), dev)
-    _tensor(xq.scales, "x scales", torch.uint8, (rows, D // 16), dev)
-    _tensor(xq.gscale, "x global scale", torch.float32, (1,), dev)
-    if wg.D != D:
+    xc, wc = xq.codes, wg.codes
+    dev, D2 = _gpu(xc.device), xc.shape[-1]
+    if wc.dim() != 3 or wc.shape[2] != D2 or D2 % 8:
         raise RouterError("grouped weights do not match x")
-    _tensor(wg.codes, "w codes", torch.uint8, (wg.G, wg.N, D // 2), dev)
-    _tensor(wg.scales, "w scales", torch.uint8, (wg.G, wg.N, D // 16), dev)
-    _tensor(wg.gscale, "w global scales", torch.float32, (wg.G,), dev)
-    return dev
+    G, N = wc.shape[:2]
+    _tensor(xc, "x codes", torch.uint8, (rows, D2), dev)
+    _tensor(xq.scales, "x scales", torch.uint8, (rows, D2 // 8), dev)
+    _tensor(xq.gscale, "x global scale", torch.float32, (1,), dev)
+    _tensor(wc, "w codes", torch.uint8, (G, N, D2), dev)
+    _tensor(wg.scales, "w scales", torch.uint8, (G, N, D2 // 8), dev)
+    _tensor(wg.gscale, "w global scales", torch.float32, (G,), dev)
+    return dev, G, N, 2 * D2
 
 
 def grouped_plan(topk_idx, G, workspace, first_expert=0, out=None):
@@ -412,58 +428,54 @@ def grouped_plan(topk_idx, G, workspace, first_expert=0, out=None):
     T, k = topk_idx.shape
     dev = topk_idx.device
     _check_workspace(workspace, dev)
-    with _on(dev):
-        if out is None:
-            out = empty_plan(T, k, G, dev)
-        elif (out.T, out.k) != (T, k):
+    if out is None:
+        out = empty_plan(T, k, max(int(G), 0), dev)
+    else:
+        if (out.T, out.k) != (T, k):
             raise RouterError("the plan does not match topk_idx")
         _check_plan(out, dev, G)
-        _check(load_library().grouped_plan(_ptr(topk_idx), T, k, int(first_expert), G, _ptr(out.offsets),
-                                           _ptr(out.rows), _ptr(out.pos), _ptr(workspace.buf), workspace.nbytes,
-                                           _stream()))
+    _call(load_library().grouped_plan, dev, topk_idx, T, k, int(first_expert), G, out.offsets, out.rows, out.pos,
+          workspace.buf, workspace.nbytes)
     return out
 
 
 def grouped_swiglu(xq, wg, plan, bias=None, out=None):
     """grouped_swiglu: out [T * k, F] bf16, row p being silu(gate) * up of its token's row of xq [T, D] under its
     expert's weights wg [G, 2F, D] (F gate rows, then F up rows) and bias [G, 2F] fp32; rows of no expert are zeros."""
-    dev = _check_grouped(xq, wg, plan.T)
-    _check_plan(plan, dev, wg.G)
-    if wg.N % 2:
+    dev, G, N, D = _check_grouped(xq, wg, plan.T)
+    _check_plan(plan, dev, G)
+    if N % 2:
         raise RouterError("gate and up weights need an even number of rows")
-    R, F = plan.T * plan.k, wg.N // 2
+    R, F = plan.T * plan.k, N // 2
     if bias is not None:
-        _tensor(bias, "bias", torch.float32, (wg.G, wg.N), dev)
-    with _on(dev):
-        if out is None:
-            out = torch.empty((R, F), dtype=torch.bfloat16, device=dev)
+        _tensor(bias, "bias", torch.float32, (G, N), dev)
+    if out is None:
+        out = torch.empty((R, F), dtype=torch.bfloat16, device=dev)
+    else:
         _tensor(out, "out", torch.bfloat16, (R, F), dev)
-        _check(load_library().grouped_swiglu(_ptr(xq.codes), _ptr(xq.scales), _ptr(xq.gscale), _ptr(wg.codes),
-                                             _ptr(wg.scales), _ptr(wg.gscale), _ptr(bias), _ptr(plan.offsets),
-                                             _ptr(plan.rows), plan.T, plan.k, wg.G, F, xq.D, _ptr(out), _stream()))
+    _call(load_library().grouped_swiglu, dev, xq.codes, xq.scales, xq.gscale, wg.codes, wg.scales, wg.gscale, bias,
+          plan.offsets, plan.rows, plan.T, plan.k, G, F, D, out)
     return out
 
 
 def grouped_combine(hq, wg, plan, topk_w, workspace, bias=None, residual=None, out=None):
     """grouped_combine: out [T, D] bf16 = residual + the topk_w-weighted sum of each token's rows of hq [T * k, F]
     times its expert's weights wg [G, D, F] plus bias [G, D] fp32; residual may be out itself."""
-    T, k, D = plan.T, plan.k, wg.N
-    dev = _check_grouped(hq, wg, T * k)
-    _check_plan(plan, dev, wg.G)
+    T, k = plan.T, plan.k
+    dev, G, D, F = _check_grouped(hq, wg, T * k)
+    _check_plan(plan, dev, G)
     _check_workspace(workspace, dev)
     _tensor(topk_w, "topk_w", torch.float32, (T, k), dev)
     if bias is not None:
-        _tensor(bias, "bias", torch.float32, (wg.G, D), dev)
+        _tensor(bias, "bias", torch.float32, (G, D), dev)
     if residual is not None:
         _tensor(residual, "residual", torch.bfloat16, (T, D), dev)
-    with _on(dev):
-        if out is None:
-            out = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+    if out is None:
+        out = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+    else:
         _tensor(out, "out", torch.bfloat16, (T, D), dev)
-        _check(load_library().grouped_combine(_ptr(hq.codes), _ptr(hq.scales), _ptr(hq.gscale), _ptr(wg.codes),
-                                              _ptr(wg.scales), _ptr(wg.gscale), _ptr(bias), _ptr(plan.offsets),
-                                              _ptr(plan.pos), _ptr(topk_w), _ptr(residual), T, k, wg.G, D, hq.D,
-                                              _ptr(out), _ptr(workspace.buf), workspace.nbytes, _stream()))
+    _call(load_library().grouped_combine, dev, hq.codes, hq.scales, hq.gscale, wg.codes, wg.scales, wg.gscale, bias,
+          plan.offsets, plan.pos, topk_w, residual, T, k, G, D, F, out, workspace.buf, workspace.nbytes)
     return out
 
 
@@ -503,7 +515,8 @@ def lmhead_penalize(logits, workspace, history=None, prompt=None, lengths=None, 
         raise RouterError("out must have the dtype, shape, device and row stride of logits")
     L = ldh = ldm = nbias = 0
     if history is not None:
-        L, ldh = history.shape[-1], _rows_tensor(history, "history", (torch.int32,), T)
+        ldh = _rows_tensor(history, "history", (torch.int32,), T)
+        L = history.shape[1]
     for name, t, dtype in (("lengths", lengths, torch.int32), ("prompt", prompt, torch.int32),
                            ("repetition", repetition, torch.float32), ("frequency", frequency, torch.float32),
                            ("presence", presence, torch.float32)):
@@ -523,14 +536,13 @@ def lmhead_penalize(logits, workspace, history=None, prompt=None, lengths=None, 
     for name, t in (("history", history), ("mask", mask)):
         if t is not None and t.device != dev:
             raise RouterError(f"{name} must be on {dev}")
-    with _on(dev):
-        idx = torch.empty(T, dtype=torch.int32, device=dev)
-        logit = torch.empty(T, dtype=torch.float32, device=dev)
-        _check(load_library().lmhead_penalize(
-            _ptr(logits), 0 if logits.dtype == torch.float32 else 1, T, N, ld, _ptr(history), L, ldh, _ptr(lengths),
-            _ptr(prompt), _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(start), _ptr(token), _ptr(value),
-            nbias, _ptr(mask), ldm, _ptr(out), _ptr(idx), _ptr(logit), _ptr(workspace.buf), workspace.nbytes,
-            _stream()))
+    if history is not None and L == 0:
+        history = lengths = prompt = None
+    idx = torch.empty(T, dtype=torch.int32, device=dev)
+    logit = torch.empty(T, dtype=torch.float32, device=dev)
+    _call(load_library().lmhead_penalize, dev, logits, 0 if logits.dtype == torch.float32 else 1, T, N, ld, history, L,
+          ldh, lengths, prompt, repetition, frequency, presence, start, token, value, nbias, mask, ldm, out, idx, logit,
+          workspace.buf, workspace.nbytes)
     return idx, logit, out
 
 
