@@ -27,7 +27,7 @@ struct ExpertArgs {
   const int32_t* rows;     // swiglu: [R]
   void* out;               // swiglu: bf16 [R, N/2]; combine: fp32 [R, N] products
   int T, k, R, G, N, D;
-  int col_tiles, nsteps;
+  int col_tiles;
   Take take;      // which experts this launch takes
   int tile_cols;  // column tiles of the 128-row tile kernel
 };
@@ -75,177 +75,6 @@ __device__ __forceinline__ void zero_rows(const ExpertArgs& a, const RowTile& t,
   for (int64_t i = threadIdx.x; i < t.nr * per_row; i += nthreads) out[i] = u32x4_t{0u, 0u, 0u, 0u};
 }
 
-// Scale row offsets of a tile of gathered rows (A) and paired weight rows
-// (B), from a table in LDS.
-struct TableRows {
-  const uint32_t* tab;
-  int bm;
-  __device__ __forceinline__ uint32_t operator()(bool isA, int rr) const { return tab[isA ? rr : bm + rr]; }
-};
-
-// LDS of one tile: the A tiles, the scale windows and the row table.
-template <bool GLU, int BM, int NTW, int KS, bool STAGED>
-struct ExpertLds {
-  alignas(16) _Float16 abuf[KS][2][BM * kMmaARow];
-  alignas(16) uint8_t swin[STAGED ? mma_win_bytes<BM, NTW>() : 16];
-  uint32_t srow[GLU ? BM + 128 * NTW : 1];
-};
-
-// One tile of up to BM rows of an expert times 128 NTW weight rows on the
-// shared MFMA tile. GLU: the rows are gathered, and each 32-column tile holds
-// 16 gate rows and the 16 up rows of the same outputs, so that one lane swap
-// brings the two halves of an output together.
-template <bool GLU, int BM, int NTW, int KS, bool STAGED>
-__device__ __forceinline__ void experts_tile(const ExpertArgs& a, const RowTile& rt, int ct,
-                                             ExpertLds<GLU, BM, NTW, KS, STAGED>& lds) {
-  static_assert(KS == mma_ksplit<BM, NTW>(), "K groups as the main loop has them");
-  constexpr int BN = 128 * NTW;
-  static_assert(KS == 1 || BM * BN * sizeof(float) <= sizeof(_Float16) * KS * 2 * BM * kMmaARow,
-                "the epilogue's partial sums fit in the A tiles' LDS");
-  _Float16* abuf = &lds.abuf[0][0][0];
-  uint32_t* srow = lds.srow;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wt = wave & 3, grp = wave >> 2;
-  const int row0 = rt.row0, nr = rt.nr;
-  const float gsa = load_early(a.gsa), gsw = load_early(a.gsw + rt.g);
-  const int64_t rowc = a.D / 2, rows = a.D / 16;
-  const int r = lane & 31, h = lane >> 5, F = a.N >> 1;
-  const int64_t we = (int64_t)rt.g * a.N;
-  MmaPtrs<BM, NTW> P;
-  if constexpr (GLU) {
-    const int f0 = ct * (BN / 2);
-    P.xc = make_rsrc(a.xc, a.T * rowc);
-    P.xs = make_rsrc(a.xs, a.T * rows);
-    P.wc = make_rsrc(a.wc + we * rowc, a.N * rowc);
-    P.ws = make_rsrc(a.ws + we * rows, a.N * rows);
-    const int tid = threadIdx.x & (kMmaThreads - 1), q = tid & 3;
-    P.ka = 32 * q;
-    P.kb = 32 * h;
-#pragma unroll
-    for (int i = 0; i < mma_row_slots<BM>(); ++i) {
-      const int rl = (tid >> 2) + 64 * i;
-      const int t = rl < nr ? row_token(a, row0 + min(rl, nr - 1)) : -1;
-      P.a[i] = t >= 0 ? (uint32_t)(t * rowc + 16 * q) : kMmaOob;
-      P.as[i] = t >= 0 ? (uint32_t)(t * rows + 2 * q) : kMmaOob;
-    }
-    // Column c of the tile: the 16 gate rows, then the 16 up rows, of 16 outputs.
-    auto wrow = [&](int c) {
-      const int f = f0 + 16 * (c >> 5) + (c & 15);
-      return f < F ? (c & 16 ? F + f : f) : -1;
-    };
-#pragma unroll
-    for (int t = 0; t < NTW; ++t) {
-      const int w = wrow((wt + 4 * t) * 32 + r);
-      P.b[t] = w >= 0 ? (uint32_t)(w * rowc + 16 * h) : kMmaOob;
-      P.bs[t] = w >= 0 ? (uint32_t)(w * rows + 2 * h) : kMmaOob;
-    }
-    if constexpr (STAGED) {
-      for (int i = threadIdx.x; i < BM + BN; i += kMmaThreads * KS) {
-        const int v = i < BM ? (i < nr ? row_token(a, row0 + i) : -1) : wrow(i - BM);
-        srow[i] = v >= 0 ? (uint32_t)(v * rows) : kMmaOob;
-      }
-      __syncthreads();
-    }
-  } else {
-    const int col0 = ct * BN;
-    P = mma_ptrs<BM, NTW>(a.xc + row0 * rowc, a.xs + row0 * rows, nr, a.wc + (we + col0) * rowc,
-                          a.ws + (we + col0) * rows, min(BN, a.N - col0), a.D, wt, lane);
-  }
-  constexpr int NS = mma_sets<BM, NTW>();
-  f32x16_t acc[NS][BM / 32][NTW];
-  if constexpr (GLU)
-    mma_mainloop<BM, NTW, KS, STAGED>(P, a.D, a.nsteps, abuf, lds.swin, lane, acc, TableRows{srow, BM});
-  else
-    mma_mainloop<BM, NTW, KS, STAGED>(P, a.D, a.nsteps, abuf, lds.swin, lane, acc);
-
-  // 32x32 accumulator layout: value v of lane (r, h) is row 8(v/4) + 4h +
-  // v%4, column r of its tile; wavefront wt holds the column tiles wt + 4t.
-  float* part = reinterpret_cast<float*>(abuf);  // [BM][BN], K group 1's sums
-  if (KS == 2 && grp == 1) {
-#pragma unroll
-    for (int rt2 = 0; rt2 < BM / 32; ++rt2)
-#pragma unroll
-      for (int t = 0; t < NTW; ++t)
-#pragma unroll
-        for (int v = 0; v < 16; ++v)
-          part[(rt2 * 32 + 8 * (v >> 2) + 4 * h + (v & 3)) * BN + (wt + 4 * t) * 32 + r] = acc[0][rt2][t][v];
-  }
-  if (KS == 2) __syncthreads();
-  if (grp != 0) return;
-  const float scale = gsa * gsw;
-#pragma unroll
-  for (int t = 0; t < NTW; ++t) {
-    const int c = (wt + 4 * t) * 32 + r;
-    if constexpr (GLU) {
-      const int f = ct * (BN / 2) + 16 * (wt + 4 * t) + (r & 15);
-      const bool ok = f < F;
-      float bg = 0.0f, bu = 0.0f;
-      if (a.bias) {
-        const float* b = a.bias + we + min(f, F - 1);
-        bg = b[0];
-        bu = b[F];
-      }
-#pragma unroll
-      for (int rt2 = 0; rt2 < BM / 32; ++rt2)
-#pragma unroll
-        for (int v = 0; v < 8; ++v) {
-          float y0 = acc[0][rt2][t][v], y1 = acc[0][rt2][t][v + 8];
-          if (KS == 2) {
-            const int rr = rt2 * 32 + 8 * (v >> 2) + 4 * h + (v & 3);
-            y0 += part[rr * BN + c];
-            y1 += part[(rr + 16) * BN + c];
-          }
-          // Lanes r < 16 hold gates and lanes r >= 16 ups of outputs f; after
-          // the swap the former hold both of value v, the latter of v + 8.
-          const auto sw = __builtin_amdgcn_permlane16_swap(__float_as_uint(y0), __float_as_uint(y1), false, false);
-          const float g = __uint_as_float(sw[0]) * scale + bg, u = __uint_as_float(sw[1]) * scale + bu;
-          const int rr = rt2 * 32 + 8 * (v >> 2) + (r & 16) + 4 * h + (v & 3);
-          if (rr < nr && ok)
-            static_cast<uint16_t*>(a.out)[(int64_t)(row0 + rr) * F + f] = bf16_round(silu_mul(g, u));
-        }
-    } else {
-      const int col = ct * BN + c;
-      const bool ok = col < a.N;
-      const float b = a.bias ? a.bias[we + min(col, a.N - 1)] : 0.0f;
-#pragma unroll
-      for (int rt2 = 0; rt2 < BM / 32; ++rt2)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int rr = rt2 * 32 + 8 * (v >> 2) + 4 * h + (v & 3);
-          float y = acc[0][rt2][t][v];
-          if (KS == 2) y += part[rr * BN + c];
-          if (rr < nr && ok) static_cast<float*>(a.out)[(int64_t)(row0 + rr) * a.N + col] = y * scale + b;
-        }
-    }
-  }
-}
-
-// Workgroup (row tile of up to BM rows of an expert, column tile). A ragged
-// last tile with at most half the rows takes the 64-row tile instead of the
-// 128-row one, which costs it little more than half as much.
-template <bool GLU, int BM, int NTW, int KS, bool STAGED>
-__global__ __launch_bounds__(kMmaThreads * KS) __attribute__((amdgpu_waves_per_eu(KS, KS))) void experts_mfma_kernel(
-    ExpertArgs a) {
-  constexpr int SH = BM == 32 ? 5 : (BM == 64 ? 6 : 7);
-  static_assert(BM == 1 << SH, "rows per tile");
-  constexpr bool kHalf = BM == 128 && mma_ksplit<64, NTW>() == KS;
-  __shared__ union {
-    ExpertLds<GLU, BM, NTW, KS, STAGED> full;
-    ExpertLds<GLU, kHalf ? 64 : BM, NTW, KS, STAGED> half;
-  } lds;
-  const TileScan scan(a.offsets, a.G, a.R, SH, a.take, a.tile_cols);
-  ExpertTile tile;
-  if (!expert_tile(a, scan, false, blockIdx.x, tile)) return;
-  const RowTile& rt = tile.rt;
-  const int ct = tile.ct;
-  if constexpr (kHalf) {
-    if (rt.nr <= 64) {
-      experts_tile<GLU, 64, NTW, KS, STAGED>(a, rt, ct, lds.half);
-      return;
-    }
-  }
-  experts_tile<GLU, BM, NTW, KS, STAGED>(a, rt, ct, lds.full);
-}
-
 // Few rows per expert (up to MR per tile): a stream of the hit experts'
 // weights through MFMA. Wavefront = 32 weight rows (GLU: 16 gate rows and the
 // 16 up rows of the same outputs) times MR rows on 16x16x32 MFMAs, weights as
@@ -266,7 +95,8 @@ __global__ __launch_bounds__(kMmaThreads * KS) __attribute__((amdgpu_waves_per_e
 constexpr int kEsWaves = 4;
 constexpr int kEsThreads = 64 * kEsWaves;
 constexpr int kEsRows = 32;       // weight rows per wavefront
-constexpr int kEsSmallGrid = 256 * 6;  // workgroups that share a launch's items: two rounds of three per CU
+constexpr int kEsSharedGrid = 256 * 6;  // workgroups that share a launch's items
+constexpr int kEsManyItems = 12288;
 constexpr int kEsScaleLd = 36;    // LDS bytes per row of a scale window (32 + 4)
 
 template <int MR, int KB>
@@ -276,10 +106,14 @@ struct StreamLds {
   alignas(16) uint8_t scales[kEsWaves][kEsRows * kEsScaleLd];
 };
 
-// Halves offset of 16-byte piece c of row r of an x tile.
-template <int KB>
+// Halves offset of 16-byte piece c of row r of an x tile: the 16 rows of a
+// 16-row tile side by side for each piece, so that the rows of one read lie
+// in different banks whichever pieces the lanes take; XOR-swizzled so that the
+// pieces of one row do too when they are written (row-major tiles swizzled by
+// row had half of all LDS cycles in bank conflicts).
+template <int MR>
 __device__ __forceinline__ int stream_x_at(int r, int c) {
-  return r * KB + 8 * (c ^ (r & 7));
+  return ((c * (MR / 16) + (r >> 4)) * 16 + ((r ^ (c >> 2)) & 15)) * 8;
 }
 
 // One tile. ALIGNED: D % 256 == 0, so scale rows can be read 16 bytes at a
@@ -351,6 +185,10 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
     }
   };
 
+  // The weights' first loads go out before the rows are looked up.
+  load_w(0, 0);
+  load_w(1, 1);
+  load_s(0);
   // x pieces of this thread: (row, 32-value piece of the block).
   const uint8_t* xcp[XP];
   const uint8_t* xsp[XP];
@@ -383,15 +221,12 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
       const half2_t s = e4m3x2_f16(k0 + xk[i] < a.D ? xsv[i] : 0u);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<half8_t*>(&lds.x[buf][stream_x_at<KB>(r, 4 * c + j)]) = fp4x8_scaled(xv[i][j], s, j >> 1);
+        *reinterpret_cast<half8_t*>(&lds.x[buf][stream_x_at<MR>(r, 4 * c + j)]) = fp4x8_scaled(xv[i][j], s, j >> 1);
     }
   };
 
   const int nsteps = (a.D + 255) / 256;
   load_x(0);
-  load_s(0);
-  load_w(0, 0);
-  load_w(1, 1);
   store_x(0, 0);
   __syncthreads();
   f32x4_t acc[2][NT];
@@ -439,7 +274,7 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               const half8_t xf = *reinterpret_cast<const half8_t*>(
-                  &lds.x[buf][stream_x_at<KB>(16 * t + r, 32 * in + 16 * g + 4 * q + j)]);
+                  &lds.x[buf][stream_x_at<MR>(16 * t + r, 32 * in + 16 * g + 4 * q + j)]);
 #pragma unroll
               for (int m = 0; m < 2; ++m) acc[m][t] = mfma16(w[m], xf, acc[m][t]);
             }
@@ -506,10 +341,8 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
 // per CU that the LDS allows).
 template <bool GLU, int MR, int KB, bool ALIGNED, bool SHARED>
 __global__ __launch_bounds__(kEsThreads) void experts_stream_kernel(ExpertArgs a) {
-  constexpr int SH = MR == 16 ? 4 : 5;
-  static_assert(MR == 1 << SH, "rows per tile");
   __shared__ StreamLds<MR, KB> lds;
-  const TileScan scan(a.offsets, a.G, a.R, SH, a.take, a.tile_cols);
+  const TileScan scan(a.offsets, a.G, a.R, MR, a.take, a.tile_cols);
   ExpertTile tile;
   for (int b = blockIdx.x; expert_tile(a, scan, GLU, b, tile); b += gridDim.x) {
     if (GLU && tile.rt.g == a.G) zero_rows(a, tile.rt, kEsThreads);
@@ -517,6 +350,275 @@ __global__ __launch_bounds__(kEsThreads) void experts_stream_kernel(ExpertArgs a
     if (!SHARED) return;
     __syncthreads();  // the next item writes the LDS tiles
   }
+}
+
+// Many rows per expert: workgroup tile = up to 128 rows of an expert times 512
+// weight rows, 8 wavefronts, two per SIMD, so that one's conversions run
+// under the other's MFMAs. Wavefront = 64 weight rows (GLU: 32 gate rows and
+// the 32 up rows of the same outputs) times every row of the tile on 32x32x16
+// MFMAs.
+//  * B (weights): as in the stream: 256 K values per row at a time in whole
+//    lines, through 8 KB of LDS private to the wavefront into MFMA layout, one
+//    conversion for all the tile's rows.
+//  * A (rows): 128 K values per step, converted once per workgroup into one
+//    of two LDS tiles of fp16 q S values.
+//  * K order: in every 64 values lane (r, h) supplies [32h + 8j, +8) to MFMA j,
+//    on A and B alike.
+//  * RT: 32-row tiles of the row tile, so a ragged tail costs its own size.
+// Bound by the matrix cores and the clock they leave (52 % busy at 1.96 GHz):
+// T = 8192 in 3.55 ms for the launch pair, 1084 TFLOP/s on the rows alone;
+// with four wavefronts per 128 x 256 tile, one per SIMD, 4.06 ms; without the
+// loop's loads, on stale values, 2.8 ms.
+constexpr int kEtWaves = 8;
+constexpr int kEtThreads = 64 * kEtWaves;
+constexpr int kEtCols = 64 * kEtWaves;
+constexpr int kEtScaleLd = 20;  // LDS bytes per weight row of 256 K values' scales (16 + 4)
+
+struct TileLds {
+  alignas(16) _Float16 x[2][128 * 128];
+  alignas(16) uint8_t codes[kEtWaves][64 * 128];
+  alignas(16) uint8_t scales[kEtWaves][64 * kEtScaleLd];
+};
+
+// Halves offset of 16-byte piece c (of 16) of row r of an A tile: 32 rows side
+// by side for each piece, swizzled for the writes.
+__device__ __forceinline__ int tile_x_at(int r, int c) {
+  return (((r >> 5) * 16 + c) * 32 + ((r & 31) ^ (c & 12))) * 8;
+}
+
+template <bool GLU, int RT, bool ALIGNED>
+__device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile& tile, TileLds& lds) {
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const RowTile& rt = tile.rt;
+  const float gsa = load_early(a.gsa), gsw = load_early(a.gsw + rt.g);
+  const int nr = rt.nr, F = a.N >> 1;
+  const int64_t rowc = a.D / 2, rows = a.D / 16, we = (int64_t)rt.g * a.N;
+  const int o0 = (tile.ct * kEtWaves + wave) * (GLU ? 32 : 64);  // this wavefront's first output
+  // Weight row of its column c (0 .. 63), -1 past the last one (columns come and go 16 at a time).
+  auto wrow = [&](int c) {
+    const int o = GLU ? o0 + (c & 31) : o0 + c;
+    return GLU ? (o < F ? (c & 32 ? F + o : o) : -1) : (o < a.N ? o : -1);
+  };
+  const __amdgpu_buffer_rsrc_t wcr = make_rsrc(a.wc + we * rowc, a.N * rowc);
+  const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.ws + we * rows, a.N * rows);
+  // Load i takes 8 rows: a scalar offset for its first row, a lane's offset within the 8.
+  const uint32_t wlane = (uint32_t)((lane >> 3) * rowc + 16 * (lane & 7));
+  auto wbase = [&](int i, int64_t ld) { return wrow(8 * i) >= 0 ? (uint32_t)(wrow(8 * i) * ld) : kMmaOob; };
+  // Scales of 256 K values: 16 bytes of each row, or 2 bytes of 8 rows in each of 8 loads.
+  constexpr int SL = ALIGNED ? 1 : 8;
+  const uint32_t slane = ALIGNED ? (wrow(lane) >= 0 ? (uint32_t)(wrow(lane) * rows) : kMmaOob)
+                                 : (uint32_t)((lane >> 3) * rows + 2 * (lane & 7));
+  u32x4_t wv[8], sv16;
+  uint32_t sv2[SL];
+  auto load_w = [&](int batch) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      wv[i] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wcr, wlane + (wbase(i, rowc) + 128 * batch), 0, 0));
+    if constexpr (ALIGNED)
+      sv16 = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wsr, slane + 16 * batch, 0, 0));
+    else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        sv2[i] = __builtin_amdgcn_raw_buffer_load_b16(wsr, slane + (wbase(i, rows) + 16 * batch), 0, 0);
+    }
+  };
+  uint8_t* codes = lds.codes[wave];
+  uint8_t* scales = lds.scales[wave];
+  auto store_w = [&]() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = 8 * i + (lane >> 3);
+      *reinterpret_cast<u32x4_t*>(codes + row * 128 + 16 * ((lane & 7) ^ ((row >> 1) & 7))) = wv[i];
+    }
+    if constexpr (ALIGNED) {
+      uint32_t* d = reinterpret_cast<uint32_t*>(scales + lane * kEtScaleLd);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = sv16[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint16_t*>(scales + (8 * i + (lane >> 3)) * kEtScaleLd + 2 * (lane & 7)) = (uint16_t)sv2[i];
+    }
+  };
+  load_w(0);
+
+  // A: thread = (row, 32 K values of a step).
+  const int ar = threadIdx.x >> 2, aq = threadIdx.x & 3;
+  int t = -1;
+  if (ar < nr) t = GLU ? row_token(a, rt.row0 + ar) : ar;
+  const __amdgpu_buffer_rsrc_t xcr =
+      GLU ? make_rsrc(a.xc, a.T * rowc) : make_rsrc(a.xc + rt.row0 * rowc, nr * rowc);
+  const __amdgpu_buffer_rsrc_t xsr =
+      GLU ? make_rsrc(a.xs, a.T * rows) : make_rsrc(a.xs + rt.row0 * rows, nr * rows);
+  const uint32_t xo = t >= 0 ? (uint32_t)(t * rowc + 16 * aq) : kMmaOob;
+  const uint32_t xso = t >= 0 ? (uint32_t)(t * rows + 2 * aq) : kMmaOob;
+  u32x4_t xv[2];
+  uint32_t xsv[2];
+  auto load_x = [&](int k, int step) {
+    const bool ok = 128 * step + 32 * aq < a.D;  // zeros past D, whatever the weights there
+    xv[k] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(xcr, ok ? xo + 64 * step : kMmaOob, 0, 0));
+    xsv[k] = __builtin_amdgcn_raw_buffer_load_b16(xsr, ok ? xso + 8 * step : kMmaOob, 0, 0);
+  };
+  auto store_x = [&](int k, int buf, int j) {  // 8 of the 32 values
+    if (RT < 4 && ar >= 32 * RT) return;
+    const half2_t s = e4m3x2_f16(xsv[k]);
+    *reinterpret_cast<half8_t*>(&lds.x[buf][tile_x_at(ar, 4 * aq + j)]) = fp4x8_scaled(xv[k][j], s, j >> 1);
+  };
+  // A fragment of row tile i, and a lane's codes and scales of a 64-value group, of slice sl of a batch.
+  auto afrag = [&](int i, int sl) {
+    return *reinterpret_cast<const half8_t*>(&lds.x[(sl >> 3) & 1][tile_x_at(32 * i + r, 8 * ((sl >> 2) & 1) + 4 * h + (sl & 3))]);
+  };
+  u32x4_t c[2];
+  uint32_t sc[2];
+  auto read_codes = [&](int m, int group) {
+    const int row = 32 * m + r;
+    c[m] = *reinterpret_cast<const u32x4_t*>(codes + row * 128 + 16 * ((2 * group + h) ^ ((row >> 1) & 7)));
+    sc[m] = lds_u16(scales + row * kEtScaleLd + 4 * group + 2 * h);
+  };
+  auto wave_fence = [&]() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+
+  const int nbatch = (a.D + 255) / 256;
+  load_x(0, 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) store_x(0, 0, j);
+  store_w();
+  load_x(0, 1);
+  load_x(1, 2);
+  // The loop carries xsv as 32-bit values: as zero-extended 16-bit ones the
+  // compiler would extend them at the loop's start, ahead of their use, and
+  // wait there for every load in flight.
+  uint32_t zero = 0u;
+  asm volatile("" : "+v"(zero));
+  xsv[0] |= zero;
+  xsv[1] |= zero;
+  __builtin_amdgcn_sched_barrier(0);
+  load_w(1);
+  __syncthreads();
+  f32x16_t acc[RT][2];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][m][v] = 0.0f;
+
+  // One batch is 16 slices of 16 K values: two steps (A tiles) of two groups
+  // of four. In a slice the MFMAs of the first 32 columns run while the second
+  // 32 columns' weights of the slice are converted, then the other way round
+  // for the next slice, so that each has one register set; A fragment i is
+  // read right after its last MFMA of the slice before, the codes of a group
+  // at the end of the one before. The next batch's codes go to LDS when the
+  // last group of this one has been read, and the loads for the batch after
+  // follow at once (x before the weights: loads complete in order). No
+  // register may spill here: its reload would wait for every load in flight.
+  half8_t A[RT], w[2];
+  read_codes(0, 0);
+  read_codes(1, 0);
+  w[0] = fp4x8_scaled(c[0][0], e4m3x2_f16(sc[0]), 0);
+  for (int b = 0; b < nbatch; ++b) {
+    static_for<0, 16>([&](auto slc) {
+      constexpr int sl = decltype(slc)::value, u = sl >> 3, j = sl & 3, group = sl >> 2;
+      constexpr bool first = (sl & 7) == 0, last = (sl & 7) == 7;
+      if constexpr (first) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) A[i] = afrag(i, sl);
+      }
+      static_for<0, 2>([&](auto mc) {
+        constexpr int m = decltype(mc)::value, jn = m == 0 ? j : (j + 1) & 3;
+        // Phase m: MFMAs of columns 32 m; w[1 - m] is converted, for this
+        // slice (m = 0) or the next (m = 1).
+        static_for<0, RT>([&](auto ic) {
+          constexpr int i = decltype(ic)::value;
+          acc[i][m] = mfma32(A[i], w[m], acc[i][m]);
+          if constexpr (m == 1 && !last) A[i] = afrag(i, sl + 1);
+          static_for<i * 4 / RT, (i + 1) * 4 / RT>([&](auto kc) {
+            constexpr int k = decltype(kc)::value;
+            const half2_t s2 = e4m3x2_f16(sc[1 - m]);
+            const _Float16 sv = (jn >> 1) ? s2[1] : s2[0];
+            reinterpret_cast<half2_t*>(&w[1 - m])[k] =
+                __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[1 - m][jn], 1.0f, k) * half2_t{sv, sv};
+          });
+          __builtin_amdgcn_sched_barrier(0);
+        });
+        if constexpr (m == 0 && j == 3 && sl != 15) read_codes(1, group + 1);
+        if constexpr (m == 0 && sl == 15) read_codes(1, 0);
+        if constexpr (m == 1 && j == 2 && sl != 14) read_codes(0, group + 1);
+        if constexpr (m == 1 && sl == 14) read_codes(0, 0);
+        if constexpr (m == 0 && sl == 13) {
+          wave_fence();
+          store_w();
+          wave_fence();
+          load_x(1, 2 * b + 4);
+          __builtin_amdgcn_sched_barrier(0);
+          load_w(b + 2);
+        }
+      });
+      // The next step's A tile, a quarter in each of four slices; its
+      // registers take the step after the next one's.
+      if constexpr ((sl & 7) >= 1 && (sl & 7) < 5) store_x(u, u ^ 1, (sl & 7) - 1);
+      if constexpr (sl == 5) load_x(0, 2 * b + 3);
+      if constexpr (last) __syncthreads();
+    });
+  }
+
+  // Value v of lane (r, h): row 8 (v / 4) + 4 h + v % 4 of its 32-row tile, column r of its 32 weight rows.
+  const float scale = gsa * gsw;
+  if constexpr (GLU) {
+    const int f = o0 + r;
+    if (f >= F) return;
+    const float bg = a.bias ? a.bias[we + f] : 0.0f, bu = a.bias ? a.bias[we + F + f] : 0.0f;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)rt.row0 * F + f;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int row = 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
+        if (row < nr)
+          out[(int64_t)row * F] = bf16_round(silu_mul(acc[i][0][v] * scale + bg, acc[i][1][v] * scale + bu));
+      }
+  } else {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int n = o0 + 32 * m + r;
+      if (n >= a.N) continue;
+      const float b = a.bias ? a.bias[we + n] : 0.0f;
+      float* out = static_cast<float*>(a.out) + (int64_t)rt.row0 * a.N + n;
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int row = 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
+          if (row < nr) out[(int64_t)row * a.N] = acc[i][m][v] * scale + b;
+        }
+    }
+  }
+}
+
+// Rows per tile: 128, or 96 with scale rows that need 2-byte loads (8 more
+// registers, which 128 rows' accumulators do not leave).
+template <bool ALIGNED>
+constexpr int wide_rows() {
+  return ALIGNED ? 128 : 96;
+}
+
+template <bool GLU, bool ALIGNED>
+__global__ __launch_bounds__(kEtThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void experts_wide_kernel(
+    ExpertArgs a) {
+  __shared__ TileLds lds;
+  const TileScan scan(a.offsets, a.G, a.R, wide_rows<ALIGNED>(), a.take, a.tile_cols);
+  ExpertTile tile;
+  if (!expert_tile(a, scan, false, blockIdx.x, tile)) return;
+  const int nr = tile.rt.nr;
+  if (ALIGNED && nr > 96) wide_tile<GLU, ALIGNED ? 4 : 3, ALIGNED>(a, tile, lds);
+  else if (nr > 64) wide_tile<GLU, 3, ALIGNED>(a, tile, lds);
+  else if (nr > 32) wide_tile<GLU, 2, ALIGNED>(a, tile, lds);
+  else wide_tile<GLU, 1, ALIGNED>(a, tile, lds);
 }
 
 // out[t, n] = residual[t, n] + sum_j w[t, j] y[pos[t, j], n], j in order, 8
@@ -567,52 +669,56 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 // Dispatch. The host knows the rows (R) and experts (G), not the experts'
 // sizes.
 // ---------------------------------------------------------------------------
-template <bool GLU, int BM, int NTW>
-static hipError_t launch_mfma(ExpertArgs a, hipStream_t stream) {
-  constexpr int KS = mma_ksplit<BM, NTW>(), BN = 128 * NTW, SH = BM == 32 ? 5 : (BM == 64 ? 6 : 7);
-  a.col_tiles = (a.N + BN - 1) / BN;
-  a.nsteps = mma_padded_steps<BM, NTW>(a.D);
-  const int64_t nwg = max_row_tiles(a.R, a.G, SH) * a.col_tiles;
+template <bool GLU>
+static hipError_t launch_wide(ExpertArgs a, hipStream_t stream) {
+  a.col_tiles = (a.N + kEtCols - 1) / kEtCols;
+  const bool al = a.D % 256 == 0;
+  const int64_t nwg = max_row_tiles(a.R, a.G, al ? wide_rows<true>() : wide_rows<false>()) * a.col_tiles;
   if (nwg >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-  if (a.D % 256 == 0) experts_mfma_kernel<GLU, BM, NTW, KS, true><<<(int)nwg, kMmaThreads * KS, 0, stream>>>(a);
-  else experts_mfma_kernel<GLU, BM, NTW, KS, false><<<(int)nwg, kMmaThreads * KS, 0, stream>>>(a);
+  if (al) experts_wide_kernel<GLU, true><<<(int)nwg, kEtThreads, 0, stream>>>(a);
+  else experts_wide_kernel<GLU, false><<<(int)nwg, kEtThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <bool GLU, int MR, int KB, bool SHARED>
-static hipError_t launch_stream(ExpertArgs a, hipStream_t stream) {
-  a.col_tiles = (a.N + kEsRows * kEsWaves - 1) / (kEsRows * kEsWaves);
-  const int64_t items = max_row_tiles(a.R, a.G, MR == 16 ? 4 : 5) * a.col_tiles;
-  if (items >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-  // A launch of small experts beside the large ones is mostly empty: there
-  // each workgroup takes several items (129 thousand workgroups that had
-  // nothing to do took 140 us at T = 8192).
-  const int nwg = (int)(SHARED ? std::min<int64_t>(items, kEsSmallGrid) : items);
+static hipError_t launch_stream_t(const ExpertArgs& a, int nwg, hipStream_t stream) {
   if (a.D % 256 == 0) experts_stream_kernel<GLU, MR, KB, true, SHARED><<<nwg, kEsThreads, 0, stream>>>(a);
   else experts_stream_kernel<GLU, MR, KB, false, SHARED><<<nwg, kEsThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-// By the mean number of rows per expert, were every slot's expert held here:
-// up to 8 (T = 64 of 256 experts, k = 8: 433 us with 16-row tiles, 478 with
-// 32, 650 with the 128-row ones), up to 32 (T = 1024: 1211 us with 32-row
-// tiles, 1484 with 16, 1229 with 128); beyond that two launches share the
-// experts by their sizes, which only the device knows (an expert-parallel
-// rank's experts have a fraction of the mean, and a layer's popular experts
-// several times its others' rows).
+template <bool GLU, int MR, int KB>
+static hipError_t launch_stream(ExpertArgs a, hipStream_t stream) {
+  a.col_tiles = (a.N + kEsRows * kEsWaves - 1) / (kEsRows * kEsWaves);
+  const int64_t items = max_row_tiles(a.R, a.G, MR) * a.col_tiles;
+  if (items >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
+  // A launch of small experts beside the large ones is mostly empty, and a
+  // workgroup without work takes about a nanosecond (129 thousand of them
+  // took 140 us at T = 8192): past kEsManyItems each takes several items.
+  if (a.take == Take::kSmall && items > kEsManyItems) return launch_stream_t<GLU, MR, KB, true>(a, kEsSharedGrid, stream);
+  return launch_stream_t<GLU, MR, KB, false>(a, (int)items, stream);
+}
+
+// By the mean number of rows per expert, were every slot's expert held here.
+// D = 7168, F = 2048, 256 experts, k = 8, grouped_swiglu:
+//   up to 8: 16-row tiles (T = 64: 430 us; 32-row 478, 128-row tiles 650);
+//   up to 16: 32-row tiles (T = 512: 860 us; 16-row 968, shared by size 882);
+//   beyond: two launches share the experts by their sizes, which only the
+//   device knows (T = 1024: 1035 us, 32-row tiles alone 1180; an
+//   expert-parallel rank's experts have a fraction of the mean, and a layer's
+//   popular experts several times its others' rows).
 template <bool GLU>
 static hipError_t launch_products(ExpertArgs a, hipStream_t stream) {
   const int64_t mean = a.R / a.G;
   a.take = Take::kAll;
-  if (mean <= 8) return launch_stream<GLU, 16, 512, false>(a, stream);
-  if (mean <= 32) return launch_stream<GLU, 32, 256, false>(a, stream);
-  constexpr int NTW = 2;
-  a.tile_cols = (a.N + 128 * NTW - 1) / (128 * NTW);
+  if (mean <= 8) return launch_stream<GLU, 16, 512>(a, stream);
+  if (mean <= 16) return launch_stream<GLU, 32, 256>(a, stream);
+  a.tile_cols = (a.N + kEtCols - 1) / kEtCols;
   a.take = Take::kSmall;
-  const hipError_t e = launch_stream<GLU, 32, 256, true>(a, stream);
+  const hipError_t e = launch_stream<GLU, 32, 256>(a, stream);
   if (e != hipSuccess) return e;
   a.take = Take::kLarge;
-  return launch_mfma<GLU, 128, NTW>(a, stream);
+  return launch_wide<GLU>(a, stream);
 }
 
 }  // namespace nvr
@@ -668,7 +774,7 @@ int grouped_swiglu(const uint8_t* x_codes, const uint8_t* x_scales, const float*
     return ROUTER_EINVAL;
   if (T == 0) return ROUTER_OK;
   const nvr::ExpertArgs a{x_codes, x_scales, gsa, w_codes, w_scales, gsw, bias, offsets, rows, out,
-                          (int)T, (int)k, (int)(T * k), (int)G, (int)(2 * F), (int)D, 0, 0, nvr::Take::kAll, 0};
+                          (int)T, (int)k, (int)(T * k), (int)G, (int)(2 * F), (int)D, 0, nvr::Take::kAll, 0};
   return status_from(nvr::launch_products<true>(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -689,7 +795,7 @@ int grouped_combine(const uint8_t* h_codes, const uint8_t* h_scales, const float
   if (workspace_bytes < nvr::kScratchOffset + combine_scratch(T, k, D)) return ROUTER_EINVAL;
   float* y = reinterpret_cast<float*>(static_cast<char*>(workspace) + nvr::kScratchOffset);
   const nvr::ExpertArgs a{h_codes, h_scales, gsh, w_codes, w_scales, gsw, bias, offsets, nullptr, y,
-                          (int)T, (int)k, (int)(T * k), (int)G, (int)D, (int)F, 0, 0, nvr::Take::kAll, 0};
+                          (int)T, (int)k, (int)(T * k), (int)G, (int)D, (int)F, 0, nvr::Take::kAll, 0};
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t cwg = (T * (D / 8) + 255) / 256;
   if (cwg >= (int64_t(1) << 31)) return ROUTER_EUNSUPPORTED;

@@ -3,7 +3,7 @@
 //
 // Rows are sorted by expert: expert g owns rows offsets[g] .. offsets[g + 1] -
 // 1, and the rows from offsets[G] to R belong to no expert held here. A tile
-// is up to 2^sh consecutive rows of one expert; tiles are numbered expert by
+// is up to tr consecutive rows of one expert; tiles are numbered expert by
 // expert, the rows of no expert last. The host knows neither the sizes nor
 // the number of tiles, only that there are at most
 //   sum_g ceil(n_g / B) <= R / B + (experts with rows) <= R / B + min(R, G + 1)
@@ -34,37 +34,44 @@ struct RowTile {
   int nr;    // rows
 };
 
-// Experts by size: those with more rows than kSmallExpert are large when
-// there are enough of them to fill the GPU with 128-row tiles, i.e. when
-// `tile_cols` column tiles of their 128-row tiles give kMinTileItems work
-// items; otherwise every expert is small.
+// Experts by size: those with more rows than kSmallExpert are large (limits
+// of 32 and 64 rows: T = 2048 in 1400 and 1500 us) when there are enough of
+// them to fill the GPU with 128-row tiles, i.e. when `tile_cols` column tiles
+// of their 128-row tiles give kMinTileItems work items; otherwise every
+// expert is small.
 constexpr int kSmallExpert = 32;
-constexpr int kMinTileItems = 512;
+constexpr int kMinTileItems = 256;
 enum class Take { kAll, kSmall, kLarge };
 
-// Every wavefront scans the offsets by itself: lane l holds experts 8l ..
-// 8l + 7. Offsets are clamped to [0, R] and a decreasing pair counts as no
-// rows (a precondition violation then stays inside the caller's buffers).
+// Every wavefront scans the offsets by itself: lane l holds `per` = G / 64
+// (rounded up) adjacent experts. Offsets are clamped to [0, R] and a
+// decreasing pair counts as no rows (a precondition violation then stays
+// inside the caller's buffers).
 struct TileScan {
   int off[kGroupsPerLane + 1];
   int before;   // tiles of the experts of lower lanes
   int experts;  // tiles of every expert taken
-  int G, R, sh, above, upto;
+  int end;      // first row of no expert
+  int G, R, tr, per, above, upto;
 
-  __device__ __forceinline__ TileScan(const int32_t* offsets, int G_, int R_, int sh_, Take take, int tile_cols)
-      : G(G_), R(R_), sh(sh_), above(0), upto(0x7FFFFFFF) {
-    const int lane = threadIdx.x & 63;
+  __device__ __forceinline__ TileScan(const int32_t* offsets, int G_, int R_, int tr_, Take take, int tile_cols)
+      : G(G_), R(R_), tr(tr_), per((G_ + 63) >> 6), above(0), upto(0x7FFFFFFF) {
+    const int e0 = per * (int)(threadIdx.x & 63);
 #pragma unroll
-    for (int i = 0; i <= kGroupsPerLane; ++i) off[i] = offsets[min(kGroupsPerLane * lane + i, G)];
+    for (int i = 0; i <= kGroupsPerLane; ++i)
+      if (i <= per) off[i] = offsets[min(e0 + i, G)];
+    end = min(max(offsets[G], 0), R);
 #pragma unroll
-    for (int i = 0; i <= kGroupsPerLane; ++i) off[i] = min(max(off[i], 0), R);
+    for (int i = 0; i <= kGroupsPerLane; ++i)
+      if (i <= per) off[i] = min(max(off[i], 0), R);
     if (take != Take::kAll) {
       int big = 0;
 #pragma unroll
-      for (int i = 0; i < kGroupsPerLane; ++i) {
-        const int n = off[i + 1] - off[i];
-        big += n > kSmallExpert ? (n + 127) >> 7 : 0;
-      }
+      for (int i = 0; i < kGroupsPerLane; ++i)
+        if (i < per) {
+          const int n = off[i + 1] - off[i];
+          big += n > kSmallExpert ? (n + 127) >> 7 : 0;
+        }
       big = __builtin_amdgcn_readlane(wave_prefix_sum(big), 63);
       const bool split = (int64_t)big * tile_cols >= kMinTileItems;
       if (take == Take::kSmall) upto = split ? kSmallExpert : upto;
@@ -72,24 +79,21 @@ struct TileScan {
     }
     int mine = 0;
 #pragma unroll
-    for (int i = 0; i < kGroupsPerLane; ++i) mine += tiles(i);
+    for (int i = 0; i < kGroupsPerLane; ++i)
+      if (i < per) mine += tiles(i);
     const int incl = wave_prefix_sum(mine);
     before = incl - mine;
     experts = __builtin_amdgcn_readlane(incl, 63);
   }
   __device__ __forceinline__ int tiles(int i) const {
     const int n = off[i + 1] - off[i];
-    return n > above && n <= upto ? (n + (1 << sh) - 1) >> sh : 0;
+    return n > above && n <= upto ? (n + tr - 1) / tr : 0;
   }
-  // Tiles of the rows of no expert.
-  __device__ __forceinline__ int others() const { return (R - end() + (1 << sh) - 1) >> sh; }
-  // First row of no expert.
-  __device__ __forceinline__ int end() const { return __builtin_amdgcn_readlane(off[kGroupsPerLane], 63); }
-
-  // Tile n of the rows of no expert.
+  // Tiles of the rows of no expert, and the n-th of them.
+  __device__ __forceinline__ int others() const { return (R - end + tr - 1) / tr; }
   __device__ __forceinline__ RowTile none(int n) const {
-    const int row0 = end() + (n << sh);
-    return {G, row0, min(1 << sh, R - row0)};
+    const int row0 = end + n * tr;
+    return {G, row0, min(tr, R - row0)};
   }
 
   // Work item n < experts * cols: an expert's row tiles times `cols` column
@@ -99,17 +103,18 @@ struct TileScan {
     const int q = n / cols;  // a tile of the same expert
     int g = 0, first = 0, rows = 0, base = 0, m = 0, c = before;
 #pragma unroll
-    for (int i = 0; i < kGroupsPerLane; ++i) {
-      const int k = tiles(i);
-      if (q >= c && q < c + k) {
-        g = kGroupsPerLane * (int)(threadIdx.x & 63) + i;
-        first = off[i];
-        rows = off[i + 1] - off[i];
-        base = c;
-        m = k;
+    for (int i = 0; i < kGroupsPerLane; ++i)
+      if (i < per) {
+        const int k = tiles(i);
+        if (q >= c && q < c + k) {
+          g = per * (int)(threadIdx.x & 63) + i;
+          first = off[i];
+          rows = off[i + 1] - off[i];
+          base = c;
+          m = k;
+        }
+        c += k;
       }
-      c += k;
-    }
     const int lane = (int)__builtin_ctzll(__ballot(m > 0));  // one lane holds the expert
     g = __builtin_amdgcn_readlane(g, lane);
     first = __builtin_amdgcn_readlane(first, lane);
@@ -118,13 +123,13 @@ struct TileScan {
     m = __builtin_amdgcn_readlane(m, lane);
     const int i = n - base * cols;  // of m * cols
     ct = i / m;
-    const int r0 = (i - ct * m) << sh;
-    return {g, first + r0, min(1 << sh, rows - r0)};
+    const int r0 = (i - ct * m) * tr;
+    return {g, first + r0, min(tr, rows - r0)};
   }
 };
 
 // Upper bound on the tiles of the experts and of the rows of no expert.
-inline int64_t max_row_tiles(int64_t R, int64_t G, int sh) { return (R >> sh) + (R < G + 1 ? R : G + 1); }
+inline int64_t max_row_tiles(int64_t R, int64_t G, int tr) { return R / tr + (R < G + 1 ? R : G + 1); }
 
 // Workgroup b's number among `total` when the 8 XCDs (workgroups go to them
 // in turn) each take a contiguous range of numbers.

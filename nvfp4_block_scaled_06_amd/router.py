@@ -366,11 +366,11 @@ def _call(fn, device, *args):
     """One library call on the tensors' device and its current stream (tensors as pointers, None and empty ones as
     NULL); raises on a non-zero status."""
     i = device.index
-    if torch.cuda.current_device() != i:
+    if torch._C._cuda_getDevice() != i:
         with torch.cuda.device(i):
             return _call(fn, device, *args)
     a = [(x.data_ptr() or None) if isinstance(x, torch.Tensor) else x for x in args]
-    status = fn(*a, torch.cuda.current_stream(i).cuda_stream)
+    status = fn(*a, torch._C._cuda_getCurrentRawStream(i))
     if status != ROUTER_OK:
         _check(status)
 

@@ -127,17 +127,17 @@ SWIGLU = [
     (4, 8, 256, 0, 256, 32, 256, "one", False),       # all rows in one of many experts
     (200, 8, 200, 0, 200, 144, 768, "one", True),     # 1600 rows of it, 100 tiles
     (9, 3, 512, 5, 500, 48, 288, "skewed", False),    # many experts
-    # Up to 32: 32-row tiles.
+    # Up to 16: 32-row tiles.
     (64, 4, 16, 0, 16, 144, 512, "skewed", True),
     (50, 4, 16, 0, 16, 64, 1056, "skewed", False),
     (16, 16, 16, 0, 16, 16, 32, "repeat", True),
     (300, 3, 32, 1, 30, 176, 992, "holes", True),
-    # More: shared by size, all small here (too few rows for 128-row tiles) ...
+    # More: shared by size, all small here (too few rows to fill the GPU with 128-row tiles) ...
     (100, 4, 12, 2, 8, 80, 768, "holes", True),
     (200, 2, 8, 0, 8, 208, 2080, "skewed", False),
     (129, 1, 3, 0, 1, 128, 256, "one", False),        # an expert without rows
     (40, 8, 4, 0, 4, 32, 256, "none", True),          # no rows at all
-    # ... and with 512 of those tiles and small experts beside them, scales staged and not.
+    # ... and with enough of those tiles and small experts beside them, scale rows 16-byte aligned and not.
     (1400, 8, 40, 0, 40, 704, 512, "skewed", True),
     (1300, 8, 44, 3, 38, 1408, 416, "holes", True),
 ]
@@ -328,9 +328,9 @@ def test_binding_refusals(dev, ws):
             pytest.fail(f"call {i} was not refused")
 
 
-def test_large_layer_sampled(dev):
-    """Prefill sizes (4096 slots a wide layer): sampled rows and tokens against the oracle."""
-    T, D, E, k, F = 2048, 2048, 32, 8, 768
+@pytest.mark.parametrize("T,D,E,k,F", [(2048, 2048, 32, 8, 768), (1200, 2080, 16, 6, 1312)])
+def test_large_layer_sampled(dev, T, D, E, k, F):
+    """Prefill sizes: sampled rows and tokens against the oracle."""
     wsl = rt.Workspace(max(rt.workspace_bytes(T, D, E, k), rt.grouped_workspace_bytes(T, k, E, D, F)), dev)
     x, gate, bias, w13, w2 = layer_inputs(dev, wsl, T, D, E, k, F, seed=11)
     log(f"large layer T={T} D={D} E={E} k={k} F={F}")
