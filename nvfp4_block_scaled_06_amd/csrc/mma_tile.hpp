@@ -199,15 +199,6 @@ constexpr int kMmaWinLd = 68;  // LDS bytes per row and window (64 + 4)
 template <int BM, int NTW>
 constexpr int mma_win_bytes() { return 2 * (BM + 128 * NTW) * kMmaWinLd; }  // both windows
 
-// Byte offset of the scale row of tile row rr (of A, or of B) within its
-// descriptor. DenseRows: a tile's rows are consecutive rows of D / 16 = rows
-// scale bytes. A tile of gathered or paired rows passes an object of its own
-// with the same operator (an offset of kMmaOob or more reads zeros).
-struct DenseRows {
-  int rows;
-  __device__ __forceinline__ uint32_t operator()(bool, int rr) const { return (uint32_t)(rr * rows); }
-};
-
 // One window's loads, in flight between their issue and their LDS store:
 // piece p = tid + NT j (j < NL) is bytes [16 (p % 4), +16) of the window's
 // 64 bytes of row p / 4. A wavefront's 64 pieces are 16 whole rows, all of
@@ -218,8 +209,8 @@ struct ScaleWin {
   static constexpr int ROWS = BM + 128 * NTW, NP = 4 * ROWS, NT = kMmaThreads * KS, NL = (NP + NT - 1) / NT;
   u32x4_t v[NL];
 
-  template <int J, class RowOff>
-  __device__ __forceinline__ void load(const MmaPtrs<BM, NTW>& P, int win, int rows, const RowOff& row_off) {
+  template <int J>
+  __device__ __forceinline__ void load(const MmaPtrs<BM, NTW>& P, int win, int rows) {
     const int tid = threadIdx.x;
     const int p = tid + NT * J, row = p >> 2, part = p & 3;
     // The wavefront's first row, as a scalar: A or B is uniform per wavefront.
@@ -227,7 +218,7 @@ struct ScaleWin {
     const bool isA = row_w < BM;
     const int rr = isA ? row : row - BM;
     const int byte = 64 * win + 16 * part;
-    const uint32_t off = (p < NP && byte < rows) ? row_off(isA, rr) + (uint32_t)byte : kMmaOob;
+    const uint32_t off = (p < NP && byte < rows) ? (uint32_t)(rr * rows + byte) : kMmaOob;
     v[J] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(isA ? P.xs : P.ws, off, 0, 0));
   }
 
@@ -422,11 +413,10 @@ __device__ __forceinline__ void mma_step(MmaAFrags<BM, NTW>& A, half8_t (&B)[NTW
 // first steps) read them. swin holds mma_win_bytes()
 // bytes. Leaves acc[0] holding this group's sums (the two accumulator sets
 // added).
-template <int BM, int NTW, int KS, bool STAGED, class RowOff>
+template <int BM, int NTW, int KS, bool STAGED>
 __device__ __forceinline__ void mma_mainloop(const MmaPtrs<BM, NTW>& P, int D, int nsteps, _Float16* abuf_base,
                                              uint8_t* swin, int lane,
-                                             f32x16_t (&acc)[mma_sets<BM, NTW>()][BM / 32][NTW],
-                                             const RowOff& row_off) {
+                                             f32x16_t (&acc)[mma_sets<BM, NTW>()][BM / 32][NTW]) {
   constexpr int NS = mma_sets<BM, NTW>(), SL = mma_row_slots<BM>();
   constexpr int RING = mma_ring<BM, NTW>(), SPI = KS * RING, IPW = kMmaWin / SPI, POS = IPW * RING;
   static_assert(kMmaWin % SPI == 0, "a window holds whole ring passes");
@@ -467,7 +457,7 @@ __device__ __forceinline__ void mma_mainloop(const MmaPtrs<BM, NTW>& P, int D, i
   ScaleWin<BM, NTW, KS> win;
   uint32_t aw[SL], bw[NTW][2];
   if constexpr (STAGED) {
-    static_for<0, ScaleWin<BM, NTW, KS>::NL>([&](auto jc) { win.template load<decltype(jc)::value>(P, 0, rows, row_off); });
+    static_for<0, ScaleWin<BM, NTW, KS>::NL>([&](auto jc) { win.template load<decltype(jc)::value>(P, 0, rows); });
     static_for<0, ScaleWin<BM, NTW, KS>::NL>([&](auto jc) { win.template store<decltype(jc)::value>(swin); });
     __syncthreads();
     a_words(0, grp, aw);
@@ -506,7 +496,7 @@ __device__ __forceinline__ void mma_mainloop(const MmaPtrs<BM, NTW>& P, int D, i
           constexpr int NL = ScaleWin<BM, NTW, KS>::NL, NLP = POS / 2;
           if constexpr (pos < NLP)
             static_for<pos * NL / NLP, (pos + 1) * NL / NLP>(
-                [&](auto jc) { win.template load<decltype(jc)::value>(P, wi + 1, rows, row_off); });
+                [&](auto jc) { win.template load<decltype(jc)::value>(P, wi + 1, rows); });
           // The next step is the next window's when sw + KS reaches kMmaWin.
           if constexpr (sw + KS < kMmaWin) {
             a_words(wb, sw + KS + grp, an);
@@ -540,13 +530,6 @@ __device__ __forceinline__ void mma_mainloop(const MmaPtrs<BM, NTW>& P, int D, i
 #pragma unroll
       for (int t = 0; t < NTW; ++t) acc[0][rt][t] += acc[NS - 1][rt][t];
   }
-}
-
-template <int BM, int NTW, int KS, bool STAGED>
-__device__ __forceinline__ void mma_mainloop(const MmaPtrs<BM, NTW>& P, int D, int nsteps, _Float16* abuf_base,
-                                             uint8_t* swin, int lane,
-                                             f32x16_t (&acc)[mma_sets<BM, NTW>()][BM / 32][NTW]) {
-  mma_mainloop<BM, NTW, KS, STAGED>(P, D, nsteps, abuf_base, swin, lane, acc, DenseRows{D / 16});
 }
 
 // K steps of 128 elements for D, padded to a whole number of scale windows
