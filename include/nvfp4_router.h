@@ -341,7 +341,7 @@ int grouped_plan(const int32_t* topk_idx, int64_t T, int64_t k, int64_t first_ex
  *                            otherwise).
  *   out                      [T * k, F] bf16.
  * Code pointers and out 16-byte, scale pointers 2-byte, the rest 4-byte
- * aligned. One launch, no workspace.
+ * aligned. No workspace.
  */
 int grouped_swiglu(const uint8_t* x_codes, const uint8_t* x_scales, const float* gsa, const uint8_t* w_codes,
                    const uint8_t* w_scales, const float* gsw, const float* bias, const int32_t* offsets,

@@ -90,6 +90,9 @@ __device__ __forceinline__ void zero_rows(const ExpertArgs& a, const RowTile& t,
 //  * Scales: windows of 512 K (32 bytes per row), likewise.
 //  * x: KB K values of the tile's rows, converted to fp16 q S once per
 //    workgroup into one of two LDS tiles (one barrier per KB).
+//  * KG = 2: two groups of four wavefronts take the 512-value windows in turn
+//    and group 0 adds group 1's sums (fixed order). With few workgroups a
+//    wavefront's own chain of steps bounds the time, not the memory.
 //  * Past D the x tile holds zeros, so whatever finite weights a padded step
 //    reads there add nothing.
 constexpr int kEsWaves = 4;
@@ -97,13 +100,14 @@ constexpr int kEsThreads = 64 * kEsWaves;
 constexpr int kEsRows = 32;       // weight rows per wavefront
 constexpr int kEsSharedGrid = 256 * 6;  // workgroups that share a launch's items
 constexpr int kEsManyItems = 12288;
+constexpr int kEsFewItems = 256;
 constexpr int kEsScaleLd = 36;    // LDS bytes per row of a scale window (32 + 4)
 
-template <int MR, int KB>
+template <int MR, int KB, int KG>
 struct StreamLds {
   alignas(16) _Float16 x[2][MR * KB];
-  alignas(16) uint8_t codes[kEsWaves][kEsRows * 128];
-  alignas(16) uint8_t scales[kEsWaves][kEsRows * kEsScaleLd];
+  alignas(16) uint8_t codes[KG * kEsWaves][kEsRows * 128];
+  alignas(16) uint8_t scales[KG * kEsWaves][kEsRows * kEsScaleLd];
 };
 
 // Halves offset of 16-byte piece c of row r of an x tile: the 16 rows of a
@@ -118,20 +122,20 @@ __device__ __forceinline__ int stream_x_at(int r, int c) {
 
 // One tile. ALIGNED: D % 256 == 0, so scale rows can be read 16 bytes at a
 // time.
-template <bool GLU, int MR, int KB, bool ALIGNED>
-__device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTile& tile, StreamLds<MR, KB>& lds) {
-  constexpr int NT = MR / 16, NTHREADS = kEsThreads;
-  static_assert(KB == 256 || KB == 512, "whole steps");
+template <bool GLU, int MR, int KB, int KG, bool ALIGNED>
+__device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTile& tile, StreamLds<MR, KB, KG>& lds) {
+  constexpr int NT = MR / 16, NTHREADS = KG * kEsThreads;
+  static_assert(KG == 1 ? KB == 256 || KB == 512 : KB == 512 * KG, "whole steps, and a window for each K group");
   constexpr int XP = MR * (KB / 32) / NTHREADS;  // 32-value pieces of x per thread and block
   static_assert(XP * NTHREADS == MR * (KB / 32), "whole pieces per thread");
-  constexpr int SPB = KB / 256;  // steps per x block
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int SPB = KB / 256 / KG;  // steps per x block of a K group
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, grp = KG == 1 ? 0 : wave / kEsWaves;
   const RowTile& rt = tile.rt;
   const float gsa = load_early(a.gsa), gsw = load_early(a.gsw + rt.g);
   const int nr = rt.nr, F = a.N >> 1;
   const int64_t rowc = a.D / 2, rows = a.D / 16, we = (int64_t)rt.g * a.N;
   // This wavefront's first output (GLU) or weight row, and its two 16-row tiles.
-  const int o0 = (tile.ct * kEsWaves + wave) * (GLU ? 16 : 32);
+  const int o0 = (tile.ct * kEsWaves + wave % kEsWaves) * (GLU ? 16 : 32);
   const bool live0 = o0 < (GLU ? F : a.N), live1 = GLU ? live0 : o0 + 16 < a.N;
   auto wrow = [&](int m) { return GLU ? (m ? F + o0 : o0) : o0 + 16 * m; };
 
@@ -186,9 +190,9 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
   };
 
   // The weights' first loads go out before the rows are looked up.
-  load_w(0, 0);
-  load_w(1, 1);
-  load_s(0);
+  load_w(0, 2 * grp);
+  load_w(1, 2 * grp + 1);
+  load_s(grp);
   // x pieces of this thread: (row, 32-value piece of the block).
   const uint8_t* xcp[XP];
   const uint8_t* xsp[XP];
@@ -235,14 +239,14 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[m][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int r = lane & 15, q = lane >> 4;
-  for (int s0 = 0; s0 < nsteps; s0 += 2) {
+  for (int w0 = 0; 2 * w0 < nsteps; w0 += KG) {  // windows, one for each K group
     // The window's scales; the next one's loads.
     store_s();
-    load_s((s0 >> 1) + 1);
+    load_s(w0 + grp + KG);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int step = s0 + u;
-      const int block = step / SPB, in = u % SPB, buf = block & 1;
+      const int step = 2 * (w0 + grp) + u;
+      const int block = KG == 1 ? step / SPB : w0 / KG, in = u % SPB, buf = block & 1;
       // Before the weight loads: loads complete in order, and the wait for x
       // at the end of the block must not wait for weights two steps ahead.
       if (in == 0) load_x((block + 1) * KB);
@@ -252,7 +256,7 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
         const int row = 8 * i + (lane >> 3);
         *reinterpret_cast<u32x4_t*>(my_codes + row * 128 + 16 * ((lane & 7) ^ (row & 7))) = wv[u][i];
       }
-      load_w(u, step + 2);
+      load_w(u, step + 2 * KG);
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -274,7 +278,7 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               const half8_t xf = *reinterpret_cast<const half8_t*>(
-                  &lds.x[buf][stream_x_at<MR>(16 * t + r, 32 * in + 16 * g + 4 * q + j)]);
+                  &lds.x[buf][stream_x_at<MR>(16 * t + r, 32 * (SPB * grp + in) + 16 * g + 4 * q + j)]);
 #pragma unroll
               for (int m = 0; m < 2; ++m) acc[m][t] = mfma16(w[m], xf, acc[m][t]);
             }
@@ -291,6 +295,19 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
     }
   }
 
+  if constexpr (KG == 2) {
+    // The x tiles are done with: group 1's sums go through the first.
+    float* part = reinterpret_cast<float*>(&lds.x[0][0]) + (wave % kEsWaves) * (64 * 8 * NT) + lane;
+    static_assert(kEsWaves * 64 * 8 * NT * sizeof(float) <= sizeof(lds.x), "partial sums fit");
+    if (grp == 1) {
+#pragma unroll
+      for (int i = 0; i < 8 * NT; ++i) part[64 * i] = acc[i / (4 * NT)][(i >> 2) % NT][i & 3];
+    }
+    __syncthreads();
+    if (grp == 1) return;
+#pragma unroll
+    for (int i = 0; i < 8 * NT; ++i) acc[i / (4 * NT)][(i >> 2) % NT][i & 3] += part[64 * i];
+  }
   // Lane (r, q), value v of tile m: row r (+ 16 t), weight row 4 q + v of the tile.
   const float scale = gsa * gsw;
   if constexpr (GLU) {
@@ -339,14 +356,14 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
 // SHARED: workgroups take items in turn; else one item each (the loop around
 // the tile costs some 50 registers, and with them one of the three workgroups
 // per CU that the LDS allows).
-template <bool GLU, int MR, int KB, bool ALIGNED, bool SHARED>
-__global__ __launch_bounds__(kEsThreads) void experts_stream_kernel(ExpertArgs a) {
-  __shared__ StreamLds<MR, KB> lds;
+template <bool GLU, int MR, int KB, int KG, bool ALIGNED, bool SHARED>
+__global__ __launch_bounds__(KG * kEsThreads) void experts_stream_kernel(ExpertArgs a) {
+  __shared__ StreamLds<MR, KB, KG> lds;
   const TileScan scan(a.offsets, a.G, a.R, MR, a.take, a.tile_cols);
   ExpertTile tile;
   for (int b = blockIdx.x; expert_tile(a, scan, GLU, b, tile); b += gridDim.x) {
-    if (GLU && tile.rt.g == a.G) zero_rows(a, tile.rt, kEsThreads);
-    else stream_tile<GLU, MR, KB, ALIGNED>(a, tile, lds);
+    if (GLU && tile.rt.g == a.G) zero_rows(a, tile.rt, KG * kEsThreads);
+    else stream_tile<GLU, MR, KB, KG, ALIGNED>(a, tile, lds);
     if (!SHARED) return;
     __syncthreads();  // the next item writes the LDS tiles
   }
@@ -622,7 +639,10 @@ __global__ __launch_bounds__(kEtThreads) __attribute__((amdgpu_waves_per_eu(2, 2
 }
 
 // out[t, n] = residual[t, n] + sum_j w[t, j] y[pos[t, j], n], j in order, 8
-// columns per thread.
+// columns per thread. Bound by HBM: at T = 8192, D = 7168 it reads the 1.88 GB
+// of products at 5 TB/s. (Sums by the last workgroup of a column tile, for one
+// launch at few rows, gained nothing: T = 1 23.4 us against 23.8, T = 4 62
+// against 59.)
 struct CombineArgs {
   const float* y;  // [R, N]
   const int32_t* pos;
@@ -680,10 +700,10 @@ static hipError_t launch_wide(ExpertArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool GLU, int MR, int KB, bool SHARED>
+template <bool GLU, int MR, int KB, int KG, bool SHARED>
 static hipError_t launch_stream_t(const ExpertArgs& a, int nwg, hipStream_t stream) {
-  if (a.D % 256 == 0) experts_stream_kernel<GLU, MR, KB, true, SHARED><<<nwg, kEsThreads, 0, stream>>>(a);
-  else experts_stream_kernel<GLU, MR, KB, false, SHARED><<<nwg, kEsThreads, 0, stream>>>(a);
+  if (a.D % 256 == 0) experts_stream_kernel<GLU, MR, KB, KG, true, SHARED><<<nwg, KG * kEsThreads, 0, stream>>>(a);
+  else experts_stream_kernel<GLU, MR, KB, KG, false, SHARED><<<nwg, KG * kEsThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -692,11 +712,19 @@ static hipError_t launch_stream(ExpertArgs a, hipStream_t stream) {
   a.col_tiles = (a.N + kEsRows * kEsWaves - 1) / (kEsRows * kEsWaves);
   const int64_t items = max_row_tiles(a.R, a.G, MR) * a.col_tiles;
   if (items >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-  // A launch of small experts beside the large ones is mostly empty, and a
-  // workgroup without work takes about a nanosecond (129 thousand of them
-  // took 140 us at T = 8192): past kEsManyItems each takes several items.
-  if (a.take == Take::kSmall && items > kEsManyItems) return launch_stream_t<GLU, MR, KB, true>(a, kEsSharedGrid, stream);
-  return launch_stream_t<GLU, MR, KB, false>(a, (int)items, stream);
+  if constexpr (MR == 16) {
+    // One workgroup per CU at most: two K groups (grouped_swiglu at T = 1:
+    // 27.7 us against 31.5; grouped_combine's 448 workgroups of 8 steps:
+    // 27.4 against 23.7).
+    if (items <= kEsFewItems) return launch_stream_t<GLU, MR, 1024, 2, false>(a, (int)items, stream);
+  } else {
+    // A launch of small experts beside the large ones is mostly empty, and a
+    // workgroup without work takes about a nanosecond (129 thousand of them
+    // took 140 us at T = 8192): past kEsManyItems each takes several items.
+    if (a.take == Take::kSmall && items > kEsManyItems)
+      return launch_stream_t<GLU, MR, KB, 1, true>(a, kEsSharedGrid, stream);
+  }
+  return launch_stream_t<GLU, MR, KB, 1, false>(a, (int)items, stream);
 }
 
 // By the mean number of rows per expert, were every slot's expert held here.
@@ -773,8 +801,11 @@ int grouped_swiglu(const uint8_t* x_codes, const uint8_t* x_scales, const float*
       !aligned(out, 16))
     return ROUTER_EINVAL;
   if (T == 0) return ROUTER_OK;
-  const nvr::ExpertArgs a{x_codes, x_scales, gsa, w_codes, w_scales, gsw, bias, offsets, rows, out,
-                          (int)T, (int)k, (int)(T * k), (int)G, (int)(2 * F), (int)D, 0, nvr::Take::kAll, 0};
+  nvr::ExpertArgs a{};
+  a.xc = x_codes; a.xs = x_scales; a.gsa = gsa;
+  a.wc = w_codes; a.ws = w_scales; a.gsw = gsw;
+  a.bias = bias; a.offsets = offsets; a.rows = rows; a.out = out;
+  a.T = (int)T; a.k = (int)k; a.R = (int)(T * k); a.G = (int)G; a.N = (int)(2 * F); a.D = (int)D;
   return status_from(nvr::launch_products<true>(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -794,15 +825,18 @@ int grouped_combine(const uint8_t* h_codes, const uint8_t* h_scales, const float
   if (T == 0) return ROUTER_OK;
   if (workspace_bytes < nvr::kScratchOffset + combine_scratch(T, k, D)) return ROUTER_EINVAL;
   float* y = reinterpret_cast<float*>(static_cast<char*>(workspace) + nvr::kScratchOffset);
-  const nvr::ExpertArgs a{h_codes, h_scales, gsh, w_codes, w_scales, gsw, bias, offsets, nullptr, y,
-                          (int)T, (int)k, (int)(T * k), (int)G, (int)D, (int)F, 0, nvr::Take::kAll, 0};
-  const hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t cwg = (T * (D / 8) + 255) / 256;
   if (cwg >= (int64_t(1) << 31)) return ROUTER_EUNSUPPORTED;
-  const hipError_t e = nvr::launch_products<false>(a, s);
-  if (e != hipSuccess) return status_from(e);
   const nvr::CombineArgs c{y, pos, topk_w, static_cast<const uint16_t*>(residual), static_cast<uint16_t*>(out),
                            (int)T, (int)k, (int)(T * k), (int)D};
+  nvr::ExpertArgs a{};
+  a.xc = h_codes; a.xs = h_scales; a.gsa = gsh;
+  a.wc = w_codes; a.ws = w_scales; a.gsw = gsw;
+  a.bias = bias; a.offsets = offsets; a.out = y;
+  a.T = (int)T; a.k = (int)k; a.R = (int)(T * k); a.G = (int)G; a.N = (int)D; a.D = (int)F;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = nvr::launch_products<false>(a, s);
+  if (e != hipSuccess) return status_from(e);
   nvr::combine_kernel<<<(int)cwg, 256, 0, s>>>(c);
   return status_from(hipGetLastError());
 }

@@ -127,6 +127,8 @@ SWIGLU = [
     (4, 8, 256, 0, 256, 32, 256, "one", False),       # all rows in one of many experts
     (200, 8, 200, 0, 200, 144, 768, "one", True),     # 1600 rows of it, 100 tiles
     (9, 3, 512, 5, 500, 48, 288, "skewed", False),    # many experts
+    (40, 8, 96, 0, 96, 288, 416, "skewed", True),     # more workgroups than compute units, D % 256 != 0
+    (32, 2, 64, 60, 64, 160, 768, "none", False),     # no rows, few slots
     # Up to 16: 32-row tiles.
     (64, 4, 16, 0, 16, 144, 512, "skewed", True),
     (50, 4, 16, 0, 16, 64, 1056, "skewed", False),
