@@ -742,6 +742,8 @@ static hipError_t launch_products(ExpertArgs a, hipStream_t stream) {
   if (mean <= 8) return launch_stream<GLU, 16, 512>(a, stream);
   if (mean <= 16) return launch_stream<GLU, 32, 256>(a, stream);
   a.tile_cols = (a.N + kEtCols - 1) / kEtCols;
+  // No split by any sizes: no launch for it.
+  if (max_row_tiles(a.R, a.G, 128) * a.tile_cols < kMinTileItems) return launch_stream<GLU, 32, 256>(a, stream);
   a.take = Take::kSmall;
   const hipError_t e = launch_stream<GLU, 32, 256>(a, stream);
   if (e != hipSuccess) return e;

@@ -36,11 +36,12 @@ struct RowTile {
 
 // Experts by size: those with more rows than kSmallExpert are large (limits
 // of 32 and 64 rows: T = 2048 in 1400 and 1500 us) when there are enough of
-// them to fill the GPU with 128-row tiles, i.e. when `tile_cols` column tiles
-// of their 128-row tiles give kMinTileItems work items; otherwise every
-// expert is small.
+// them for 128-row tiles, i.e. when `tile_cols` column tiles of their 128-row
+// tiles give kMinTileItems work items (for 128 x 512 tiles of full rows the
+// stream takes as long at about 90 of them, with 64 rows each at 100);
+// otherwise every expert is small.
 constexpr int kSmallExpert = 32;
-constexpr int kMinTileItems = 256;
+constexpr int kMinTileItems = 128;
 enum class Take { kAll, kSmall, kLarge };
 
 // Every wavefront scans the offsets by itself: lane l holds `per` = G / 64
