@@ -30,6 +30,7 @@ struct ExpertArgs {
   int col_tiles;
   Take take;      // which experts this launch takes
   int tile_cols;  // column tiles of the 128-row tile kernel
+  int max_tiles;  // no plan gives more row tiles
 };
 
 // Token of row p, or -1.
@@ -45,13 +46,15 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return g * sigmoid
 // come first, numbered so that consecutive items (the row tiles of one column
 // tile of an expert, then its next column tile) run on one XCD and share its
 // L2; then, if `others` (grouped_swiglu), one item per row tile of no expert.
-// False behind the last item.
+// False behind the last item, and for offsets that no plan gives and that ask
+// for more tiles than R rows can.
 struct ExpertTile {
   RowTile rt;
   int ct;
 };
 __device__ __forceinline__ bool expert_tile(const ExpertArgs& a, const TileScan& scan, bool others, int b,
                                             ExpertTile& t) {
+  if (scan.experts > a.max_tiles) return false;
   const int products = scan.experts * a.col_tiles;
   if (b < products) {
     t.rt = scan.at(xcd_order(b, products), a.col_tiles, t.ct);
@@ -693,7 +696,8 @@ template <bool GLU>
 static hipError_t launch_wide(ExpertArgs a, hipStream_t stream) {
   a.col_tiles = (a.N + kEtCols - 1) / kEtCols;
   const bool al = a.D % 256 == 0;
-  const int64_t nwg = max_row_tiles(a.R, a.G, al ? wide_rows<true>() : wide_rows<false>()) * a.col_tiles;
+  a.max_tiles = (int)max_row_tiles(a.R, a.G, al ? wide_rows<true>() : wide_rows<false>());
+  const int64_t nwg = (int64_t)a.max_tiles * a.col_tiles;
   if (nwg >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
   if (al) experts_wide_kernel<GLU, true><<<(int)nwg, kEtThreads, 0, stream>>>(a);
   else experts_wide_kernel<GLU, false><<<(int)nwg, kEtThreads, 0, stream>>>(a);
@@ -710,7 +714,8 @@ static hipError_t launch_stream_t(const ExpertArgs& a, int nwg, hipStream_t stre
 template <bool GLU, int MR, int KB>
 static hipError_t launch_stream(ExpertArgs a, hipStream_t stream) {
   a.col_tiles = (a.N + kEsRows * kEsWaves - 1) / (kEsRows * kEsWaves);
-  const int64_t items = max_row_tiles(a.R, a.G, MR) * a.col_tiles;
+  a.max_tiles = (int)max_row_tiles(a.R, a.G, MR);
+  const int64_t items = (int64_t)a.max_tiles * a.col_tiles;
   if (items >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
   if constexpr (MR == 16) {
     // One workgroup per CU at most: two K groups (grouped_swiglu at T = 1:

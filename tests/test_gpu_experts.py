@@ -139,7 +139,12 @@ SWIGLU = [
     (200, 2, 8, 0, 8, 208, 2080, "skewed", False),
     (129, 1, 3, 0, 1, 128, 256, "one", False),        # an expert without rows
     (40, 8, 4, 0, 4, 32, 256, "none", True),          # no rows at all
-    # ... and with enough of those tiles and small experts beside them, scale rows 16-byte aligned and not.
+    # ... (a rank's part: only the device knows that they are) ...
+    (600, 8, 128, 10, 16, 640, 512, "skewed", False),
+    # ... and with enough of those tiles and small experts beside them, scale rows 16-byte aligned and not, and so
+    # many work items that the small experts' workgroups take several.
+    (1400, 8, 40, 0, 40, 2080, 256, "skewed", False),
+    (1300, 8, 44, 3, 38, 2144, 96, "holes", True),
     (1400, 8, 40, 0, 40, 704, 512, "skewed", True),
     (1300, 8, 44, 3, 38, 1408, 416, "holes", True),
 ]
@@ -164,8 +169,10 @@ def test_swiglu(dev, ws, T, k, E, first, G, F, D, kind, with_bias):
 
 
 COMBINE = [(T, k, E, first, G, max(16, F), 32 * max(1, D // 64), kind, b, i % 2 == 0)
-           for i, (T, k, E, first, G, F, D, kind, b) in enumerate(SWIGLU[:-2])]
-COMBINE += [(1400, 8, 40, 0, 40, 1360, 512, "skewed", True, True), (1300, 8, 44, 3, 38, 2816, 352, "holes", True, False)]
+           for i, (T, k, E, first, G, F, D, kind, b) in enumerate(SWIGLU[:-4])]
+COMBINE += [(60, 8, 96, 0, 96, 288, 768, "skewed", True, True), (1400, 8, 40, 0, 40, 4160, 256, "skewed", False, True),
+            (1300, 8, 44, 3, 38, 4288, 96, "holes", True, False), (1400, 8, 40, 0, 40, 1360, 512, "skewed", True, True),
+            (1300, 8, 44, 3, 38, 2816, 352, "holes", True, False)]
 
 
 @pytest.mark.parametrize("T,k,E,first,G,N,F,kind,with_bias,with_residual", COMBINE)
