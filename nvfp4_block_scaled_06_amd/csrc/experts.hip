@@ -614,7 +614,7 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
           const int row = 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
-          if (row < nr) out[(int64_t)row * a.N] = acc[i][m][v] * scale + b;
+          if (row < nr) __builtin_nontemporal_store(acc[i][m][v] * scale + b, out + (int64_t)row * a.N);
         }
     }
   }
@@ -643,7 +643,10 @@ __global__ __launch_bounds__(kEtThreads) __attribute__((amdgpu_waves_per_eu(2, 2
 
 // out[t, n] = residual[t, n] + sum_j w[t, j] y[pos[t, j], n], j in order, 8
 // columns per thread. Bound by HBM: at T = 8192, D = 7168 it reads the 1.88 GB
-// of products at 5 TB/s. (Sums by the last workgroup of a column tile, for one
+// of products at 5 TB/s. The products are written past the caches, which they
+// would fill with lines that only this kernel reads, and every choice's loads
+// are in flight at once: 2.45 ms for the whole call instead of 2.49. (Read
+// past the caches too: 2.63 ms. Sums by the last workgroup of a column tile, for one
 // launch at few rows, gained nothing: T = 1 23.4 us against 23.8, T = 4 62
 // against 59.)
 struct CombineArgs {
@@ -674,6 +677,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) acc[q] = 0.0f;
   }
+#pragma unroll 8
   for (int j = 0; j < a.k; ++j) {
     const int p = a.pos[t * a.k + j];
     if (p < 0 || p >= a.R) continue;  // an expert held elsewhere: its weight is not read
