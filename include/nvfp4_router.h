@@ -391,8 +391,9 @@ int grouped_combine(const uint8_t* h_codes, const uint8_t* h_scales, const float
  * The token with the largest x (a tie going to the lower one, -inf and NaN
  * never chosen) is the row's choice, made before the logits are rounded to
  * their type.
- *   logits, out    [T, N] of `dtype`, `ld` >= N elements between rows; out
- *                  may be logits itself, and must not overlap it otherwise.
+ *   logits, out    [T, N] of `dtype`, `ld` and `ld_out` >= N elements between
+ *                  rows; out may be logits itself (with the same stride), and
+ *                  must not overlap it otherwise.
  *   history        NULL or [T, L] int32 with ld_history >= L elements
  *                  between rows; tokens outside [0, N) are ignored.
  *   lengths        NULL (every row has L) or [T] int32, clamped to [0, L].
@@ -421,8 +422,8 @@ int lmhead_penalize(const void* logits, int dtype, int64_t T, int64_t N, int64_t
                     int64_t L, int64_t ld_history, const int32_t* lengths, const int32_t* prompt,
                     const float* repetition, const float* frequency, const float* presence,
                     const int32_t* bias_start, const int32_t* bias_token, const float* bias_value, int64_t nbias,
-                    const uint32_t* mask, int64_t ld_mask, void* out, int32_t* out_idx, float* out_logit,
-                    void* workspace, size_t workspace_bytes, void* stream);
+                    const uint32_t* mask, int64_t ld_mask, void* out, int64_t ld_out, int32_t* out_idx,
+                    float* out_logit, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Measurement aid, not part of the router path: reads `bytes` of `buf`

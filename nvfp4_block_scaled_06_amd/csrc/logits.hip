@@ -40,7 +40,7 @@ constexpr uint32_t kPenBias = 0x80000000u, kPenSeen = 0x40000000u;  // flags abo
 struct PenArgs {
   const void* in;
   void* out;
-  int64_t ld;  // elements between rows, of both
+  int64_t ld, ld_out;  // elements between rows
   int T, N, chunks, segs, row0;
   const int32_t* history;
   int64_t ld_history;
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(kPenThreads) void penalize_kernel(PenArgs a) {
   const int t = a.row0 + blockIdx.x / a.segs, seg = blockIdx.x % a.segs;
   const int first = (int)((int64_t)a.chunks * seg / a.segs), last = (int)((int64_t)a.chunks * (seg + 1) / a.segs);
   const E* in = static_cast<const E*>(a.in) + t * a.ld;
-  E* out = static_cast<E*>(a.out) + t * a.ld;
+  E* out = static_cast<E*>(a.out) + t * a.ld_out;
   typedef E vec_t __attribute__((ext_vector_type(VE)));
   typedef typename std::conditional<VEC, vec_t, E>::type ev_t;
   ev_t v[PER];
@@ -298,14 +298,15 @@ extern "C" int lmhead_penalize(const void* logits, int dtype, int64_t T, int64_t
                                const int32_t* prompt, const float* repetition, const float* frequency,
                                const float* presence, const int32_t* bias_start, const int32_t* bias_token,
                                const float* bias_value, int64_t nbias, const uint32_t* mask, int64_t ld_mask,
-                               void* out, int32_t* out_idx, float* out_logit, void* workspace,
+                               void* out, int64_t ld_out, int32_t* out_idx, float* out_logit, void* workspace,
                                size_t workspace_bytes, void* stream) {
-  if (!pen_shape_ok(T, N) || ld < N || (dtype != ROUTER_F32 && dtype != ROUTER_BF16)) return ROUTER_EINVAL;
+  if (!pen_shape_ok(T, N) || ld < N || ld_out < N || (dtype != ROUTER_F32 && dtype != ROUTER_BF16)) return ROUTER_EINVAL;
   if (T == 0) return ROUTER_OK;
   const size_t esize = dtype == ROUTER_F32 ? 4 : 2;
   if (!logits || !out || !out_idx || !out_logit || !aligned(logits, esize) || !aligned(out, esize) ||
       !aligned(out_idx, 4) || !aligned(out_logit, 4))
     return ROUTER_EINVAL;
+  if (out == logits && ld != ld_out && T > 1) return ROUTER_EINVAL;
   if (history && (L < 0 || L >= (int64_t(1) << 30) || ld_history < L || !aligned(history, 4))) return ROUTER_EINVAL;
   if (!history && (lengths || prompt)) return ROUTER_EINVAL;
   if (!aligned(lengths, 4) || !aligned(prompt, 4) || !aligned(repetition, 4) || !aligned(frequency, 4) ||
@@ -320,13 +321,14 @@ extern "C" int lmhead_penalize(const void* logits, int dtype, int64_t T, int64_t
                      workspace_bytes < lmhead_penalize_workspace_bytes(T, N)))
     return ROUTER_EINVAL;
   char* base = static_cast<char*>(workspace);
-  const bool vec = aligned(logits, 16) && aligned(out, 16) && (ld * (int64_t)esize) % 16 == 0;
+  const bool vec = aligned(logits, 16) && aligned(out, 16) && (ld * (int64_t)esize) % 16 == 0 &&
+                   (ld_out * (int64_t)esize) % 16 == 0;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   for (int64_t row0 = 0; row0 < T; row0 += nvr::kMaxCounters) {
     const int64_t rows = pen_rows(T - row0);
     const int64_t segs = pen_segs(rows, chunks);
-    const nvr::PenArgs a{logits, out, ld, (int)T, (int)N, (int)chunks, (int)segs, (int)row0, history, ld_history, (int)L,
-                         lengths, prompt, repetition, frequency, presence, bias_start, bias_token, bias_value,
+    const nvr::PenArgs a{logits, out, ld, ld_out, (int)T, (int)N, (int)chunks, (int)segs, (int)row0, history,
+                         ld_history, (int)L, lengths, prompt, repetition, frequency, presence, bias_start, bias_token, bias_value,
                          (int)nbias, mask, ld_mask, out_idx, out_logit,
                          chunks > 1 ? reinterpret_cast<uint64_t*>(base + nvr::kScratchOffset) : nullptr,
                          reinterpret_cast<uint32_t*>(base)};

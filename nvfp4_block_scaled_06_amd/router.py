@@ -79,7 +79,7 @@ def load_library(path=LIB_PATH):
     L.lmhead_penalize_workspace_bytes.argtypes = [i64, i64]
     L.lmhead_penalize_workspace_bytes.restype = sz
     L.lmhead_penalize.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64,
-                                  vp, i64, vp, vp, vp, vp, sz, vp]
+                                  vp, i64, vp, i64, vp, vp, vp, sz, vp]
     L.lmhead_penalize.restype = ctypes.c_int
     _lib = L
     return L
@@ -509,10 +509,10 @@ def lmhead_penalize(logits, workspace, history=None, prompt=None, lengths=None, 
     dev = logits.device
     _check_workspace(workspace, dev)
     if out is None:
-        out = torch.empty_strided((T, N), (ld, 1), dtype=logits.dtype, device=dev)
-    if out.dtype != logits.dtype or out.shape != logits.shape or out.device != dev or \
-            _rows_tensor(out, "out", (logits.dtype,), T) != ld:
-        raise RouterError("out must have the dtype, shape, device and row stride of logits")
+        out = torch.empty((T, N), dtype=logits.dtype, device=dev)
+    ldo = _rows_tensor(out, "out", (logits.dtype,), T)
+    if out.shape != logits.shape or out.device != dev:
+        raise RouterError("out must have the dtype, shape and device of logits")
     L = ldh = ldm = nbias = 0
     if history is not None:
         ldh = _rows_tensor(history, "history", (torch.int32,), T)
@@ -541,8 +541,8 @@ def lmhead_penalize(logits, workspace, history=None, prompt=None, lengths=None, 
     idx = torch.empty(T, dtype=torch.int32, device=dev)
     logit = torch.empty(T, dtype=torch.float32, device=dev)
     _call(load_library().lmhead_penalize, dev, logits, 0 if logits.dtype == torch.float32 else 1, T, N, ld, history, L,
-          ldh, lengths, prompt, repetition, frequency, presence, start, token, value, nbias, mask, ldm, out, idx, logit,
-          workspace.buf, workspace.nbytes)
+          ldh, lengths, prompt, repetition, frequency, presence, start, token, value, nbias, mask, ldm, out, ldo, idx,
+          logit, workspace.buf, workspace.nbytes)
     return idx, logit, out
 
 

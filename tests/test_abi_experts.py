@@ -95,9 +95,9 @@ def test_combine_refusals(lib):
 
 def test_penalize_refusals(lib):
     c = Call(lib.lmhead_penalize, logits=P, dtype=0, T=2, N=5000, ld=5000, history=P, L=16, ldh=16, lengths=P,
-             prompt=P, rep=P, freq=P, pres=P, bstart=P, btok=P, bval=P, nbias=4, mask=P, ldm=157, out=P, idx=P,
-             logit=P, work=P, nbytes=1 << 20, s=None)
-    for bad in [dict(dtype=2), dict(T=-1), dict(N=0), dict(ld=4999), dict(logits=None), dict(out=None), dict(idx=None),
+             prompt=P, rep=P, freq=P, pres=P, bstart=P, btok=P, bval=P, nbias=4, mask=P, ldm=157, out=off(1 << 20), ldo=5000,
+             idx=P, logit=P, work=P, nbytes=1 << 20, s=None)
+    for bad in [dict(dtype=2), dict(T=-1), dict(N=0), dict(ld=4999), dict(ldo=4999), dict(out=P, ldo=5001), dict(logits=None), dict(out=None), dict(idx=None),
                 dict(logit=None), dict(L=-1), dict(ldh=15), dict(history=None), dict(btok=None), dict(bval=None),
                 dict(nbias=-1), dict(ldm=156), dict(work=None), dict(nbytes=STATE), dict(work=off(64)),
                 dict(logits=off(2)), dict(out=off(2)), dict(dtype=1, logits=off(1)), dict(history=off(2)),

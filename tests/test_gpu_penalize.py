@@ -108,6 +108,28 @@ def test_row_strides(dev, dtype):
         assert torch.all(buf[rest] == 7.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("ldo", [5003, 5008, 5016])
+def test_logits_of_every_position(dev, dtype, ldo):
+    """The last position's logits of [T, S, N]: the output's rows have a stride of their own."""
+    T, S, N = 3, 4, 5003
+    x, a = make(T, N, 50, 8, True, dtype, ldo, dev)
+    every = torch.full((T, S, N), 7.0, dtype=dtype, device=dev)
+    every[:, -1] = torch.from_numpy(x).to(dev)
+    ws = rt.Workspace(rt.lmhead_penalize_workspace_bytes(T, N), dev)
+    wide = on_dev(a, dev)
+    log(f"output stride {ldo}, {dtype}")
+    idx, logit, out = rt.lmhead_penalize(every[:, -1], ws, **wide)
+    assert out.is_contiguous()
+    buf = torch.full((T, ldo), 7.0, dtype=dtype, device=dev)
+    i2, l2, o2 = rt.lmhead_penalize(every[:, -1], ws, out=buf[:, :N], **wide)
+    torch.cuda.synchronize()
+    check(x, a, dtype, idx, logit, out)
+    assert torch.equal(o2.nan_to_num(), out.nan_to_num()) and torch.equal(i2, idx) and torch.equal(l2, logit)
+    assert torch.all(buf[:, N:] == 7.0)
+    assert torch.equal(every[:, -1].cpu(), torch.from_numpy(x).to(dtype)) and torch.all(every[:, :-1] == 7.0)
+
+
 def test_special_values(dev):
     """Masked infinities and NaN, rows that the mask empties, ties, and nothing but the logits."""
     N = 4100
