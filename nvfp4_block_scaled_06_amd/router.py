@@ -351,8 +351,8 @@ def grouped_workspace_bytes(T, k, G, D, F):
 
 def _tensor(t, name, dtype, shape, device):
     """A contiguous GPU tensor of this dtype, shape and device, or RouterError."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or t.device != device or \
-            not t.is_contiguous():
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
         raise RouterError(f"{name} must be a contiguous {dtype} {tuple(shape)} on {device}")
 
 
@@ -389,7 +389,7 @@ class GroupedPlan:
 
 def empty_plan(T, k, G, device="cuda"):
     buf = torch.empty(G + 1 + 2 * T * k, dtype=torch.int32, device=device)
-    offsets, rows, pos = buf.split((G + 1, T * k, T * k))
+    offsets, rows, pos = buf.split_with_sizes((G + 1, T * k, T * k))
     return GroupedPlan(offsets, rows, pos, T, k)
 
 
@@ -490,9 +490,13 @@ def _rows_tensor(t, name, dtypes, T):
     """A GPU matrix of T rows whose elements are adjacent inside a row; returns its row stride."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() != 2 or t.shape[0] != T:
         raise RouterError(f"{name} must be a GPU matrix of {T} rows of {' or '.join(map(str, dtypes))}")
-    if t.shape[1] > 1 and t.stride(1) != 1 or T > 1 and t.stride(0) < t.shape[1]:
+    n = t.shape[1]
+    if t.is_contiguous():
+        return n
+    ld, step = t.stride()
+    if n > 1 and step != 1 or T > 1 and ld < n:
         raise RouterError(f"{name} must hold its rows contiguously")
-    return max(t.stride(0), t.shape[1]) if T > 1 else t.shape[1]
+    return ld if T > 1 else n
 
 
 def lmhead_penalize(logits, workspace, history=None, prompt=None, lengths=None, repetition=None, frequency=None,
@@ -508,20 +512,30 @@ def lmhead_penalize(logits, workspace, history=None, prompt=None, lengths=None, 
     ld = _rows_tensor(logits, "logits", (torch.float32, torch.bfloat16), T)
     dev = logits.device
     _check_workspace(workspace, dev)
+    ldo = N
     if out is None:
         out = torch.empty((T, N), dtype=logits.dtype, device=dev)
-    ldo = _rows_tensor(out, "out", (logits.dtype,), T)
-    if out.shape != logits.shape or out.device != dev:
-        raise RouterError("out must have the dtype, shape and device of logits")
+    else:
+        ldo = _rows_tensor(out, "out", (logits.dtype,), T)
+        if out.shape != logits.shape or out.device != dev:
+            raise RouterError("out must have the dtype, shape and device of logits")
     L = ldh = ldm = nbias = 0
     if history is not None:
         ldh = _rows_tensor(history, "history", (torch.int32,), T)
         L = history.shape[1]
-    for name, t, dtype in (("lengths", lengths, torch.int32), ("prompt", prompt, torch.int32),
-                           ("repetition", repetition, torch.float32), ("frequency", frequency, torch.float32),
-                           ("presence", presence, torch.float32)):
-        if t is not None:
-            _tensor(t, name, dtype, (T,), dev)
+        if history.device != dev:
+            raise RouterError(f"history must be on {dev}")
+    rows = (T,)
+    if lengths is not None:
+        _tensor(lengths, "lengths", torch.int32, rows, dev)
+    if prompt is not None:
+        _tensor(prompt, "prompt", torch.int32, rows, dev)
+    if repetition is not None:
+        _tensor(repetition, "repetition", torch.float32, rows, dev)
+    if frequency is not None:
+        _tensor(frequency, "frequency", torch.float32, rows, dev)
+    if presence is not None:
+        _tensor(presence, "presence", torch.float32, rows, dev)
     start = token = value = None
     if bias is not None:
         start, token, value = bias
@@ -533,9 +547,8 @@ def lmhead_penalize(logits, workspace, history=None, prompt=None, lengths=None, 
         ldm = _rows_tensor(mask, "mask", (torch.int32, torch.uint32), T)
         if mask.shape[1] * 32 < N:
             raise RouterError("mask has too few words")
-    for name, t in (("history", history), ("mask", mask)):
-        if t is not None and t.device != dev:
-            raise RouterError(f"{name} must be on {dev}")
+        if mask.device != dev:
+            raise RouterError(f"mask must be on {dev}")
     if history is not None and L == 0:
         history = lengths = prompt = None
     idx = torch.empty(T, dtype=torch.int32, device=dev)
