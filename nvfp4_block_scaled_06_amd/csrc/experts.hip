@@ -78,6 +78,29 @@ __device__ __forceinline__ void zero_rows(const ExpertArgs& a, const RowTile& t,
   for (int64_t i = threadIdx.x; i < t.nr * per_row; i += nthreads) out[i] = u32x4_t{0u, 0u, 0u, 0u};
 }
 
+// One load of SW bytes of weight scales, and its way into LDS (4-byte aligned
+// there, or 2-byte for SW = 2).
+template <int SW>
+struct ScaleLoad {
+  static_assert(SW == 16 || SW == 4 || SW == 2, "a buffer load's sizes");
+  uint32_t v[(SW + 3) / 4];
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    if constexpr (SW == 16) {
+      const u32x4_t x = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = x[i];
+    } else if constexpr (SW == 4) v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+    else v[0] = __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
+  }
+  __device__ __forceinline__ void store(uint8_t* d) const {
+    if constexpr (SW == 2) *reinterpret_cast<uint16_t*>(d) = (uint16_t)v[0];
+    else {
+#pragma unroll
+      for (int i = 0; i < SW / 4; ++i) reinterpret_cast<uint32_t*>(d)[i] = v[i];
+    }
+  }
+};
+
 // Few rows per expert (up to MR per tile): a stream of the hit experts'
 // weights through MFMA. Wavefront = 32 weight rows (GLU: 16 gate rows and the
 // 16 up rows of the same outputs) times MR rows on 16x16x32 MFMAs, weights as
@@ -129,9 +152,8 @@ __device__ __forceinline__ int stream_x_at(int r, int c) {
   return ((c * (MR / 16) + (r >> 4)) * 16 + ((r ^ (c >> 2)) & 15)) * 8;
 }
 
-// One tile. ALIGNED: D % 256 == 0, so scale rows can be read 16 bytes at a
-// time.
-template <bool GLU, int MR, int KB, int KG, bool ALIGNED>
+// One tile. SW: bytes of a weight scale load (see scale_width).
+template <bool GLU, int MR, int KB, int KG, int SW>
 __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTile& tile, StreamLds<MR, KB, KG>& lds) {
   constexpr int NT = MR / 16, NTHREADS = KG * kEsThreads;
   static_assert(KG == 1 ? KB == 256 || KB == 512 : KB == 512 * KG, "whole steps, and a window for each K group");
@@ -161,41 +183,25 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
     for (int i = 0; i < 4; ++i)
       wv[slot][i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wcr, wo[i] + 128 * step, 0, kNtAux));
   };
-  // Scale window: lane = (row lane / 2, 16 bytes) of the 32 rows, or 2 bytes
-  // of 4 rows in each of 8 loads.
-  constexpr int SL = ALIGNED ? 1 : 8;
+  // Scale window: SP pieces of SW bytes per row, 64 / SP rows in each of SL loads.
+  constexpr int SP = 32 / SW, SL = SP / 2;
+  const int srow = lane / SP, sbyte = SW * (lane % SP);
   uint32_t so[SL];
-  if constexpr (ALIGNED) {
-    const int m = lane >> 5;
-    so[0] = (m ? live1 : live0) ? (uint32_t)((wrow(m) + ((lane >> 1) & 15)) * rows + 16 * (lane & 1)) : kMmaOob;
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int m = i >> 2;
-      so[i] = (m ? live1 : live0) ? (uint32_t)((wrow(m) + 4 * (i & 3) + (lane >> 4)) * rows + 2 * (lane & 15)) : kMmaOob;
-    }
+  for (int i = 0; i < SL; ++i) {
+    const int row = 64 / SP * i + srow, m = SL == 1 ? row >> 4 : i / (SL / 2);
+    so[i] = (m ? live1 : live0) ? (uint32_t)((wrow(m) + (row & 15)) * rows + sbyte) : kMmaOob;
   }
-  u32x4_t sv16;
-  uint32_t sv2[SL];
+  ScaleLoad<SW> sv[SL];
   auto load_s = [&](int win) {
-    if constexpr (ALIGNED) sv16 = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wsr, so[0] + 32 * win, 0, 0));
-    else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sv2[i] = __builtin_amdgcn_raw_buffer_load_b16(wsr, so[i] + 32 * win, 0, 0);
-    }
+    for (int i = 0; i < SL; ++i) sv[i].load(wsr, so[i] + 32 * win);
   };
   uint8_t* my_codes = lds.codes[wave];
   uint8_t* my_scales = lds.scales[wave];
   auto store_s = [&]() {
-    if constexpr (ALIGNED) {
-      uint32_t* d = reinterpret_cast<uint32_t*>(my_scales + (lane >> 1) * kEsScaleLd + 16 * (lane & 1));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = sv16[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<uint16_t*>(my_scales + (4 * i + (lane >> 4)) * kEsScaleLd + 2 * (lane & 15)) = (uint16_t)sv2[i];
-    }
+    for (int i = 0; i < SL; ++i) sv[i].store(my_scales + (64 / SP * i + srow) * kEsScaleLd + sbyte);
   };
 
   // The weights' first loads go out before the rows are looked up.
@@ -365,14 +371,14 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
 // SHARED: workgroups take items in turn; else one item each (the loop around
 // the tile costs some 50 registers, and with them one of the three workgroups
 // per CU that the LDS allows).
-template <bool GLU, int MR, int KB, int KG, bool ALIGNED, bool SHARED>
+template <bool GLU, int MR, int KB, int KG, int SW, bool SHARED>
 __global__ __launch_bounds__(KG * kEsThreads) void experts_stream_kernel(ExpertArgs a) {
   __shared__ StreamLds<MR, KB, KG> lds;
   const TileScan scan(a.offsets, a.G, a.R, MR, a.take, a.tile_cols);
   ExpertTile tile;
   for (int b = blockIdx.x; expert_tile(a, scan, GLU, b, tile); b += gridDim.x) {
     if (GLU && tile.rt.g == a.G) zero_rows(a, tile.rt, KG * kEsThreads);
-    else stream_tile<GLU, MR, KB, KG, ALIGNED>(a, tile, lds);
+    else stream_tile<GLU, MR, KB, KG, SW>(a, tile, lds);
     if (!SHARED) return;
     __syncthreads();  // the next item writes the LDS tiles
   }
@@ -414,7 +420,7 @@ __device__ __forceinline__ int tile_x_at(int r, int c) {
   return (((r >> 5) * 16 + c) * 32 + ((r & 31) ^ (c & 12))) * 8;
 }
 
-template <bool GLU, int RT, bool ALIGNED>
+template <bool GLU, int RT, int SW>
 __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile& tile, TileLds& lds) {
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -432,25 +438,21 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
   const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.ws + we * rows, a.N * rows);
   // Load i takes 8 rows: a scalar offset for its first row, a lane's offset within the 8.
   const uint32_t wlane = (uint32_t)((lane >> 3) * rowc + 16 * (lane & 7));
-  auto wbase = [&](int i, int64_t ld) { return wrow(8 * i) >= 0 ? (uint32_t)(wrow(8 * i) * ld) : kMmaOob; };
-  // Scales of 256 K values: 16 bytes of each row, or 2 bytes of 8 rows in each of 8 loads.
-  constexpr int SL = ALIGNED ? 1 : 8;
-  const uint32_t slane = ALIGNED ? (wrow(lane) >= 0 ? (uint32_t)(wrow(lane) * rows) : kMmaOob)
-                                 : (uint32_t)((lane >> 3) * rows + 2 * (lane & 7));
-  u32x4_t wv[8], sv16;
-  uint32_t sv2[SL];
+  auto wbase = [&](int c, int64_t ld) { return wrow(c) >= 0 ? (uint32_t)(wrow(c) * ld) : kMmaOob; };
+  // Scales of 256 K values: SL pieces of SW bytes per row, SR rows in each of SL loads.
+  constexpr int SL = 16 / SW, SR = 64 / SL;
+  const int srow = lane / SL, sbyte = SW * (lane % SL);
+  const uint32_t slane = SL > 1 ? (uint32_t)(srow * rows + sbyte)
+                                : (wrow(lane) >= 0 ? (uint32_t)(wrow(lane) * rows) : kMmaOob);
+  u32x4_t wv[8];
+  ScaleLoad<SW> sv[SL];
   auto load_w = [&](int batch) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       wv[i] = __builtin_bit_cast(
-          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wcr, wlane + (wbase(i, rowc) + 128 * batch), 0, 0));
-    if constexpr (ALIGNED)
-      sv16 = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wsr, slane + 16 * batch, 0, 0));
-    else {
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wcr, wlane + (wbase(8 * i, rowc) + 128 * batch), 0, 0));
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        sv2[i] = __builtin_amdgcn_raw_buffer_load_b16(wsr, slane + (wbase(i, rows) + 16 * batch), 0, 0);
-    }
+    for (int i = 0; i < SL; ++i) sv[i].load(wsr, slane + ((SL > 1 ? wbase(SR * i, rows) : 0u) + 16 * batch));
   };
   uint8_t* codes = lds.codes[wave];
   uint8_t* scales = lds.scales[wave];
@@ -460,15 +462,8 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
       const int row = 8 * i + (lane >> 3);
       *reinterpret_cast<u32x4_t*>(codes + row * 128 + 16 * ((lane & 7) ^ ((row >> 1) & 7))) = wv[i];
     }
-    if constexpr (ALIGNED) {
-      uint32_t* d = reinterpret_cast<uint32_t*>(scales + lane * kEtScaleLd);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = sv16[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<uint16_t*>(scales + (8 * i + (lane >> 3)) * kEtScaleLd + 2 * (lane & 7)) = (uint16_t)sv2[i];
-    }
+    for (int i = 0; i < SL; ++i) sv[i].store(scales + (SR * i + srow) * kEtScaleLd + sbyte);
   };
   load_w(0);
 
@@ -628,25 +623,25 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
   }
 }
 
-// Rows per tile: 128, or 96 with scale rows that need 2-byte loads (8 more
-// registers, which 128 rows' accumulators do not leave).
-template <bool ALIGNED>
+// Rows per tile: 128, or 96 with scale rows that need 2-byte loads (more
+// registers than 128 rows' accumulators leave).
+template <int SW>
 constexpr int wide_rows() {
-  return ALIGNED ? 128 : 96;
+  return SW > 2 ? 128 : 96;
 }
 
-template <bool GLU, bool ALIGNED>
+template <bool GLU, int SW>
 __global__ __launch_bounds__(kEtThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void experts_wide_kernel(
     ExpertArgs a) {
   __shared__ TileLds lds;
-  const TileScan scan(a.offsets, a.G, a.R, wide_rows<ALIGNED>(), a.take, a.tile_cols);
+  const TileScan scan(a.offsets, a.G, a.R, wide_rows<SW>(), a.take, a.tile_cols);
   ExpertTile tile;
   if (!expert_tile(a, scan, false, blockIdx.x, tile)) return;
   const int nr = tile.rt.nr;
-  if (ALIGNED && nr > 96) wide_tile<GLU, ALIGNED ? 4 : 3, ALIGNED>(a, tile, lds);
-  else if (nr > 64) wide_tile<GLU, 3, ALIGNED>(a, tile, lds);
-  else if (nr > 32) wide_tile<GLU, 2, ALIGNED>(a, tile, lds);
-  else wide_tile<GLU, 1, ALIGNED>(a, tile, lds);
+  if (wide_rows<SW>() > 96 && nr > 96) wide_tile<GLU, wide_rows<SW>() / 32, SW>(a, tile, lds);
+  else if (nr > 64) wide_tile<GLU, 3, SW>(a, tile, lds);
+  else if (nr > 32) wide_tile<GLU, 2, SW>(a, tile, lds);
+  else wide_tile<GLU, 1, SW>(a, tile, lds);
 }
 
 // out[t, n] = residual[t, n] + sum_j w[t, j] y[pos[t, j], n], j in order, 8
@@ -704,22 +699,35 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 // Dispatch. The host knows the rows (R) and experts (G), not the experts'
 // sizes.
 // ---------------------------------------------------------------------------
+// Bytes of a weight scale load: the widest pieces that are aligned and never
+// reach past a row. They decide the number of loads and registers: for D a
+// multiple of 256 pieces of 4 bytes cost 1 - 1.6 % (T = 8192 and 1024); for
+// other multiples of 64 pieces of 2 bytes cost 10 - 15 % (K = 128: 337 us
+// against 302; K = 960: 54.9 against 47.1).
+static int scale_width(const ExpertArgs& a) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.ws);
+  return a.D % 256 == 0 && p % 16 == 0 ? 16 : a.D % 64 == 0 && p % 4 == 0 ? 4 : 2;
+}
+
 template <bool GLU>
 static hipError_t launch_wide(ExpertArgs a, hipStream_t stream) {
   a.col_tiles = (a.N + kEtCols - 1) / kEtCols;
-  const bool al = a.D % 256 == 0;
-  a.max_tiles = (int)max_row_tiles(a.R, a.G, al ? wide_rows<true>() : wide_rows<false>());
+  const int sw = scale_width(a);
+  a.max_tiles = (int)max_row_tiles(a.R, a.G, sw > 2 ? wide_rows<4>() : wide_rows<2>());
   const int64_t nwg = (int64_t)a.max_tiles * a.col_tiles;
   if (nwg >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-  if (al) experts_wide_kernel<GLU, true><<<(int)nwg, kEtThreads, 0, stream>>>(a);
-  else experts_wide_kernel<GLU, false><<<(int)nwg, kEtThreads, 0, stream>>>(a);
+  if (sw == 16) experts_wide_kernel<GLU, 16><<<(int)nwg, kEtThreads, 0, stream>>>(a);
+  else if (sw == 4) experts_wide_kernel<GLU, 4><<<(int)nwg, kEtThreads, 0, stream>>>(a);
+  else experts_wide_kernel<GLU, 2><<<(int)nwg, kEtThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <bool GLU, int MR, int KB, int KG, bool SHARED>
 static hipError_t launch_stream_t(const ExpertArgs& a, int nwg, hipStream_t stream) {
-  if (a.D % 256 == 0) experts_stream_kernel<GLU, MR, KB, KG, true, SHARED><<<nwg, KG * kEsThreads, 0, stream>>>(a);
-  else experts_stream_kernel<GLU, MR, KB, KG, false, SHARED><<<nwg, KG * kEsThreads, 0, stream>>>(a);
+  const int sw = scale_width(a);
+  if (sw == 16) experts_stream_kernel<GLU, MR, KB, KG, 16, SHARED><<<nwg, KG * kEsThreads, 0, stream>>>(a);
+  else if (sw == 4) experts_stream_kernel<GLU, MR, KB, KG, 4, SHARED><<<nwg, KG * kEsThreads, 0, stream>>>(a);
+  else experts_stream_kernel<GLU, MR, KB, KG, 2, SHARED><<<nwg, KG * kEsThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

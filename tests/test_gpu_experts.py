@@ -308,6 +308,44 @@ def test_other_stream_and_repeatability(dev, ws):
     assert torch.equal(got, want)
 
 
+def shifted(t, by):
+    """The same values, `by` bytes past a 16-byte boundary."""
+    buf = torch.empty(t.numel() + 16, dtype=torch.uint8, device=t.device)
+    view = buf[by:by + t.numel()].view(t.shape)
+    assert view.data_ptr() % 16 == by
+    return view.copy_(t)
+
+
+@pytest.mark.parametrize("T,k,E,F,D", [
+    (2, 4, 16, 48, 64), (30, 4, 24, 96, 448), (50, 4, 16, 176, 256), (40, 4, 16, 144, 832), (1400, 8, 40, 704, 192),
+    (1400, 8, 40, 704, 256), (1400, 8, 40, 704, 576),
+])
+def test_scale_alignment(dev, ws, T, k, E, F, D):
+    """D a multiple of 64 or of 256, the weights' scales at every alignment: the same bits each time, few rows and many."""
+    log(f"scale alignment T={T} k={k} E={E} F={F} D={D}")
+    idx = routing(T, k, E, T + F, "skewed")
+    off, rows, pos = er.plan_ref(idx, E)
+    plan = make_plan(idx, E, 0, ws, dev)
+    xq = rt.quantize(to_dev(bits((T, D), T, 2.0), dev), ws)
+    hq = rt.quantize(to_dev(bits((T * k, D), T, 0.5), dev), ws)
+    wg = rt.quantize_grouped_weights(to_dev(bits((E, 2 * F, D), D, D ** -0.5), dev), ws)
+    w = np.random.default_rng(T).uniform(0.05, 0.6, (T, k)).astype(np.float32)
+    wt = torch.from_numpy(w).to(dev)
+    h, out = rt.grouped_swiglu(xq, wg, plan), rt.grouped_combine(hq, wg, plan, wt, ws)
+    torch.cuda.synchronize()
+    ref, bound = er.swiglu_ref(host(xq), host_groups(wg), off, rows, k)
+    fails = er.check_close("h", f64(h), ref, bound)
+    ref, bound = er.combine_ref(host(hq), host_groups(wg), off, pos, w)
+    fails += er.check_close("out", f64(out), ref, bound)
+    assert not fails, "\n".join(fails)
+    for by in (2, 4, 8):
+        wb = rt.GroupedWeights(wg.codes, shifted(wg.scales, by), wg.gscale)
+        log(f"weight scales at {by} bytes")
+        assert torch.equal(rt.grouped_swiglu(xq, wb, plan), h), by
+        assert torch.equal(rt.grouped_combine(hq, wb, plan, wt, ws), out), by
+        torch.cuda.synchronize()
+
+
 def test_binding_refusals(dev, ws):
     T, D, E, k, F = 4, 64, 4, 2, 32
     x, gate, bias, w13, w2 = layer_inputs(dev, ws, T, D, E, k, F)
