@@ -340,8 +340,8 @@ int grouped_plan(const int32_t* topk_idx, int64_t T, int64_t k, int64_t first_ex
  *                            below 2^31 - 65536 (ROUTER_EUNSUPPORTED
  *                            otherwise).
  *   out                      [T * k, F] bf16.
- * Code pointers and out 16-byte, scale pointers 2-byte, the rest 4-byte
- * aligned. No workspace.
+ * Code pointers and out 16-byte, x_scales 2-byte, the rest 4-byte aligned. No
+ * workspace.
  */
 int grouped_swiglu(const uint8_t* x_codes, const uint8_t* x_scales, const float* gsa, const uint8_t* w_codes,
                    const uint8_t* w_scales, const float* gsw, const float* bias, const int32_t* offsets,
@@ -367,7 +367,7 @@ int grouped_swiglu(const uint8_t* x_codes, const uint8_t* x_scales, const float*
  *                            ROUTER_MAX_GATE_D, D * F / 2 below 2^31 - 65536
  *                            (ROUTER_EUNSUPPORTED otherwise).
  *   workspace                grouped_workspace_bytes(T, k, G, D, F) bytes.
- * Code pointers, residual and out 16-byte, scale pointers 2-byte, workspace
+ * Code pointers, residual and out 16-byte, h_scales 2-byte, workspace
  * 256-byte, the rest 4-byte aligned.
  */
 int grouped_combine(const uint8_t* h_codes, const uint8_t* h_scales, const float* gsh, const uint8_t* w_codes,

@@ -78,26 +78,32 @@ __device__ __forceinline__ void zero_rows(const ExpertArgs& a, const RowTile& t,
   for (int64_t i = threadIdx.x; i < t.nr * per_row; i += nthreads) out[i] = u32x4_t{0u, 0u, 0u, 0u};
 }
 
+// How weight scales are read: in pieces of 16 bytes (K a multiple of 256), of
+// 4 bytes (of 64), or of 4 bytes where the odd rows start 2 bytes past a
+// multiple of 4 (other multiples of 32): a window of those takes one piece
+// more, from the multiple below, and its scales lie 2 bytes further on in
+// LDS. Weights have a multiple of 16 rows, so no piece passes an expert's end.
+// (2-byte pieces in twice as many loads, whose registers left the wide tiles
+// 96 rows: K = 2016, 112 rows per expert 197 us against 178; K = 6048, 514
+// against 486.)
+enum class Scales { k16, k4, kSkewed };
+
 // One load of SW bytes of weight scales, and its way into LDS (4-byte aligned
-// there, or 2-byte for SW = 2).
+// there).
 template <int SW>
 struct ScaleLoad {
-  static_assert(SW == 16 || SW == 4 || SW == 2, "a buffer load's sizes");
-  uint32_t v[(SW + 3) / 4];
+  static_assert(SW == 16 || SW == 4, "a buffer load's sizes");
+  uint32_t v[SW / 4];
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
     if constexpr (SW == 16) {
       const u32x4_t x = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = x[i];
-    } else if constexpr (SW == 4) v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
-    else v[0] = __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
+    } else v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
   }
   __device__ __forceinline__ void store(uint8_t* d) const {
-    if constexpr (SW == 2) *reinterpret_cast<uint16_t*>(d) = (uint16_t)v[0];
-    else {
 #pragma unroll
-      for (int i = 0; i < SW / 4; ++i) reinterpret_cast<uint32_t*>(d)[i] = v[i];
-    }
+    for (int i = 0; i < SW / 4; ++i) reinterpret_cast<uint32_t*>(d)[i] = v[i];
   }
 };
 
@@ -152,8 +158,8 @@ __device__ __forceinline__ int stream_x_at(int r, int c) {
   return ((c * (MR / 16) + (r >> 4)) * 16 + ((r ^ (c >> 2)) & 15)) * 8;
 }
 
-// One tile. SW: bytes of a weight scale load (see scale_width).
-template <bool GLU, int MR, int KB, int KG, int SW>
+// One tile.
+template <bool GLU, int MR, int KB, int KG, Scales S>
 __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTile& tile, StreamLds<MR, KB, KG>& lds) {
   constexpr int NT = MR / 16, NTHREADS = KG * kEsThreads;
   static_assert(KG == 1 ? KB == 256 || KB == 512 : KB == 512 * KG, "whole steps, and a window for each K group");
@@ -183,25 +189,35 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
     for (int i = 0; i < 4; ++i)
       wv[slot][i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wcr, wo[i] + 128 * step, 0, kNtAux));
   };
-  // Scale window: SP pieces of SW bytes per row, 64 / SP rows in each of SL loads.
-  constexpr int SP = 32 / SW, SL = SP / 2;
+  // Scale window: SP pieces of SW bytes per row, 64 / SP rows in each of SL loads; and a load of the rows' last pieces.
+  constexpr bool SKEW = S == Scales::kSkewed;
+  constexpr int SW = S == Scales::k16 ? 16 : 4, SP = 32 / SW, SL = SP / 2;
   const int srow = lane / SP, sbyte = SW * (lane % SP);
-  uint32_t so[SL];
+  auto sbase = [&](int m, int row) {
+    const uint32_t at = (uint32_t)((wrow(m) + (row & 15)) * rows);
+    return (m ? live1 : live0) ? (SKEW ? at & ~3u : at) : kMmaOob;
+  };
+  uint32_t so[SL], so_last = 0u;
 #pragma unroll
   for (int i = 0; i < SL; ++i) {
-    const int row = 64 / SP * i + srow, m = SL == 1 ? row >> 4 : i / (SL / 2);
-    so[i] = (m ? live1 : live0) ? (uint32_t)((wrow(m) + (row & 15)) * rows + sbyte) : kMmaOob;
+    const int row = 64 / SP * i + srow;
+    so[i] = sbase(SL == 1 ? row >> 4 : i / (SL / 2), row) + sbyte;
   }
+  if constexpr (SKEW) so_last = lane < 32 ? sbase(lane >> 4, lane) + 32 : kMmaOob;
   ScaleLoad<SW> sv[SL];
+  ScaleLoad<4> sv_last;
   auto load_s = [&](int win) {
 #pragma unroll
     for (int i = 0; i < SL; ++i) sv[i].load(wsr, so[i] + 32 * win);
+    if constexpr (SKEW) sv_last.load(wsr, so_last + 32 * win);
   };
   uint8_t* my_codes = lds.codes[wave];
   uint8_t* my_scales = lds.scales[wave];
   auto store_s = [&]() {
 #pragma unroll
     for (int i = 0; i < SL; ++i) sv[i].store(my_scales + (64 / SP * i + srow) * kEsScaleLd + sbyte);
+    if constexpr (SKEW)
+      if (lane < 32) sv_last.store(my_scales + lane * kEsScaleLd + 32);
   };
 
   // The weights' first loads go out before the rows are looked up.
@@ -254,6 +270,7 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[m][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int r = lane & 15, q = lane >> 4;
+  const uint8_t* row_scales = my_scales + r * kEsScaleLd + 2 * q + (SKEW ? 2 * (r & 1) : 0);
   for (int w0 = 0; 2 * w0 < nsteps; w0 += KG) {  // windows, one for each K group
     // The window's scales; the next one's loads.
     store_s();
@@ -283,7 +300,7 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             c[m] = *reinterpret_cast<const u32x4_t*>(my_codes + (16 * m + r) * 128 + 16 * ((4 * g + q) ^ (r & 7)));
-            s[m] = e4m3x2_f16(lds_u16(my_scales + (16 * m + r) * kEsScaleLd + 16 * u + 8 * g + 2 * q));
+            s[m] = e4m3x2_f16(lds_u16(row_scales + 16 * m * kEsScaleLd + 16 * u + 8 * g));
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -371,14 +388,14 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
 // SHARED: workgroups take items in turn; else one item each (the loop around
 // the tile costs some 50 registers, and with them one of the three workgroups
 // per CU that the LDS allows).
-template <bool GLU, int MR, int KB, int KG, int SW, bool SHARED>
+template <bool GLU, int MR, int KB, int KG, Scales S, bool SHARED>
 __global__ __launch_bounds__(KG * kEsThreads) void experts_stream_kernel(ExpertArgs a) {
   __shared__ StreamLds<MR, KB, KG> lds;
   const TileScan scan(a.offsets, a.G, a.R, MR, a.take, a.tile_cols);
   ExpertTile tile;
   for (int b = blockIdx.x; expert_tile(a, scan, GLU, b, tile); b += gridDim.x) {
     if (GLU && tile.rt.g == a.G) zero_rows(a, tile.rt, KG * kEsThreads);
-    else stream_tile<GLU, MR, KB, KG, SW>(a, tile, lds);
+    else stream_tile<GLU, MR, KB, KG, S>(a, tile, lds);
     if (!SHARED) return;
     __syncthreads();  // the next item writes the LDS tiles
   }
@@ -405,6 +422,7 @@ __global__ __launch_bounds__(KG * kEsThreads) void experts_stream_kernel(ExpertA
 // Full tiles of even experts: 1233 TFLOP/s (256 rows each).
 constexpr int kEtWaves = 8;
 constexpr int kEtThreads = 64 * kEtWaves;
+constexpr int kEtRows = 128;
 constexpr int kEtCols = 64 * kEtWaves;
 constexpr int kEtScaleLd = 20;  // LDS bytes per weight row of 256 K values' scales (16 + 4)
 
@@ -420,7 +438,7 @@ __device__ __forceinline__ int tile_x_at(int r, int c) {
   return (((r >> 5) * 16 + c) * 32 + ((r & 31) ^ (c & 12))) * 8;
 }
 
-template <bool GLU, int RT, int SW>
+template <bool GLU, int RT, Scales S>
 __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile& tile, TileLds& lds) {
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -439,11 +457,14 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
   // Load i takes 8 rows: a scalar offset for its first row, a lane's offset within the 8.
   const uint32_t wlane = (uint32_t)((lane >> 3) * rowc + 16 * (lane & 7));
   auto wbase = [&](int c, int64_t ld) { return wrow(c) >= 0 ? (uint32_t)(wrow(c) * ld) : kMmaOob; };
-  // Scales of 256 K values: SL pieces of SW bytes per row, SR rows in each of SL loads.
-  constexpr int SL = 16 / SW, SR = 64 / SL;
+  // Scales of 256 K values: SL pieces of SW bytes per row, SR rows in each of SL loads; and a load of the rows' last
+  // pieces.
+  constexpr bool SKEW = S == Scales::kSkewed;
+  constexpr int SW = S == Scales::k16 ? 16 : 4, SL = 16 / SW, SR = 64 / SL;
   const int srow = lane / SL, sbyte = SW * (lane % SL);
-  const uint32_t slane = SL > 1 ? (uint32_t)(srow * rows + sbyte)
-                                : (wrow(lane) >= 0 ? (uint32_t)(wrow(lane) * rows) : kMmaOob);
+  auto sown = [&](int c) { return wrow(c) >= 0 ? (uint32_t)(wrow(c) * rows) & ~3u : kMmaOob; };
+  auto slane = [&](int c) { return SL > 1 ? ((uint32_t)(c / SL * rows) & ~3u) + SW * (c % SL) : sown(c); };
+  ScaleLoad<4> sv_last;
   u32x4_t wv[8];
   ScaleLoad<SW> sv[SL];
   auto load_w = [&](int batch) {
@@ -451,8 +472,11 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
     for (int i = 0; i < 8; ++i)
       wv[i] = __builtin_bit_cast(
           u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wcr, wlane + (wbase(8 * i, rowc) + 128 * batch), 0, 0));
+    int c = lane;
+    if constexpr (SKEW) asm volatile("" : "+v"(c));  // offsets computed here each time: no registers hold them
 #pragma unroll
-    for (int i = 0; i < SL; ++i) sv[i].load(wsr, slane + ((SL > 1 ? wbase(SR * i, rows) : 0u) + 16 * batch));
+    for (int i = 0; i < SL; ++i) sv[i].load(wsr, slane(c) + ((SL > 1 ? wbase(SR * i, rows) : 0u) + 16 * batch));
+    if constexpr (SKEW) sv_last.load(wsr, sown(c) + 16 + 16 * batch);
   };
   uint8_t* codes = lds.codes[wave];
   uint8_t* scales = lds.scales[wave];
@@ -464,6 +488,7 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
     }
 #pragma unroll
     for (int i = 0; i < SL; ++i) sv[i].store(scales + (SR * i + srow) * kEtScaleLd + sbyte);
+    if constexpr (SKEW) sv_last.store(scales + lane * kEtScaleLd + 16);
   };
   load_w(0);
 
@@ -498,7 +523,7 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
   auto read_codes = [&](int m, int group) {
     const int row = 32 * m + r;
     c[m] = *reinterpret_cast<const u32x4_t*>(codes + row * 128 + 16 * ((2 * group + h) ^ ((row >> 1) & 7)));
-    sc[m] = lds_u16(scales + row * kEtScaleLd + 4 * group + 2 * h);
+    sc[m] = lds_u16(scales + row * kEtScaleLd + 4 * group + 2 * h + (SKEW ? 2 * (r & 1) : 0));
   };
   auto wave_fence = [&]() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -623,25 +648,18 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
   }
 }
 
-// Rows per tile: 128, or 96 with scale rows that need 2-byte loads (more
-// registers than 128 rows' accumulators leave).
-template <int SW>
-constexpr int wide_rows() {
-  return SW > 2 ? 128 : 96;
-}
-
-template <bool GLU, int SW>
+template <bool GLU, Scales S>
 __global__ __launch_bounds__(kEtThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void experts_wide_kernel(
     ExpertArgs a) {
   __shared__ TileLds lds;
-  const TileScan scan(a.offsets, a.G, a.R, wide_rows<SW>(), a.take, a.tile_cols);
+  const TileScan scan(a.offsets, a.G, a.R, kEtRows, a.take, a.tile_cols);
   ExpertTile tile;
   if (!expert_tile(a, scan, false, blockIdx.x, tile)) return;
   const int nr = tile.rt.nr;
-  if (wide_rows<SW>() > 96 && nr > 96) wide_tile<GLU, wide_rows<SW>() / 32, SW>(a, tile, lds);
-  else if (nr > 64) wide_tile<GLU, 3, SW>(a, tile, lds);
-  else if (nr > 32) wide_tile<GLU, 2, SW>(a, tile, lds);
-  else wide_tile<GLU, 1, SW>(a, tile, lds);
+  if (nr > 96) wide_tile<GLU, 4, S>(a, tile, lds);
+  else if (nr > 64) wide_tile<GLU, 3, S>(a, tile, lds);
+  else if (nr > 32) wide_tile<GLU, 2, S>(a, tile, lds);
+  else wide_tile<GLU, 1, S>(a, tile, lds);
 }
 
 // out[t, n] = residual[t, n] + sum_j w[t, j] y[pos[t, j], n], j in order, 8
@@ -699,35 +717,37 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 // Dispatch. The host knows the rows (R) and experts (G), not the experts'
 // sizes.
 // ---------------------------------------------------------------------------
-// Bytes of a weight scale load: the widest pieces that are aligned and never
-// reach past a row. They decide the number of loads and registers: for D a
-// multiple of 256 pieces of 4 bytes cost 1 - 1.6 % (T = 8192 and 1024); for
-// other multiples of 64 pieces of 2 bytes cost 10 - 15 % (K = 128: 337 us
-// against 302; K = 960: 54.9 against 47.1).
-static int scale_width(const ExpertArgs& a) {
-  const uintptr_t p = reinterpret_cast<uintptr_t>(a.ws);
-  return a.D % 256 == 0 && p % 16 == 0 ? 16 : a.D % 64 == 0 && p % 4 == 0 ? 4 : 2;
+// The widest pieces that are aligned and never reach past a row (4-byte ones
+// where 16 bytes would do cost 1 - 1.6 % at T = 8192 and 1024).
+static Scales scales_of(const ExpertArgs& a) {
+  if (a.D % 256 == 0 && reinterpret_cast<uintptr_t>(a.ws) % 16 == 0) return Scales::k16;
+  return a.D % 64 == 0 ? Scales::k4 : Scales::kSkewed;
 }
 
 template <bool GLU>
 static hipError_t launch_wide(ExpertArgs a, hipStream_t stream) {
   a.col_tiles = (a.N + kEtCols - 1) / kEtCols;
-  const int sw = scale_width(a);
-  a.max_tiles = (int)max_row_tiles(a.R, a.G, sw > 2 ? wide_rows<4>() : wide_rows<2>());
+  a.max_tiles = (int)max_row_tiles(a.R, a.G, kEtRows);
   const int64_t nwg = (int64_t)a.max_tiles * a.col_tiles;
   if (nwg >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
-  if (sw == 16) experts_wide_kernel<GLU, 16><<<(int)nwg, kEtThreads, 0, stream>>>(a);
-  else if (sw == 4) experts_wide_kernel<GLU, 4><<<(int)nwg, kEtThreads, 0, stream>>>(a);
-  else experts_wide_kernel<GLU, 2><<<(int)nwg, kEtThreads, 0, stream>>>(a);
+  switch (scales_of(a)) {
+    case Scales::k16: experts_wide_kernel<GLU, Scales::k16><<<(int)nwg, kEtThreads, 0, stream>>>(a); break;
+    case Scales::k4: experts_wide_kernel<GLU, Scales::k4><<<(int)nwg, kEtThreads, 0, stream>>>(a); break;
+    case Scales::kSkewed: experts_wide_kernel<GLU, Scales::kSkewed><<<(int)nwg, kEtThreads, 0, stream>>>(a); break;
+  }
   return hipGetLastError();
 }
 
 template <bool GLU, int MR, int KB, int KG, bool SHARED>
 static hipError_t launch_stream_t(const ExpertArgs& a, int nwg, hipStream_t stream) {
-  const int sw = scale_width(a);
-  if (sw == 16) experts_stream_kernel<GLU, MR, KB, KG, 16, SHARED><<<nwg, KG * kEsThreads, 0, stream>>>(a);
-  else if (sw == 4) experts_stream_kernel<GLU, MR, KB, KG, 4, SHARED><<<nwg, KG * kEsThreads, 0, stream>>>(a);
-  else experts_stream_kernel<GLU, MR, KB, KG, 2, SHARED><<<nwg, KG * kEsThreads, 0, stream>>>(a);
+  constexpr int NT = KG * kEsThreads;
+  switch (scales_of(a)) {
+    case Scales::k16: experts_stream_kernel<GLU, MR, KB, KG, Scales::k16, SHARED><<<nwg, NT, 0, stream>>>(a); break;
+    case Scales::k4: experts_stream_kernel<GLU, MR, KB, KG, Scales::k4, SHARED><<<nwg, NT, 0, stream>>>(a); break;
+    case Scales::kSkewed:
+      experts_stream_kernel<GLU, MR, KB, KG, Scales::kSkewed, SHARED><<<nwg, NT, 0, stream>>>(a);
+      break;
+  }
   return hipGetLastError();
 }
 
@@ -823,7 +843,7 @@ int grouped_swiglu(const uint8_t* x_codes, const uint8_t* x_scales, const float*
   if (st != ROUTER_OK) return st;
   if (!gsa || !w_codes || !w_scales || !gsw || !offsets) return ROUTER_EINVAL;
   if (T > 0 && (!x_codes || !x_scales || !rows || !out)) return ROUTER_EINVAL;
-  if (!aligned(x_codes, 16) || !aligned(w_codes, 16) || !aligned(x_scales, 2) || !aligned(w_scales, 2) ||
+  if (!aligned(x_codes, 16) || !aligned(w_codes, 16) || !aligned(x_scales, 2) || !aligned(w_scales, 4) ||
       !aligned(gsa, 4) || !aligned(gsw, 4) || !aligned(bias, 4) || !aligned(offsets, 4) || !aligned(rows, 4) ||
       !aligned(out, 16))
     return ROUTER_EINVAL;
@@ -845,7 +865,7 @@ int grouped_combine(const uint8_t* h_codes, const uint8_t* h_scales, const float
   if (st != ROUTER_OK) return st;
   if (!gsh || !w_codes || !w_scales || !gsw || !offsets) return ROUTER_EINVAL;
   if (T > 0 && (!h_codes || !h_scales || !pos || !topk_w || !out || !workspace)) return ROUTER_EINVAL;
-  if (!aligned(h_codes, 16) || !aligned(w_codes, 16) || !aligned(h_scales, 2) || !aligned(w_scales, 2) ||
+  if (!aligned(h_codes, 16) || !aligned(w_codes, 16) || !aligned(h_scales, 2) || !aligned(w_scales, 4) ||
       !aligned(gsh, 4) || !aligned(gsw, 4) || !aligned(bias, 4) || !aligned(offsets, 4) || !aligned(pos, 4) ||
       !aligned(topk_w, 4) || !aligned(residual, 16) || !aligned(out, 16) || !aligned(workspace, 256))
     return ROUTER_EINVAL;

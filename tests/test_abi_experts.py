@@ -65,7 +65,7 @@ def test_swiglu_refusals(lib):
              F=64, D=256, out=P, s=None)
     for bad in [dict(T=-1), dict(k=0), dict(G=0), dict(F=0), dict(F=24), dict(D=0), dict(D=40), dict(xc=None),
                 dict(xs=None), dict(gsa=None), dict(wc=None), dict(ws=None), dict(gsw=None), dict(offsets=None),
-                dict(rows=None), dict(out=None), dict(xc=off(8)), dict(wc=off(8)), dict(xs=off(1)), dict(ws=off(1)),
+                dict(rows=None), dict(out=None), dict(xc=off(8)), dict(wc=off(8)), dict(xs=off(1)), dict(ws=off(2)),
                 dict(gsa=off(2)), dict(gsw=off(2)), dict(bias=off(2)), dict(offsets=off(2)), dict(rows=off(2)),
                 dict(out=off(8))]:
         assert c(**bad) == EINVAL, bad
@@ -82,7 +82,7 @@ def test_combine_refusals(lib):
     for bad in [dict(T=-1), dict(k=0), dict(G=0), dict(D=0), dict(D=24), dict(F=0), dict(F=40), dict(hc=None),
                 dict(hs=None), dict(gsh=None), dict(wc=None), dict(ws=None), dict(gsw=None), dict(offsets=None),
                 dict(pos=None), dict(w=None), dict(out=None), dict(work=None), dict(nbytes=STATE), dict(work=off(128)),
-                dict(hc=off(8)), dict(wc=off(8)), dict(hs=off(1)), dict(ws=off(1)), dict(gsh=off(2)), dict(gsw=off(2)),
+                dict(hc=off(8)), dict(wc=off(8)), dict(hs=off(1)), dict(ws=off(2)), dict(gsh=off(2)), dict(gsw=off(2)),
                 dict(bias=off(2)), dict(offsets=off(2)), dict(pos=off(2)), dict(w=off(2)), dict(residual=off(8)),
                 dict(out=off(8))]:
         assert c(**bad) == EINVAL, bad

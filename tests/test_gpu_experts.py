@@ -318,10 +318,11 @@ def shifted(t, by):
 
 @pytest.mark.parametrize("T,k,E,F,D", [
     (2, 4, 16, 48, 64), (30, 4, 24, 96, 448), (50, 4, 16, 176, 256), (40, 4, 16, 144, 832), (1400, 8, 40, 704, 192),
-    (1400, 8, 40, 704, 256), (1400, 8, 40, 704, 576),
+    (1400, 8, 40, 704, 256), (1400, 8, 40, 704, 576), (1400, 8, 40, 704, 544), (20, 4, 16, 48, 352),
 ])
 def test_scale_alignment(dev, ws, T, k, E, F, D):
-    """D a multiple of 64 or of 256, the weights' scales at every alignment: the same bits each time, few rows and many."""
+    """D a multiple of 256, 64 or 32, the weights' scales at every alignment: the same bits each time, few rows and
+    many; scales that no 4-byte load may touch are refused."""
     log(f"scale alignment T={T} k={k} E={E} F={F} D={D}")
     idx = routing(T, k, E, T + F, "skewed")
     off, rows, pos = er.plan_ref(idx, E)
@@ -338,7 +339,10 @@ def test_scale_alignment(dev, ws, T, k, E, F, D):
     ref, bound = er.combine_ref(host(hq), host_groups(wg), off, pos, w)
     fails += er.check_close("out", f64(out), ref, bound)
     assert not fails, "\n".join(fails)
-    for by in (2, 4, 8):
+    for call in (lambda w2: rt.grouped_swiglu(xq, w2, plan), lambda w2: rt.grouped_combine(hq, w2, plan, wt, ws)):
+        with pytest.raises(rt.RouterError):
+            call(rt.GroupedWeights(wg.codes, shifted(wg.scales, 2), wg.gscale))
+    for by in (4, 8, 12):
         wb = rt.GroupedWeights(wg.codes, shifted(wg.scales, by), wg.gscale)
         log(f"weight scales at {by} bytes")
         assert torch.equal(rt.grouped_swiglu(xq, wb, plan), h), by
