@@ -727,9 +727,11 @@ static Scales scales_of(const ExpertArgs& a) {
 template <bool GLU>
 static hipError_t launch_wide(ExpertArgs a, hipStream_t stream) {
   a.col_tiles = (a.N + kEtCols - 1) / kEtCols;
-  a.max_tiles = (int)max_row_tiles(a.R, a.G, kEtRows);
-  const int64_t nwg = (int64_t)a.max_tiles * a.col_tiles;
-  if (nwg >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
+  // Tiles of 64 rows only while kOneRound work items take them all.
+  a.max_tiles = (int)max_row_tiles(a.R, a.G, kEtRows / 2);
+  const int64_t nwg = std::max(max_row_tiles(a.R, a.G, kEtRows) * a.col_tiles,
+                               std::min(a.max_tiles * (int64_t)a.col_tiles, (int64_t)kOneRound));
+  if (a.max_tiles * (int64_t)a.col_tiles >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
   switch (scales_of(a)) {
     case Scales::k16: experts_wide_kernel<GLU, Scales::k16><<<(int)nwg, kEtThreads, 0, stream>>>(a); break;
     case Scales::k4: experts_wide_kernel<GLU, Scales::k4><<<(int)nwg, kEtThreads, 0, stream>>>(a); break;

@@ -141,6 +141,9 @@ SWIGLU = [
     (40, 8, 4, 0, 4, 32, 256, "none", True),          # no rows at all
     # ... (a rank's part: only the device knows that they are) ...
     (600, 8, 128, 10, 16, 640, 512, "skewed", False),
+    # ... with 64-row tiles, one for each compute unit at most ...
+    (300, 7, 40, 0, 40, 1024, 256, "skewed", True),
+    (260, 8, 30, 2, 24, 1200, 352, "holes", False),
     # ... and with enough of those tiles and small experts beside them, scale rows 16-byte aligned and not, and so
     # many work items that the small experts' workgroups take several.
     (1400, 8, 40, 0, 40, 2080, 256, "skewed", False),
@@ -170,7 +173,8 @@ def test_swiglu(dev, ws, T, k, E, first, G, F, D, kind, with_bias):
 
 COMBINE = [(T, k, E, first, G, max(16, F), 32 * max(1, D // 64), kind, b, i % 2 == 0)
            for i, (T, k, E, first, G, F, D, kind, b) in enumerate(SWIGLU[:-4])]
-COMBINE += [(60, 8, 96, 0, 96, 288, 768, "skewed", True, True), (1400, 8, 40, 0, 40, 4160, 256, "skewed", False, True),
+COMBINE += [(300, 7, 40, 0, 40, 2048, 256, "skewed", True, True), (260, 8, 30, 2, 24, 2400, 352, "holes", False, False),
+            (60, 8, 96, 0, 96, 288, 768, "skewed", True, True), (1400, 8, 40, 0, 40, 4160, 256, "skewed", False, True),
             (1300, 8, 44, 3, 38, 4288, 96, "holes", True, False), (1400, 8, 40, 0, 40, 1360, 512, "skewed", True, True),
             (1300, 8, 44, 3, 38, 2816, 352, "holes", True, False)]
 
