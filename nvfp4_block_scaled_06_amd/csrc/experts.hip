@@ -786,7 +786,12 @@ template <bool GLU>
 static hipError_t launch_products(ExpertArgs a, hipStream_t stream) {
   const int64_t mean = a.R / a.G;
   a.take = Take::kAll;
-  if (mean <= 8) return launch_stream<GLU, 16, 512>(a, stream);
+  // Also more rows of few experts, while their 16-row tiles are few enough
+  // for two K groups (T = 32, two experts held, D = 7168, F = 768: 22.4 us,
+  // 32-row tiles 31.7; level at K of 512 and less).
+  const int64_t stream_cols = (a.N + kEsRows * kEsWaves - 1) / (kEsRows * kEsWaves);
+  if (mean <= 8 || max_row_tiles(a.R, a.G, 16) * stream_cols <= kEsFewItems)
+    return launch_stream<GLU, 16, 512>(a, stream);
   if (mean <= 16) return launch_stream<GLU, 32, 256>(a, stream);
   a.tile_cols = (a.N + kEtCols - 1) / kEtCols;
   // No split by any sizes: no launch for it.

@@ -129,7 +129,11 @@ SWIGLU = [
     (9, 3, 512, 5, 500, 48, 288, "skewed", False),    # many experts
     (40, 8, 96, 0, 96, 288, 416, "skewed", True),     # more workgroups than compute units, D % 256 != 0
     (32, 2, 64, 60, 64, 160, 768, "none", False),     # no rows, few slots
-    # Up to 16: 32-row tiles.
+    # Up to 16: 32-row tiles, and 16-row tiles for few work items.
+    (64, 4, 16, 0, 16, 1040, 512, "skewed", True),
+    (50, 4, 16, 0, 16, 1040, 448, "skewed", False),
+    (80, 4, 16, 0, 16, 1056, 352, "skewed", True),
+    (37, 3, 9, 2, 3, 640, 1600, "holes", True),
     (64, 4, 16, 0, 16, 144, 512, "skewed", True),
     (50, 4, 16, 0, 16, 64, 1056, "skewed", False),
     (16, 16, 16, 0, 16, 16, 32, "repeat", True),
