@@ -107,6 +107,17 @@ struct ScaleLoad {
   }
 };
 
+// v in the lanes whose 32 K values lie before the row's end, 0 in those past
+// it: each LANES lanes hold the next 32 of a uniform `left` (a multiple of 32)
+// K values. The lanes come as a scalar mask: the wide tiles have no register
+// for a lane's own bound (spills of 3). Costs up to 0.7 % (T = 1, 64, 1024;
+// K = 7104, 7136, 2016, 1984), at T = 1 and K = 7104 1.6 %.
+template <int LANES>
+__device__ __forceinline__ uint32_t within(uint32_t v, int left) {
+  const int n = __builtin_amdgcn_readfirstlane(min(max(left, 0) / 32 * LANES, 64));
+  return __builtin_amdgcn_inverse_ballot_w64(n < 64 ? (1ull << n) - 1ull : ~0ull) ? v : 0u;
+}
+
 // Few rows per expert (up to MR per tile): a stream of the hit experts'
 // weights through MFMA. Wavefront = 32 weight rows (GLU: 16 gate rows and the
 // 16 up rows of the same outputs) times MR rows on 16x16x32 MFMAs, weights as
@@ -125,9 +136,9 @@ struct ScaleLoad {
 //  * KG = 2: two groups of four wavefronts take the 512-value windows in turn
 //    and group 0 adds group 1's sums (fixed order). With few workgroups a
 //    wavefront's own chain of steps bounds the time, not the memory.
-//  * Past D the x tile holds zeros, so whatever finite weights a padded step
-//    reads there add nothing (every code and scale byte decodes to a finite
-//    value).
+//  * Past D the x tile holds zeros, and what a padded step reads of the next
+//    weight row there takes a scale of zero: codes are finite, but scale bytes
+//    0x7F and 0xFF are NaN, and 0 NaN is NaN.
 // Bound by HBM: grouped_swiglu at T = 64, D = 7168, F = 2048, k = 8 reads the
 // 2.7 GB of the 165 of 256 experts that tokens hit under a mild skew in 450
 // us, 6.1 TB/s; at
@@ -300,7 +311,8 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
             c[m] = *reinterpret_cast<const u32x4_t*>(my_codes + (16 * m + r) * 128 + 16 * ((4 * g + q) ^ (r & 7)));
-            s[m] = e4m3x2_f16(lds_u16(row_scales + 16 * m * kEsScaleLd + 16 * u + 8 * g));
+            const uint32_t sw = lds_u16(row_scales + 16 * m * kEsScaleLd + 16 * u + 8 * g);
+            s[m] = e4m3x2_f16(S == Scales::k16 ? sw : within<16>(sw, a.D - (256 * step + 128 * g)));
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -413,6 +425,7 @@ __global__ __launch_bounds__(KG * kEsThreads) void experts_stream_kernel(ExpertA
 //    of two LDS tiles of fp16 q S values.
 //  * K order: in every 64 values lane (r, h) supplies [32h + 8j, +8) to MFMA j,
 //    on A and B alike.
+//  * Past D, as in the stream: x of zeros, weight scales of zero.
 //  * RT: 32-row tiles of the row tile, so a ragged tail costs its own size.
 // Bound by the matrix cores and the clock that their power leaves (58 % busy
 // at 1.82 GHz): grouped_swiglu at T = 8192, D = 7168, F = 2048, 256 experts
@@ -520,10 +533,11 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
   };
   u32x4_t c[2];
   uint32_t sc[2];
-  auto read_codes = [&](int m, int group) {
+  auto read_codes = [&](int m, int batch, int group) {
     const int row = 32 * m + r;
     c[m] = *reinterpret_cast<const u32x4_t*>(codes + row * 128 + 16 * ((2 * group + h) ^ ((row >> 1) & 7)));
     sc[m] = lds_u16(scales + row * kEtScaleLd + 4 * group + 2 * h + (SKEW ? 2 * (r & 1) : 0));
+    if constexpr (S != Scales::k16) sc[m] = within<32>(sc[m], a.D - (256 * batch + 64 * group));
   };
   auto wave_fence = [&]() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -566,8 +580,8 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
   // follow at once (x before the weights: loads complete in order). No
   // register may spill here: its reload would wait for every load in flight.
   half8_t A[RT], w[2];
-  read_codes(0, 0);
-  read_codes(1, 0);
+  read_codes(0, 0, 0);
+  read_codes(1, 0, 0);
   w[0] = fp4x8_scaled(c[0][0], e4m3x2_f16(sc[0]), 0);
   for (int b = 0; b < nbatch; ++b) {
     static_for<0, 16>([&](auto slc) {
@@ -594,10 +608,10 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
           });
           __builtin_amdgcn_sched_barrier(0);
         });
-        if constexpr (m == 0 && j == 3 && sl != 15) read_codes(1, group + 1);
-        if constexpr (m == 0 && sl == 15) read_codes(1, 0);
-        if constexpr (m == 1 && j == 2 && sl != 14) read_codes(0, group + 1);
-        if constexpr (m == 1 && sl == 14) read_codes(0, 0);
+        if constexpr (m == 0 && j == 3 && sl != 15) read_codes(1, b, group + 1);
+        if constexpr (m == 0 && sl == 15) read_codes(1, b + 1, 0);
+        if constexpr (m == 1 && j == 2 && sl != 14) read_codes(0, b, group + 1);
+        if constexpr (m == 1 && sl == 14) read_codes(0, b + 1, 0);
         if constexpr (m == 0 && sl == 13) {
           wave_fence();
           store_w();

@@ -358,6 +358,53 @@ def test_scale_alignment(dev, ws, T, k, E, F, D):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("T,k,E,F,D", [
+    (2, 4, 8, 48, 448), (2, 4, 8, 48, 352), (2, 4, 8, 80, 1120), (40, 8, 96, 288, 448), (40, 8, 96, 288, 416),
+    (40, 8, 96, 288, 1056), (64, 4, 16, 1040, 448), (64, 4, 16, 1040, 352), (300, 7, 40, 1024, 192),
+    (1400, 8, 40, 704, 832), (1400, 8, 40, 704, 544), (1400, 8, 40, 704, 288), (1400, 8, 40, 2080, 96),
+    (1400, 8, 40, 704, 256), (2, 4, 8, 48, 512),
+])
+def test_a_nan_scale_stays_in_its_row(dev, ws, T, k, E, F, D):
+    """Weight rows whose scales are all NaN make their own outputs NaN and change no bit of the others, at every K: two
+    K groups, 16- and 32-row tiles, 64- and 128-row tiles, small experts beside them. So does a token's row of x."""
+    log(f"nan scales T={T} k={k} E={E} F={F} D={D}")
+    idx = routing(T, k, E, T + F, "skewed")
+    off, rows, _ = er.plan_ref(idx, E)
+    plan = make_plan(idx, E, 0, ws, dev)
+    xq = rt.quantize(to_dev(bits((T, D), T, 2.0), dev), ws)
+    hq = rt.quantize(to_dev(bits((T * k, D), T, 0.5), dev), ws)
+    wg = rt.quantize_grouped_weights(to_dev(bits((E, 2 * F, D), D, D ** -0.5), dev), ws)
+    w = torch.from_numpy(np.random.default_rng(T).uniform(0.05, 0.6, (T, k)).astype(np.float32)).to(dev)
+
+    def both(x, h, wt):
+        return rt.grouped_swiglu(x, wt, plan), rt.grouped_combine(h, wt, plan, w, ws)
+
+    clean = both(xq, hq, wg)
+    bad_row = 1 + 37 * np.arange(E) % (2 * F - 1)  # one of each expert's rows; the row before it is sound
+    scales = wg.scales.clone()
+    scales[torch.arange(E), torch.from_numpy(bad_row)] = torch.tensor([0x7F, 0xFF], dtype=torch.uint8,
+                                                                      device=dev).repeat(D // 32)
+    bad = both(xq, hq, rt.GroupedWeights(wg.codes, scales, wg.gscale))
+    expert = np.repeat(np.arange(E), np.diff(off))
+    nan_h, nan_out = np.zeros((T * k, F), bool), np.zeros((T, 2 * F), bool)
+    nan_h[np.arange(T * k), bad_row[expert] % F] = True
+    nan_out[rows // k, bad_row[expert]] = True
+    t = T // 2
+    xs, hs = xq.scales.clone(), hq.scales.clone()
+    xs[t, 0] = hs[int(off[-1]) // 2, -1] = 0x7F
+    one = both(rt.NVFP4Tensor(xq.codes, xs, xq.gscale), rt.NVFP4Tensor(hq.codes, hs, hq.gscale), wg)
+    torch.cuda.synchronize()
+    nan_x, nan_t = np.zeros((T * k, F), bool), np.zeros((T, 2 * F), bool)
+    nan_x[rows // k == t] = True
+    nan_t[rows[int(off[-1]) // 2] // k] = True
+    for what, got, want, nan in (("h", bad[0], clean[0], nan_h), ("out", bad[1], clean[1], nan_out),
+                                 ("h of x", one[0], clean[0], nan_x), ("out of h", one[1], clean[1], nan_t)):
+        nan = torch.from_numpy(nan).to(dev)
+        assert not torch.any(torch.isnan(want))
+        assert torch.equal(torch.isnan(got), nan), (what, int(torch.isnan(got).sum()), int(nan.sum()))
+        assert torch.equal(got[~nan], want[~nan]), what
+
+
 def test_binding_refusals(dev, ws):
     T, D, E, k, F = 4, 64, 4, 2, 32
     x, gate, bias, w13, w2 = layer_inputs(dev, ws, T, D, E, k, F)
