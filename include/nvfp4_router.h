@@ -402,8 +402,10 @@ int grouped_combine(const uint8_t* h_codes, const uint8_t* h_scales, const float
  *   repetition, frequency, presence   NULL (1, 0, 0) or [T] fp32: r, f, p.
  *   bias_start     NULL or [T + 1] int32: row t's biases are entries
  *                  bias_start[t] .. bias_start[t + 1] - 1 of bias_token
- *                  (int32) and bias_value (fp32), nbias entries in all. A
- *                  token listed twice in a row takes its last value.
+ *                  (int32) and bias_value (fp32), nbias entries in all
+ *                  (starts are clamped to [0, nbias], an end before its start
+ *                  is no entry, tokens outside [0, N) are ignored). A token
+ *                  listed twice in a row takes its last value.
  *   mask           NULL or [T, ld_mask] 32-bit words, ld_mask >= N / 32
  *                  rounded up: bit n % 32 of word n / 32 is set where token n
  *                  is allowed.

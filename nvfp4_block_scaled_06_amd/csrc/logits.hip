@@ -123,15 +123,16 @@ __global__ __launch_bounds__(kPenThreads) void penalize_kernel(PenArgs a) {
     const int i = threadIdx.x + j * NT;
     held[j] = i < len ? h[i] : -1;  // -1: in no chunk
   }
-  // And the first NT of its biases.
-  int b0 = 0, b1 = 0;
+  // And the first NT of its nb biases. Both ends are clamped, and indices count
+  // from b0 and are unsigned: whatever the starts are, none passes nbias.
+  uint32_t b0 = 0u, nb = 0u;
   if (a.bias_start) {
-    b0 = max(a.bias_start[t], 0);
-    b1 = min(a.bias_start[t + 1], a.nbias);
+    b0 = (uint32_t)min(max(a.bias_start[t], 0), a.nbias);
+    nb = (uint32_t)max(min(a.bias_start[t + 1], a.nbias), (int)b0) - b0;
   }
   int held_token = -1;
   float held_value = 0.0f;
-  if (b0 + (int)threadIdx.x < b1) {
+  if (threadIdx.x < nb) {
     held_token = a.bias_token[b0 + threadIdx.x];
     held_value = a.bias_value[b0 + threadIdx.x];
   }
@@ -157,15 +158,15 @@ __global__ __launch_bounds__(kPenThreads) void penalize_kernel(PenArgs a) {
 #pragma unroll
     for (int j = 0; j < kPenHeld; ++j) count(held[j], threadIdx.x + j * NT);
     for (int i = threadIdx.x + kPenHeld * NT; i < len; i += NT) count(h[i], i);
-    auto list = [&](int tok, float value, int i) {
+    auto list = [&](int tok, float value, uint32_t i) {
       const uint32_t n = (uint32_t)tok - (uint32_t)n0;
       if (n < (uint32_t)nn) {
-        atomicMax(&entry[n], ((unsigned long long)(i + 1) << 32) | __float_as_uint(value));
+        atomicMax(&entry[n], ((unsigned long long)(i + 1u) << 32) | __float_as_uint(value));
         atomicOr(&state[n], kPenBias);
       }
     };
-    list(held_token, held_value, b0 + threadIdx.x);
-    for (int i = b0 + threadIdx.x + NT; i < b1; i += NT) list(a.bias_token[i], a.bias_value[i], i);
+    list(held_token, held_value, threadIdx.x);
+    for (uint32_t i = threadIdx.x + NT; i < nb; i += NT) list(a.bias_token[b0 + i], a.bias_value[b0 + i], i);
     // Everything else that this chunk reads is requested before the next
     // chunk's logits: loads complete in order.
     uint32_t allowed[PER];

@@ -130,6 +130,30 @@ def test_logits_of_every_position(dev, dtype, ldo):
     assert torch.equal(every[:, -1].cpu(), torch.from_numpy(x).to(dtype)) and torch.all(every[:, :-1] == 7.0)
 
 
+def test_bias_starts_out_of_range(dev):
+    """Starts that no list has are clamped to its ends; a row that ends before it starts has no biases."""
+    lo, hi = np.iinfo(np.int32).min, np.iinfo(np.int32).max
+    n, N, r = 700, 9001, np.random.default_rng(3)
+    starts = np.array([hi, -5, hi - 300, 3, lo, n + 1, 650, 640, hi, lo, lo, n - 1, hi, hi], dtype=np.int32)
+    rows = np.clip(starts, 0, n)
+    T = len(starts) - 1
+    tok = r.permutation(N)[:n].astype(np.int32)
+    val = r.standard_normal(n).astype(np.float32)
+    x = r.standard_normal((T, N)).astype(np.float32)
+    parts = [np.arange(rows[t], max(rows[t + 1], rows[t])) for t in range(T)]
+    assert [len(q) for q in parts] == [0, 700, 0, 0, 700, 0, 0, 60, 0, 0, 699, 1, 0]
+    listed = np.concatenate(parts)
+    want = (np.concatenate([[0], np.cumsum([len(q) for q in parts])]), tok[listed], val[listed])
+    ws = rt.Workspace(rt.lmhead_penalize_workspace_bytes(T, N), dev)
+    log("bias starts out of range")
+    got = rt.lmhead_penalize(torch.from_numpy(x).to(dev), ws, **on_dev({"bias": (starts, tok, val)}, dev))
+    torch.cuda.synchronize()
+    check(x, {"bias": want}, torch.float32, *got)
+    none = rt.lmhead_penalize(torch.from_numpy(x).to(dev), ws, **on_dev({"bias": (starts, tok[:0], val[:0])}, dev))
+    torch.cuda.synchronize()
+    check(x, {}, torch.float32, *none)
+
+
 def test_special_values(dev):
     """Masked infinities and NaN, rows that the mask empties, ties, and nothing but the logits."""
     N = 4100
