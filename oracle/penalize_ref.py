@@ -57,6 +57,47 @@ def penalize_ref(logits, history=None, prompt=None, lengths=None, repetition=Non
     return x, 1.01 * err
 
 
+def penalize_rows(x, history=None, lengths=None, prompt=None, repetition=None, frequency=None, presence=None, bias=None,
+                  mask=None):
+    """penalize_ref, a row at a time instead of a token at a time: the same operations, for large inputs."""
+    x = np.array(x, dtype=np.float64)
+    err = np.zeros_like(x)
+    T, N = x.shape
+
+    def inside(v):
+        return v[(v >= 0) & (v < N)]
+
+    with np.errstate(invalid="ignore", over="ignore"):
+        for t in range(T):
+            r, f, p = (d if v is None else float(v[t]) for v, d in ((repetition, 1.0), (frequency, 0.0), (presence, 0.0)))
+            h = np.zeros(0, dtype=np.int64) if history is None else history[t].astype(np.int64)
+            if lengths is not None:
+                h = h[:max(int(lengths[t]), 0)]
+            seen = np.unique(inside(h))
+            v = np.where(x[t, seen] > 0, x[t, seen] / r, x[t, seen] * r)
+            x[t, seen] = v
+            err[t, seen] += U32 * np.abs(v)
+            made, c = np.unique(inside(h[0 if prompt is None else max(int(prompt[t]), 0):]), return_counts=True)
+            v = x[t, made] - f * c
+            err[t, made] += U32 * (np.abs(f * c) + np.abs(v))
+            v = v - p
+            x[t, made] = v
+            err[t, made] += U32 * np.abs(v)
+            if bias is not None:
+                a, b = max(int(bias[0][t]), 0), min(int(bias[0][t + 1]), len(bias[1]))
+                tok, at = np.unique(bias[1][a:max(a, b)][::-1].astype(np.int64), return_index=True)  # the last of each
+                value = bias[2][a:max(a, b)][::-1][at].astype(np.float64)
+                ok = (tok >= 0) & (tok < N)
+                v = x[t, tok[ok]] + value[ok]
+                x[t, tok[ok]] = v
+                err[t, tok[ok]] += U32 * np.abs(v)
+            if mask is not None:
+                words = np.ascontiguousarray(mask[t], dtype=np.uint32).astype("<u4")
+                off = np.unpackbits(words.view(np.uint8), bitorder="little")[:N] == 0
+                x[t, off], err[t, off] = -np.inf, 0.0
+    return x, 1.01 * err
+
+
 def check_choice(idx, logit, x, err):
     """Failures of the greedy choice: the first maximum, or another token where the fp32 values may order them
     otherwise; -1 and -inf where nothing is above -inf."""

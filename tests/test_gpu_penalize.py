@@ -130,6 +130,64 @@ def test_logits_of_every_position(dev, dtype, ldo):
     assert torch.equal(every[:, -1].cpu(), torch.from_numpy(x).to(dtype)) and torch.all(every[:, :-1] == 7.0)
 
 
+def check_rows(x, a, dtype, idx, logit, out):
+    """check() with the oracle that takes a row at a time."""
+    ref, err = pr.penalize_rows(x, **a)
+    out = out.float().cpu().numpy()
+    fails = pr.check_choice(idx.cpu().numpy(), logit.cpu().numpy().astype(np.float64), ref, err)
+    assert not fails, "\n".join(fails[:5])
+    bound = err + (2.0 ** -8 * (np.abs(ref) + err) if dtype == torch.bfloat16 else 0.0)
+    with np.errstate(invalid="ignore"):
+        ok = (out == ref) | (np.abs(out - ref) <= bound)
+    assert np.all(ok), (np.argwhere(~ok)[:5], out[~ok][:5], ref[~ok][:5])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,N,L,nbias", [(5, 9001, 4097, 513), (5, 9001, 9000, 1500), (9, 4096, 4608, 1024),
+                                         (70, 49160, 4500, 700)])
+def test_long_lists(dev, T, N, L, nbias, dtype):
+    """Histories past the 4096 tokens, and biases past the 512 of a row, that stay in registers: prompts that end on
+    either side of the 4096th token, tokens biased on both sides of the 512th entry, whose last value counts."""
+    log(f"T={T} N={N} L={L} nbias={nbias} {dtype}")
+    x, a = make(T, N, L, 0, True, dtype, N + L, dev)
+    r = np.random.default_rng(L)
+    a["lengths"][:5] = L, L, L, 4096, 4097
+    a["prompt"][:5] = 0, 4095, 4097, 4000, 4096
+    tok = r.integers(-1, N + 1, (T, nbias)).astype(np.int32)
+    tok[:, 512:] = np.where(r.random((T, nbias - 512)) < 0.5, tok[:, :nbias - 512], tok[:, 512:])
+    tok[:, 512], tok[:, -1] = tok[:, 0], tok[:, 511]
+    a["bias"] = (np.arange(0, T * nbias + 1, nbias, dtype=np.int32), tok.reshape(-1),
+                 r.standard_normal(T * nbias).astype(np.float32))
+    ws = rt.Workspace(rt.lmhead_penalize_workspace_bytes(T, N), dev)
+    got = rt.lmhead_penalize(torch.from_numpy(x).to(dev).to(dtype), ws, **on_dev(a, dev))
+    torch.cuda.synchronize()
+    check_rows(x, a, dtype, *got)
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,N", [(100, 65541), (257, 16389), (780, 8195)])
+def test_workgroups_of_several_chunks(dev, T, N, dtype, shift):
+    """More chunks of 4096 tokens than resident workgroups: each takes several in turn, of a row's (17, 5 and 3) that one
+    or several workgroups share; 16 bytes and one element at a time, out of place and in place."""
+    log(f"T={T} N={N} {dtype} shift {shift}")
+    x, a = make(T, N, 700, 40, True, dtype, N, dev)
+    ld = (N + 15) // 8 * 8
+    buf = torch.full((T * ld + 16,), 7.0, dtype=dtype, device=dev)
+    view = buf[shift:shift + T * ld].view(T, ld)[:, :N]
+    view.copy_(torch.from_numpy(x).to(dev))
+    ws = rt.Workspace(rt.lmhead_penalize_workspace_bytes(T, N), dev)
+    up = on_dev(a, dev)
+    idx, logit, out = rt.lmhead_penalize(view, ws, **up)
+    i2, l2, _ = rt.lmhead_penalize(view, ws, out=view, **up)
+    torch.cuda.synchronize()
+    check_rows(x, a, dtype, idx, logit, out)
+    assert torch.equal(view, out) and torch.equal(i2, idx) and torch.equal(l2, logit)
+    rest = torch.ones_like(buf, dtype=torch.bool)
+    rest[shift:shift + T * ld].view(T, ld)[:, :N] = False
+    assert torch.all(buf[rest] == 7.0)
+
+
 def test_bias_starts_out_of_range(dev):
     """Starts that no list has are clamped to its ends; a row that ends before it starts has no biases."""
     lo, hi = np.iinfo(np.int32).min, np.iinfo(np.int32).max

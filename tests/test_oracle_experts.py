@@ -71,3 +71,23 @@ def test_penalize_hand_case():
     assert not pr.check_choice([-1], [-np.inf], empty, e) and pr.check_choice([0], [4.0], empty, e)
     tie, e = pr.penalize_ref(np.array([[1.0, 3.0, 3.0]]))
     assert not pr.check_choice([1], [3.0], tie, e) and pr.check_choice([2], [3.0], tie, e)
+
+
+@pytest.mark.parametrize("T,N,L,nbias,mask", [(3, 70, 90, 40, True), (2, 33, 5, 0, True), (4, 64, 0, 12, False),
+                                              (3, 40, 300, 80, False)])
+def test_penalize_by_rows_is_penalize(T, N, L, nbias, mask):
+    rng = np.random.default_rng(N)
+    x = 3 * rng.standard_normal((T, N))
+    x[0, :3] = np.nan, np.inf, -np.inf
+    a = dict(repetition=rng.uniform(0.8, 1.5, T), frequency=rng.uniform(-0.5, 0.5, T), presence=rng.uniform(-1, 1, T))
+    if L:
+        a.update(history=rng.integers(-2, N + 2, (T, L)), lengths=rng.integers(-1, L + 3, T),
+                 prompt=rng.integers(-1, L + 3, T))
+    if nbias:
+        start = np.concatenate([[0], np.cumsum(rng.integers(0, nbias, T))])
+        start[1] = -3  # an empty row, and one from the list's beginning
+        a["bias"] = (start, rng.integers(-1, N + 1, start[-1]), rng.standard_normal(start[-1]))
+    if mask:
+        a["mask"] = rng.integers(0, 2 ** 32, (T, (N + 31) // 32), dtype=np.uint32)
+    for got, want in zip(pr.penalize_rows(x, **a), pr.penalize_ref(x, **a)):
+        np.testing.assert_array_equal(got, want)
