@@ -295,8 +295,10 @@ int grouped_gemm(const uint8_t* x_codes, const uint8_t* x_scales, const float* g
  *
  * Bytes of workspace for grouped_plan and grouped_combine with these sizes
  * (D: hidden size, the combined output's columns; F: the experts' inner
- * size); 0 for invalid sizes. The workspace's state prefix is the router
- * calls' (see router_workspace_bytes); neither call touches it.
+ * size); 0 for sizes that neither grouped_swiglu nor grouped_combine takes. A
+ * layer of both needs D % 32 == 0 and F % 32 == 0. The workspace's state
+ * prefix is the router calls' (see router_workspace_bytes); neither call
+ * touches it.
  */
 size_t grouped_workspace_bytes(int64_t T, int64_t k, int64_t G, int64_t D, int64_t F);
 

@@ -842,6 +842,14 @@ int check_sizes(int64_t T, int64_t k, int64_t G, int64_t N, int64_t K, int64_t o
   return ROUTER_OK;
 }
 
+int check_swiglu(int64_t T, int64_t k, int64_t G, int64_t F, int64_t D) {
+  return F < 16 || F % 16 != 0 ? ROUTER_EINVAL : check_sizes(T, k, G, 2 * F, D, T);
+}
+
+int check_combine(int64_t T, int64_t k, int64_t G, int64_t D, int64_t F) {
+  return D < 16 || D % 16 != 0 ? ROUTER_EINVAL : check_sizes(T, k, G, D, F, 0);
+}
+
 size_t combine_scratch(int64_t T, int64_t k, int64_t N) { return (size_t)(T * k) * (size_t)N * sizeof(float); }
 
 }  // namespace
@@ -849,8 +857,7 @@ size_t combine_scratch(int64_t T, int64_t k, int64_t N) { return (size_t)(T * k)
 extern "C" {
 
 size_t grouped_workspace_bytes(int64_t T, int64_t k, int64_t G, int64_t D, int64_t F) {
-  if (F < 1 || D < 1 || F > ROUTER_MAX_GATE_D || check_sizes(T, k, G, 1, 32, 0) != ROUTER_OK || D > ROUTER_MAX_GATE_D)
-    return 0;
+  if (check_swiglu(T, k, G, F, D) != ROUTER_OK && check_combine(T, k, G, D, F) != ROUTER_OK) return 0;
   const size_t p = nvr::plan_scratch_bytes(T * k, G), c = combine_scratch(T, k, D);
   return nvr::kScratchOffset + (p > c ? p : c);
 }
@@ -859,8 +866,7 @@ int grouped_swiglu(const uint8_t* x_codes, const uint8_t* x_scales, const float*
                    const uint8_t* w_scales, const float* gsw, const float* bias, const int32_t* offsets,
                    const int32_t* rows, int64_t T, int64_t k, int64_t G, int64_t F, int64_t D, void* out,
                    void* stream) {
-  if (F < 16 || F % 16 != 0) return ROUTER_EINVAL;
-  const int st = check_sizes(T, k, G, 2 * F, D, T);
+  const int st = check_swiglu(T, k, G, F, D);
   if (st != ROUTER_OK) return st;
   if (!gsa || !w_codes || !w_scales || !gsw || !offsets) return ROUTER_EINVAL;
   if (T > 0 && (!x_codes || !x_scales || !rows || !out)) return ROUTER_EINVAL;
@@ -881,8 +887,7 @@ int grouped_combine(const uint8_t* h_codes, const uint8_t* h_scales, const float
                     const uint8_t* w_scales, const float* gsw, const float* bias, const int32_t* offsets,
                     const int32_t* pos, const float* topk_w, const void* residual, int64_t T, int64_t k, int64_t G,
                     int64_t D, int64_t F, void* out, void* workspace, size_t workspace_bytes, void* stream) {
-  if (D < 16 || D % 16 != 0) return ROUTER_EINVAL;
-  const int st = check_sizes(T, k, G, D, F, 0);
+  const int st = check_combine(T, k, G, D, F);
   if (st != ROUTER_OK) return st;
   if (!gsh || !w_codes || !w_scales || !gsw || !offsets) return ROUTER_EINVAL;
   if (T > 0 && (!h_codes || !h_scales || !pos || !topk_w || !out || !workspace)) return ROUTER_EINVAL;

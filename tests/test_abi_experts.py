@@ -50,6 +50,26 @@ def test_workspace_sizes(lib):
         assert lib.lmhead_penalize_workspace_bytes(*bad) == 0, bad
 
 
+def test_workspace_sizes_are_the_calls_sizes(lib):
+    """Zero for just the sizes that both products refuse."""
+    swiglu = Call(lib.grouped_swiglu, xc=P, xs=P, gsa=None, wc=P, ws=P, gsw=P, bias=None, offsets=P, rows=P, T=4, k=2,
+                  G=8, F=64, D=256, out=P, s=None)
+    combine = Call(lib.grouped_combine, hc=P, hs=P, gsh=None, wc=P, ws=P, gsw=P, bias=None, offsets=P, pos=P, w=P,
+                   residual=None, T=4, k=2, G=8, D=64, F=256, out=P, work=P, nbytes=1 << 20, s=None)
+    taken = []
+    for D, F in [(17, 32), (32, 33), (8, 32), (32, 8), (40, 40), (48, 32), (32, 48), (48, 48), (32, 1360), (16, 32),
+                 (32, 16), (16, 16), (1 << 16, 1 << 17), (1 << 17, 1 << 16), (1 << 22, 512), (512, 1 << 22),
+                 (32, (1 << 22) + 32), ((1 << 22) + 32, 32), (1 << 15, 1 << 16), (2048, 7168)]:
+        # A missing scale is refused as EINVAL, after the sizes; sizes that the layouts allow but that are too large
+        # or no multiple of 32 are unsupported.
+        a, b = swiglu(D=D, F=F), combine(D=D, F=F)
+        ok = [a == EINVAL and F >= 16 and F % 16 == 0 and D >= 16 and D % 16 == 0,
+              b == EINVAL and D >= 16 and D % 16 == 0 and F >= 16 and F % 16 == 0]
+        assert (lib.grouped_workspace_bytes(4, 2, 8, D, F) > 0) == any(ok), (D, F, a, b)
+        taken.append(any(ok))
+    assert any(taken) and not all(taken)
+
+
 def test_plan_refusals(lib):
     c = Call(lib.grouped_plan, idx=P, T=4, k=2, first=0, G=8, offsets=P, rows=P, pos=P, ws=P, nbytes=1 << 20, s=None)
     for bad in [dict(T=-1), dict(k=0), dict(G=0), dict(first=-1), dict(idx=None), dict(offsets=None), dict(rows=None),
