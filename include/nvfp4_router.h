@@ -296,7 +296,9 @@ int grouped_gemm(const uint8_t* x_codes, const uint8_t* x_scales, const float* g
  * Bytes of workspace for grouped_plan and grouped_combine with these sizes
  * (D: hidden size, the combined output's columns; F: the experts' inner
  * size); 0 for sizes that neither grouped_swiglu nor grouped_combine takes. A
- * layer of both needs D % 32 == 0 and F % 32 == 0. The workspace's state
+ * layer of both needs D % 32 == 0 and F % 32 == 0. grouped_combine keeps
+ * T * k * D fp32 products there, whatever share of the experts is held (7.5 GB
+ * at T = 32768, k = 8, D = 7168). The workspace's state
  * prefix is the router calls' (see router_workspace_bytes); neither call
  * touches it.
  */

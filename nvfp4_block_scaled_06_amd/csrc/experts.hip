@@ -139,11 +139,13 @@ __device__ __forceinline__ uint32_t within(uint32_t v, int left) {
 //  * Past D the x tile holds zeros, and what a padded step reads of the next
 //    weight row there takes a scale of zero: codes are finite, but scale bytes
 //    0x7F and 0xFF are NaN, and 0 NaN is NaN.
-// Bound by HBM: grouped_swiglu at T = 64, D = 7168, F = 2048, k = 8 reads the
-// 2.7 GB of the 165 of 256 experts that tokens hit under a mild skew in 450
-// us, 6.1 TB/s; at
-// T = 1 (132 MB, 24 us in the kernel) by the latency of a workgroup's chain
-// of steps.
+// Bound by HBM: grouped_swiglu at T = 64, D = 7168, F = 2048, k = 8 needs the
+// 2.7 GB of the 165 of 256 experts that tokens hit under a mild skew, reads
+// 2.9 GB and takes 450 us, 6.5 TB/s; grouped_combine needs 1.36 GB, reads 1.62
+// and takes 267 us, 6.1 TB/s. The loads ahead have no bound at K: what they
+// read past it (of the rows that follow) is more the shorter K is. At T = 1
+// (132 MB, 26 us in the kernel) by the latency of a workgroup's chain of
+// steps.
 constexpr int kEsWaves = 4;
 constexpr int kEsThreads = 64 * kEsWaves;
 constexpr int kEsRows = 32;       // weight rows per wavefront
@@ -801,8 +803,8 @@ static hipError_t launch_products(ExpertArgs a, hipStream_t stream) {
   const int64_t mean = a.R / a.G;
   a.take = Take::kAll;
   // Also more rows of few experts, while their 16-row tiles are few enough
-  // for two K groups (T = 32, two experts held, D = 7168, F = 768: 22.4 us,
-  // 32-row tiles 31.7; level at K of 512 and less).
+  // for two K groups (T = 32, k = 2, two experts, D = 7168, F = 768: 22.0 us,
+  // 32-row tiles 31.4; level at K of 512 and less).
   const int64_t stream_cols = (a.N + kEsRows * kEsWaves - 1) / (kEsRows * kEsWaves);
   if (mean <= 8 || max_row_tiles(a.R, a.G, 16) * stream_cols <= kEsFewItems)
     return launch_stream<GLU, 16, 512>(a, stream);

@@ -43,8 +43,9 @@ struct RowTile {
 constexpr int kSmallExpert = 32;
 constexpr int kMinTileItems = 128;
 // Those tiles have 64 rows instead as long as every compute unit then has one
-// of them at most (47 experts of 58 rows, 5 column tiles: 230 us with 128 rows,
-// 215 with 64; 130 of 49 rows, 2 column tiles: 71 and 63).
+// of them at most (47 experts of 58 rows, K = 7168, 5 column tiles: swiglu 205
+// us with 128 rows, 187 with 64, combine 217 and 200; 130 of 49 rows, K = 4096,
+// 2 column tiles: swiglu 138 and 118).
 constexpr int kOneRound = 256;
 enum class Take { kAll, kSmall, kLarge };
 

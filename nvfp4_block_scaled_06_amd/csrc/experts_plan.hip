@@ -11,10 +11,11 @@
 // histograms' LDS atomics may run in any order.
 //
 // Bound by latency: the chain of load, count, scan and place. T = 1, k = 8,
-// 256 experts: 3.3 us in one workgroup of four wavefronts. T = 32768, k = 8,
+// 256 experts: 3.2 us in one workgroup of four wavefronts. T = 32768, k = 8,
 // 384 experts: 3.2 us for the 64 chunks' histograms and 10.4 us to place the
-// slots (3.1 MB in all), 16.1 us for a call; 28.7 us before the threads shared
-// the chunks' histograms.
+// slots (3.1 MB in all), each as the profiler takes it by itself; 12.6 us a
+// call in a row of calls without the profiler, 28.7 us before the threads
+// shared the chunks' histograms.
 #include "../../include/nvfp4_router.h"
 #include "experts_common.hpp"
 
