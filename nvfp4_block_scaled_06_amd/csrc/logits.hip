@@ -25,7 +25,7 @@
 // 4.6 TB/s with nontemporal accesses (65.5 without; the logits fill the
 // caches twice over), 123 us with a workgroup per chunk that re-reads the
 // history and looks at every token's counts by itself. In bf16 42 us, 3.3
-// TB/s: the work in LDS per chunk is the same. T = 1: 7.0 us.
+// TB/s: as many instructions for a token as in fp32. T = 1: 7.0 us.
 #include "../../include/nvfp4_router.h"
 #include <type_traits>
 
