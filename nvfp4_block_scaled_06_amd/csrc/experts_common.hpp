@@ -81,7 +81,8 @@ struct TileScan {
         }
       big = __builtin_amdgcn_readlane(wave_prefix_sum(big), 63);
       if (take == Take::kLarge) {
-        half = __builtin_amdgcn_readlane(wave_prefix_sum(half), 63);
+        // Only counts up to kOneRound matter.
+        half = __builtin_amdgcn_readlane(wave_prefix_sum(min(half, kOneRound + 1)), 63);
         if ((int64_t)half * tile_cols <= kOneRound) sh = 6;
       }
       const bool split = (int64_t)big * tile_cols >= kMinTileItems;
@@ -92,6 +93,9 @@ struct TileScan {
 #pragma unroll
     for (int i = 0; i < kGroupsPerLane; ++i)
       if (i < per) mine += tiles(i);
+    // Offsets that no plan gives may name R rows for every other expert: 2^31
+    // tiles of R near 2^30. A plan's tiles are at most R / 128 + G where R is large.
+    mine = min(mine, 1 << 24);
     const int incl = wave_prefix_sum(mine);
     before = incl - mine;
     experts = __builtin_amdgcn_readlane(incl, 63);

@@ -12,6 +12,8 @@ from oracle import quant_ref, router_ref
 
 pytestmark = pytest.mark.gpu
 
+STATE = 4096 + 131072  # ROUTER_WORKSPACE_STATE_BYTES
+
 
 def log(msg):
     print(f"[gpu-experts] {msg}", flush=True)
@@ -403,6 +405,45 @@ def test_a_nan_scale_stays_in_its_row(dev, ws, T, k, E, F, D):
         assert not torch.any(torch.isnan(want))
         assert torch.equal(torch.isnan(got), nan), (what, int(torch.isnan(got).sum()), int(nan.sum()))
         assert torch.equal(got[~nan], want[~nan]), what
+
+
+@pytest.mark.parametrize("T,k,G,F,D", [(2, 4, 8, 48, 352), (64, 4, 16, 1040, 448), (300, 7, 40, 1024, 192),
+                                       (1400, 8, 40, 704, 288), (1400, 8, 40, 2080, 96)])
+@pytest.mark.parametrize("kind", ["every other", "stray", "falling", "past the end"])
+def test_offsets_that_no_plan_gives(dev, ws, T, k, G, F, D, kind):
+    """Offsets, rows and positions of no plan: their results are undefined, what lies around the outputs is untouched,
+    and the next call with a plan is right."""
+    log(f"offsets {kind} T={T} k={k} G={G} F={F} D={D}")
+    R, r = T * k, np.random.default_rng(G)
+    lo, hi = np.iinfo(np.int32).min, np.iinfo(np.int32).max
+    off = {"every other": np.arange(G + 1) % 2 * R, "stray": r.integers(lo, hi, G + 1),
+           "falling": R - np.arange(G + 1) * (R // G), "past the end": np.arange(G + 1) * R}[kind].astype(np.int32)
+    idx = routing(T, k, G, T + F, "skewed")
+    plan = make_plan(idx, G, 0, ws, dev)
+    stray = [torch.from_numpy(v.astype(np.int32)).to(dev) for v in (off, r.integers(lo, hi, R), r.integers(lo, hi, R))]
+    bad = [rt.GroupedPlan(*stray, T, k), rt.GroupedPlan(stray[0], plan.rows, plan.pos, T, k)]
+    xq = rt.quantize(to_dev(bits((T, D), T, 2.0), dev), ws)
+    hq = rt.quantize(to_dev(bits((R, D), T, 0.5), dev), ws)
+    wg = rt.quantize_grouped_weights(to_dev(bits((G, 2 * F, D), D, D ** -0.5), dev), ws)
+    w = torch.from_numpy(r.uniform(0.05, 0.6, (T, k)).astype(np.float32)).to(dev)
+    used = rt.grouped_workspace_bytes(T, k, G, 2 * F, D)
+    wsl = rt.Workspace(used + (1 << 20), dev)
+    wsl.buf[used:] = 77
+    want = rt.grouped_swiglu(xq, wg, plan), rt.grouped_combine(hq, wg, plan, w, ws)
+    guard = 1 << 16
+    outs = []
+    for rows, cols in ((R, F), (T, 2 * F)):
+        buf = torch.full((2 * guard + rows * cols,), 7.0, dtype=torch.bfloat16, device=dev)
+        outs.append((buf, buf[guard:guard + rows * cols].view(rows, cols)))
+    torch.cuda.synchronize()
+    for p in bad + [plan]:
+        rt.grouped_swiglu(xq, wg, p, out=outs[0][1])
+        rt.grouped_combine(hq, wg, p, w, wsl, out=outs[1][1])
+        torch.cuda.synchronize()
+        for buf, _ in outs:
+            assert torch.all(buf[:guard] == 7.0) and torch.all(buf[-guard:] == 7.0)
+        assert torch.all(wsl.buf[used:] == 77) and torch.all(wsl.buf[:STATE] == 0)
+    assert torch.equal(outs[0][1], want[0]) and torch.equal(outs[1][1], want[1])
 
 
 def test_binding_refusals(dev, ws):
