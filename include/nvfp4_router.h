@@ -379,7 +379,7 @@ int grouped_combine(const uint8_t* h_codes, const uint8_t* h_scales, const float
                     const int32_t* pos, const float* topk_w, const void* residual, int64_t T, int64_t k, int64_t G,
                     int64_t D, int64_t F, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
-#define ROUTER_F32 0  /* dtype of lmhead_penalize's logits */
+#define ROUTER_F32 0  /* dtype of logits */
 #define ROUTER_BF16 1
 
 /*
@@ -430,6 +430,55 @@ int lmhead_penalize(const void* logits, int dtype, int64_t T, int64_t N, int64_t
                     const int32_t* bias_start, const int32_t* bias_token, const float* bias_value, int64_t nbias,
                     const uint32_t* mask, int64_t ld_mask, void* out, int64_t ld_out, int32_t* out_idx,
                     float* out_logit, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Routing on given logits: the rules of choice beside router_gate_topk's own
+ * (which is ROUTER_SIGMOID with a bias, one group and renormalised weights,
+ * fused behind the gate). For row t, with s = sigmoid(l) or softmax(l) over the
+ * E logits l and key = s + bias:
+ *   - the experts form `groups` groups of E / groups neighbours; a group's
+ *     score is the sum of its group_top (1 or 2) largest keys, and experts
+ *     outside the topk_groups groups with the largest scores (a tie going to
+ *     the lower group) are left out;
+ *   - topk_idx [T, k] int32: the k largest keys among the rest, in descending
+ *     order, a tie going to the lower expert;
+ *   - topk_w [T, k] fp32: routed_scale * s / (renormalize ? sum of the chosen
+ *     s : 1), the bias left out.
+ * The order is that of keys computed in 64 bits. An expert whose logit is
+ * -infinity or NaN, or whose key is, is never chosen (it counts as -infinity
+ * in its group); where fewer than k remain, the places left hold -1 and weight
+ * 0, which grouped_plan takes as slots of no expert. Renormalised weights hold
+ * for any finite logits, however small their s. A logit of +infinity makes
+ * softmax weights NaN.
+ *   logits        [T, E] of `dtype`, ld >= E elements between rows.
+ *   bias          NULL or [E] fp32.
+ *   scoring       ROUTER_SIGMOID or ROUTER_SOFTMAX.
+ *   T, E, k       T >= 0; 1 <= k <= topk_groups * (E / groups); E % groups == 0;
+ *                 1 <= topk_groups <= groups (ROUTER_EINVAL otherwise); E > 512,
+ *                 k > 32 and groups > ROUTER_MAX_GROUPS give
+ *                 ROUTER_EUNSUPPORTED.
+ * Pointers are aligned to their element. One launch, no workspace.
+ */
+#define ROUTER_SIGMOID 0
+#define ROUTER_SOFTMAX 1
+#define ROUTER_MAX_GROUPS 64
+int router_select(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int scoring,
+                  int64_t groups, int64_t topk_groups, int64_t group_top, int renormalize, float routed_scale,
+                  int64_t k, int32_t* topk_idx, float* topk_w, void* stream);
+
+/*
+ * The gradient of router_select's logits, grad_logits [T, E] of the logits'
+ * type, from that of its weights, grad_w [T, k] fp32, for the choice topk_idx
+ * (places outside [0, E) are left out, whatever their grad_w; an expert named
+ * twice takes part twice). The choice itself has no gradient, and so the bias
+ * and the groups have none. Rows are written whole, with ld_grad >= E
+ * elements between them; grad_logits must not overlap the logits. Without
+ * renormalisation softmax scores give every expert a gradient, otherwise the
+ * chosen ones alone have one. fp32 until the one rounding.
+ */
+int router_select_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const int32_t* topk_idx,
+                           const float* grad_w, int scoring, int renormalize, float routed_scale, int64_t k,
+                           void* grad_logits, int64_t ld_grad, void* stream);
 
 /*
  * Measurement aid, not part of the router path: reads `bytes` of `buf`

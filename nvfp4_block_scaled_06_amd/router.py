@@ -19,7 +19,7 @@ EXPORTS = ("router_workspace_bytes", "router_workspace_init", "router_quantize",
            "router_forward", "router_forward_noalloc", "router_status_string", "router_probe_read",
            "router_probe_mfma", "lmhead_workspace_bytes", "lmhead_argmax", "grouped_offsets", "grouped_gemm",
            "grouped_workspace_bytes", "grouped_plan", "grouped_swiglu", "grouped_combine",
-           "lmhead_penalize_workspace_bytes", "lmhead_penalize")
+           "lmhead_penalize_workspace_bytes", "lmhead_penalize", "router_select", "router_select_backward")
 ROUTER_ESCRATCH = -4
 STATIC_SCRATCH_BYTES = 16 << 20
 
@@ -81,6 +81,11 @@ def load_library(path=LIB_PATH):
     L.lmhead_penalize.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64,
                                   vp, i64, vp, i64, vp, vp, vp, sz, vp]
     L.lmhead_penalize.restype = ctypes.c_int
+    ci, fl = ctypes.c_int, ctypes.c_float
+    L.router_select.argtypes = [vp, ci, i64, i64, i64, vp, ci, i64, i64, i64, ci, fl, i64, vp, vp, vp]
+    L.router_select.restype = ci
+    L.router_select_backward.argtypes = [vp, ci, i64, i64, i64, vp, vp, ci, ci, fl, i64, vp, i64, vp]
+    L.router_select_backward.restype = ci
     _lib = L
     return L
 
@@ -557,6 +562,67 @@ def lmhead_penalize(logits, workspace, history=None, prompt=None, lengths=None, 
           ldh, lengths, prompt, repetition, frequency, presence, start, token, value, nbias, mask, ldm, out, ldo, idx,
           logit, workspace.buf, workspace.nbytes)
     return idx, logit, out
+
+
+SCORING = {"sigmoid": 0, "softmax": 1}
+
+
+def _scoring(name):
+    if name not in SCORING:
+        raise RouterError(f"scoring must be one of {tuple(SCORING)}")
+    return SCORING[name]
+
+
+def select(logits, k, bias=None, scoring="sigmoid", groups=1, topk_groups=1, group_top=2, renormalize=True,
+           routed_scale=1.0, out=None):
+    """router_select: the k experts of each row of logits [T, E] (fp32 or bf16) and their weights.
+
+    Scores by "sigmoid" or "softmax", a bias [E] fp32 that moves the choice only, and of `groups` groups of neighbouring
+    experts the topk_groups with the largest sums of their group_top (1 or 2) best. Returns ``(topk_idx [T, k] int32,
+    topk_w [T, k] fp32)``, as router_gate_topk gives them to grouped_plan and grouped_combine; -1 and 0 where masked
+    logits (-inf, NaN) leave nothing to choose."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise RouterError("logits must be a GPU matrix")
+    T, E = logits.shape
+    ld = _rows_tensor(logits, "logits", (torch.float32, torch.bfloat16), T)
+    dev = logits.device
+    if bias is not None:
+        _tensor(bias, "bias", torch.float32, (E,), dev)
+    if out is None:
+        if k < 1:
+            raise RouterError("k must be at least 1")
+        out = (torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty((T, k), dtype=torch.float32, device=dev))
+    else:
+        _tensor(out[0], "topk_idx", torch.int32, (T, k), dev)
+        _tensor(out[1], "topk_w", torch.float32, (T, k), dev)
+    _call(load_library().router_select, dev, logits, 0 if logits.dtype == torch.float32 else 1, T, E, ld, bias,
+          _scoring(scoring), groups, topk_groups, group_top, 1 if renormalize else 0, routed_scale, k, out[0], out[1])
+    return out
+
+
+def select_backward(logits, topk_idx, grad_w, scoring="sigmoid", renormalize=True, routed_scale=1.0, out=None):
+    """router_select_backward: the gradient of select's logits [T, E], in their type, from grad_w [T, k] fp32, the
+    gradient of its weights, for its choice topk_idx [T, k] int32."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise RouterError("logits must be a GPU matrix")
+    T, E = logits.shape
+    ld = _rows_tensor(logits, "logits", (torch.float32, torch.bfloat16), T)
+    dev = logits.device
+    if not isinstance(topk_idx, torch.Tensor) or topk_idx.dim() != 2:
+        raise RouterError("topk_idx must be a GPU matrix")
+    k = topk_idx.shape[1]
+    _tensor(topk_idx, "topk_idx", torch.int32, (T, k), dev)
+    _tensor(grad_w, "grad_w", torch.float32, (T, k), dev)
+    ldo = E
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    else:
+        ldo = _rows_tensor(out, "out", (logits.dtype,), T)
+        if out.shape != logits.shape or out.device != dev:
+            raise RouterError("out must have the dtype, shape and device of logits")
+    _call(load_library().router_select_backward, dev, logits, 0 if logits.dtype == torch.float32 else 1, T, E, ld,
+          topk_idx, grad_w, _scoring(scoring), 1 if renormalize else 0, routed_scale, k, out, ldo)
+    return out
 
 
 MFMA_PROBE_SINK = 1024 * 256
