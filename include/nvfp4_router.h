@@ -432,6 +432,69 @@ int lmhead_penalize(const void* logits, int dtype, int64_t T, int64_t N, int64_t
                     float* out_logit, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Losses of the lm_head over its whole vocabulary, with the gradient of x, and
+ * without T x N logits in memory: z[t, n] = gsa * gsw * sum_d xhat[t, d] *
+ * what[n, d], lmhead_argmax's logits, are taken in pieces of the vocabulary.
+ *
+ * lmhead_loss, the cross entropy (the negative log-probability of a token):
+ *   lse[t] = log sum_n e^z[t, n];  loss[t] = lse[t] - z[t, targets[t]]
+ *   dx[t, d] = weight[t] * gsw * sum_n (e^(z[t, n] - lse[t]) - [n = targets[t]]) * what[n, d]
+ * A target outside [0, N) (-100, for example) gives loss 0 and a gradient of
+ * zeros.
+ *
+ * lmhead_distill, the divergence from a teacher of which K logits per token
+ * are known, at a temperature tau:
+ *   lse[t] = log sum_n e^(z[t, n] / tau)
+ *   logq[t, j] = z[t, tokens[t, j]] / tau - lse[t]
+ *   p[t, j] = softmax over j of teacher[t, j] / tau
+ *   loss[t] = tau^2 * sum_j p[t, j] * (log p[t, j] - logq[t, j])
+ *   dx[t, d] = weight[t] * gsw * tau * sum_n (e^(z[t, n] / tau - lse[t]) - sum_{j: tokens[t, j] = n} p[t, j]) * what[n, d]
+ * Places whose token is outside [0, N) are left out whatever their teacher's
+ * logit is, and have logq 0; -infinity is p = 0; a row without any place, or
+ * with -infinity alone, has loss 0 and a gradient of zeros. A token may be
+ * named more than once. Teacher logits of NaN or +infinity make their row's
+ * loss and gradient NaN.
+ *
+ * dx is the gradient of sum_t weight[t] * loss[t] with respect to the
+ * dequantized x (the quantization of x passes it through); the 4-bit weights
+ * have none.
+ *   x_codes, x_scales, gsa   router_quantize outputs for x [T, D] (16- and
+ *                            2-byte aligned).
+ *   w_codes, w_scales, gsw   the weights in the same format: [N, D/2],
+ *                            [N, D/16] (16- and 4-byte aligned).
+ *   targets                  [T] int32.
+ *   tokens, teacher          [T, K] int32 and [T, K] of `dtype`.
+ *   temperature              2^-20 to 2^20.
+ *   weight                   NULL (1) or [T] fp32; for dx alone.
+ *   T, D, N, K               T >= 0; D >= 32, D % 32 == 0; N, K >= 1
+ *                            (ROUTER_EINVAL otherwise); T >
+ *                            ROUTER_MAX_LOSS_ROWS, D > ROUTER_MAX_GATE_D, N >
+ *                            2^30 and K > ROUTER_MAX_TEACHER give
+ *                            ROUTER_EUNSUPPORTED.
+ *   loss, lse, logq          [T], [T], [T, K] fp32 out.
+ *   dx                       NULL (no gradient) or [T, D] bf16 out (16-byte
+ *                            aligned).
+ *   workspace                lmhead_loss_workspace_bytes(T, D, N, dx != NULL)
+ *                            bytes, 256-byte aligned, for either call; its
+ *                            state prefix (see router_workspace_bytes) is not
+ *                            touched. 0 for sizes that the calls refuse.
+ * Products are exact with fp32 sums in a fixed order, so results repeat bit for
+ * bit. In dx the columns' softmax weights are rounded to 11 bits, those of the
+ * named tokens to 24, and dx to bf16 at the end.
+ */
+#define ROUTER_MAX_LOSS_ROWS (1 << 18)
+#define ROUTER_MAX_TEACHER 1024
+size_t lmhead_loss_workspace_bytes(int64_t T, int64_t D, int64_t N, int grad);
+int lmhead_loss(const uint8_t* x_codes, const uint8_t* x_scales, const float* gsa, const uint8_t* w_codes,
+                const uint8_t* w_scales, const float* gsw, const int32_t* targets, const float* weight, int64_t T,
+                int64_t D, int64_t N, float* loss, float* lse, void* dx, void* workspace, size_t workspace_bytes,
+                void* stream);
+int lmhead_distill(const uint8_t* x_codes, const uint8_t* x_scales, const float* gsa, const uint8_t* w_codes,
+                   const uint8_t* w_scales, const float* gsw, const int32_t* tokens, const void* teacher, int dtype,
+                   int64_t K, float temperature, const float* weight, int64_t T, int64_t D, int64_t N, float* loss,
+                   float* lse, float* logq, void* dx, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Routing on given logits: the rules of choice beside router_gate_topk's own
  * (which is ROUTER_SIGMOID with a bias, one group and renormalised weights,
  * fused behind the gate). For row t, with s = sigmoid(l) or softmax(l) over the

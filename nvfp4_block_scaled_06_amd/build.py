@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4_router.so")
 SOURCES = ["router_api.hip", "quantize.hip", "gate.hip", "gate_mfma_e4.hip", "gate_mfma_e8.hip", "gate_mfma_e16.hip", "gate_mfma_e24.hip", "gate_mfma_e32.hip", "gate_decode.hip", "gate_batch.hip", "probe.hip", "lmhead.hip", "grouped.hip",
-           "experts_plan.hip", "experts.hip", "logits.hip", "select.hip"]
+           "experts_plan.hip", "experts.hip", "logits.hip", "select.hip", "loss.hip"]
 
 COMPILE_FLAGS = [
     "--offload-arch=gfx950",

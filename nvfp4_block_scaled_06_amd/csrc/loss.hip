@@ -1,0 +1,643 @@
+// Losses of the NVFP4 lm_head over its whole vocabulary, with their gradients
+// (gfx950), without T x N logits in memory.
+//
+//   z[t, n] = gsa gsw sum_d xhat[t, d] what[n, d],   xhat, what = q S
+//   lmhead_loss:    lse = log sum_n e^z;  loss = lse - z[t, target]
+//   lmhead_distill: q = softmax(z / tau), p = softmax(teacher / tau) over the
+//                   teacher's K tokens;  loss = tau^2 sum_j p_j (log p_j - log q_j)
+//   both:           dx = weight gsw tau sum_n (q_n - p_n) what[n]
+// Cross entropy is the case of one token with p = 1 and tau = 1.
+//
+// The vocabulary is taken in pieces. A piece's products stay in registers and
+// give each row a maximum and a sum for every block of columns
+// (softmax_block.hpp); with a gradient they also leave the columns' weights
+// e = 2^(y - m), fp16, and a second product sum_n e[t, n] what[n] is added to
+// what the pieces before gave. The weights of a piece are those of the
+// softmax up to a factor per row, which the pieces after may change: as a row's
+// maximum rises, its sums so far shrink. So the gradient needs two products,
+// not the three of computing the logits again once their sum is known.
+//
+// The K tokens of the loss do not take part in that second product: their
+// weights are set to zero there, and q_j - p_j, in fp32, multiplies their rows
+// at the end. Where q is near p nothing is lost to fp16.
+#include "../../include/nvfp4_router.h"
+#include "experts_tile.hpp"
+
+#include <algorithm>
+
+namespace nvr {
+
+constexpr int kHeadTokens = 1024;  // ROUTER_MAX_TEACHER
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// ---------------------------------------------------------------------------
+// Logits of a piece: the experts' tiles, one matrix.
+// ---------------------------------------------------------------------------
+template <Out M, int MR, int KB, Scales S>
+__global__ __launch_bounds__(kEsThreads) void head_stream_kernel(ExpertArgs a, int row_tiles) {
+  __shared__ StreamLds<MR, KB, 1> lds;
+  // The row tiles of one column tile side by side on one XCD: they read the same weights.
+  const int n = xcd_order(blockIdx.x, gridDim.x), ct = n / row_tiles, row0 = (n - ct * row_tiles) * MR;
+  const ExpertTile tile{{0, row0, min(MR, a.R - row0)}, ct};
+  stream_tile<M, MR, KB, 1, S>(a, tile, lds);
+}
+
+template <Out M, Scales S>
+__global__ __launch_bounds__(kEtThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_wide_kernel(
+    ExpertArgs a, int row_tiles) {
+  __shared__ TileLds lds;
+  const int n = xcd_order(blockIdx.x, gridDim.x), ct = n / row_tiles, row0 = (n - ct * row_tiles) * kEtRows;
+  const ExpertTile tile{{0, row0, min(kEtRows, a.R - row0)}, ct};
+  const int nr = tile.rt.nr;
+  if (nr > 96) wide_tile<M, 4, S>(a, tile, lds);
+  else if (nr > 64) wide_tile<M, 3, S>(a, tile, lds);
+  else if (nr > 32) wide_tile<M, 2, S>(a, tile, lds);
+  else wide_tile<M, 1, S>(a, tile, lds);
+}
+
+// ---------------------------------------------------------------------------
+// The tokens of the loss.
+// ---------------------------------------------------------------------------
+struct HeadArgs {
+  const uint8_t* xc;
+  const uint8_t* xs;
+  const float* gsa;
+  const uint8_t* wc;
+  const uint8_t* ws;
+  const float* gsw;
+  int T, D, N, K;
+  const int32_t* tokens;  // [T, K]
+  const void* teacher;    // NULL (cross entropy: K = 1, p = 1) or [T, K]
+  int teacher_bf16;
+  float tau;
+  const float* weight;  // NULL (1) or [T]
+  const float2* stats;  // [T, blocks] (m, s)
+  int blocks;
+  float* loss;
+  float* lse;
+  float* logq;  // [T, K]; NULL for cross entropy
+  void* dx;     // bf16 [T, D]
+};
+
+__device__ __forceinline__ float teacher_at(const HeadArgs& a, int64_t i) {
+  return (a.teacher_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.teacher)[i] << 16)
+                         : static_cast<const float*>(a.teacher)[i]) / a.tau;
+}
+
+__device__ __forceinline__ float2 soft_join(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  if (!(m > -__builtin_inff())) return a;  // nothing yet
+  return make_float2(m, a.y * __builtin_amdgcn_exp2f(a.x - m) + b.y * __builtin_amdgcn_exp2f(b.x - m));
+}
+
+__device__ __forceinline__ float2 wave_join(float2 v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = soft_join(v, make_float2(__shfl_xor(v.x, o), __shfl_xor(v.y, o)));
+  return v;
+}
+
+// Teacher's largest entry and sum of exponentials of row t, over entries that
+// name a token: (m, sum); sum 0 for a row without any. Every wavefront takes
+// the whole row.
+__device__ __forceinline__ float2 teacher_row(const HeadArgs& a, int64_t t) {
+  const int lane = threadIdx.x & 63;
+  float m = -__builtin_inff();
+  for (int j = lane; j < a.K; j += 64) {
+    const int n = a.tokens[t * a.K + j];
+    if (n >= 0 && n < a.N) {
+      const float v = teacher_at(a, t * a.K + j);
+      m = v != v ? v : fmaxf(m, v);  // a NaN of a token that counts stays one
+    }
+  }
+  const bool nan = __ballot(m != m) != 0;
+  m = wave_max(m);
+  if (nan) return make_float2(__builtin_nanf(""), __builtin_nanf(""));
+  if (!(m > -__builtin_inff())) return make_float2(0.0f, 0.0f);
+  float s = 0.0f;
+  for (int j = lane; j < a.K; j += 64) {
+    const int n = a.tokens[t * a.K + j];
+    if (n >= 0 && n < a.N) s += expf(teacher_at(a, t * a.K + j) - m);
+  }
+  return make_float2(m, wave_sum(s));
+}
+
+// One workgroup per row: lse from the blocks' sums, the logits of the row's
+// tokens by themselves (a wavefront per token: its weight row against x), and
+// the loss. Exact products, fp32 sums in a fixed order.
+constexpr int kTokWaves = 4;
+__global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a) {
+  __shared__ float2 part[kTokWaves];
+  __shared__ float terms[kTokWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x;
+  const float scale = load_early(a.gsa) * load_early(a.gsw) / a.tau;
+  float2 v = make_float2(-__builtin_inff(), 0.0f);
+  for (int i = threadIdx.x; i < a.blocks; i += 64 * kTokWaves) v = soft_join(v, a.stats[t * a.blocks + i]);
+  v = wave_join(v);
+  if (lane == 0) part[wave] = v;
+  __syncthreads();
+  v = part[0];
+#pragma unroll
+  for (int w = 1; w < kTokWaves; ++w) v = soft_join(v, part[w]);
+  const float lse = v.x * kLn2 + logf(v.y);
+  float2 tr = make_float2(0.0f, 1.0f);  // log p = 0 for cross entropy
+  if (a.teacher) tr = teacher_row(a, t);
+  const float logs = a.teacher ? logf(tr.y) : 0.0f;
+
+  const int nch = a.D >> 5;
+  const int64_t rowc = a.D / 2, rows = a.D / 16;
+  const uint8_t *xc = a.xc + t * rowc, *xs = a.xs + t * rows;
+  float sum = 0.0f;
+  for (int j = wave; j < a.K; j += kTokWaves) {
+    const int n = a.tokens[t * a.K + j];
+    const bool valid = n >= 0 && n < a.N;
+    float logq = 0.0f;
+    if (valid) {
+      const uint8_t *wc = a.wc + n * rowc, *ws = a.ws + n * rows;
+      float acc = 0.0f;
+      for (int c = lane; c < nch; c += 64) {
+        const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(xc + 16 * c), wv = *reinterpret_cast<const u32x4_t*>(wc + 16 * c);
+        const uint32_t xb = *reinterpret_cast<const uint16_t*>(xs + 2 * c), wb = *reinterpret_cast<const uint16_t*>(ws + 2 * c);
+        const half2_t xsc = e4m3x2_f16(xb), wsc = e4m3x2_f16(wb);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          acc += dot8(fp4x8_scaled(xv[2 * i + 1], xsc, i), fp4x8_scaled(wv[2 * i + 1], wsc, i),
+                      dot8(fp4x8_scaled(xv[2 * i], xsc, i), fp4x8_scaled(wv[2 * i], wsc, i), 0.0f));
+      }
+      logq = wave_sum(acc) * scale - lse;
+      if (a.teacher) {
+        const float lp = teacher_at(a, t * a.K + j) - tr.x - logs, p = expf(lp);
+        if (p != 0.0f) sum += p * (lp - logq);  // p log p is 0 at 0
+      } else {
+        sum -= logq;
+      }
+    }
+    if (a.logq && lane == 0) a.logq[t * a.K + j] = logq;
+  }
+  if (lane == 0) terms[wave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float l = terms[0];
+#pragma unroll
+    for (int w = 1; w < kTokWaves; ++w) l += terms[w];
+    a.loss[t] = tr.y == 0.0f ? 0.0f : l * a.tau * a.tau;
+    a.lse[t] = lse;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient, per piece: one scale for a row's weights.
+// ---------------------------------------------------------------------------
+struct NormArgs {
+  const float2* stats;  // [T, blocks]: those of this piece come first in each row
+  int blocks, used, block_shift;  // columns per block: 1 << block_shift
+  const float2* before;     // NULL or [T]: (m, s) of the pieces before
+  float2* after;            // [T]
+  float* shrink;            // [T]: factor of the sums so far
+  float* ref;               // [T]: m for the next piece
+  _Float16* e;
+  int64_t ld_e;
+  int T, K, n0, cols, seg;  // seg: columns per workgroup, a multiple of 64
+  const int32_t* tokens;
+};
+
+constexpr int kNormThreads = 256;
+__global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a) {
+  __shared__ float2 part[kNormThreads / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x;
+  const float2* st = a.stats + t * a.blocks;
+  float2 v = make_float2(-__builtin_inff(), 0.0f);
+  for (int i = threadIdx.x; i < a.used; i += kNormThreads) v = soft_join(v, st[i]);
+  v = wave_join(v);
+  if (lane == 0) part[wave] = v;
+  __syncthreads();
+  v = part[0];
+#pragma unroll
+  for (int w = 1; w < kNormThreads / 64; ++w) v = soft_join(v, part[w]);
+  const float2 old = a.before ? a.before[t] : make_float2(-__builtin_inff(), 0.0f);
+  v = soft_join(v, old);
+  if (blockIdx.y == 0 && threadIdx.x == 0) {
+    a.after[t] = v;
+    a.shrink[t] = a.before ? __builtin_amdgcn_exp2f(old.x - v.x) : 0.0f;
+    a.ref[t] = v.x;
+  }
+  // Weights of blocks whose m is lower than the row's.
+  const int c0 = blockIdx.y * a.seg, c1 = min(c0 + a.seg, (a.cols + 31) & ~31);
+  _Float16* e = a.e + t * a.ld_e;
+  for (int c = c0 + 8 * threadIdx.x; c < c1; c += 8 * kNormThreads) {
+    const float m = st[c >> a.block_shift].x;
+    if (m == v.x) continue;
+    const float f = __builtin_amdgcn_exp2f(m - v.x);
+    half8_t h = *reinterpret_cast<const half8_t*>(e + c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (_Float16)((float)h[i] * f);
+    *reinterpret_cast<half8_t*>(e + c) = h;
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < a.K; j += kNormThreads) {
+    const int64_t c = (int64_t)a.tokens[t * a.K + j] - a.n0;
+    if (c >= c0 && c < min(c1, a.cols)) e[c] = (_Float16)0.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient, per piece: sum_n e[t, n] what[n, d].
+//
+// The product runs over the weights' rows, whose codes lie along d: eight rows'
+// words are put together pair by pair (the even and the odd codes of two rows'
+// words give two words whose bytes hold one column's codes of both), so a
+// conversion of a byte gives one column's two neighbours in n, and a lane ends
+// up with 16 columns of 8 rows in MFMA layout, without LDS: lane (r, q) takes
+// columns 16 r .. 16 r + 15 of its wavefront's 256, one for each of 16 tiles.
+// A load takes 8 bytes of each of 64 lanes: whole 128-byte lines of 4 rows.
+// ---------------------------------------------------------------------------
+struct GradArgs {
+  const _Float16* e;
+  int64_t ld_e;
+  const uint8_t* wc;  // of the piece
+  const uint8_t* ws;
+  int T, D, cols, splits, steps;  // steps of 32 rows per split
+  float* part;                    // [splits, T, D]
+  const float* shrink;            // NULL: the first piece
+};
+
+constexpr int kGsWaves = 4;
+constexpr int kGsCols = 256;  // per wavefront
+
+template <int NT>
+__global__ __launch_bounds__(64 * kGsWaves) void head_grad_kernel(GradArgs a) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+  const int d0 = (blockIdx.x * kGsWaves + wave) * kGsCols, dl = d0 + 16 * r;
+  const int split = blockIdx.y, row0 = blockIdx.z * (16 * NT);
+  const int64_t rowc = a.D / 2, rows = a.D / 16;
+  const int n0 = split * a.steps * 32, n1 = min(n0 + a.steps * 32, a.cols);
+  if (d0 >= a.D) return;
+  const int64_t nrows = max(n1 - n0, 0);
+  const __amdgpu_buffer_rsrc_t wcr = make_rsrc(a.wc + n0 * rowc, nrows * rowc);
+  const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.ws + n0 * rows, nrows * rows);
+  const uint32_t oc = dl < a.D ? (uint32_t)(8 * q * rowc + dl / 2) : kMmaOob;
+  const uint32_t os = dl < a.D ? (uint32_t)(8 * q * rows + dl / 16) : kMmaOob;
+  const _Float16* ep[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) ep[t] = a.e + (int64_t)min(row0 + 16 * t + r, a.T - 1) * a.ld_e + n0 + 8 * q;
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  u32x2_t wv[8];
+  uint32_t sv[8];
+  half8_t ev[NT];
+  auto load = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      wv[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(wcr, oc + (uint32_t)((32 * s + i) * rowc), 0, 0));
+      sv[i] = __builtin_amdgcn_raw_buffer_load_b8(wsr, os + (uint32_t)((32 * s + i) * rows), 0, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) ev[t] = *reinterpret_cast<const half8_t*>(ep[t] + 32 * s);
+  };
+  f32x4_t acc[NT][16];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[t][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int nsteps = (int)((nrows + 31) / 32);
+  if (nsteps > 0) load(0);
+  for (int s = 0; s < nsteps; ++s) {
+    uint32_t c[2][2][4];  // word, even / odd columns, pair of rows
+    half2_t sc[4];
+    half8_t A[NT];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const uint32_t x = wv[2 * p][w], y = wv[2 * p + 1][w];
+        c[w][0][p] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
+        c[w][1][p] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+      }
+      sc[p] = e4m3x2_f16(sv[2 * p] | (sv[2 * p + 1] << 8));
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) A[t] = ev[t];
+    if (s + 1 < nsteps) load(s + 1);
+    static_for<0, 16>([&](auto ic) {
+      constexpr int i = decltype(ic)::value, w = i >> 3, odd = i & 1, b = (i & 7) >> 1;
+      half8_t B;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const half2_t h = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[w][odd][p], 1.0f, b) * sc[p];
+        B[2 * p] = h[0];
+        B[2 * p + 1] = h[1];
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[t][i] = mfma16(A[t], B, acc[t][i]);
+    });
+  }
+  // Lane (r, q), value v of tile i: row 4 q + v, column 16 r + i.
+  if (dl >= a.D) return;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int row = row0 + 16 * t + 4 * q + v;
+      if (row >= a.T) continue;
+      float* out = a.part + ((int64_t)split * a.T + row) * a.D + dl;
+      const float f = a.shrink ? a.shrink[row] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32x4_t y = {acc[t][4 * i][v], acc[t][4 * i + 1][v], acc[t][4 * i + 2][v], acc[t][4 * i + 3][v]};
+        f32x4_t* o = reinterpret_cast<f32x4_t*>(out) + i;
+        if (a.shrink) y += *o * f;
+        *o = y;
+      }
+    }
+}
+
+// dx: the splits' sums, divided by the softmax's, and the loss's own tokens.
+struct DxArgs {
+  HeadArgs h;
+  const float* part;
+  int splits;
+};
+
+constexpr int kDxThreads = 256;
+__global__ __launch_bounds__(kDxThreads) void head_dx_kernel(DxArgs a) {
+  __shared__ float coef[kHeadTokens];
+  __shared__ int tok[kHeadTokens];
+  const HeadArgs& h = a.h;
+  const int64_t t = blockIdx.x;
+  const float2 soft = h.stats[t];  // (m, s) of the whole row
+  const float gsw = load_early(h.gsw);
+  float2 tr = make_float2(0.0f, 1.0f);
+  if (h.teacher) tr = teacher_row(h, t);
+  bool any = false;
+  for (int j = threadIdx.x; j < h.K; j += kDxThreads) {
+    const int n = h.tokens[t * h.K + j];
+    const bool valid = n >= 0 && n < h.N;
+    float c = 0.0f;
+    if (valid) {
+      const float q = expf(h.teacher ? h.logq[t * h.K + j] : -h.loss[t]);
+      const float p = h.teacher ? expf(teacher_at(h, t * h.K + j) - tr.x) / tr.y : 1.0f;
+      // A token named more than once has its whole p at its first place.
+      c = -p;
+      bool first = true;
+      for (int i = 0; i < j; ++i) first = first && h.tokens[t * h.K + i] != n;
+      if (first) c += q;
+    }
+    any = any || valid;
+    coef[j] = c;
+    tok[j] = valid ? n : 0;
+  }
+  any = __syncthreads_or(any) != 0;
+  const float weight = h.weight ? h.weight[t] : 1.0f;
+  const bool used = any && tr.y != 0.0f;
+  const float norm = 1.0f / (soft.y * kWeightOne), f = weight * gsw * h.tau;
+  uint16_t* out = static_cast<uint16_t*>(h.dx) + t * h.D;
+  for (int d = (blockIdx.y * kDxThreads + threadIdx.x) * 8; d < h.D; d += gridDim.y * kDxThreads * 8) {
+    u32x4_t o = {0u, 0u, 0u, 0u};
+    if (used) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+      for (int s = 0; s < a.splits; ++s) {
+        const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.part + ((int64_t)s * h.T + t) * h.D + d);
+        const f32x4_t u = p[0], v = p[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[i] += u[i];
+          y[4 + i] += v[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= norm;
+      for (int j = 0; j < h.K; ++j) {
+        const float c = coef[j];
+        if (c == 0.0f) continue;
+        const uint32_t code = *reinterpret_cast<const uint32_t*>(h.wc + (int64_t)tok[j] * (h.D / 2) + d / 2);
+        const half8_t w = fp4x8_to_f16(code, e4m3_f16(h.ws[(int64_t)tok[j] * (h.D / 16) + d / 16]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fmaf(c, (float)w[i], y[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = bf16_round2(y[2 * i] * f, y[2 * i + 1] * f);
+    }
+    *reinterpret_cast<u32x4_t*>(out + d) = o;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Dispatch.
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxRange = (int64_t(1) << 31) - 65536;  // bytes a 32-bit buffer offset reaches
+
+// Everything that follows from the sizes. `wide`: the logits' tiles.
+struct HeadPlan {
+  bool wide;
+  int block_shift;   // columns of a statistics block
+  int64_t piece;     // columns of a piece, a multiple of 512
+  int64_t pieces;
+  int64_t blocks;    // statistics blocks per row kept at a time
+  int row_tiles16;   // 16-row tiles of a workgroup of the second product
+  int64_t splits;    // of a piece's rows in the second product
+  int64_t ld_e;
+  size_t stats_at, state_at, shrink_at, ref_at, e_at, part_at, bytes;
+};
+
+static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
+  HeadPlan p{};
+  const int64_t wide_items = ((T + kEtRows - 1) / kEtRows) * ((N + kEtCols - 1) / kEtCols);
+  p.wide = T > 32 && wide_items >= kMinTileItems;
+  p.block_shift = p.wide ? 6 : 5;
+  int64_t piece = kMaxRange / (D / 2) / 512 * 512;  // a piece's codes lie within a buffer's range
+  // A piece's weights take 256 MB at most, but 4096 columns at least.
+  if (grad) piece = std::min(piece, std::max((int64_t(1) << 27) / std::max(T, int64_t(1)) / 512 * 512, int64_t(4096)));
+  piece = std::max(piece, int64_t(512));
+  p.piece = std::min(piece, (N + 511) / 512 * 512);
+  p.pieces = (N + p.piece - 1) / p.piece;
+  const int64_t cols = grad ? p.piece : N;
+  p.blocks = (cols + (int64_t(1) << p.block_shift) - 1) >> p.block_shift;
+  p.row_tiles16 = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+  const int64_t wgs = ((D + kGsWaves * kGsCols - 1) / (kGsWaves * kGsCols)) * ((T + 16 * p.row_tiles16 - 1) / (16 * p.row_tiles16));
+  p.splits = std::max(int64_t(1), std::min((512 + wgs - 1) / wgs, (std::min(p.piece, N) + 255) / 256));
+  p.ld_e = p.piece;
+  size_t at = kScratchOffset;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = (at + bytes + 255) / 256 * 256;
+    return here;
+  };
+  p.stats_at = take((size_t)T * p.blocks * sizeof(float2));
+  if (grad) {
+    p.state_at = take((size_t)T * 2 * sizeof(float2));
+    p.shrink_at = take((size_t)T * sizeof(float));
+    p.ref_at = take((size_t)T * sizeof(float));
+    p.e_at = take((size_t)T * p.ld_e * sizeof(_Float16));
+    p.part_at = take((size_t)p.splits * T * D * sizeof(float));
+  }
+  p.bytes = at;
+  return p;
+}
+
+template <Out M>
+static hipError_t launch_logits(const ExpertArgs& a, bool wide, hipStream_t stream) {
+  const Scales sc = scales_of(a);
+  if (wide) {
+    const int row_tiles = (a.R + kEtRows - 1) / kEtRows, grid = row_tiles * ((a.N + kEtCols - 1) / kEtCols);
+    if (sc == Scales::k16) head_wide_kernel<M, Scales::k16><<<grid, kEtThreads, 0, stream>>>(a, row_tiles);
+    else if (sc == Scales::k4) head_wide_kernel<M, Scales::k4><<<grid, kEtThreads, 0, stream>>>(a, row_tiles);
+    else head_wide_kernel<M, Scales::kSkewed><<<grid, kEtThreads, 0, stream>>>(a, row_tiles);
+    return hipGetLastError();
+  }
+  const int col_tiles = (a.N + kEsRows * kEsWaves - 1) / (kEsRows * kEsWaves);
+  if (a.R <= 16) {
+    if (sc == Scales::k16) head_stream_kernel<M, 16, 512, Scales::k16><<<col_tiles, kEsThreads, 0, stream>>>(a, 1);
+    else if (sc == Scales::k4) head_stream_kernel<M, 16, 512, Scales::k4><<<col_tiles, kEsThreads, 0, stream>>>(a, 1);
+    else head_stream_kernel<M, 16, 512, Scales::kSkewed><<<col_tiles, kEsThreads, 0, stream>>>(a, 1);
+    return hipGetLastError();
+  }
+  const int row_tiles = (a.R + 31) / 32, grid = row_tiles * col_tiles;
+  if (sc == Scales::k16) head_stream_kernel<M, 32, 256, Scales::k16><<<grid, kEsThreads, 0, stream>>>(a, row_tiles);
+  else if (sc == Scales::k4) head_stream_kernel<M, 32, 256, Scales::k4><<<grid, kEsThreads, 0, stream>>>(a, row_tiles);
+  else head_stream_kernel<M, 32, 256, Scales::kSkewed><<<grid, kEsThreads, 0, stream>>>(a, row_tiles);
+  return hipGetLastError();
+}
+
+static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream_t stream) {
+  const HeadPlan p = head_plan(in.T, in.D, in.N, grad);
+  HeadArgs h = in;
+  ExpertArgs a{};
+  a.xc = h.xc; a.xs = h.xs; a.gsa = h.gsa; a.gsw = h.gsw;
+  a.T = a.R = h.T; a.k = 1; a.G = 1; a.D = h.D;
+  float2* stats = reinterpret_cast<float2*>(ws + p.stats_at);
+  a.soft.scale = kLog2e / h.tau;
+  a.soft.blocks = (int)p.blocks;
+  hipError_t e;
+  if (!grad) {
+    for (int64_t i = 0; i < p.pieces; ++i) {
+      const int64_t n0 = i * p.piece;
+      a.wc = h.wc + n0 * (h.D / 2);
+      a.ws = h.ws + n0 * (h.D / 16);
+      a.N = (int)std::min(p.piece, h.N - n0);
+      a.soft.stats = stats + (n0 >> p.block_shift);
+      if ((e = launch_logits<Out::kSums>(a, p.wide, stream)) != hipSuccess) return e;
+    }
+    h.stats = stats;
+    h.blocks = (int)p.blocks;
+    head_tokens_kernel<<<h.T, 64 * kTokWaves, 0, stream>>>(h);
+    return hipGetLastError();
+  }
+  float2* state = reinterpret_cast<float2*>(ws + p.state_at);
+  float* shrink = reinterpret_cast<float*>(ws + p.shrink_at);
+  float* ref = reinterpret_cast<float*>(ws + p.ref_at);
+  float* part = reinterpret_cast<float*>(ws + p.part_at);
+  a.soft.stats = stats;
+  a.soft.e = reinterpret_cast<_Float16*>(ws + p.e_at);
+  a.soft.ld_e = p.ld_e;
+  for (int64_t i = 0; i < p.pieces; ++i) {
+    const int64_t n0 = i * p.piece;
+    a.wc = h.wc + n0 * (h.D / 2);
+    a.ws = h.ws + n0 * (h.D / 16);
+    a.N = (int)std::min(p.piece, h.N - n0);
+    a.soft.ref = i ? ref : nullptr;
+    if ((e = launch_logits<Out::kWeights>(a, p.wide, stream)) != hipSuccess) return e;
+    NormArgs n{};
+    n.stats = stats; n.blocks = (int)p.blocks; n.block_shift = p.block_shift;
+    n.used = (a.N + (1 << p.block_shift) - 1) >> p.block_shift;
+    n.before = i ? state + ((i - 1) & 1) * (int64_t)h.T : nullptr;
+    n.after = state + (i & 1) * (int64_t)h.T;
+    n.shrink = shrink; n.ref = ref; n.e = a.soft.e; n.ld_e = p.ld_e;
+    n.T = h.T; n.K = h.K; n.n0 = (int)n0; n.cols = a.N; n.tokens = h.tokens;
+    const int segs = (int)std::max<int64_t>(1, std::min<int64_t>((a.N + 2047) / 2048, (1024 + h.T - 1) / h.T));
+    n.seg = (int)(((a.N + segs - 1) / segs + 63) / 64 * 64);
+    head_norm_kernel<<<dim3(h.T, segs), kNormThreads, 0, stream>>>(n);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    GradArgs g{};
+    g.e = a.soft.e; g.ld_e = p.ld_e; g.wc = a.wc; g.ws = a.ws; g.T = h.T; g.D = h.D; g.cols = a.N;
+    g.splits = (int)p.splits;
+    g.steps = (int)(((a.N + 31) / 32 + p.splits - 1) / p.splits);
+    g.part = part; g.shrink = i ? shrink : nullptr;
+    const dim3 grid((h.D + kGsWaves * kGsCols - 1) / (kGsWaves * kGsCols), (int)p.splits,
+                    (h.T + 16 * p.row_tiles16 - 1) / (16 * p.row_tiles16));
+    if (p.row_tiles16 == 1) head_grad_kernel<1><<<grid, 64 * kGsWaves, 0, stream>>>(g);
+    else if (p.row_tiles16 == 2) head_grad_kernel<2><<<grid, 64 * kGsWaves, 0, stream>>>(g);
+    else head_grad_kernel<4><<<grid, 64 * kGsWaves, 0, stream>>>(g);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  h.stats = state + ((p.pieces - 1) & 1) * (int64_t)h.T;
+  h.blocks = 1;
+  head_tokens_kernel<<<h.T, 64 * kTokWaves, 0, stream>>>(h);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  DxArgs d{h, part, (int)p.splits};
+  head_dx_kernel<<<dim3(h.T, h.T >= 256 ? 1 : (h.D + kDxThreads * 8 - 1) / (kDxThreads * 8)), kDxThreads, 0, stream>>>(d);
+  return hipGetLastError();
+}
+
+}  // namespace nvr
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int check_head_sizes(int64_t T, int64_t D, int64_t N) {
+  if (T < 0 || D < 32 || D % 32 != 0 || N < 1) return ROUTER_EINVAL;
+  if (T > ROUTER_MAX_LOSS_ROWS || D > ROUTER_MAX_GATE_D || N > (int64_t(1) << 30)) return ROUTER_EUNSUPPORTED;
+  return ROUTER_OK;
+}
+
+int head_call(nvr::HeadArgs& h, int64_t T, int64_t D, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+              void* stream) {
+  const int st = check_head_sizes(T, D, N);
+  if (st != ROUTER_OK) return st;
+  if (K < 1) return ROUTER_EINVAL;
+  if (K > ROUTER_MAX_TEACHER) return ROUTER_EUNSUPPORTED;
+  if (!h.gsa || !h.gsw || !h.wc || !h.ws) return ROUTER_EINVAL;
+  if (T > 0 && (!h.xc || !h.xs || !h.tokens || !h.loss || !h.lse)) return ROUTER_EINVAL;
+  if (!aligned(h.xc, 16) || !aligned(h.wc, 16) || !aligned(h.xs, 2) || !aligned(h.ws, 4) || !aligned(h.gsa, 4) ||
+      !aligned(h.gsw, 4) || !aligned(h.tokens, 4) || !aligned(h.weight, 4) || !aligned(h.loss, 4) ||
+      !aligned(h.lse, 4) || !aligned(h.logq, 4) || !aligned(h.dx, 16) ||
+      !aligned(h.teacher, h.teacher_bf16 ? 2 : 4))
+    return ROUTER_EINVAL;
+  if (T == 0) return ROUTER_OK;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < lmhead_loss_workspace_bytes(T, D, N, h.dx != nullptr))
+    return ROUTER_EINVAL;
+  h.T = (int)T; h.D = (int)D; h.N = (int)N; h.K = (int)K;
+  const hipError_t e = nvr::launch_head(h, h.dx != nullptr, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ROUTER_OK : ROUTER_EHIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lmhead_loss_workspace_bytes(int64_t T, int64_t D, int64_t N, int grad) {
+  if (check_head_sizes(T, D, N) != ROUTER_OK) return 0;
+  return nvr::head_plan(T, D, N, grad != 0).bytes;
+}
+
+int lmhead_loss(const uint8_t* x_codes, const uint8_t* x_scales, const float* gsa, const uint8_t* w_codes,
+                const uint8_t* w_scales, const float* gsw, const int32_t* targets, const float* weight, int64_t T,
+                int64_t D, int64_t N, float* loss, float* lse, void* dx, void* workspace, size_t workspace_bytes,
+                void* stream) {
+  nvr::HeadArgs h{};
+  h.xc = x_codes; h.xs = x_scales; h.gsa = gsa;
+  h.wc = w_codes; h.ws = w_scales; h.gsw = gsw;
+  h.tokens = targets; h.weight = weight; h.tau = 1.0f;
+  h.loss = loss; h.lse = lse; h.dx = dx;
+  return head_call(h, T, D, N, 1, workspace, workspace_bytes, stream);
+}
+
+int lmhead_distill(const uint8_t* x_codes, const uint8_t* x_scales, const float* gsa, const uint8_t* w_codes,
+                   const uint8_t* w_scales, const float* gsw, const int32_t* tokens, const void* teacher, int dtype,
+                   int64_t K, float temperature, const float* weight, int64_t T, int64_t D, int64_t N, float* loss,
+                   float* lse, float* logq, void* dx, void* workspace, size_t workspace_bytes, void* stream) {
+  if ((dtype != ROUTER_F32 && dtype != ROUTER_BF16) || !(temperature >= 0x1p-20f && temperature <= 0x1p20f))
+    return ROUTER_EINVAL;
+  if (T > 0 && (!teacher || !logq)) return ROUTER_EINVAL;
+  nvr::HeadArgs h{};
+  h.xc = x_codes; h.xs = x_scales; h.gsa = gsa;
+  h.wc = w_codes; h.ws = w_scales; h.gsw = gsw;
+  h.tokens = tokens; h.teacher = teacher; h.teacher_bf16 = dtype == ROUTER_BF16;
+  h.weight = weight; h.tau = temperature;
+  h.loss = loss; h.lse = lse; h.logq = logq; h.dx = dx;
+  return head_call(h, T, D, N, K, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,130 @@
+// A tile's part of a softmax over the columns (gfx950): what a wavefront does
+// with its block of logits z[row, column] instead of storing them.
+//
+// In base 2, with y = z log2(e) / temperature, each row of a block gives
+// (m, s) with m >= its largest y and s = sum 2^(y - m); joined over the blocks
+// of a row they give log sum e^z. kWeights also keeps 2^(y - m) itself, as
+// fp16 times 2^15: relative error 2^-11 down to 2^-29 of the row's largest,
+// absolute 2^-40 below (bf16 would keep 2^-8 of each). `ref` lets m start at
+// what earlier columns have reached, so that few blocks have a scale of their
+// own.
+#pragma once
+
+#include "mma_tile.hpp"
+
+namespace nvr {
+
+struct SoftmaxOut {
+  float scale;        // log2(e) / temperature
+  const float* ref;   // NULL or [T]: a lower bound of m
+  float2* stats;      // [T, blocks] (m, s)
+  int blocks;         // stride of stats
+  _Float16* e;        // [T, ld_e]
+  int64_t ld_e;
+};
+
+constexpr float kWeightOne = 32768.0f;  // a weight of 1 in fp16
+
+// The larger / the sum of a value and its partner 16 or 32 lanes away.
+__device__ __forceinline__ float max_across16(float v) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float sum_across16(float v) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+__device__ __forceinline__ float max_across32(float v) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float sum_across32(float v) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v) {
+  return __int_as_float(dpp_i<CTRL>(__float_as_int(v)));
+}
+
+// Block of 32 columns from the stream's accumulators: lane (r, q), value v of
+// tile m: row r (+ 16 t), column 16 m + 4 q + v.
+template <bool KEEP, int NT>
+__device__ __forceinline__ void softmax_block16(const SoftmaxOut& o, const f32x4_t (&acc)[2][NT], float scale,
+                                                int row0, int nr, int col0, int N) {
+  if (col0 >= N) return;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const float sc = scale * o.scale;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int row = 16 * t + r;
+    float y[8], m = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y[i] = col0 + 16 * (i >> 2) + 4 * q + (i & 3) < N ? acc[i >> 2][t][i & 3] * sc : -__builtin_inff();
+      m = fmaxf(m, y[i]);
+    }
+    m = max_across32(max_across16(m));
+    if (KEEP && o.ref && row < nr) m = fmaxf(m, o.ref[row0 + row]);
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      y[i] = __builtin_amdgcn_exp2f(y[i] - m);
+      s += y[i];
+    }
+    s = sum_across32(sum_across16(s));
+    if (row >= nr) continue;
+    if (q == 0) o.stats[(int64_t)(row0 + row) * o.blocks + (col0 >> 5)] = make_float2(m, s);
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+        half4_t h;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) h[v] = (_Float16)(y[4 * i + v] * kWeightOne);
+        *reinterpret_cast<half4_t*>(o.e + (int64_t)(row0 + row) * o.ld_e + col0 + 16 * i + 4 * q) = h;
+      }
+    }
+  }
+}
+
+// Block of 64 columns from a wide tile's accumulators: lane (r, h), value v of
+// row tile i: row 32 i + 8 (v / 4) + 4 h + v % 4, columns r and 32 + r.
+template <bool KEEP, int RT>
+__device__ __forceinline__ void softmax_block32(const SoftmaxOut& o, const f32x16_t (&acc)[RT][2], float scale,
+                                                int row0, int nr, int col0, int N) {
+  if (col0 >= N) return;
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const float sc = scale * o.scale;
+  const bool in0 = col0 + r < N, in1 = col0 + 32 + r < N;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int row = 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
+      const float y0 = in0 ? acc[i][0][v] * sc : -__builtin_inff(), y1 = in1 ? acc[i][1][v] * sc : -__builtin_inff();
+      float m = fmaxf(y0, y1);
+      m = fmaxf(m, dpp_f<kDppXor1>(m));
+      m = fmaxf(m, dpp_f<kDppXor2>(m));
+      m = fmaxf(m, dpp_f<kDppHalfMirror>(m));
+      m = fmaxf(m, dpp_f<kDppMirror>(m));
+      m = max_across16(m);
+      if (KEEP && o.ref && row < nr) m = fmaxf(m, o.ref[row0 + row]);
+      const float e0 = __builtin_amdgcn_exp2f(y0 - m), e1 = __builtin_amdgcn_exp2f(y1 - m);
+      float s = e0 + e1;
+      s += dpp_f<kDppXor1>(s);
+      s += dpp_f<kDppXor2>(s);
+      s += dpp_f<kDppHalfMirror>(s);
+      s += dpp_f<kDppMirror>(s);
+      s = sum_across16(s);
+      if (row >= nr) continue;
+      if (r == 0) o.stats[(int64_t)(row0 + row) * o.blocks + (col0 >> 6)] = make_float2(m, s);
+      if constexpr (KEEP) {
+        _Float16* e = o.e + (int64_t)(row0 + row) * o.ld_e + col0 + r;
+        e[0] = (_Float16)(e0 * kWeightOne);
+        e[32] = (_Float16)(e1 * kWeightOne);
+      }
+    }
+}
+
+}  // namespace nvr

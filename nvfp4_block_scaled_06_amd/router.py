@@ -19,7 +19,8 @@ EXPORTS = ("router_workspace_bytes", "router_workspace_init", "router_quantize",
            "router_forward", "router_forward_noalloc", "router_status_string", "router_probe_read",
            "router_probe_mfma", "lmhead_workspace_bytes", "lmhead_argmax", "grouped_offsets", "grouped_gemm",
            "grouped_workspace_bytes", "grouped_plan", "grouped_swiglu", "grouped_combine",
-           "lmhead_penalize_workspace_bytes", "lmhead_penalize", "router_select", "router_select_backward")
+           "lmhead_penalize_workspace_bytes", "lmhead_penalize", "router_select", "router_select_backward",
+           "lmhead_loss_workspace_bytes", "lmhead_loss", "lmhead_distill")
 ROUTER_ESCRATCH = -4
 STATIC_SCRATCH_BYTES = 16 << 20
 
@@ -86,6 +87,13 @@ def load_library(path=LIB_PATH):
     L.router_select.restype = ci
     L.router_select_backward.argtypes = [vp, ci, i64, i64, i64, vp, vp, ci, ci, fl, i64, vp, i64, vp]
     L.router_select_backward.restype = ci
+    L.lmhead_loss_workspace_bytes.argtypes = [i64, i64, i64, ci]
+    L.lmhead_loss_workspace_bytes.restype = sz
+    L.lmhead_loss.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+    L.lmhead_loss.restype = ci
+    L.lmhead_distill.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ci, i64, fl, vp, i64, i64, i64, vp, vp, vp, vp, vp, sz,
+                                 vp]
+    L.lmhead_distill.restype = ci
     _lib = L
     return L
 
@@ -562,6 +570,75 @@ def lmhead_penalize(logits, workspace, history=None, prompt=None, lengths=None, 
           ldh, lengths, prompt, repetition, frequency, presence, start, token, value, nbias, mask, ldm, out, ldo, idx,
           logit, workspace.buf, workspace.nbytes)
     return idx, logit, out
+
+
+def lmhead_loss_workspace_bytes(T, D, N, want_grad=False):
+    n = load_library().lmhead_loss_workspace_bytes(T, D, N, 1 if want_grad else 0)
+    if n == 0:
+        raise RouterError(f"invalid lm_head loss sizes T={T} D={D} N={N}")
+    return int(n)
+
+
+def _check_head(xq, wq, weight, workspace, want_grad, out):
+    """Operands of the lm_head's losses: x [T, D] and weights [N, D] on one device; returns it, the sizes and dx."""
+    xc, wc = xq.codes, wq.codes
+    dev = _gpu(xc.device)
+    if xc.dim() != 2 or wc.dim() != 2 or xc.shape[1] != wc.shape[1] or xc.shape[1] % 8:
+        raise RouterError("lm_head weights do not match x")
+    T, D2 = xc.shape
+    N = wc.shape[0]
+    _tensor(xc, "x codes", torch.uint8, (T, D2), dev)
+    _tensor(xq.scales, "x scales", torch.uint8, (T, D2 // 8), dev)
+    _tensor(xq.gscale, "x global scale", torch.float32, (1,), dev)
+    _tensor(wc, "w codes", torch.uint8, (N, D2), dev)
+    _tensor(wq.scales, "w scales", torch.uint8, (N, D2 // 8), dev)
+    _tensor(wq.gscale, "w global scale", torch.float32, (1,), dev)
+    _check_workspace(workspace, dev)
+    if weight is not None:
+        _tensor(weight, "weight", torch.float32, (T,), dev)
+    if out is not None:
+        if not want_grad:
+            raise RouterError("out is the gradient's: want_grad is needed")
+        _tensor(out, "out", torch.bfloat16, (T, 2 * D2), dev)
+    elif want_grad:
+        out = torch.empty((T, 2 * D2), dtype=torch.bfloat16, device=dev)
+    return dev, T, 2 * D2, N, out
+
+
+def lmhead_loss(xq, wq, targets, workspace, weight=None, want_grad=False, out=None):
+    """lmhead_loss: cross entropy of the NVFP4 lm_head wq [N, D] on xq [T, D] for targets [T] int32 (outside [0, N):
+    ignored), without the logits in memory. Returns ``(loss [T] fp32, lse [T] fp32, dx)``; with want_grad dx [T, D] bf16
+    is the gradient of sum(weight * loss) with respect to the dequantized x (weight [T] fp32, None for ones), else
+    None."""
+    dev, T, D, N, out = _check_head(xq, wq, weight, workspace, want_grad, out)
+    _tensor(targets, "targets", torch.int32, (T,), dev)
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    _call(load_library().lmhead_loss, dev, xq.codes, xq.scales, xq.gscale, wq.codes, wq.scales, wq.gscale, targets,
+          weight, T, D, N, loss, lse, out, workspace.buf, workspace.nbytes)
+    return loss, lse, out
+
+
+def lmhead_distill(xq, wq, tokens, teacher, workspace, temperature=1.0, weight=None, want_grad=False, out=None):
+    """lmhead_distill: divergence of the NVFP4 lm_head's distribution from a teacher's, of which the logits teacher
+    [T, K] (fp32 or bf16) of tokens [T, K] int32 are known (outside [0, N): no entry), at a temperature. Returns
+    ``(loss [T] fp32, lse [T] fp32, logq [T, K] fp32, dx)``: logq is the lm_head's own log-probability of each token,
+    dx as in lmhead_loss."""
+    dev, T, D, N, out = _check_head(xq, wq, weight, workspace, want_grad, out)
+    if not isinstance(tokens, torch.Tensor) or tokens.dim() != 2:
+        raise RouterError("tokens must be a GPU matrix")
+    K = tokens.shape[1]
+    _tensor(tokens, "tokens", torch.int32, (T, K), dev)
+    if not isinstance(teacher, torch.Tensor) or teacher.dtype not in (torch.float32, torch.bfloat16):
+        raise RouterError("teacher must be a float32 or bfloat16 tensor")
+    _tensor(teacher, "teacher", teacher.dtype, (T, K), dev)
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    logq = torch.empty((T, K), dtype=torch.float32, device=dev)
+    _call(load_library().lmhead_distill, dev, xq.codes, xq.scales, xq.gscale, wq.codes, wq.scales, wq.gscale, tokens,
+          teacher, 0 if teacher.dtype == torch.float32 else 1, K, temperature, weight, T, D, N, loss, lse, logq, out,
+          workspace.buf, workspace.nbytes)
+    return loss, lse, logq, out
 
 
 SCORING = {"sigmoid": 0, "softmax": 1}
