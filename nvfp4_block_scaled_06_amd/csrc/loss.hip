@@ -198,6 +198,7 @@ struct NormArgs {
   _Float16* e;
   int64_t ld_e;
   int T, K, n0, cols, seg;  // seg: columns per workgroup, a multiple of 64
+  int rescale;              // 0: the product takes the blocks' m into account
   const int32_t* tokens;
 };
 
@@ -225,7 +226,7 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a) {
   // Weights of blocks whose m is lower than the row's.
   const int c0 = blockIdx.y * a.seg, c1 = min(c0 + a.seg, (a.cols + 31) & ~31);
   _Float16* e = a.e + t * a.ld_e;
-  for (int c = c0 + 8 * threadIdx.x; c < c1; c += 8 * kNormThreads) {
+  for (int c = c0 + 8 * threadIdx.x; a.rescale && c < c1; c += 8 * kNormThreads) {
     const float m = st[c >> a.block_shift].x;
     if (m == v.x) continue;
     const float f = __builtin_amdgcn_exp2f(m - v.x);
@@ -237,20 +238,17 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a) {
   __syncthreads();
   for (int j = threadIdx.x; j < a.K; j += kNormThreads) {
     const int64_t c = (int64_t)a.tokens[t * a.K + j] - a.n0;
-    if (c >= c0 && c < min(c1, a.cols)) e[c] = (_Float16)0.0f;
+    if (c >= c0 && c < min(c1, a.cols)) e[weight_place(c)] = (_Float16)0.0f;
   }
 }
 
 // ---------------------------------------------------------------------------
 // Gradient, per piece: sum_n e[t, n] what[n, d].
 //
-// The product runs over the weights' rows, whose codes lie along d: eight rows'
-// words are put together pair by pair (the even and the odd codes of two rows'
-// words give two words whose bytes hold one column's codes of both), so a
-// conversion of a byte gives one column's two neighbours in n, and a lane ends
-// up with 16 columns of 8 rows in MFMA layout, without LDS: lane (r, q) takes
-// columns 16 r .. 16 r + 15 of its wavefront's 256, one for each of 16 tiles.
-// A load takes 8 bytes of each of 64 lanes: whole 128-byte lines of 4 rows.
+// The product runs over the weights' rows, whose codes lie along d. The words
+// of rows n and n + 4 are put together so that each byte holds one column's
+// codes of both: a conversion of a byte then gives what MFMA wants, one
+// column's values of two n.
 // ---------------------------------------------------------------------------
 struct GradArgs {
   const _Float16* e;
@@ -262,6 +260,10 @@ struct GradArgs {
   const float* shrink;            // NULL: the first piece
 };
 
+// Few rows: a stream of the weights. Lane (r, q) takes columns 16 r .. 16 r +
+// 15 of its wavefront's 256, one for each of 16 tiles, and rows 8 q .. 8 q + 7
+// of 32, straight from memory in MFMA layout: a load takes 8 bytes for each
+// lane, whole 128-byte lines of 4 rows.
 constexpr int kGsWaves = 4;
 constexpr int kGsCols = 256;  // per wavefront
 
@@ -309,11 +311,11 @@ __global__ __launch_bounds__(64 * kGsWaves) void head_grad_kernel(GradArgs a) {
     for (int p = 0; p < 4; ++p) {
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        const uint32_t x = wv[2 * p][w], y = wv[2 * p + 1][w];
+        const uint32_t x = wv[p][w], y = wv[p + 4][w];
         c[w][0][p] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
         c[w][1][p] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
       }
-      sc[p] = e4m3x2_f16(sv[2 * p] | (sv[2 * p + 1] << 8));
+      sc[p] = e4m3x2_f16(sv[p] | (sv[p + 4] << 8));
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) A[t] = ev[t];
@@ -349,6 +351,222 @@ __global__ __launch_bounds__(64 * kGsWaves) void head_grad_kernel(GradArgs a) {
         *o = y;
       }
     }
+}
+
+// Many rows: tiles of 128 rows times 512 columns, 8 wavefronts, two per SIMD,
+// 32x32x16 MFMAs, 128 weight rows per step.
+//  * Weights: loaded in whole lines by the workgroup (8 rows x 8 bytes per
+//    thread), bytes transposed in registers, and kept in LDS as [byte
+//    column][n], so that a lane reads its two columns' codes of 16 rows at
+//    once. Wavefront w takes the columns 16 r + 2 w and 16 r + 2 w + 1 of lane
+//    r, all in the scale block r. Scales likewise, as [block][n].
+//  * Softmax weights: on their way into LDS they are brought to the row's m
+//    from their block's, a second rounding to fp16 where those differ.
+//  * K order: in every 32 rows lane (r, h) supplies [16 h + 8 j, +8) to MFMA j.
+// Both double-buffered in LDS, one barrier per step; a step's loads go out a
+// step before they are written there.
+constexpr int kGwThreads = 512;
+constexpr int kGwRows = 128, kGwCols = 512, kGwStep = 128;
+constexpr int kGwLd = 144;  // LDS bytes per byte column or scale block: 128 rows and 16 of padding
+
+struct GradWideArgs {
+  GradArgs g;
+  const float2* stats;  // [T, blocks] of the piece, blocks of 64 columns
+  int blocks;
+  const float* ref;     // [T]: the row's m
+  int row_tiles, col_tiles;
+};
+
+struct GradLds {
+  alignas(16) _Float16 x[2][kGwRows * kGwStep];
+  alignas(16) uint8_t codes[2][(kGwCols / 2) * kGwLd];
+  alignas(16) uint8_t scales[2][(kGwCols / 16) * kGwLd];
+};
+
+// Halves offset of 16-byte piece c (of 16) of row r of the softmax weights.
+__device__ __forceinline__ int grad_x_at(int r, int c) {
+  return (((r >> 5) * 16 + c) * 32 + ((r & 31) ^ (4 * (c & 3)))) * 8;
+}
+
+// Bytes 0 .. 3 of four words -> four words of one byte place each.
+__device__ __forceinline__ void byte_transpose4(const uint32_t (&a)[4], uint32_t (&o)[4]) {
+  const uint32_t t0 = __builtin_amdgcn_perm(a[1], a[0], 0x05010400u), t1 = __builtin_amdgcn_perm(a[1], a[0], 0x07030602u);
+  const uint32_t t2 = __builtin_amdgcn_perm(a[3], a[2], 0x05010400u), t3 = __builtin_amdgcn_perm(a[3], a[2], 0x07030602u);
+  o[0] = __builtin_amdgcn_perm(t2, t0, 0x05040100u);
+  o[1] = __builtin_amdgcn_perm(t2, t0, 0x07060302u);
+  o[2] = __builtin_amdgcn_perm(t3, t1, 0x05040100u);
+  o[3] = __builtin_amdgcn_perm(t3, t1, 0x07060302u);
+}
+
+// S4: rows of scales start at multiples of 4 bytes (D a multiple of 64).
+template <int RT, bool S4>
+__device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, int nr, int ct, int split, GradLds& lds) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t rowc = a.g.D / 2, rows = a.g.D / 16;
+  const int d0 = ct * kGwCols;
+  const int n0 = split * a.g.steps * kGwStep, n1 = min(n0 + a.g.steps * kGwStep, a.g.cols);
+  const int64_t nrows = max(n1 - n0, 0);
+  const int nsteps = (int)((nrows + kGwStep - 1) / kGwStep);
+  const __amdgpu_buffer_rsrc_t wcr = make_rsrc(a.g.wc + n0 * rowc, nrows * rowc);
+  const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.g.ws + n0 * rows, nrows * rows);
+  // Codes: rows 8 o .. 8 o + 7 of a step, bytes 8 c .. 8 c + 7 of the tile's 256.
+  const int o = tid >> 5, c = tid & 31;
+  const uint32_t oc = d0 + 16 * c < a.g.D ? (uint32_t)(8 * o * rowc + d0 / 2 + 8 * c) : kMmaOob;
+  u32x2_t wv[8];
+  // Scales: rows 2 p and 2 p + 1, blocks 4 b .. 4 b + 3 of the tile's 32.
+  const int p = tid >> 3, b = tid & 7;
+  const uint32_t os = d0 + 64 * b < a.g.D ? (uint32_t)(2 * p * rows + d0 / 16 + 4 * b) : kMmaOob;
+  const uint32_t os2 = d0 + 64 * b + 32 < a.g.D ? os + 2 : kMmaOob;
+  uint32_t sv[2][2];
+  // Softmax weights: row ar, 16-byte pieces aq, aq + 4, aq + 8, aq + 12.
+  const int ar = tid >> 2, aq = tid & 3;
+  const bool arow = ar < nr;
+  const __amdgpu_buffer_rsrc_t er = make_rsrc(a.g.e + (int64_t)row0 * a.g.ld_e, (int64_t)nr * a.g.ld_e * 2);
+  const uint32_t oe = arow ? (uint32_t)(ar * a.g.ld_e * 2 + 2 * (n0 + 8 * aq)) : kMmaOob;
+  const float2* st = a.stats + (int64_t)(row0 + (arow ? ar : 0)) * a.blocks + n0 / 64;
+  const float ref = a.ref[row0 + (arow ? ar : 0)];
+  u32x4_t ev[4];
+  float mv[2];
+  auto load = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = n0 + kGwStep * s + 32 * i;  // of the piece
+      ev[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                              er, k + 8 * aq < a.g.cols ? oe + 2 * (kGwStep * s + 32 * i) : kMmaOob, 0, 0));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) mv[i] = n0 + kGwStep * s + 64 * i < a.g.cols ? st[2 * s + i].x : -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      wv[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(wcr, oc + (uint32_t)((kGwStep * s + i) * rowc), 0, 0));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t at = (uint32_t)((kGwStep * s + i) * rows);
+      if constexpr (S4) sv[i][0] = __builtin_amdgcn_raw_buffer_load_b32(wsr, os + at, 0, 0);
+      else {
+        sv[i][0] = __builtin_amdgcn_raw_buffer_load_b16(wsr, os + at, 0, 0);
+        sv[i][1] = __builtin_amdgcn_raw_buffer_load_b16(wsr, os2 + at, 0, 0);
+      }
+    }
+  };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = __builtin_amdgcn_exp2f(mv[i >> 1] - ref);  // below fp16's range where a block's m is far lower
+      half8_t v = __builtin_bit_cast(half8_t, ev[i]);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = (_Float16)((float)v[q] * f);
+      *reinterpret_cast<half8_t*>(&lds.x[buf][grad_x_at(ar, 4 * i + aq)]) = v;
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t lo[4], hi[4];
+      byte_transpose4({wv[0][w], wv[1][w], wv[2][w], wv[3][w]}, lo);
+      byte_transpose4({wv[4][w], wv[5][w], wv[6][w], wv[7][w]}, hi);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x2_t*>(&lds.codes[buf][((4 * w + i) * 32 + c) * kGwLd + 8 * o]) = u32x2_t{lo[i], hi[i]};
+    }
+    const uint32_t s0 = S4 ? sv[0][0] : sv[0][0] | (sv[0][1] << 16), s1 = S4 ? sv[1][0] : sv[1][0] | (sv[1][1] << 16);
+    const uint32_t t0 = __builtin_amdgcn_perm(s1, s0, 0x05010400u), t1 = __builtin_amdgcn_perm(s1, s0, 0x07030602u);
+    uint8_t* d = &lds.scales[buf][4 * b * kGwLd + 2 * p];
+    *reinterpret_cast<uint16_t*>(d) = (uint16_t)t0;
+    *reinterpret_cast<uint16_t*>(d + kGwLd) = (uint16_t)(t0 >> 16);
+    *reinterpret_cast<uint16_t*>(d + 2 * kGwLd) = (uint16_t)t1;
+    *reinterpret_cast<uint16_t*>(d + 3 * kGwLd) = (uint16_t)(t1 >> 16);
+  };
+
+  f32x16_t acc[RT][2];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][m][v] = 0.0f;
+  if (nsteps > 0) {
+    load(0);
+    store(0);
+    load(1);
+    __syncthreads();
+  }
+  for (int s = 0; s < nsteps; ++s) {
+    const int buf = s & 1;
+    static_for<0, 4>([&](auto gc) {
+      constexpr int g = decltype(gc)::value;
+      const u32x4_t cw = *reinterpret_cast<const u32x4_t*>(&lds.codes[buf][(wave * 32 + r) * kGwLd + 32 * g + 16 * h]);
+      const u32x4_t sw = *reinterpret_cast<const u32x4_t*>(&lds.scales[buf][r * kGwLd + 32 * g + 16 * h]);
+      static_for<0, 2>([&](auto jc) {
+        constexpr int j = decltype(jc)::value;
+        const uint32_t x = cw[2 * j], y = cw[2 * j + 1];
+        const uint32_t col[2] = {(x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u)};
+        const uint32_t p01 = __builtin_amdgcn_perm(sw[2 * j + 1], sw[2 * j], 0x05010400u);
+        const uint32_t p23 = __builtin_amdgcn_perm(sw[2 * j + 1], sw[2 * j], 0x07030602u);
+        const half2_t sc[4] = {e4m3x2_f16(p01), e4m3x2_f16(p01 >> 16), e4m3x2_f16(p23), e4m3x2_f16(p23 >> 16)};
+        half8_t w[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const half2_t q0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(col[m], 1.0f, 0) * sc[0];
+          const half2_t q1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(col[m], 1.0f, 1) * sc[1];
+          const half2_t q2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(col[m], 1.0f, 2) * sc[2];
+          const half2_t q3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(col[m], 1.0f, 3) * sc[3];
+          w[m] = half8_t{q0[0], q0[1], q1[0], q1[1], q2[0], q2[1], q3[0], q3[1]};
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const half8_t A = *reinterpret_cast<const half8_t*>(&lds.x[buf][grad_x_at(32 * i + r, 4 * g + 2 * h + j)]);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) acc[i][m] = mfma32(A, w[m], acc[i][m]);
+        }
+      });
+      if constexpr (g == 1) {
+        if (s + 1 < nsteps) {
+          store(buf ^ 1);
+          load(s + 2);
+        }
+      }
+    });
+    __syncthreads();
+  }
+
+  // Value v of lane (r, h): row 8 (v / 4) + 4 h + v % 4 of its 32-row tile, columns 16 r + 2 wave and the next.
+  const int d = d0 + 16 * r + 2 * wave;
+  if (d >= a.g.D) return;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int row = 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
+      if (row >= nr) continue;
+      float2* out = reinterpret_cast<float2*>(a.g.part + ((int64_t)split * a.g.T + row0 + row) * a.g.D + d);
+      float2 y = make_float2(acc[i][0][v], acc[i][1][v]);
+      if (a.g.shrink) {
+        const float f = a.g.shrink[row0 + row];
+        const float2 old = *out;
+        y.x = fmaf(old.x, f, y.x);
+        y.y = fmaf(old.y, f, y.y);
+      }
+      *out = y;
+    }
+}
+
+template <bool S4>
+__global__ __launch_bounds__(kGwThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_grad_wide_kernel(
+    GradWideArgs a) {
+  __shared__ GradLds lds;
+  // 8 row tiles times 4 column tiles of one split side by side on one XCD: they
+  // read the same weights and the same softmax weights.
+  const int tiles = a.row_tiles * a.col_tiles;
+  const int n = xcd_order(blockIdx.x, gridDim.x), split = n / tiles, t = n - split * tiles;
+  const int band = t / (8 * a.col_tiles), in = t - band * 8 * a.col_tiles;
+  const int bandrows = min(8, a.row_tiles - 8 * band);
+  const int ct = in / bandrows, row0 = (8 * band + in - ct * bandrows) * kGwRows;
+  const int nr = min(kGwRows, a.g.T - row0);
+  if (nr > 96) grad_wide_tile<4, S4>(a, row0, nr, ct, split, lds);
+  else if (nr > 64) grad_wide_tile<3, S4>(a, row0, nr, ct, split, lds);
+  else if (nr > 32) grad_wide_tile<2, S4>(a, row0, nr, ct, split, lds);
+  else grad_wide_tile<1, S4>(a, row0, nr, ct, split, lds);
 }
 
 // dx: the splits' sums, divided by the softmax's, and the loss's own tokens.
@@ -435,8 +653,9 @@ struct HeadPlan {
   int64_t piece;     // columns of a piece, a multiple of 512
   int64_t pieces;
   int64_t blocks;    // statistics blocks per row kept at a time
-  int row_tiles16;   // 16-row tiles of a workgroup of the second product
-  int64_t splits;    // of a piece's rows in the second product
+  bool wide_grad;    // the second product's tiles
+  int row_tiles16;   // 16-row tiles of a workgroup of its stream
+  int64_t splits;    // of a piece's rows there
   int64_t ld_e;
   size_t stats_at, state_at, shrink_at, ref_at, e_at, part_at, bytes;
 };
@@ -455,8 +674,22 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   const int64_t cols = grad ? p.piece : N;
   p.blocks = (cols + (int64_t(1) << p.block_shift) - 1) >> p.block_shift;
   p.row_tiles16 = T <= 16 ? 1 : T <= 32 ? 2 : 4;
-  const int64_t wgs = ((D + kGsWaves * kGsCols - 1) / (kGsWaves * kGsCols)) * ((T + 16 * p.row_tiles16 - 1) / (16 * p.row_tiles16));
-  p.splits = std::max(int64_t(1), std::min((512 + wgs - 1) / wgs, (std::min(p.piece, N) + 255) / 256));
+  p.wide_grad = p.wide;
+  const int64_t rows = std::min(p.piece, N);
+  if (p.wide_grad) {
+    // Splits that leave the last round of 256 workgroups fullest, one each per compute unit.
+    const int64_t tiles = ((T + kGwRows - 1) / kGwRows) * ((D + kGwCols - 1) / kGwCols);
+    const int64_t most = std::max(int64_t(1), std::min(int64_t(64), rows / 2048));
+    double best = 0.0;
+    p.splits = 1;
+    for (int64_t s = 1; s <= most; ++s) {
+      const double use = (double)(tiles * s) / (double)((tiles * s + 255) / 256 * 256);
+      if (use > best + 0.03) best = use, p.splits = s;
+    }
+  } else {
+    const int64_t wgs = ((D + kGsWaves * kGsCols - 1) / (kGsWaves * kGsCols)) * ((T + 16 * p.row_tiles16 - 1) / (16 * p.row_tiles16));
+    p.splits = std::max(int64_t(1), std::min((512 + wgs - 1) / wgs, (rows + 255) / 256));
+  }
   p.ld_e = p.piece;
   size_t at = kScratchOffset;
   auto take = [&](size_t bytes) {
@@ -545,7 +778,8 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
     n.after = state + (i & 1) * (int64_t)h.T;
     n.shrink = shrink; n.ref = ref; n.e = a.soft.e; n.ld_e = p.ld_e;
     n.T = h.T; n.K = h.K; n.n0 = (int)n0; n.cols = a.N; n.tokens = h.tokens;
-    const int segs = (int)std::max<int64_t>(1, std::min<int64_t>((a.N + 2047) / 2048, (1024 + h.T - 1) / h.T));
+    n.rescale = !p.wide_grad;
+    const int segs = !n.rescale ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>((a.N + 2047) / 2048, (1024 + h.T - 1) / h.T));
     n.seg = (int)(((a.N + segs - 1) / segs + 63) / 64 * 64);
     head_norm_kernel<<<dim3(h.T, segs), kNormThreads, 0, stream>>>(n);
     if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -554,6 +788,15 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
     g.splits = (int)p.splits;
     g.steps = (int)(((a.N + 31) / 32 + p.splits - 1) / p.splits);
     g.part = part; g.shrink = i ? shrink : nullptr;
+    if (p.wide_grad) {
+      g.steps = (int)(((a.N + kGwStep - 1) / kGwStep + p.splits - 1) / p.splits);
+      const GradWideArgs w{g, stats, (int)p.blocks, ref, (h.T + kGwRows - 1) / kGwRows, (h.D + kGwCols - 1) / kGwCols};
+      const int grid = w.row_tiles * w.col_tiles * (int)p.splits;
+      if (h.D % 64 == 0) head_grad_wide_kernel<true><<<grid, kGwThreads, 0, stream>>>(w);
+      else head_grad_wide_kernel<false><<<grid, kGwThreads, 0, stream>>>(w);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      continue;
+    }
     const dim3 grid((h.D + kGsWaves * kGsCols - 1) / (kGsWaves * kGsCols), (int)p.splits,
                     (h.T + 16 * p.row_tiles16 - 1) / (16 * p.row_tiles16));
     if (p.row_tiles16 == 1) head_grad_kernel<1><<<grid, 64 * kGsWaves, 0, stream>>>(g);

@@ -25,6 +25,11 @@ struct SoftmaxOut {
 
 constexpr float kWeightOne = 32768.0f;  // a weight of 1 in fp16
 
+// Where the weight of column n stands in its row of e: in every 8 columns n
+// and n + 4 are neighbours, as the conversion of the gradient's product takes
+// the weights' rows (loss.hip).
+__device__ __forceinline__ int64_t weight_place(int64_t n) { return (n & ~int64_t(7)) | ((n & 3) << 1) | ((n >> 2) & 1); }
+
 // The larger / the sum of a value and its partner 16 or 32 lanes away.
 __device__ __forceinline__ float max_across16(float v) {
   const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -73,16 +78,28 @@ __device__ __forceinline__ void softmax_block16(const SoftmaxOut& o, const f32x4
       s += y[i];
     }
     s = sum_across32(sum_across16(s));
+    // In weight_place's order: of two lanes q that hold 8 columns the even one
+    // takes both first pairs, the odd one both second pairs.
+    half2_t w[4];
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const half2_t a = {(_Float16)(y[4 * i] * kWeightOne), (_Float16)(y[4 * i + 1] * kWeightOne)};
+        const half2_t b = {(_Float16)(y[4 * i + 2] * kWeightOne), (_Float16)(y[4 * i + 3] * kWeightOne)};
+        const auto p = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
+                                                        false, false);
+        w[2 * i] = __builtin_bit_cast(half2_t, (uint32_t)p[0]);
+        w[2 * i + 1] = __builtin_bit_cast(half2_t, (uint32_t)p[1]);
+      }
+    }
     if (row >= nr) continue;
     if (q == 0) o.stats[(int64_t)(row0 + row) * o.blocks + (col0 >> 5)] = make_float2(m, s);
     if constexpr (KEEP) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
-        half4_t h;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) h[v] = (_Float16)(y[4 * i + v] * kWeightOne);
-        *reinterpret_cast<half4_t*>(o.e + (int64_t)(row0 + row) * o.ld_e + col0 + 16 * i + 4 * q) = h;
+        *reinterpret_cast<half4_t*>(o.e + (int64_t)(row0 + row) * o.ld_e + col0 + 16 * i + 4 * q) =
+            half4_t{w[2 * i][0], w[2 * i + 1][0], w[2 * i][1], w[2 * i + 1][1]};
       }
     }
   }
@@ -120,7 +137,7 @@ __device__ __forceinline__ void softmax_block32(const SoftmaxOut& o, const f32x1
       if (row >= nr) continue;
       if (r == 0) o.stats[(int64_t)(row0 + row) * o.blocks + (col0 >> 6)] = make_float2(m, s);
       if constexpr (KEEP) {
-        _Float16* e = o.e + (int64_t)(row0 + row) * o.ld_e + col0 + r;
+        _Float16* e = o.e + (int64_t)(row0 + row) * o.ld_e + col0 + weight_place(r);
         e[0] = (_Float16)(e0 * kWeightOne);
         e[32] = (_Float16)(e1 * kWeightOne);
       }
