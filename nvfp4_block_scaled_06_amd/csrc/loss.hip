@@ -363,8 +363,8 @@ __global__ __launch_bounds__(64 * kGsWaves) void head_grad_kernel(GradArgs a) {
 //  * Softmax weights: on their way into LDS they are brought to the row's m
 //    from their block's, a second rounding to fp16 where those differ.
 //  * K order: in every 32 rows lane (r, h) supplies [16 h + 8 j, +8) to MFMA j.
-// Both double-buffered in LDS, one barrier per step; a step's loads go out a
-// step before they are written there.
+// All double-buffered in LDS, one barrier per step; a step's loads go out a step
+// before they are written there.
 constexpr int kGwThreads = 512;
 constexpr int kGwRows = 128, kGwCols = 512, kGwStep = 128;
 constexpr int kGwLd = 144;  // LDS bytes per byte column or scale block: 128 rows and 16 of padding
@@ -429,15 +429,28 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
   const float ref = a.ref[row0 + (arow ? ar : 0)];
   u32x4_t ev[4];
   float mv[2];
-  auto load = [&](int s) {
+  // A step's loads and stores, half the softmax weights or half the codes at a time. Nothing is read past the split's
+  // rows (zeros) or the piece's columns.
+  auto load_x = [&](int s, int u) {
+    const int k = n0 + kGwStep * s + 64 * u;  // of the piece
+    mv[u] = k < a.g.cols ? st[2 * s + u].x : -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = n0 + kGwStep * s + 32 * i;  // of the piece
-      ev[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                              er, k + 8 * aq < a.g.cols ? oe + 2 * (kGwStep * s + 32 * i) : kMmaOob, 0, 0));
+    for (int i = 2 * u; i < 2 * u + 2; ++i)
+      ev[i] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                       er, k + 32 * (i & 1) + 8 * aq < a.g.cols ? oe + 2 * (kGwStep * s + 32 * i) : kMmaOob, 0, 0));
+  };
+  auto store_x = [&](int buf, int u) {
+    const float f = __builtin_amdgcn_exp2f(mv[u] - ref);  // below fp16's range where a block's m is far lower
+#pragma unroll
+    for (int i = 2 * u; i < 2 * u + 2; ++i) {
+      half8_t v = __builtin_bit_cast(half8_t, ev[i]);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = (_Float16)((float)v[q] * f);
+      *reinterpret_cast<half8_t*>(&lds.x[buf][grad_x_at(ar, 4 * i + aq)]) = v;
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) mv[i] = n0 + kGwStep * s + 64 * i < a.g.cols ? st[2 * s + i].x : -__builtin_inff();
+  };
+  auto load_w = [&](int s) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       wv[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(wcr, oc + (uint32_t)((kGwStep * s + i) * rowc), 0, 0));
@@ -451,24 +464,15 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
       }
     }
   };
-  auto store = [&](int buf) {
+  auto store_c = [&](int buf, int w) {
+    uint32_t lo[4], hi[4];
+    byte_transpose4({wv[0][w], wv[1][w], wv[2][w], wv[3][w]}, lo);
+    byte_transpose4({wv[4][w], wv[5][w], wv[6][w], wv[7][w]}, hi);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float f = __builtin_amdgcn_exp2f(mv[i >> 1] - ref);  // below fp16's range where a block's m is far lower
-      half8_t v = __builtin_bit_cast(half8_t, ev[i]);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = (_Float16)((float)v[q] * f);
-      *reinterpret_cast<half8_t*>(&lds.x[buf][grad_x_at(ar, 4 * i + aq)]) = v;
-    }
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      uint32_t lo[4], hi[4];
-      byte_transpose4({wv[0][w], wv[1][w], wv[2][w], wv[3][w]}, lo);
-      byte_transpose4({wv[4][w], wv[5][w], wv[6][w], wv[7][w]}, hi);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<u32x2_t*>(&lds.codes[buf][((4 * w + i) * 32 + c) * kGwLd + 8 * o]) = u32x2_t{lo[i], hi[i]};
-    }
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<u32x2_t*>(&lds.codes[buf][((4 * w + i) * 32 + c) * kGwLd + 8 * o]) = u32x2_t{lo[i], hi[i]};
+  };
+  auto store_s = [&](int buf) {
     const uint32_t s0 = S4 ? sv[0][0] : sv[0][0] | (sv[0][1] << 16), s1 = S4 ? sv[1][0] : sv[1][0] | (sv[1][1] << 16);
     const uint32_t t0 = __builtin_amdgcn_perm(s1, s0, 0x05010400u), t1 = __builtin_amdgcn_perm(s1, s0, 0x07030602u);
     uint8_t* d = &lds.scales[buf][4 * b * kGwLd + 2 * p];
@@ -485,49 +489,91 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][m][v] = 0.0f;
+
+  // A step is 8 slices of 16 rows. In a slice the MFMAs of the even columns run
+  // while the odd columns' weights of the slice are converted, then the other
+  // way round for the next slice; softmax weight fragment i is read right
+  // after its last MFMA of the slice before, a group's codes (32 rows) during
+  // the last slice of the group before. The step's one barrier stands before
+  // its last slice: by then every wavefront has read this buffer to the end and
+  // written the next one, whose first fragments the last slice reads.
+  half8_t A[RT], w[2];
+  u32x4_t cw, sw;
+  uint32_t col[2];
+  half2_t sc[4];
+  auto afrag = [&](int i, int buf, int sl) {
+    return *reinterpret_cast<const half8_t*>(&lds.x[buf][grad_x_at(32 * i + r, 4 * (sl >> 1) + 2 * h + (sl & 1))]);
+  };
+  auto read_codes = [&](int buf, int g) {
+    cw = *reinterpret_cast<const u32x4_t*>(&lds.codes[buf][(wave * 32 + r) * kGwLd + 32 * g + 16 * h]);
+    sw = *reinterpret_cast<const u32x4_t*>(&lds.scales[buf][r * kGwLd + 32 * g + 16 * h]);
+  };
+  auto prepare = [&](auto jc) {  // columns and scales of a slice
+    constexpr int j = decltype(jc)::value;
+    const uint32_t x = cw[2 * j], y = cw[2 * j + 1];
+    const uint32_t p01 = __builtin_amdgcn_perm(sw[2 * j + 1], sw[2 * j], 0x05010400u);
+    const uint32_t p23 = __builtin_amdgcn_perm(sw[2 * j + 1], sw[2 * j], 0x07030602u);
+    col[0] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
+    col[1] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+    sc[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p01, 1.0f, false);
+    sc[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p01, 1.0f, true);
+    sc[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p23, 1.0f, false);
+    sc[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p23, 1.0f, true);
+  };
+  auto convert = [&](auto mc, auto kc) {
+    constexpr int m = decltype(mc)::value, k = decltype(kc)::value;
+    reinterpret_cast<half2_t*>(&w[m])[k] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(col[m], 1.0f, k) * sc[k];
+  };
   if (nsteps > 0) {
-    load(0);
-    store(0);
-    load(1);
+    load_x(0, 0);
+    load_x(0, 1);
+    load_w(0);
+    store_x(0, 0);
+    store_x(0, 1);
+    store_c(0, 0);
+    store_c(0, 1);
+    store_s(0);
+    load_x(1, 0);
+    load_x(1, 1);
+    load_w(1);
     __syncthreads();
+    read_codes(0, 0);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) A[i] = afrag(i, 0, 0);
+    prepare(IntC<0>{});
+    static_for<0, 4>([&](auto kc) { convert(IntC<0>{}, kc); });
   }
   for (int s = 0; s < nsteps; ++s) {
     const int buf = s & 1;
-    static_for<0, 4>([&](auto gc) {
-      constexpr int g = decltype(gc)::value;
-      const u32x4_t cw = *reinterpret_cast<const u32x4_t*>(&lds.codes[buf][(wave * 32 + r) * kGwLd + 32 * g + 16 * h]);
-      const u32x4_t sw = *reinterpret_cast<const u32x4_t*>(&lds.scales[buf][r * kGwLd + 32 * g + 16 * h]);
-      static_for<0, 2>([&](auto jc) {
-        constexpr int j = decltype(jc)::value;
-        const uint32_t x = cw[2 * j], y = cw[2 * j + 1];
-        const uint32_t col[2] = {(x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u)};
-        const uint32_t p01 = __builtin_amdgcn_perm(sw[2 * j + 1], sw[2 * j], 0x05010400u);
-        const uint32_t p23 = __builtin_amdgcn_perm(sw[2 * j + 1], sw[2 * j], 0x07030602u);
-        const half2_t sc[4] = {e4m3x2_f16(p01), e4m3x2_f16(p01 >> 16), e4m3x2_f16(p23), e4m3x2_f16(p23 >> 16)};
-        half8_t w[2];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const half2_t q0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(col[m], 1.0f, 0) * sc[0];
-          const half2_t q1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(col[m], 1.0f, 1) * sc[1];
-          const half2_t q2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(col[m], 1.0f, 2) * sc[2];
-          const half2_t q3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(col[m], 1.0f, 3) * sc[3];
-          w[m] = half8_t{q0[0], q0[1], q1[0], q1[1], q2[0], q2[1], q3[0], q3[1]};
-        }
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const half8_t A = *reinterpret_cast<const half8_t*>(&lds.x[buf][grad_x_at(32 * i + r, 4 * g + 2 * h + j)]);
-#pragma unroll
-          for (int m = 0; m < 2; ++m) acc[i][m] = mfma32(A, w[m], acc[i][m]);
-        }
+    static_for<0, 8>([&](auto slc) {
+      constexpr int sl = decltype(slc)::value;
+      if constexpr (sl == 7) __syncthreads();
+      if constexpr (sl & 1) read_codes(sl == 7 ? buf ^ 1 : buf, ((sl >> 1) + 1) & 3);
+      static_for<0, RT>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        acc[i][0] = mfma32(A[i], w[0], acc[i][0]);
+        static_for<i * 4 / RT, (i + 1) * 4 / RT>([&](auto kc) { convert(IntC<1>{}, kc); });
+        __builtin_amdgcn_sched_barrier(0);
       });
-      if constexpr (g == 1) {
-        if (s + 1 < nsteps) {
-          store(buf ^ 1);
-          load(s + 2);
-        }
+      prepare(IntC<(sl + 1) & 1>{});
+      static_for<0, RT>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        acc[i][1] = mfma32(A[i], w[1], acc[i][1]);
+        A[i] = afrag(i, sl == 7 ? buf ^ 1 : buf, (sl + 1) & 7);
+        static_for<i * 4 / RT, (i + 1) * 4 / RT>([&](auto kc) { convert(IntC<0>{}, kc); });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      // The next step's data into LDS, the one after's from memory.
+      if constexpr (sl == 0 || sl == 1) {
+        store_x(buf ^ 1, sl);
+        load_x(s + 2, sl);
+      }
+      if constexpr (sl == 2 || sl == 3) store_c(buf ^ 1, sl - 2);
+      if constexpr (sl == 4) {
+        store_s(buf ^ 1);
+        load_w(s + 2);
       }
     });
-    __syncthreads();
   }
 
   // Value v of lane (r, h): row 8 (v / 4) + 4 h + v % 4 of its 32-row tile, columns 16 r + 2 wave and the next.
