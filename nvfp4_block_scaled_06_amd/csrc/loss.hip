@@ -58,6 +58,15 @@ __global__ __launch_bounds__(kEtThreads) __attribute__((amdgpu_waves_per_eu(2, 2
 // ---------------------------------------------------------------------------
 // The tokens of the loss.
 // ---------------------------------------------------------------------------
+// A row's tokens that the gradient multiplies by themselves: q - p, for each
+// place that names a token.
+struct TokenList {
+  int count;  // -1: the row has no gradient
+  int pad;
+  int token[kHeadTokens];
+  float coef[kHeadTokens];
+};
+
 struct HeadArgs {
   const uint8_t* xc;
   const uint8_t* xs;
@@ -71,12 +80,13 @@ struct HeadArgs {
   int teacher_bf16;
   float tau;
   const float* weight;  // NULL (1) or [T]
-  const float2* stats;  // [T, blocks] (m, s)
-  int blocks;
+  const float2* stats;  // [T, blocks] (m, s), the first `used` of each row
+  int blocks, used;
   float* loss;
   float* lse;
   float* logq;  // [T, K]; NULL for cross entropy
   void* dx;     // bf16 [T, D]
+  TokenList* lists;  // with a gradient: [T]
 };
 
 __device__ __forceinline__ float teacher_at(const HeadArgs& a, int64_t i) {
@@ -121,19 +131,96 @@ __device__ __forceinline__ float2 teacher_row(const HeadArgs& a, int64_t t) {
   return make_float2(m, wave_sum(s));
 }
 
-// One workgroup per row: lse from the blocks' sums, the logits of the row's
-// tokens by themselves (a wavefront per token: its weight row against x), and
-// the loss. Exact products, fp32 sums in a fixed order.
+// (m, s) of n blocks, by NT threads of which this is one; 8 loads in flight.
+template <int NT>
+__device__ __forceinline__ float2 thread_join(const float2* st, int n) {
+  float2 v = make_float2(-__builtin_inff(), 0.0f);
+  for (int i0 = threadIdx.x; i0 < n; i0 += 8 * NT) {
+    float2 u[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) u[q] = i0 + q * NT < n ? st[i0 + q * NT] : make_float2(-__builtin_inff(), 0.0f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v = soft_join(v, u[q]);
+  }
+  return v;
+}
+
+// Logits of up to U tokens against row t of x, by a wavefront; exact block
+// products, fp32 sums in a fixed order. A token outside [0, N) gives anything.
+template <int U>
+__device__ __forceinline__ void token_dots(const HeadArgs& a, int64_t t, const int (&n)[U], float (&z)[U]) {
+  const int lane = threadIdx.x & 63, nch = a.D >> 5;
+  const int64_t rowc = a.D / 2, rows = a.D / 16;
+  const uint8_t *xc = a.xc + t * rowc, *xs = a.xs + t * rows;
+  int64_t row[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    row[u] = n[u] >= 0 && n[u] < a.N ? n[u] : 0;
+    z[u] = 0.0f;
+  }
+  for (int c = lane; c < nch; c += 64) {
+    u32x4_t wv[U];
+    uint32_t wb[U];
+    const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(xc + 16 * c);
+    const uint32_t xb = *reinterpret_cast<const uint16_t*>(xs + 2 * c);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      wv[u] = *reinterpret_cast<const u32x4_t*>(a.wc + row[u] * rowc + 16 * c);
+      wb[u] = *reinterpret_cast<const uint16_t*>(a.ws + row[u] * rows + 2 * c);
+    }
+    const half2_t xsc = e4m3x2_f16(xb);
+    half8_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = fp4x8_scaled(xv[i], xsc, i >> 1);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const half2_t wsc = e4m3x2_f16(wb[u]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        z[u] += dot8(x[2 * i + 1], fp4x8_scaled(wv[u][2 * i + 1], wsc, i),
+                     dot8(x[2 * i], fp4x8_scaled(wv[u][2 * i], wsc, i), 0.0f));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) z[u] = wave_sum(z[u]);
+}
+
+// More tokens than a row's workgroup has wavefronts: their logits (over tau)
+// go to logq first, 16 tokens of a row per workgroup, each wavefront's four
+// weight rows in flight together.
 constexpr int kTokWaves = 4;
-__global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a) {
+constexpr int kTokPerWave = 4;
+__global__ __launch_bounds__(64 * kTokWaves) void head_dots_kernel(HeadArgs a) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x;
+  const int j0 = (blockIdx.y * kTokWaves + wave) * kTokPerWave;
+  if (j0 >= a.K) return;
+  const float scale = load_early(a.gsa) * load_early(a.gsw) / a.tau;
+  int n[kTokPerWave];
+  float z[kTokPerWave];
+#pragma unroll
+  for (int u = 0; u < kTokPerWave; ++u) n[u] = a.tokens[t * a.K + min(j0 + u, a.K - 1)];
+  token_dots<kTokPerWave>(a, t, n, z);
+#pragma unroll
+  for (int u = 0; u < kTokPerWave; ++u)
+    if (lane == u && j0 + u < a.K) a.logq[t * a.K + j0 + u] = z[u] * scale;
+}
+
+// One workgroup per row: lse from the blocks' sums, and the loss. Up to as
+// many tokens as wavefronts have their logits computed here, `dots` says.
+__global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a, int dots) {
   __shared__ float2 part[kTokWaves];
-  __shared__ float terms[kTokWaves];
+  __shared__ float terms[kTokWaves], zs[kTokWaves], lz[kHeadTokens];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = blockIdx.x;
   const float scale = load_early(a.gsa) * load_early(a.gsw) / a.tau;
-  float2 v = make_float2(-__builtin_inff(), 0.0f);
-  for (int i = threadIdx.x; i < a.blocks; i += 64 * kTokWaves) v = soft_join(v, a.stats[t * a.blocks + i]);
-  v = wave_join(v);
+  if (dots && wave < a.K) {
+    const int n[1] = {a.tokens[t * a.K + wave]};
+    float z[1];
+    token_dots<1>(a, t, n, z);
+    if (lane == 0) zs[wave] = z[0] * scale;
+  }
+  float2 v = wave_join(thread_join<64 * kTokWaves>(a.stats + t * a.blocks, a.used));
   if (lane == 0) part[wave] = v;
   __syncthreads();
   v = part[0];
@@ -143,37 +230,24 @@ __global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a)
   float2 tr = make_float2(0.0f, 1.0f);  // log p = 0 for cross entropy
   if (a.teacher) tr = teacher_row(a, t);
   const float logs = a.teacher ? logf(tr.y) : 0.0f;
-
-  const int nch = a.D >> 5;
-  const int64_t rowc = a.D / 2, rows = a.D / 16;
-  const uint8_t *xc = a.xc + t * rowc, *xs = a.xs + t * rows;
   float sum = 0.0f;
-  for (int j = wave; j < a.K; j += kTokWaves) {
+  for (int j = threadIdx.x; j < a.K; j += 64 * kTokWaves) {
     const int n = a.tokens[t * a.K + j];
-    const bool valid = n >= 0 && n < a.N;
     float logq = 0.0f;
-    if (valid) {
-      const uint8_t *wc = a.wc + n * rowc, *ws = a.ws + n * rows;
-      float acc = 0.0f;
-      for (int c = lane; c < nch; c += 64) {
-        const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(xc + 16 * c), wv = *reinterpret_cast<const u32x4_t*>(wc + 16 * c);
-        const uint32_t xb = *reinterpret_cast<const uint16_t*>(xs + 2 * c), wb = *reinterpret_cast<const uint16_t*>(ws + 2 * c);
-        const half2_t xsc = e4m3x2_f16(xb), wsc = e4m3x2_f16(wb);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          acc += dot8(fp4x8_scaled(xv[2 * i + 1], xsc, i), fp4x8_scaled(wv[2 * i + 1], wsc, i),
-                      dot8(fp4x8_scaled(xv[2 * i], xsc, i), fp4x8_scaled(wv[2 * i], wsc, i), 0.0f));
-      }
-      logq = wave_sum(acc) * scale - lse;
+    if (n >= 0 && n < a.N) {
+      const float z = dots ? zs[j] : a.logq[t * a.K + j];
+      lz[j] = z;
+      logq = z - lse;
       if (a.teacher) {
         const float lp = teacher_at(a, t * a.K + j) - tr.x - logs, p = expf(lp);
         if (p != 0.0f) sum += p * (lp - logq);  // p log p is 0 at 0
       } else {
-        sum -= logq;
+        sum = -logq;
       }
     }
-    if (a.logq && lane == 0) a.logq[t * a.K + j] = logq;
+    if (a.logq) a.logq[t * a.K + j] = logq;
   }
+  sum = wave_sum(sum);
   if (lane == 0) terms[wave] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -183,6 +257,29 @@ __global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a)
     a.loss[t] = tr.y == 0.0f ? 0.0f : l * a.tau * a.tau;
     a.lse[t] = lse;
   }
+  if (!a.lists) return;
+  // The first wavefront lists the places that name a token, in order. A token
+  // named more than once has its q at its first place.
+  if (wave != 0) return;
+  TokenList& list = a.lists[t];
+  int out = 0;
+  for (int j0 = 0; j0 < a.K; j0 += 64) {
+    const int j = j0 + lane;
+    const int n = j < a.K ? a.tokens[t * a.K + j] : -1;
+    const bool valid = n >= 0 && n < a.N;
+    bool first = true;
+    for (int i = 0; i < min(j0 + 64, a.K); ++i) first = first && (i >= j || a.tokens[t * a.K + i] != n);
+    const uint64_t bal = __ballot(valid);
+    if (valid) {
+      const int at = out + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(bal >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)bal, 0u));
+      const float z = dots ? zs[j] : lz[j];
+      const float p = a.teacher ? expf(teacher_at(a, t * a.K + j) - tr.x) / tr.y : 1.0f;
+      list.token[at] = n;
+      list.coef[at] = (first ? expf(z - lse) : 0.0f) - p;
+    }
+    out += (int)__popcll(bal);
+  }
+  if (lane == 0) list.count = out == 0 || tr.y == 0.0f ? -1 : out;
 }
 
 // ---------------------------------------------------------------------------
@@ -208,9 +305,7 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = blockIdx.x;
   const float2* st = a.stats + t * a.blocks;
-  float2 v = make_float2(-__builtin_inff(), 0.0f);
-  for (int i = threadIdx.x; i < a.used; i += kNormThreads) v = soft_join(v, st[i]);
-  v = wave_join(v);
+  float2 v = wave_join(thread_join<kNormThreads>(st, a.used));
   if (lane == 0) part[wave] = v;
   __syncthreads();
   v = part[0];
@@ -369,12 +464,31 @@ constexpr int kGwThreads = 512;
 constexpr int kGwRows = 128, kGwCols = 512, kGwStep = 128;
 constexpr int kGwLd = 144;  // LDS bytes per byte column or scale block: 128 rows and 16 of padding
 
+// Tiles in bands of 8 row tiles, column tile by column tile, so that 32
+// neighbours read 8 rows' softmax weights and 4 columns' weights. The first
+// `full`, whole rounds of 256 workgroups, take all of a piece's rows; each of
+// the others is shared by `splits` workgroups that take a part of the rows
+// each, so that the last rounds are full too.
+struct GradTiles {
+  int row_tiles, col_tiles, full, splits;
+  __host__ __device__ int count() const { return row_tiles * col_tiles; }
+  __device__ __forceinline__ void place(int t, int& rt, int& ct) const {
+    const int band = t / (8 * col_tiles), in = t - band * 8 * col_tiles, bandrows = min(8, row_tiles - 8 * band);
+    ct = in / bandrows;
+    rt = 8 * band + in - ct * bandrows;
+  }
+  __device__ __forceinline__ int parts(int rt, int ct) const {  // sums of a tile
+    const int band = rt >> 3, bandrows = min(8, row_tiles - 8 * band);
+    return 8 * band * col_tiles + ct * bandrows + (rt & 7) < full ? 1 : splits;
+  }
+};
+
 struct GradWideArgs {
   GradArgs g;
   const float2* stats;  // [T, blocks] of the piece, blocks of 64 columns
   int blocks;
   const float* ref;     // [T]: the row's m
-  int row_tiles, col_tiles;
+  GradTiles tiles;
 };
 
 struct GradLds {
@@ -400,13 +514,14 @@ __device__ __forceinline__ void byte_transpose4(const uint32_t (&a)[4], uint32_t
 
 // S4: rows of scales start at multiples of 4 bytes (D a multiple of 64).
 template <int RT, bool S4>
-__device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, int nr, int ct, int split, GradLds& lds) {
+__device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, int nr, int ct, int split, int steps,
+                                               GradLds& lds) {
   typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t rowc = a.g.D / 2, rows = a.g.D / 16;
   const int d0 = ct * kGwCols;
-  const int n0 = split * a.g.steps * kGwStep, n1 = min(n0 + a.g.steps * kGwStep, a.g.cols);
+  const int n0 = split * steps * kGwStep, n1 = min(n0 + steps * kGwStep, a.g.cols);
   const int64_t nrows = max(n1 - n0, 0);
   const int nsteps = (int)((nrows + kGwStep - 1) / kGwStep);
   const __amdgpu_buffer_rsrc_t wcr = make_rsrc(a.g.wc + n0 * rowc, nrows * rowc);
@@ -601,90 +716,114 @@ template <bool S4>
 __global__ __launch_bounds__(kGwThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_grad_wide_kernel(
     GradWideArgs a) {
   __shared__ GradLds lds;
-  // 8 row tiles times 4 column tiles of one split side by side on one XCD: they
-  // read the same weights and the same softmax weights.
-  const int tiles = a.row_tiles * a.col_tiles;
-  const int n = xcd_order(blockIdx.x, gridDim.x), split = n / tiles, t = n - split * tiles;
-  const int band = t / (8 * a.col_tiles), in = t - band * 8 * a.col_tiles;
-  const int bandrows = min(8, a.row_tiles - 8 * band);
-  const int ct = in / bandrows, row0 = (8 * band + in - ct * bandrows) * kGwRows;
-  const int nr = min(kGwRows, a.g.T - row0);
-  if (nr > 96) grad_wide_tile<4, S4>(a, row0, nr, ct, split, lds);
-  else if (nr > 64) grad_wide_tile<3, S4>(a, row0, nr, ct, split, lds);
-  else if (nr > 32) grad_wide_tile<2, S4>(a, row0, nr, ct, split, lds);
-  else grad_wide_tile<1, S4>(a, row0, nr, ct, split, lds);
+  const GradTiles& tl = a.tiles;
+  const int rest = tl.count() - tl.full;
+  int t = blockIdx.x, split = 0, steps = (a.g.cols + kGwStep - 1) / kGwStep;
+  if (t < tl.full) {
+    t = xcd_order(t, tl.full);
+  } else {
+    const int n = xcd_order(t - tl.full, rest * tl.splits);
+    split = n / rest;
+    t = tl.full + n - split * rest;
+    steps = (steps + tl.splits - 1) / tl.splits;
+  }
+  int rt, ct;
+  tl.place(t, rt, ct);
+  const int row0 = rt * kGwRows, nr = min(kGwRows, a.g.T - row0);
+  if (nr > 96) grad_wide_tile<4, S4>(a, row0, nr, ct, split, steps, lds);
+  else if (nr > 64) grad_wide_tile<3, S4>(a, row0, nr, ct, split, steps, lds);
+  else if (nr > 32) grad_wide_tile<2, S4>(a, row0, nr, ct, split, steps, lds);
+  else grad_wide_tile<1, S4>(a, row0, nr, ct, split, steps, lds);
 }
 
 // dx: the splits' sums, divided by the softmax's, and the loss's own tokens.
+// SHARE: a workgroup's wavefronts share 512 columns, each a quarter of the
+// splits and tokens, joined in a fixed order; otherwise each has 512 of its
+// own.
 struct DxArgs {
   HeadArgs h;
   const float* part;
-  int splits;
+  int splits;       // of every tile, or:
+  GradTiles tiles;  // if it has any
 };
 
-constexpr int kDxThreads = 256;
+constexpr int kDxWaves = 4;
+constexpr int64_t kDxManyWgs = 4096;  // from this many workgroups of 512 columns on, each wavefront has its own
+constexpr int kDxThreads = 64 * kDxWaves;
+template <bool SHARE>
 __global__ __launch_bounds__(kDxThreads) void head_dx_kernel(DxArgs a) {
-  __shared__ float coef[kHeadTokens];
-  __shared__ int tok[kHeadTokens];
+  __shared__ float joined[SHARE ? kDxWaves : 1][SHARE ? 64 : 1][9];
   const HeadArgs& h = a.h;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = blockIdx.x;
+  const TokenList& list = h.lists[t];
+  const int named = list.count;
   const float2 soft = h.stats[t];  // (m, s) of the whole row
-  const float gsw = load_early(h.gsw);
-  float2 tr = make_float2(0.0f, 1.0f);
-  if (h.teacher) tr = teacher_row(h, t);
-  bool any = false;
-  for (int j = threadIdx.x; j < h.K; j += kDxThreads) {
-    const int n = h.tokens[t * h.K + j];
-    const bool valid = n >= 0 && n < h.N;
-    float c = 0.0f;
-    if (valid) {
-      const float q = expf(h.teacher ? h.logq[t * h.K + j] : -h.loss[t]);
-      const float p = h.teacher ? expf(teacher_at(h, t * h.K + j) - tr.x) / tr.y : 1.0f;
-      // A token named more than once has its whole p at its first place.
-      c = -p;
-      bool first = true;
-      for (int i = 0; i < j; ++i) first = first && h.tokens[t * h.K + i] != n;
-      if (first) c += q;
-    }
-    any = any || valid;
-    coef[j] = c;
-    tok[j] = valid ? n : 0;
-  }
-  any = __syncthreads_or(any) != 0;
-  const float weight = h.weight ? h.weight[t] : 1.0f;
-  const bool used = any && tr.y != 0.0f;
-  const float norm = 1.0f / (soft.y * kWeightOne), f = weight * gsw * h.tau;
-  uint16_t* out = static_cast<uint16_t*>(h.dx) + t * h.D;
-  for (int d = (blockIdx.y * kDxThreads + threadIdx.x) * 8; d < h.D; d += gridDim.y * kDxThreads * 8) {
-    u32x4_t o = {0u, 0u, 0u, 0u};
-    if (used) {
-      float y[8];
+  const float f = (h.weight ? h.weight[t] : 1.0f) * load_early(h.gsw) * h.tau, norm = 1.0f / (soft.y * kWeightOne);
+  const int d = ((SHARE ? blockIdx.y : blockIdx.y * kDxWaves + wave) * 64 + lane) * 8;
+  const int first = SHARE ? wave : 0, step = SHARE ? kDxWaves : 1;
+  float y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-      for (int s = 0; s < a.splits; ++s) {
-        const f32x4_t* p = reinterpret_cast<const f32x4_t*>(a.part + ((int64_t)s * h.T + t) * h.D + d);
-        const f32x4_t u = p[0], v = p[1];
+  for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+  if (named >= 0 && d < h.D) {
+    const int splits = a.tiles.col_tiles ? a.tiles.parts((int)(t / kGwRows), d / kGwCols) : a.splits;
+    const float* part = a.part + t * h.D + d;
+    const int64_t slab = (int64_t)h.T * h.D;
+    for (int s0 = first; s0 < splits; s0 += 4 * step) {  // 4 splits' loads in flight
+      f32x4_t u[4][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[i] += u[i];
-          y[4 + i] += v[i];
-        }
+      for (int q = 0; q < 4; ++q) {
+        const f32x4_t* p = reinterpret_cast<const f32x4_t*>(part + min(s0 + q * step, splits - 1) * slab);
+        u[q][0] = p[0];
+        u[q][1] = p[1];
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= norm;
-      for (int j = 0; j < h.K; ++j) {
-        const float c = coef[j];
-        if (c == 0.0f) continue;
-        const uint32_t code = *reinterpret_cast<const uint32_t*>(h.wc + (int64_t)tok[j] * (h.D / 2) + d / 2);
-        const half8_t w = fp4x8_to_f16(code, e4m3_f16(h.ws[(int64_t)tok[j] * (h.D / 16) + d / 16]));
+      for (int q = 0; q < 4; ++q) {
+        const bool in = s0 + q * step < splits;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(c, (float)w[i], y[i]);
+        for (int i = 0; i < 8; ++i) y[i] += in ? u[q][i >> 2][i & 3] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] *= norm;
+    const uint8_t *wc = h.wc + d / 2, *ws = h.ws + d / 16;
+    const int64_t rowc = h.D / 2, rows = h.D / 16;
+    for (int j0 = first; j0 < named; j0 += 8 * step) {  // 8 rows' loads in flight
+      uint32_t code[8], sb[8];
+      float c[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int j = min(j0 + u * step, named - 1);
+        const int64_t n = list.token[j];
+        c[u] = j0 + u * step < named ? list.coef[j] : 0.0f;
+        code[u] = *reinterpret_cast<const uint32_t*>(wc + n * rowc);
+        sb[u] = ws[n * rows];
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = bf16_round2(y[2 * i] * f, y[2 * i + 1] * f);
+      for (int u = 0; u < 8; ++u) {
+        const half8_t w = fp4x8_to_f16(code[u], e4m3_f16(sb[u]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fmaf(c[u], (float)w[i], y[i]);
+      }
     }
-    *reinterpret_cast<u32x4_t*>(out + d) = o;
   }
+  if constexpr (SHARE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) joined[wave][lane][i] = y[i];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 1; w < kDxWaves; ++w)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] += joined[w][lane][i];
+  }
+  if (d >= h.D) return;
+  u32x4_t o = {0u, 0u, 0u, 0u};
+  if (named >= 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = bf16_round2(y[2 * i] * f, y[2 * i + 1] * f);
+  }
+  *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(h.dx) + t * h.D + d) = o;
 }
 
 // ---------------------------------------------------------------------------
@@ -700,10 +839,11 @@ struct HeadPlan {
   int64_t pieces;
   int64_t blocks;    // statistics blocks per row kept at a time
   bool wide_grad;    // the second product's tiles
+  GradTiles tiles;
   int row_tiles16;   // 16-row tiles of a workgroup of its stream
   int64_t splits;    // of a piece's rows there
   int64_t ld_e;
-  size_t stats_at, state_at, shrink_at, ref_at, e_at, part_at, bytes;
+  size_t stats_at, state_at, shrink_at, ref_at, e_at, part_at, lists_at, bytes;
 };
 
 static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
@@ -712,10 +852,11 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   p.wide = T > 32 && wide_items >= kMinTileItems;
   p.block_shift = p.wide ? 6 : 5;
   int64_t piece = kMaxRange / (D / 2) / 512 * 512;  // a piece's codes lie within a buffer's range
-  // A piece's weights take 256 MB at most, but 4096 columns at least.
-  if (grad) piece = std::min(piece, std::max((int64_t(1) << 27) / std::max(T, int64_t(1)) / 512 * 512, int64_t(4096)));
+  // A piece's softmax weights take 512 MB at most, but 4096 columns at least.
+  if (grad) piece = std::min(piece, std::max((int64_t(1) << 28) / std::max(T, int64_t(1)) / 512 * 512, int64_t(4096)));
   piece = std::max(piece, int64_t(512));
-  p.piece = std::min(piece, (N + 511) / 512 * 512);
+  p.pieces = (N + piece - 1) / piece;
+  p.piece = ((N + p.pieces - 1) / p.pieces + 511) / 512 * 512;  // equal pieces
   p.pieces = (N + p.piece - 1) / p.piece;
   const int64_t cols = grad ? p.piece : N;
   p.blocks = (cols + (int64_t(1) << p.block_shift) - 1) >> p.block_shift;
@@ -723,15 +864,20 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   p.wide_grad = p.wide;
   const int64_t rows = std::min(p.piece, N);
   if (p.wide_grad) {
-    // Splits that leave the last round of 256 workgroups fullest, one each per compute unit.
-    const int64_t tiles = ((T + kGwRows - 1) / kGwRows) * ((D + kGwCols - 1) / kGwCols);
-    const int64_t most = std::max(int64_t(1), std::min(int64_t(64), rows / 2048));
-    double best = 0.0;
+    // Whole rounds of 256 workgroups, one on each compute unit, then the tiles left in the splits that end soonest: a
+    // split of 1 / s takes 1 / s of a round.
+    p.tiles.row_tiles = (int)((T + kGwRows - 1) / kGwRows);
+    p.tiles.col_tiles = (int)((D + kGwCols - 1) / kGwCols);
+    p.tiles.full = p.tiles.count() / 256 * 256;
+    const int64_t rest = p.tiles.count() - p.tiles.full, most = std::min(int64_t(16), std::max(int64_t(1), rows / 2048));
+    const double whole = (double)(p.tiles.full / 256);
+    double best = whole + 1.0;
     p.splits = 1;
-    for (int64_t s = 1; s <= most; ++s) {
-      const double use = (double)(tiles * s) / (double)((tiles * s + 255) / 256 * 256);
-      if (use > best + 0.03) best = use, p.splits = s;
+    for (int64_t s = 2; rest && s <= most; ++s) {
+      const double rounds = whole + (double)((rest * s + 255) / 256) / (double)s;
+      if (rounds < 0.97 * best) best = rounds, p.splits = s;  // each split's sums are written and read once more
     }
+    p.tiles.splits = (int)p.splits;
   } else {
     const int64_t wgs = ((D + kGsWaves * kGsCols - 1) / (kGsWaves * kGsCols)) * ((T + 16 * p.row_tiles16 - 1) / (16 * p.row_tiles16));
     p.splits = std::max(int64_t(1), std::min((512 + wgs - 1) / wgs, (rows + 255) / 256));
@@ -750,6 +896,7 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
     p.ref_at = take((size_t)T * sizeof(float));
     p.e_at = take((size_t)T * p.ld_e * sizeof(_Float16));
     p.part_at = take((size_t)p.splits * T * D * sizeof(float));
+    p.lists_at = take((size_t)T * sizeof(TokenList));
   }
   p.bytes = at;
   return p;
@@ -779,6 +926,18 @@ static hipError_t launch_logits(const ExpertArgs& a, bool wide, hipStream_t stre
   return hipGetLastError();
 }
 
+static hipError_t launch_tokens(const HeadArgs& h, hipStream_t stream) {
+  const bool dots = h.K <= kTokWaves;
+  if (!dots) {
+    constexpr int per = kTokWaves * kTokPerWave;
+    head_dots_kernel<<<dim3(h.T, (h.K + per - 1) / per), 64 * kTokWaves, 0, stream>>>(h);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  head_tokens_kernel<<<h.T, 64 * kTokWaves, 0, stream>>>(h, dots);
+  return hipGetLastError();
+}
+
 static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream_t stream) {
   const HeadPlan p = head_plan(in.T, in.D, in.N, grad);
   HeadArgs h = in;
@@ -799,9 +958,8 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
       if ((e = launch_logits<Out::kSums>(a, p.wide, stream)) != hipSuccess) return e;
     }
     h.stats = stats;
-    h.blocks = (int)p.blocks;
-    head_tokens_kernel<<<h.T, 64 * kTokWaves, 0, stream>>>(h);
-    return hipGetLastError();
+    h.blocks = h.used = (int)p.blocks;
+    return launch_tokens(h, stream);
   }
   float2* state = reinterpret_cast<float2*>(ws + p.state_at);
   float* shrink = reinterpret_cast<float*>(ws + p.shrink_at);
@@ -835,9 +993,8 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
     g.steps = (int)(((a.N + 31) / 32 + p.splits - 1) / p.splits);
     g.part = part; g.shrink = i ? shrink : nullptr;
     if (p.wide_grad) {
-      g.steps = (int)(((a.N + kGwStep - 1) / kGwStep + p.splits - 1) / p.splits);
-      const GradWideArgs w{g, stats, (int)p.blocks, ref, (h.T + kGwRows - 1) / kGwRows, (h.D + kGwCols - 1) / kGwCols};
-      const int grid = w.row_tiles * w.col_tiles * (int)p.splits;
+      const GradWideArgs w{g, stats, (int)p.blocks, ref, p.tiles};
+      const int grid = p.tiles.full + (p.tiles.count() - p.tiles.full) * p.tiles.splits;
       if (h.D % 64 == 0) head_grad_wide_kernel<true><<<grid, kGwThreads, 0, stream>>>(w);
       else head_grad_wide_kernel<false><<<grid, kGwThreads, 0, stream>>>(w);
       if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -851,11 +1008,15 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   h.stats = state + ((p.pieces - 1) & 1) * (int64_t)h.T;
-  h.blocks = 1;
-  head_tokens_kernel<<<h.T, 64 * kTokWaves, 0, stream>>>(h);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  DxArgs d{h, part, (int)p.splits};
-  head_dx_kernel<<<dim3(h.T, h.T >= 256 ? 1 : (h.D + kDxThreads * 8 - 1) / (kDxThreads * 8)), kDxThreads, 0, stream>>>(d);
+  h.blocks = h.used = 1;
+  h.lists = reinterpret_cast<TokenList*>(ws + p.lists_at);
+  if ((e = launch_tokens(h, stream)) != hipSuccess) return e;
+  DxArgs d{h, part, (int)p.splits, p.tiles};
+  const int columns = (h.D + 511) / 512;
+  if ((int64_t)h.T * columns < kDxManyWgs)
+    head_dx_kernel<true><<<dim3(h.T, columns), kDxThreads, 0, stream>>>(d);
+  else
+    head_dx_kernel<false><<<dim3(h.T, (columns + kDxWaves - 1) / kDxWaves), kDxThreads, 0, stream>>>(d);
   return hipGetLastError();
 }
 
