@@ -24,6 +24,7 @@
 #include "experts_tile.hpp"
 
 #include <algorithm>
+#include <cmath>
 
 namespace nvr {
 
@@ -296,6 +297,7 @@ struct NormArgs {
   int64_t ld_e;
   int T, K, n0, cols, seg;  // seg: columns per workgroup, a multiple of 64
   int rescale;              // 0: the product takes the blocks' m into account
+  int place_bit;            // of weight_place
   const int32_t* tokens;
 };
 
@@ -333,7 +335,7 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a) {
   __syncthreads();
   for (int j = threadIdx.x; j < a.K; j += kNormThreads) {
     const int64_t c = (int64_t)a.tokens[t * a.K + j] - a.n0;
-    if (c >= c0 && c < min(c1, a.cols)) e[weight_place(c)] = (_Float16)0.0f;
+    if (c >= c0 && c < min(c1, a.cols)) e[weight_place(c, a.place_bit)] = (_Float16)0.0f;
   }
 }
 
@@ -341,9 +343,9 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a) {
 // Gradient, per piece: sum_n e[t, n] what[n, d].
 //
 // The product runs over the weights' rows, whose codes lie along d. The words
-// of rows n and n + 4 are put together so that each byte holds one column's
-// codes of both: a conversion of a byte then gives what MFMA wants, one
-// column's values of two n.
+// of two rows (weight_place's neighbours) are put together so that each byte
+// holds one column's codes of both: a conversion of a byte then gives what MFMA
+// wants, one column's values of two n.
 // ---------------------------------------------------------------------------
 struct GradArgs {
   const _Float16* e;
@@ -457,7 +459,8 @@ __global__ __launch_bounds__(64 * kGsWaves) void head_grad_kernel(GradArgs a) {
 //    r, all in the scale block r. Scales likewise, as [block][n].
 //  * Softmax weights: on their way into LDS they are brought to the row's m
 //    from their block's, a second rounding to fp16 where those differ.
-//  * K order: in every 32 rows lane (r, h) supplies [16 h + 8 j, +8) to MFMA j.
+//  * K order: in every 64 rows lane (r, h) supplies [16 h + 4 j, +4) and those
+//    32 further on to MFMA j.
 // All double-buffered in LDS, one barrier per step; a step's loads go out a step
 // before they are written there.
 constexpr int kGwThreads = 512;
@@ -530,9 +533,9 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
   const int o = tid >> 5, c = tid & 31;
   const uint32_t oc = d0 + 16 * c < a.g.D ? (uint32_t)(8 * o * rowc + d0 / 2 + 8 * c) : kMmaOob;
   u32x2_t wv[8];
-  // Scales: rows 2 p and 2 p + 1, blocks 4 b .. 4 b + 3 of the tile's 32.
-  const int p = tid >> 3, b = tid & 7;
-  const uint32_t os = d0 + 64 * b < a.g.D ? (uint32_t)(2 * p * rows + d0 / 16 + 4 * b) : kMmaOob;
+  // Scales: rows pn and pn + 32, blocks 4 b .. 4 b + 3 of the tile's 32.
+  const int p = tid >> 3, b = tid & 7, pn = p + (p & 32);
+  const uint32_t os = d0 + 64 * b < a.g.D ? (uint32_t)(pn * rows + d0 / 16 + 4 * b) : kMmaOob;
   const uint32_t os2 = d0 + 64 * b + 32 < a.g.D ? os + 2 : kMmaOob;
   uint32_t sv[2][2];
   // Softmax weights: row ar, 16-byte pieces aq, aq + 4, aq + 8, aq + 12.
@@ -556,12 +559,19 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
                        er, k + 32 * (i & 1) + 8 * aq < a.g.cols ? oe + 2 * (kGwStep * s + 32 * i) : kMmaOob, 0, 0));
   };
   auto store_x = [&](int buf, int u) {
-    const float f = __builtin_amdgcn_exp2f(mv[u] - ref);  // below fp16's range where a block's m is far lower
+    // In two factors where one would be below fp16's normal numbers.
+    const float by = mv[u] - ref;
+    const _Float16 f = (_Float16)__builtin_amdgcn_exp2f(fmaxf(by, -14.0f)), g = (_Float16)__builtin_amdgcn_exp2f(fminf(by + 14.0f, 0.0f));
+    const bool low = __ballot(by < -14.0f) != 0;
 #pragma unroll
     for (int i = 2 * u; i < 2 * u + 2; ++i) {
       half8_t v = __builtin_bit_cast(half8_t, ev[i]);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = (_Float16)((float)v[q] * f);
+      for (int q = 0; q < 8; ++q) v[q] *= f;
+      if (low) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] *= g;
+      }
       *reinterpret_cast<half8_t*>(&lds.x[buf][grad_x_at(ar, 4 * i + aq)]) = v;
     }
   };
@@ -571,7 +581,7 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
       wv[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(wcr, oc + (uint32_t)((kGwStep * s + i) * rowc), 0, 0));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t at = (uint32_t)((kGwStep * s + i) * rows);
+      const uint32_t at = (uint32_t)((kGwStep * s + 32 * i) * rows);
       if constexpr (S4) sv[i][0] = __builtin_amdgcn_raw_buffer_load_b32(wsr, os + at, 0, 0);
       else {
         sv[i][0] = __builtin_amdgcn_raw_buffer_load_b16(wsr, os + at, 0, 0);
@@ -590,7 +600,7 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
   auto store_s = [&](int buf) {
     const uint32_t s0 = S4 ? sv[0][0] : sv[0][0] | (sv[0][1] << 16), s1 = S4 ? sv[1][0] : sv[1][0] | (sv[1][1] << 16);
     const uint32_t t0 = __builtin_amdgcn_perm(s1, s0, 0x05010400u), t1 = __builtin_amdgcn_perm(s1, s0, 0x07030602u);
-    uint8_t* d = &lds.scales[buf][4 * b * kGwLd + 2 * p];
+    uint8_t* d = &lds.scales[buf][4 * b * kGwLd + 2 * p];  // a row's next to that of the row 32 further on
     *reinterpret_cast<uint16_t*>(d) = (uint16_t)t0;
     *reinterpret_cast<uint16_t*>(d + kGwLd) = (uint16_t)(t0 >> 16);
     *reinterpret_cast<uint16_t*>(d + 2 * kGwLd) = (uint16_t)t1;
@@ -608,32 +618,33 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
   // A step is 8 slices of 16 rows. In a slice the MFMAs of the even columns run
   // while the odd columns' weights of the slice are converted, then the other
   // way round for the next slice; softmax weight fragment i is read right
-  // after its last MFMA of the slice before, a group's codes (32 rows) during
-  // the last slice of the group before. The step's one barrier stands before
+  // after its last MFMA of the slice before, the codes of two slices during the
+  // last slice before them. The step's one barrier stands before
   // its last slice: by then every wavefront has read this buffer to the end and
   // written the next one, whose first fragments the last slice reads.
   half8_t A[RT], w[2];
-  u32x4_t cw, sw;
+  u32x2_t cx, cy;  // codes of two slices, rows n and n + 32
+  u32x4_t sw;
   uint32_t col[2];
   half2_t sc[4];
   auto afrag = [&](int i, int buf, int sl) {
-    return *reinterpret_cast<const half8_t*>(&lds.x[buf][grad_x_at(32 * i + r, 4 * (sl >> 1) + 2 * h + (sl & 1))]);
+    return *reinterpret_cast<const half8_t*>(&lds.x[buf][grad_x_at(32 * i + r, 8 * (sl >> 2) + 4 * h + (sl & 3))]);
   };
-  auto read_codes = [&](int buf, int g) {
-    cw = *reinterpret_cast<const u32x4_t*>(&lds.codes[buf][(wave * 32 + r) * kGwLd + 32 * g + 16 * h]);
-    sw = *reinterpret_cast<const u32x4_t*>(&lds.scales[buf][r * kGwLd + 32 * g + 16 * h]);
+  auto read_codes = [&](int buf, int pair) {
+    const uint8_t* at = &lds.codes[buf][(wave * 32 + r) * kGwLd + 64 * (pair >> 1) + 16 * h + 8 * (pair & 1)];
+    cx = *reinterpret_cast<const u32x2_t*>(at);
+    cy = *reinterpret_cast<const u32x2_t*>(at + 32);
+    sw = *reinterpret_cast<const u32x4_t*>(&lds.scales[buf][r * kGwLd + 64 * (pair >> 1) + 32 * h + 16 * (pair & 1)]);
   };
   auto prepare = [&](auto jc) {  // columns and scales of a slice
     constexpr int j = decltype(jc)::value;
-    const uint32_t x = cw[2 * j], y = cw[2 * j + 1];
-    const uint32_t p01 = __builtin_amdgcn_perm(sw[2 * j + 1], sw[2 * j], 0x05010400u);
-    const uint32_t p23 = __builtin_amdgcn_perm(sw[2 * j + 1], sw[2 * j], 0x07030602u);
+    const uint32_t x = cx[j], y = cy[j];
     col[0] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
     col[1] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
-    sc[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p01, 1.0f, false);
-    sc[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p01, 1.0f, true);
-    sc[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p23, 1.0f, false);
-    sc[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(p23, 1.0f, true);
+    sc[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw[2 * j], 1.0f, false);
+    sc[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw[2 * j], 1.0f, true);
+    sc[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw[2 * j + 1], 1.0f, false);
+    sc[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw[2 * j + 1], 1.0f, true);
   };
   auto convert = [&](auto mc, auto kc) {
     constexpr int m = decltype(mc)::value, k = decltype(kc)::value;
@@ -829,6 +840,7 @@ __global__ __launch_bounds__(kDxThreads) void head_dx_kernel(DxArgs a) {
 // ---------------------------------------------------------------------------
 // Dispatch.
 // ---------------------------------------------------------------------------
+constexpr int64_t kWideItems = 96;  // wide tiles from this many of them on
 constexpr int64_t kMaxRange = (int64_t(1) << 31) - 65536;  // bytes a 32-bit buffer offset reaches
 
 // Everything that follows from the sizes. `wide`: the logits' tiles.
@@ -849,7 +861,7 @@ struct HeadPlan {
 static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   HeadPlan p{};
   const int64_t wide_items = ((T + kEtRows - 1) / kEtRows) * ((N + kEtCols - 1) / kEtCols);
-  p.wide = T > 32 && wide_items >= kMinTileItems;
+  p.wide = T > 32 && wide_items >= kWideItems;
   p.block_shift = p.wide ? 6 : 5;
   int64_t piece = kMaxRange / (D / 2) / 512 * 512;  // a piece's codes lie within a buffer's range
   // A piece's softmax weights take 512 MB at most, but 4096 columns at least.
@@ -869,13 +881,14 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
     p.tiles.row_tiles = (int)((T + kGwRows - 1) / kGwRows);
     p.tiles.col_tiles = (int)((D + kGwCols - 1) / kGwCols);
     p.tiles.full = p.tiles.count() / 256 * 256;
-    const int64_t rest = p.tiles.count() - p.tiles.full, most = std::min(int64_t(16), std::max(int64_t(1), rows / 2048));
-    const double whole = (double)(p.tiles.full / 256);
-    double best = whole + 1.0;
+    // A step of 128 rows takes a workgroup about 3.5 us; each split's sums are written and read once more (5 TB/s).
+    const int64_t rest = p.tiles.count() - p.tiles.full, most = std::min(int64_t(64), std::max(int64_t(1), rows / 512));
+    const double steps = (double)((rows + kGwStep - 1) / kGwStep), sums = (double)T * (double)D * 8e-6 / 5.0;
+    double best = 1e30;
     p.splits = 1;
-    for (int64_t s = 2; rest && s <= most; ++s) {
-      const double rounds = whole + (double)((rest * s + 255) / 256) / (double)s;
-      if (rounds < 0.97 * best) best = rounds, p.splits = s;  // each split's sums are written and read once more
+    for (int64_t s = 1; rest && s <= most; ++s) {
+      const double us = 3.5 * std::ceil(steps / (double)s) * (double)((rest * s + 255) / 256) + sums * (double)s;
+      if (us < best) best = us, p.splits = s;
     }
     p.tiles.splits = (int)p.splits;
   } else {
@@ -983,6 +996,7 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
     n.shrink = shrink; n.ref = ref; n.e = a.soft.e; n.ld_e = p.ld_e;
     n.T = h.T; n.K = h.K; n.n0 = (int)n0; n.cols = a.N; n.tokens = h.tokens;
     n.rescale = !p.wide_grad;
+    n.place_bit = p.wide ? kWidePair : kStreamPair;
     const int segs = !n.rescale ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>((a.N + 2047) / 2048, (1024 + h.T - 1) / h.T));
     n.seg = (int)(((a.N + segs - 1) / segs + 63) / 64 * 64);
     head_norm_kernel<<<dim3(h.T, segs), kNormThreads, 0, stream>>>(n);

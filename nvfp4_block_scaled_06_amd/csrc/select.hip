@@ -15,18 +15,29 @@
 // one row of a thousand at 256 experts and k = 8).
 //
 // A row is one wavefront's, or 16 lanes' with four rows to a wavefront where
-// rows are many: a round of the choice then costs four rows as many
-// instructions as it costs one.
+// rows are many. The choice takes no k rounds over all keys: a bound that k
+// keys reach (the k-th largest of the lanes' maxima) leaves a few survivors,
+// which are put together in LDS and ranked against each other. Rows where too
+// many survive (equal logits, for example) take the rounds, as those that 32
+// bits cannot decide do.
 #include "../../include/nvfp4_router.h"
-#include <type_traits>
+#include <algorithm>
 
 #include "experts_common.hpp"
+#include "route16.hpp"
 
 namespace nvr {
 
 constexpr int kSelWaves = 4;
 constexpr int kSelThreads = 64 * kSelWaves;
-constexpr float kKeyErr = 4e-6f;  // of keys up to 1; fp32 rounding of larger ones (a large bias) scales it
+// How far apart two keys computed in 32 bits have to be for their order to
+// hold, times the larger one where that is above 1. sigmoid_fast is off by
+// s (1 - s) (|l| 2^-24 + 2^-23) for the exponential and s (2^-24 + 2^-23) for
+// the sum and the reciprocal, 2.3e-7 at most, and the bias adds 2^-24: 6e-7
+// for two keys. A softmax's sum over 512 experts (32 terms in a lane, then 4
+// to 6 steps) may be off by 38 2^-24 = 2.3e-6 for all its keys alike, each
+// exponential by 0.37 2^-23 + 2^-23 of one, the quotient by 2^-23: 3.1e-6.
+constexpr float kKeyErrSigmoid = 1e-6f, kKeyErrSoftmax = 5e-6f;
 
 struct SelectArgs {
   const void* logits;
@@ -35,7 +46,7 @@ struct SelectArgs {
   int bf16, T, E, k;
   int groups, size, kept, top, sh;  // sh: log2 of the lanes per group
   uint32_t inv;                     // 2^20 / size rounded up: e / size = e inv >> 20 for e < 512
-  int softmax, renorm, by_logit;
+  int softmax, renorm, by_logit, vec;
   float scale;
   int lds_row;  // bytes of LDS per row
   int32_t* idx;
@@ -50,32 +61,12 @@ __device__ __forceinline__ float sel_logit(const void* p, int bf16, int64_t i) {
   return l == l ? l : -__builtin_inff();  // NaN: masked
 }
 
-// Keys: unsigned integers in the order of their values; 0 for experts that cannot be chosen.
-__device__ __forceinline__ uint32_t order_key(float v) { return score_key(v); }
-__device__ __forceinline__ uint64_t order_key(double v) {
-  const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
-  return (u >> 63) ? ~u : (u | (1ull << 63));
-}
+// The value of a score_key.
 __device__ __forceinline__ float key_back(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
 // Reductions over a row's lanes, in a fixed order.
-template <int LPR>
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-  if constexpr (LPR == 64) return wave_max_u32(v);
-  else return group_max_u32<16>(v);
-}
-template <int LPR>
-__device__ __forceinline__ uint64_t row_max(uint64_t v) {
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) {
-    const uint32_t lo = (uint32_t)__shfl_xor((int)(uint32_t)v, o), hi = (uint32_t)__shfl_xor((int)(uint32_t)(v >> 32), o);
-    const uint64_t u = ((uint64_t)hi << 32) | lo;
-    v = u > v ? u : v;
-  }
-  return v;
-}
 template <int LPR>
 __device__ __forceinline__ uint32_t row_min(uint32_t v) {
   if constexpr (LPR == 64) return wave_min_u32(v);
@@ -83,18 +74,30 @@ __device__ __forceinline__ uint32_t row_min(uint32_t v) {
 }
 template <int LPR, class F>
 __device__ __forceinline__ F row_fmax(F v) {
+  if constexpr (sizeof(F) == 4) {
+    if constexpr (LPR == 64) return wave_max(v);
+    v = fmaxf(v, __int_as_float(dpp_i<kDppXor1>(__float_as_int(v))));
+    v = fmaxf(v, __int_as_float(dpp_i<kDppXor2>(__float_as_int(v))));
+    v = fmaxf(v, __int_as_float(dpp_i<kDppHalfMirror>(__float_as_int(v))));
+    return fmaxf(v, __int_as_float(dpp_i<kDppMirror>(__float_as_int(v))));
+  } else {
 #pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) {
-    const F u = __shfl_xor(v, o);
-    v = u > v ? u : v;
+    for (int o = LPR / 2; o > 0; o >>= 1) {
+      const F u = __shfl_xor(v, o);
+      v = u > v ? u : v;
+    }
+    return v;
   }
-  return v;
 }
 template <int LPR, class F>
-__device__ __forceinline__ F row_sum(F v) {
+__device__ __forceinline__ F row_total(F v) {
+  if constexpr (sizeof(F) == 4) {
+    return LPR == 64 ? wave_sum(v) : row_sum(v);
+  } else {
 #pragma unroll
-  for (int o = 1; o < LPR; o <<= 1) v += __shfl_xor(v, o);
-  return v;
+    for (int o = 1; o < LPR; o <<= 1) v += __shfl_xor(v, o);
+    return v;
+  }
 }
 
 __device__ __forceinline__ void sel_fence() {
@@ -103,123 +106,330 @@ __device__ __forceinline__ void sel_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The choice with keys of type F; lane j < k of the row gets the j-th expert,
-// -1 where none is left. True (for the whole row) where the order is closer
-// than the keys' error.
-template <int LPR, int PER, class F>
-__device__ __forceinline__ bool sel_choose(const SelectArgs& a, const float (&l)[PER], float top, char* row_lds,
-                                           int& chosen) {
-  typedef typename std::conditional<sizeof(F) == 4, uint32_t, uint64_t>::type key_t;
-  constexpr bool kWide = sizeof(F) == 8;
+// Expert of a lane's j-th logit: neighbours 4 by 4 for 16-byte loads, or lane by lane.
+template <int LPR, bool VEC>
+__device__ __forceinline__ int sel_expert(int li, int j) {
+  return VEC ? 4 * LPR * (j >> 2) + 4 * li + (j & 3) : LPR * j + li;
+}
+
+// Place of a 32-bit key in LDS: 4 words of padding after every 16, so that the
+// lanes of a row, each on a run of its own, read different banks.
+template <class F>
+__device__ __forceinline__ int sel_place(int e) {
+  return sizeof(F) == 4 ? e + ((e >> 4) << 2) : e;
+}
+
+// Groups that stay, from the row's keys in LDS: bit g << sh. `unsure`: the
+// border is closer than 2 err (a score is a sum of two keys).
+template <int LPR, class F>
+__device__ __forceinline__ uint64_t sel_groups(const SelectArgs& a, const F* vals, float err, bool& unsure) {
   const F ninf = -(F)__builtin_inff();
-  const int lane = threadIdx.x & 63, li = lane & (LPR - 1);
-  const bool exact = kWide || a.by_logit;
-  bool unsure = false;
-  F v[PER];
-  if (a.by_logit) {
-#pragma unroll
-    for (int j = 0; j < PER; ++j) v[j] = (F)l[j];
-  } else {
-    if (a.softmax) {
-      F sum = 0;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        if constexpr (kWide) v[j] = exp((double)l[j] - (double)top);
-        else v[j] = exp_fast(l[j] - top);
-        sum += v[j];
-      }
-      sum = row_sum<LPR>(sum);
-#pragma unroll
-      for (int j = 0; j < PER; ++j) v[j] /= sum;
-    } else {
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        if constexpr (kWide) v[j] = 1.0 / (1.0 + exp(-(double)l[j]));
-        else v[j] = sigmoid_fast(l[j]);
-      }
-    }
-    if (a.bias) {
-#pragma unroll
-      for (int j = 0; j < PER; ++j) v[j] += (F)a.bias[min(LPR * j + li, a.E - 1)];
+  const int lane = threadIdx.x & 63, li = lane & (LPR - 1), row = lane & ~(LPR - 1);
+  const int g = li >> a.sh, lpg = 1 << a.sh, run = (a.size + lpg - 1) >> a.sh, sub = li & (lpg - 1);
+  F b1 = ninf, b2 = ninf;
+  if (g < a.groups) {
+    const int end = min((sub + 1) * run, a.size);
+#pragma unroll 8
+    for (int i = sub * run; i < end; ++i) {
+      const F x = vals[sel_place<F>(g * a.size + i)];
+      const F lo = x < b1 ? x : b1;
+      b2 = lo > b2 ? lo : b2;
+      b1 = x > b1 ? x : b1;
     }
   }
-  key_t key[PER];
+  for (int o = 1; o < lpg; o <<= 1) {
+    const F o1 = __shfl_xor(b1, o), o2 = __shfl_xor(b2, o);
+    const F lo = o1 < b1 ? o1 : b1, hi2 = o2 > b2 ? o2 : b2;
+    b2 = lo > hi2 ? lo : hi2;
+    b1 = o1 > b1 ? o1 : b1;
+  }
+  F score = a.top == 2 && a.size > 1 ? b1 + b2 : b1;
+  if (!(score == score) || g >= a.groups) score = ninf;
+  int rank = 0;
+  for (int j = 0; j < a.groups; ++j) {
+    const F s = __shfl(score, row + (j << a.sh));
+    rank += s > score || (s == score && j < g) ? 1 : 0;
+  }
+  const bool keep = g < a.groups && rank < a.kept;
+  if (err > 0.0f) {
+    const F lowest = -row_fmax<LPR, F>(keep ? -score : ninf);
+    const F next = row_fmax<LPR, F>(!keep && g < a.groups ? score : ninf);
+    if (lowest > ninf && lowest - next <= (F)(2.0f * err) * (F)fmaxf(1.0f, fabsf((float)lowest))) unsure = true;
+  }
+  return __ballot(keep) >> row;
+}
+
+__device__ __forceinline__ bool sel_kept(const SelectArgs& a, uint64_t kept, uint32_t e) {
+  const uint32_t g = min((e * a.inv) >> 20, (uint32_t)a.groups - 1u);
+  return (kept >> (g << a.sh)) & 1ull;
+}
+
+// The choice by k rounds over the row's keys in LDS, which it uses up.
+template <int LPR, class F>
+__device__ __forceinline__ void sel_rounds(const SelectArgs& a, F* vals, int& chosen) {
+  const F ninf = -(F)__builtin_inff();
+  const int li = threadIdx.x & (LPR - 1);
+  chosen = -1;
+  for (int r = 0; r < a.k; ++r) {
+    F m = ninf;
+    uint32_t e = 0xFFFFFFFFu;
+#pragma unroll 4
+    for (int i = li; i < a.E; i += LPR) {
+      const F v = vals[sel_place<F>(i)];
+      if (v > m) {
+        m = v;
+        e = (uint32_t)i;
+      }
+    }
+    const F best = row_fmax<LPR, F>(m);
+    const uint32_t at = row_min<LPR>(m == best ? e : 0xFFFFFFFFu);
+    if (at == e && at != 0xFFFFFFFFu) vals[sel_place<F>((int)at)] = ninf;
+    if (li == r) chosen = (int)at;
+    sel_fence();
+  }
+}
+
+// Survivors that a row may have: two for each of 16 lanes, one for each of 64.
+template <int LPR>
+constexpr int sel_most() {
+  return LPR == 16 ? 32 : 64;
+}
+template <int LPR>
+struct SelScratch {
+  uint64_t cand[sel_most<LPR>() + 1];  // key << 32 | ~expert; the last one takes what does not survive
+  uint32_t key[sel_most<LPR>()];       // in order
+  int expert[sel_most<LPR>()];
+  double wide[sel_most<LPR>()];  // the survivors' keys in 64 bits, if 32 do not decide
+};
+enum : int { kSelDecided = 0, kSelOrder = 1, kSelAll = 2 };  // what 64 bits have to look at: nothing, the survivors, all keys
+
+// Expert e's key in 64 bits; `top` and `total` of the row's softmax.
+__device__ __forceinline__ double sel_wide(const SelectArgs& a, float logit, int e, double top, double total) {
+  const double x = (double)logit;
+  double d = exp(a.softmax ? x - top : -x);
+  d = a.softmax ? d / total : 1.0 / (1.0 + d);
+  if (a.bias) d += (double)a.bias[e];
+  return x > -(double)__builtin_inff() && d > -(double)__builtin_inff() ? d : -(double)__builtin_inff();
+}
+
+// The choice in 32 bits; lane j < k of the row gets the j-th expert, -1 where
+// none is left.
+template <int LPR, int PER, bool VEC>
+__device__ __forceinline__ int sel_survivors(const SelectArgs& a, const float (&v)[PER], char* row_lds, float err,
+                                             int& count, int& chosen) {
+  constexpr int MOST = sel_most<LPR>(), H = MOST / LPR;
+  SelScratch<LPR>& sc = *reinterpret_cast<SelScratch<LPR>*>(row_lds);
+  const int li = threadIdx.x & (LPR - 1);
+  uint32_t key[PER], lm = 0u;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    const bool alive = LPR * j + li < a.E && l[j] > -__builtin_inff() && v[j] > ninf;
-    if (!alive) v[j] = ninf;
-    key[j] = alive ? order_key(v[j]) : key_t(0);
+    key[j] = v[j] > -__builtin_inff() ? score_key(v[j]) : 0u;
+    lm = max(lm, key[j]);
   }
-
-  if (a.kept < a.groups) {
-    F* vals = reinterpret_cast<F*>(row_lds);
-    sel_fence();
+  // A bound that at least k keys reach.
+  uint32_t tau;
+  if constexpr (LPR == 16) {
+    const int above = count_above<1>(lm, 0);
+    tau = row_min_u32(above < a.k ? lm : 0xFFFFFFFFu);
+  } else {
+    tau = a.k <= 4    ? wave_min_of_groups<16>(group_max_u32<16>(lm))
+          : a.k <= 8  ? wave_min_of_groups<8>(group_max_u32<8>(lm))
+          : a.k <= 16 ? wave_min_of_groups<4>(group_max_u32<4>(lm))
+                      : wave_min_of_groups<2>(group_max_u32<2>(lm));
+  }
+  if (err > 0.0f && tau != 0u) {  // and all that may be the k-th
+    const float t = key_back(tau);
+    tau = score_key(t - err * fmaxf(1.0f, fabsf(t)));
+  }
+  tau = max(tau, 1u);
+  int C = 0;
+  if constexpr (LPR == 16) {
+    int cnt = 0;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) vals[LPR * j + li] = v[j];
-    sel_fence();
-    const int g = li >> a.sh, lpg = 1 << a.sh;
-    F b1 = ninf, b2 = ninf;
-    if (g < a.groups) {
-      for (int i = li & (lpg - 1); i < a.size; i += lpg) {
-        const F x = vals[g * a.size + i];
-        const F lo = x < b1 ? x : b1;
-        b2 = lo > b2 ? lo : b2;
-        b1 = x > b1 ? x : b1;
-      }
-    }
-    for (int o = 1; o < lpg; o <<= 1) {
-      const F o1 = __shfl_xor(b1, o), o2 = __shfl_xor(b2, o);
-      const F lo = o1 < b1 ? o1 : b1, hi2 = o2 > b2 ? o2 : b2;
-      b2 = lo > hi2 ? lo : hi2;
-      b1 = o1 > b1 ? o1 : b1;
-    }
-    F score = a.top == 2 && a.size > 1 ? b1 + b2 : b1;
-    if (!(score == score) || g >= a.groups) score = ninf;
-    int rank = 0;
-    for (int j = 0; j < a.groups; ++j) {
-      const F s = __shfl(score, (lane & ~(LPR - 1)) + (j << a.sh));
-      rank += s > score || (s == score && j < g) ? 1 : 0;
-    }
-    const bool keep = g < a.groups && rank < a.kept;
-    const uint64_t kept = __ballot(keep) >> (lane & ~(LPR - 1));
-    if (!exact) {
-      const F lowest = -row_fmax<LPR, F>(keep ? -score : ninf);
-      const F next = row_fmax<LPR, F>(!keep && g < a.groups ? score : ninf);
-      if (lowest > ninf && lowest - next <= (F)(2.0f * kKeyErr) * fmaxf(1.0f, fabsf((float)lowest))) unsure = true;
-    }
+    for (int j = 0; j < PER; ++j) cnt += key[j] >= tau ? 1 : 0;
+    int pos = row_scan(cnt) - cnt;
+    C = row_sum_i(cnt);
+    if (__ballot(C > MOST)) return kSelAll;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      const uint32_t e = LPR * j + li;
-      const uint32_t ge = min((uint32_t)((e * a.inv) >> 20), (uint32_t)a.groups - 1u);
-      if (!((kept >> (ge << a.sh)) & 1ull)) key[j] = key_t(0);
+      const bool in = key[j] >= tau;
+      sc.cand[in ? pos : MOST] = ((uint64_t)key[j] << 32) | ~(uint32_t)sel_expert<LPR, VEC>(li, j);
+      pos += in ? 1 : 0;
+    }
+  } else {
+    int n[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const uint64_t bal = __ballot(key[j] >= tau);
+      n[j] = C + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(bal >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)bal, 0u));
+      C += (int)__popcll(bal);
+    }
+    if (C > MOST) return kSelAll;
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      sc.cand[key[j] >= tau ? n[j] : MOST] =
+          ((uint64_t)key[j] << 32) | ~(uint32_t)sel_expert<LPR, VEC>(li, j);
+  }
+  // Entries past the count rank below all others.
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    if (li + LPR * h >= C) sc.cand[li + LPR * h] = 0ull;
+  sel_fence();
+  uint64_t mine[H];
+  int rank[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    mine[h] = sc.cand[li + LPR * h];
+    rank[h] = 0;
+  }
+#pragma unroll
+  for (int u0 = 0; u0 < MOST; u0 += 16) {
+    if (u0 && !__ballot(C > u0)) break;
+#pragma unroll
+    for (int u = u0; u < u0 + 16; ++u) {
+      const uint64_t other = sc.cand[u];
+#pragma unroll
+      for (int h = 0; h < H; ++h) rank[h] += other > mine[h] ? 1 : 0;
     }
   }
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    if (li + LPR * h < C) {
+      sc.key[rank[h]] = (uint32_t)(mine[h] >> 32);
+      sc.expert[rank[h]] = (int)~(uint32_t)mine[h];
+    }
+  }
+  sel_fence();
+  chosen = li < a.k && li < C ? sc.expert[li] : -1;
+  count = C;
+  if (err > 0.0f && li < a.k && li + 1 < C) {
+    const float p = key_back(sc.key[li]);
+    if (p - key_back(sc.key[li + 1]) <= err * fmaxf(1.0f, fabsf(p))) return kSelOrder;
+  }
+  return kSelDecided;
+}
 
-  chosen = -1;
-  key_t before = 0;
-  for (int r = 0; r <= a.k; ++r) {
-    key_t m = key[0];
+// The survivors in the order of their 64-bit keys. The bound left out nothing
+// that may be among the k largest.
+template <int LPR>
+__device__ __forceinline__ void sel_order(const SelectArgs& a, int64_t base, double top, double total, char* row_lds,
+                                          int C, int& chosen) {
+  constexpr int MOST = sel_most<LPR>(), H = MOST / LPR;
+  SelScratch<LPR>& sc = *reinterpret_cast<SelScratch<LPR>*>(row_lds);
+  const int li = threadIdx.x & (LPR - 1);
+  double mine[H];
+  int e[H], rank[H];
 #pragma unroll
-    for (int j = 1; j < PER; ++j) m = key[j] > m ? key[j] : m;
-    const key_t best = row_max<LPR>(m);
-    if constexpr (!kWide) {
-      if (!exact && r > 0 && best != 0u) {
-        const float p = key_back(before);
-        if (p - key_back(best) <= kKeyErr * fmaxf(1.0f, fabsf(p))) unsure = true;
-      }
-    }
-    if (r == a.k) break;
-    before = best;
-    // The lowest expert with that key.
-    uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-    for (int j = PER - 1; j >= 0; --j) at = key[j] == best ? (uint32_t)(LPR * j + li) : at;
-    at = best ? row_min<LPR>(at) : 0xFFFFFFFFu;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) key[j] = (uint32_t)(LPR * j + li) == at ? key_t(0) : key[j];
-    if (li == r) chosen = (int)at;
+  for (int h = 0; h < H; ++h) {
+    const int u = li + LPR * h;
+    e[h] = u < C ? (int)~(uint32_t)sc.cand[u] : 0;
+    mine[h] = sel_wide(a, sel_logit(a.logits, a.bf16, base + e[h]), e[h], top, total);
+    rank[h] = 0;
+    sc.wide[u] = mine[h];
   }
-  return unsure;
+  sel_fence();
+#pragma unroll 4
+  for (int u = 0; u < C; ++u) {
+    const double other = sc.wide[u];
+    const int at = (int)~(uint32_t)sc.cand[u];
+#pragma unroll
+    for (int h = 0; h < H; ++h) rank[h] += other > mine[h] || (other == mine[h] && at < e[h]) ? 1 : 0;
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+    if (li + LPR * h < C) sc.expert[rank[h]] = e[h];
+  sel_fence();
+  chosen = li < a.k && li < C ? sc.expert[li] : -1;
+}
+
+// The choice of the wavefront's rows, this lane's row starting at logit `base`;
+// bias in `bv`.
+template <int LPR, int PER, bool VEC>
+__device__ __forceinline__ void sel_choose(const SelectArgs& a, const float (&l)[PER], const float (&bv)[PER], float top,
+                                           float sum, int64_t base, bool live, char* row_lds, int& chosen) {
+  const float ninf = -__builtin_inff();
+  const int li = threadIdx.x & (LPR - 1);
+  const float err = a.by_logit ? 0.0f : a.softmax ? kKeyErrSoftmax : kKeyErrSigmoid;
+  const bool grouped = a.kept < a.groups;
+  float v[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) v[j] = l[j];
+  if (!a.by_logit) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      v[j] = (a.softmax ? exp_fast(l[j] - top) / sum : sigmoid_fast(l[j])) + bv[j];
+      if (!(l[j] > ninf) || !(v[j] > ninf)) v[j] = ninf;  // and those past E, whose logits are -inf
+    }
+  }
+  float* vals = reinterpret_cast<float*>(row_lds);
+  double* wide = reinterpret_cast<double*>(row_lds);
+  double total = 0.0;  // of the row's softmax, in 64 bits
+  // All keys in 64 bits into `wide`. The logits pass through the upper half of
+  // the same LDS: key i overwrites the logits 2 i - PER LPR and the next,
+  // which this or an earlier turn of the loop has read.
+  auto widen = [&]() {
+    constexpr int ALL = PER * LPR;
+    sel_fence();
+#pragma unroll
+    for (int j = 0; j < PER; ++j) vals[ALL + sel_expert<LPR, VEC>(li, j)] = l[j];
+    sel_fence();
+    if (a.softmax && total == 0.0) {
+#pragma unroll 2
+      for (int i = li; i < a.E; i += LPR) total += exp((double)vals[ALL + i] - (double)top);
+      total = row_total<LPR>(total);
+    }
+    for (int i = li; i < a.E; i += LPR) {
+      const double d = sel_wide(a, vals[ALL + i], i, (double)top, total);
+      sel_fence();
+      wide[i] = d;
+      sel_fence();
+    }
+  };
+  uint64_t kept = ~0ull;
+  if (grouped) {
+    bool border = false;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) vals[sel_place<float>(sel_expert<LPR, VEC>(li, j))] = v[j];
+    sel_fence();
+    kept = sel_groups<LPR, float>(a, vals, err, border);
+    if (__ballot(border && live)) {
+      widen();
+      kept = sel_groups<LPR, double>(a, wide, 0.0f, border);
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (!sel_kept(a, kept, sel_expert<LPR, VEC>(li, j))) v[j] = ninf;
+    sel_fence();
+  }
+  int C = 0;
+  const int state = sel_survivors<LPR, PER, VEC>(a, v, row_lds, err, C, chosen);
+  const bool all = __ballot(live && state == kSelAll) != 0;
+  if (!all && !__ballot(live && state == kSelOrder)) return;
+  if (a.by_logit) {  // exact as it is: too many survivors
+    sel_fence();
+#pragma unroll
+    for (int j = 0; j < PER; ++j) vals[sel_place<float>(sel_expert<LPR, VEC>(li, j))] = v[j];
+    sel_fence();
+    sel_rounds<LPR, float>(a, vals, chosen);
+    return;
+  }
+  if (!all) {
+    sel_fence();
+    if (a.softmax && total == 0.0) {
+#pragma unroll 2
+      for (int i = li; i < a.E; i += LPR) total += exp((double)sel_logit(a.logits, a.bf16, base + i) - (double)top);
+      total = row_total<LPR>(total);
+    }
+    sel_order<LPR>(a, base, (double)top, total, row_lds, C, chosen);
+    return;
+  }
+  widen();
+  if (grouped) {
+    for (int i = li; i < a.E; i += LPR)
+      if (!sel_kept(a, kept, (uint32_t)i)) wide[i] = -(double)__builtin_inff();
+    sel_fence();
+  }
+  sel_rounds<LPR, double>(a, wide, chosen);
 }
 
 // s of a logit, up to a factor common to the row that makes the largest of the
@@ -229,7 +439,7 @@ __device__ __forceinline__ float sel_score(float l, float m, bool softmax) {
   return softmax ? expf(l - m) : expf(fminf(l, 0.0f) - m) / (1.0f + expf(-fabsf(l)));
 }
 
-template <int LPR, int PER>
+template <int LPR, int PER, bool VEC>
 __global__ __launch_bounds__(kSelThreads) void select_kernel(SelectArgs a) {
   extern __shared__ __attribute__((aligned(16))) char sel_lds[];
   constexpr int ROWS = 64 / LPR;
@@ -237,15 +447,44 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(SelectArgs a) {
   const int in_wg = wave * ROWS + lane / LPR;
   const int64_t row = (int64_t)blockIdx.x * (kSelWaves * ROWS) + in_wg;
   const bool live = row < a.T;
+  if (!__ballot(live)) return;
   const int64_t base = (live ? row : a.T - 1) * a.ld;
   char* row_lds = sel_lds + in_wg * a.lds_row;
+  const float ninf = -__builtin_inff();
   float l[PER];
+  if constexpr (VEC) {
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int e = LPR * j + li;
-    l[j] = sel_logit(a.logits, a.bf16, base + min(e, a.E - 1));
-    if (e >= a.E) l[j] = -__builtin_inff();
+    for (int q = 0; q < PER / 4; ++q) {
+      const int e = sel_expert<LPR, VEC>(li, 4 * q);
+      if (e + 4 <= a.E) {
+        if (a.bf16) {
+          const u32x2_t u = *reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(a.logits) + base + e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l[4 * q + i] = i & 1 ? bf16_hi(u[i >> 1]) : bf16_lo(u[i >> 1]);
+        } else {
+          const f32x4_t u = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(a.logits) + base + e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l[4 * q + i] = u[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[4 * q + i] = e + i < a.E ? sel_logit(a.logits, a.bf16, base + e + i) : ninf;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) l[j] = l[j] == l[j] ? l[j] : ninf;
+  } else {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int e = LPR * j + li;
+      l[j] = sel_logit(a.logits, a.bf16, base + min(e, a.E - 1));
+      if (e >= a.E) l[j] = ninf;
+    }
   }
+  float bv[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) bv[j] = a.bias ? a.bias[min(sel_expert<LPR, VEC>(li, j), a.E - 1)] : 0.0f;
   float top = 0.0f, sum = 1.0f;  // softmax over the whole row, where that is needed
   if (a.softmax && !(a.by_logit && a.renorm)) {
     top = l[0];
@@ -255,25 +494,17 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(SelectArgs a) {
     sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < PER; ++j) sum += exp_fast(l[j] - top);
-    sum = row_sum<LPR>(sum);
+    sum = row_total<LPR>(sum);
   }
   int chosen;
-  const bool unsure = sel_choose<LPR, PER, float>(a, l, top, row_lds, chosen);
-  if (__ballot(unsure && live)) sel_choose<LPR, PER, double>(a, l, top, row_lds, chosen);
-
-  // The chosen ones' logits, through LDS.
-  float* ll = reinterpret_cast<float*>(row_lds);
-  sel_fence();
-#pragma unroll
-  for (int j = 0; j < PER; ++j) ll[LPR * j + li] = l[j];
-  sel_fence();
+  sel_choose<LPR, PER, VEC>(a, l, bv, top, sum, base, live, row_lds, chosen);
   const bool mine = chosen >= 0;
-  const float cl = mine ? ll[chosen] : -__builtin_inff();
+  const float cl = mine ? sel_logit(a.logits, a.bf16, base + chosen) : ninf;
   float m = a.softmax ? top : 0.0f;
   if (a.renorm) m = row_fmax<LPR, float>(a.softmax ? cl : fminf(cl, 0.0f));
   const float s = mine ? sel_score(cl, m, a.softmax) : 0.0f;
   float total = sum;  // 1 for plain sigmoid scores
-  if (a.renorm) total = row_sum<LPR>(s);
+  if (a.renorm) total = row_total<LPR>(s);
   if (live && li < a.k) {
     a.idx[row * a.k + li] = chosen;
     a.w[row * a.k + li] = mine ? a.scale * (s / total) : 0.0f;
@@ -338,7 +569,7 @@ __global__ __launch_bounds__(kSelThreads) void select_grad_kernel(SelectGradArgs
       l[j] = exp_fast(l[j] - top);
       sum += l[j];
     }
-    sum = row_sum<LPR>(sum);
+    sum = row_total<LPR>(sum);
     if (!(sum > 0.0f) && sum == sum) sum = 1.0f;
   }
   float m = a.softmax ? top : 0.0f;
@@ -348,10 +579,10 @@ __global__ __launch_bounds__(kSelThreads) void select_grad_kernel(SelectGradArgs
   }
   const float s = e >= 0 ? sel_score(cl, m, a.softmax) : 0.0f;
   float total = sum;
-  if (a.renorm) total = row_sum<LPR>(s);
+  if (a.renorm) total = row_total<LPR>(s);
   const float u = s > 0.0f || s != s ? s / total : 0.0f;
   float dot = 0.0f;
-  if (a.softmax || a.renorm) dot = row_sum<LPR>(u * gw);
+  if (a.softmax || a.renorm) dot = row_total<LPR>(u * gw);
   float mine = a.scale * u * (dense ? gw : a.renorm ? gw - dot : gw);
   if (!a.softmax) mine *= e >= 0 ? sel_score(-cl, 0.0f, false) : 0.0f;
 
@@ -384,34 +615,52 @@ __global__ __launch_bounds__(kSelThreads) void select_grad_kernel(SelectGradArgs
 // 16 lanes to a row from this many rows on, where a row's places and groups
 // fit into 16 lanes.
 constexpr int64_t kSelManyRows = 1024;
+static bool select_many(int64_t T, int64_t k, int64_t groups) { return T >= kSelManyRows && k <= 16 && groups <= 16; }
 
-template <int LPR, int PER, class A>
-static hipError_t launch_select_t(A& a, hipStream_t stream, bool values64) {
+template <int LPR, int PER, bool VEC>
+static hipError_t launch_select_t(SelectArgs a, hipStream_t stream) {
   constexpr int ROWS = kSelWaves * (64 / LPR);
-  a.lds_row = PER * LPR * (values64 ? 8 : 4);
+  a.lds_row = std::max(PER * LPR * (a.by_logit ? 5 : 8), (int)(sizeof(SelScratch<LPR>) + 15) / 16 * 16);
   const int grid = (int)((a.T + (int64_t)ROWS - 1) / ROWS);
-  if constexpr (std::is_same<A, SelectArgs>::value)
-    select_kernel<LPR, PER><<<grid, kSelThreads, (size_t)ROWS * a.lds_row, stream>>>(a);
-  else
-    select_grad_kernel<LPR, PER><<<grid, kSelThreads, (size_t)ROWS * a.lds_row, stream>>>(a);
+  select_kernel<LPR, PER, VEC><<<grid, kSelThreads, (size_t)ROWS * a.lds_row, stream>>>(a);
   return hipGetLastError();
 }
 
-template <class A>
-static hipError_t launch_select(A a, int groups, hipStream_t stream) {
-  const bool values64 = groups > 1;
-  if (a.T >= kSelManyRows && a.k <= 16 && groups <= 16) {
-    if (a.E <= 64) return launch_select_t<16, 4>(a, stream, values64);
-    if (a.E <= 128) return launch_select_t<16, 8>(a, stream, values64);
-    if (a.E <= 256) return launch_select_t<16, 16>(a, stream, values64);
-    if (a.E <= 384) return launch_select_t<16, 24>(a, stream, values64);
-    return launch_select_t<16, 32>(a, stream, values64);
+// 16-byte loads where they give each of 16 lanes some experts; a wavefront's
+// loads of neighbours are whole lines anyway.
+static hipError_t launch_select(const SelectArgs& a, hipStream_t stream) {
+  if (select_many(a.T, a.k, a.groups)) {
+    if (a.E <= 64) return launch_select_t<16, 4, false>(a, stream);
+    if (a.E <= 128) return a.vec ? launch_select_t<16, 8, true>(a, stream) : launch_select_t<16, 8, false>(a, stream);
+    if (a.E <= 256) return a.vec ? launch_select_t<16, 16, true>(a, stream) : launch_select_t<16, 16, false>(a, stream);
+    if (a.E <= 384) return a.vec ? launch_select_t<16, 24, true>(a, stream) : launch_select_t<16, 24, false>(a, stream);
+    return a.vec ? launch_select_t<16, 32, true>(a, stream) : launch_select_t<16, 32, false>(a, stream);
   }
-  if (a.E <= 64) return launch_select_t<64, 1>(a, stream, values64);
-  if (a.E <= 128) return launch_select_t<64, 2>(a, stream, values64);
-  if (a.E <= 256) return launch_select_t<64, 4>(a, stream, values64);
-  if (a.E <= 384) return launch_select_t<64, 6>(a, stream, values64);
-  return launch_select_t<64, 8>(a, stream, values64);
+  if (a.E <= 64) return launch_select_t<64, 1, false>(a, stream);
+  if (a.E <= 128) return launch_select_t<64, 2, false>(a, stream);
+  if (a.E <= 256) return launch_select_t<64, 4, false>(a, stream);
+  return launch_select_t<64, 8, false>(a, stream);
+}
+
+template <int LPR, int PER>
+static hipError_t launch_select_grad_t(SelectGradArgs a, hipStream_t stream) {
+  constexpr int ROWS = kSelWaves * (64 / LPR);
+  a.lds_row = PER * LPR * 4;
+  const int grid = (int)((a.T + (int64_t)ROWS - 1) / ROWS);
+  select_grad_kernel<LPR, PER><<<grid, kSelThreads, (size_t)ROWS * a.lds_row, stream>>>(a);
+  return hipGetLastError();
+}
+
+static hipError_t launch_select_grad(const SelectGradArgs& a, hipStream_t stream) {
+  if (select_many(a.T, a.k, 1)) {
+    if (a.E <= 64) return launch_select_grad_t<16, 4>(a, stream);
+    if (a.E <= 128) return launch_select_grad_t<16, 8>(a, stream);
+    if (a.E <= 256) return launch_select_grad_t<16, 16>(a, stream);
+    return launch_select_grad_t<16, 32>(a, stream);
+  }
+  if (a.E <= 128) return launch_select_grad_t<64, 2>(a, stream);
+  if (a.E <= 256) return launch_select_grad_t<64, 4>(a, stream);
+  return launch_select_grad_t<64, 8>(a, stream);
 }
 
 }  // namespace nvr
@@ -453,14 +702,16 @@ int router_select(const void* logits, int dtype, int64_t T, int64_t E, int64_t l
   a.logits = logits; a.ld = ld; a.bias = bias; a.bf16 = dtype == ROUTER_BF16;
   a.T = (int)T; a.E = (int)E; a.k = (int)k;
   a.groups = (int)groups; a.size = (int)(E / groups); a.kept = (int)topk_groups; a.top = (int)group_top;
-  const int lanes = T >= nvr::kSelManyRows && k <= 16 && groups <= 16 ? 16 : 64;
+  const int lanes = nvr::select_many(T, k, groups) ? 16 : 64;
   while ((2 << a.sh) * groups <= lanes) ++a.sh;
   a.inv = (uint32_t)(((1u << 20) + a.size - 1) / a.size);
   a.softmax = scoring == ROUTER_SOFTMAX; a.renorm = renormalize != 0;
   a.by_logit = !bias && (groups == 1 || group_top == 1);
+  const size_t piece = dtype == ROUTER_F32 ? 16 : 8;  // four logits
+  a.vec = aligned(logits, piece) && (size_t)ld * piece / 4 % piece == 0;
   a.scale = routed_scale;
   a.idx = topk_idx; a.w = topk_w;
-  const hipError_t e = nvr::launch_select(a, (int)groups, static_cast<hipStream_t>(stream));
+  const hipError_t e = nvr::launch_select(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ROUTER_OK : ROUTER_EHIP;
 }
 
@@ -481,7 +732,7 @@ int router_select_backward(const void* logits, int dtype, int64_t T, int64_t E, 
   a.T = (int)T; a.E = (int)E; a.k = (int)k;
   a.softmax = scoring == ROUTER_SOFTMAX; a.renorm = renormalize != 0; a.scale = routed_scale;
   a.out = grad_logits; a.ld_out = ld_grad;
-  const hipError_t e = nvr::launch_select(a, 1, static_cast<hipStream_t>(stream));
+  const hipError_t e = nvr::launch_select_grad(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? ROUTER_OK : ROUTER_EHIP;
 }
 

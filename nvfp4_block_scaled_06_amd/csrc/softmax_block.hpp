@@ -25,10 +25,15 @@ struct SoftmaxOut {
 
 constexpr float kWeightOne = 32768.0f;  // a weight of 1 in fp16
 
-// Where the weight of column n stands in its row of e: in every 8 columns n
-// and n + 4 are neighbours, as the conversion of the gradient's product takes
-// the weights' rows (loss.hip).
-__device__ __forceinline__ int64_t weight_place(int64_t n) { return (n & ~int64_t(7)) | ((n & 3) << 1) | ((n >> 2) & 1); }
+// Where the weight of column n stands in its row of e: n and n + 2^bit are
+// neighbours, as the conversion of the gradient's product takes the weights'
+// rows (loss.hip): n + 4 in a stream's rows (bit 2), n + 32 in a wide tile's
+// (bit 5), where a lane holds both.
+__device__ __forceinline__ int64_t weight_place(int64_t n, int bit) {
+  const int64_t low = (int64_t(1) << bit) - 1;
+  return (n & ~(2 * low + 1)) | ((n & low) << 1) | ((n >> bit) & 1);
+}
+constexpr int kStreamPair = 2, kWidePair = 5;
 
 // The larger / the sum of a value and its partner 16 or 32 lanes away.
 __device__ __forceinline__ float max_across16(float v) {
@@ -137,9 +142,8 @@ __device__ __forceinline__ void softmax_block32(const SoftmaxOut& o, const f32x1
       if (row >= nr) continue;
       if (r == 0) o.stats[(int64_t)(row0 + row) * o.blocks + (col0 >> 6)] = make_float2(m, s);
       if constexpr (KEEP) {
-        _Float16* e = o.e + (int64_t)(row0 + row) * o.ld_e + col0 + weight_place(r);
-        e[0] = (_Float16)(e0 * kWeightOne);
-        e[32] = (_Float16)(e1 * kWeightOne);
+        *reinterpret_cast<half2_t*>(o.e + (int64_t)(row0 + row) * o.ld_e + col0 + 2 * r) =
+            half2_t{(_Float16)(e0 * kWeightOne), (_Float16)(e1 * kWeightOne)};
       }
     }
 }

@@ -668,7 +668,7 @@ def select(logits, k, bias=None, scoring="sigmoid", groups=1, topk_groups=1, gro
     if out is None:
         if k < 1:
             raise RouterError("k must be at least 1")
-        out = (torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty((T, k), dtype=torch.float32, device=dev))
+        out = (logits.new_empty((T, k), dtype=torch.int32), logits.new_empty((T, k), dtype=torch.float32))
     else:
         _tensor(out[0], "topk_idx", torch.int32, (T, k), dev)
         _tensor(out[1], "topk_w", torch.float32, (T, k), dev)
@@ -692,7 +692,7 @@ def select_backward(logits, topk_idx, grad_w, scoring="sigmoid", renormalize=Tru
     _tensor(grad_w, "grad_w", torch.float32, (T, k), dev)
     ldo = E
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        out = logits.new_empty((T, E))
     else:
         ldo = _rows_tensor(out, "out", (logits.dtype,), T)
         if out.shape != logits.shape or out.device != dev:
