@@ -45,10 +45,10 @@ __global__ __launch_bounds__(kEsThreads) void head_stream_kernel(ExpertArgs a, i
 
 template <Out M, Scales S>
 __global__ __launch_bounds__(kEtThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_wide_kernel(
-    ExpertArgs a, int row_tiles) {
+    ExpertArgs a, int row_tiles, int tile_rows) {
   __shared__ TileLds lds;
-  const int n = xcd_order(blockIdx.x, gridDim.x), ct = n / row_tiles, row0 = (n - ct * row_tiles) * kEtRows;
-  const ExpertTile tile{{0, row0, min(kEtRows, a.R - row0)}, ct};
+  const int n = xcd_order(blockIdx.x, gridDim.x), ct = n / row_tiles, row0 = (n - ct * row_tiles) * tile_rows;
+  const ExpertTile tile{{0, row0, min(tile_rows, a.R - row0)}, ct};
   const int nr = tile.rt.nr;
   if (nr > 96) wide_tile<M, 4, S>(a, tile, lds);
   else if (nr > 64) wide_tile<M, 3, S>(a, tile, lds);
@@ -207,26 +207,38 @@ __global__ __launch_bounds__(64 * kTokWaves) void head_dots_kernel(HeadArgs a) {
     if (lane == u && j0 + u < a.K) a.logq[t * a.K + j0 + u] = z[u] * scale;
 }
 
-// One workgroup per row: lse from the blocks' sums, and the loss. Up to as
-// many tokens as wavefronts have their logits computed here, `dots` says.
-__global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a, int dots) {
-  __shared__ float2 part[kTokWaves];
-  __shared__ float terms[kTokWaves], zs[kTokWaves], lz[kHeadTokens];
+// A row's loss by its workgroup, from its logits' sum (m, s). Up to as many
+// tokens as wavefronts have their logits computed here (first by row_dots),
+// `dots` says.
+struct TokLds {
+  float2 part[kTokWaves];
+  float terms[kTokWaves], zs[kTokWaves], lz[kHeadTokens];
+  int tk[kHeadTokens];
+};
+
+__device__ __forceinline__ void row_dots(const HeadArgs& a, int64_t t, TokLds& lds) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = blockIdx.x;
-  const float scale = load_early(a.gsa) * load_early(a.gsw) / a.tau;
-  if (dots && wave < a.K) {
-    const int n[1] = {a.tokens[t * a.K + wave]};
-    float z[1];
-    token_dots<1>(a, t, n, z);
-    if (lane == 0) zs[wave] = z[0] * scale;
-  }
-  float2 v = wave_join(thread_join<64 * kTokWaves>(a.stats + t * a.blocks, a.used));
-  if (lane == 0) part[wave] = v;
+  if (wave >= a.K) return;
+  const int n[1] = {a.tokens[t * a.K + wave]};
+  float z[1];
+  token_dots<1>(a, t, n, z);
+  if (lane == 0) lds.zs[wave] = z[0] * (load_early(a.gsa) * load_early(a.gsw) / a.tau);
+}
+
+// (m, s) of a row's blocks, by a workgroup of kTokWaves wavefronts.
+__device__ __forceinline__ float2 row_join(const float2* st, int n, TokLds& lds) {
+  float2 v = wave_join(thread_join<64 * kTokWaves>(st, n));
+  if ((threadIdx.x & 63) == 0) lds.part[threadIdx.x >> 6] = v;
   __syncthreads();
-  v = part[0];
+  v = lds.part[0];
 #pragma unroll
-  for (int w = 1; w < kTokWaves; ++w) v = soft_join(v, part[w]);
+  for (int w = 1; w < kTokWaves; ++w) v = soft_join(v, lds.part[w]);
+  return v;
+}
+
+__device__ __forceinline__ void row_loss(const HeadArgs& a, int64_t t, float2 v, int dots, TokLds& lds) {
+  float (&terms)[kTokWaves] = lds.terms, (&zs)[kTokWaves] = lds.zs, (&lz)[kHeadTokens] = lds.lz;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float lse = v.x * kLn2 + logf(v.y);
   float2 tr = make_float2(0.0f, 1.0f);  // log p = 0 for cross entropy
   if (a.teacher) tr = teacher_row(a, t);
@@ -234,6 +246,7 @@ __global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a,
   float sum = 0.0f;
   for (int j = threadIdx.x; j < a.K; j += 64 * kTokWaves) {
     const int n = a.tokens[t * a.K + j];
+    lds.tk[j] = n;
     float logq = 0.0f;
     if (n >= 0 && n < a.N) {
       const float z = dots ? zs[j] : a.logq[t * a.K + j];
@@ -263,13 +276,15 @@ __global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a,
   // named more than once has its q at its first place.
   if (wave != 0) return;
   TokenList& list = a.lists[t];
+  const int* tk = lds.tk;
   int out = 0;
   for (int j0 = 0; j0 < a.K; j0 += 64) {
     const int j = j0 + lane;
-    const int n = j < a.K ? a.tokens[t * a.K + j] : -1;
+    const int n = j < a.K ? tk[j] : -1;
     const bool valid = n >= 0 && n < a.N;
     bool first = true;
-    for (int i = 0; i < min(j0 + 64, a.K); ++i) first = first && (i >= j || a.tokens[t * a.K + i] != n);
+#pragma unroll 8
+    for (int i = 0; i < min(j0 + 64, a.K); ++i) first = first && (i >= j || tk[i] != n);
     const uint64_t bal = __ballot(valid);
     if (valid) {
       const int at = out + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(bal >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)bal, 0u));
@@ -281,6 +296,13 @@ __global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a,
     out += (int)__popcll(bal);
   }
   if (lane == 0) list.count = out == 0 || tr.y == 0.0f ? -1 : out;
+}
+
+__global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a, int dots) {
+  __shared__ TokLds lds;
+  const int64_t t = blockIdx.x;
+  if (dots) row_dots(a, t, lds);
+  row_loss(a, t, row_join(a.stats + t * a.blocks, a.used, lds), dots, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -301,18 +323,16 @@ struct NormArgs {
   const int32_t* tokens;
 };
 
-constexpr int kNormThreads = 256;
-__global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a) {
-  __shared__ float2 part[kNormThreads / 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// LAST: the sums are complete, and the first workgroup of a row goes on to
+// its loss.
+constexpr int kNormThreads = 64 * kTokWaves;
+template <bool LAST>
+__global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, HeadArgs ha, int dots) {
+  __shared__ TokLds lds;
   const int64_t t = blockIdx.x;
   const float2* st = a.stats + t * a.blocks;
-  float2 v = wave_join(thread_join<kNormThreads>(st, a.used));
-  if (lane == 0) part[wave] = v;
-  __syncthreads();
-  v = part[0];
-#pragma unroll
-  for (int w = 1; w < kNormThreads / 64; ++w) v = soft_join(v, part[w]);
+  if (LAST && dots && blockIdx.y == 0) row_dots(ha, t, lds);
+  float2 v = row_join(st, a.used, lds);
   const float2 old = a.before ? a.before[t] : make_float2(-__builtin_inff(), 0.0f);
   v = soft_join(v, old);
   if (blockIdx.y == 0 && threadIdx.x == 0) {
@@ -337,6 +357,7 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a) {
     const int64_t c = (int64_t)a.tokens[t * a.K + j] - a.n0;
     if (c >= c0 && c < min(c1, a.cols)) e[weight_place(c, a.place_bit)] = (_Float16)0.0f;
   }
+  if (LAST && blockIdx.y == 0) row_loss(ha, t, v, dots, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -465,7 +486,8 @@ __global__ __launch_bounds__(64 * kGsWaves) void head_grad_kernel(GradArgs a) {
 // before they are written there.
 constexpr int kGwThreads = 512;
 constexpr int kGwRows = 128, kGwCols = 512, kGwStep = 128;
-constexpr int kGwLd = 144;  // LDS bytes per byte column or scale block: 128 rows and 16 of padding
+constexpr int kGwLd = 144;       // LDS bytes per byte column: 128 rows and 16 of padding
+constexpr int kGwScaleLd = 272;  // and per scale block
 
 // Tiles in bands of 8 row tiles, column tile by column tile, so that 32
 // neighbours read 8 rows' softmax weights and 4 columns' weights. The first
@@ -497,7 +519,7 @@ struct GradWideArgs {
 struct GradLds {
   alignas(16) _Float16 x[2][kGwRows * kGwStep];
   alignas(16) uint8_t codes[2][(kGwCols / 2) * kGwLd];
-  alignas(16) uint8_t scales[2][(kGwCols / 16) * kGwLd];
+  alignas(16) uint8_t scales[2][(kGwCols / 16) * kGwScaleLd];  // fp16
 };
 
 // Halves offset of 16-byte piece c (of 16) of row r of the softmax weights.
@@ -547,16 +569,14 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
   const float ref = a.ref[row0 + (arow ? ar : 0)];
   u32x4_t ev[4];
   float mv[2];
-  // A step's loads and stores, half the softmax weights or half the codes at a time. Nothing is read past the split's
-  // rows (zeros) or the piece's columns.
+  // A step's loads and stores, half the softmax weights or half the codes at a time. Weights' rows past the split's
+  // are zeros; softmax weights past its last step are not wanted, and its last step's are read again.
+  const int last = nsteps - 1;
   auto load_x = [&](int s, int u) {
-    const int k = n0 + kGwStep * s + 64 * u;  // of the piece
-    mv[u] = k < a.g.cols ? st[2 * s + u].x : -__builtin_inff();
+    mv[u] = st[2 * min(s, last) + u].x;
 #pragma unroll
     for (int i = 2 * u; i < 2 * u + 2; ++i)
-      ev[i] = __builtin_bit_cast(
-          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                       er, k + 32 * (i & 1) + 8 * aq < a.g.cols ? oe + 2 * (kGwStep * s + 32 * i) : kMmaOob, 0, 0));
+      ev[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(er, oe + 2 * (kGwStep * min(s, last) + 32 * i), 0, 0));
   };
   auto store_x = [&](int buf, int u) {
     // In two factors where one would be below fp16's normal numbers.
@@ -600,11 +620,12 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
   auto store_s = [&](int buf) {
     const uint32_t s0 = S4 ? sv[0][0] : sv[0][0] | (sv[0][1] << 16), s1 = S4 ? sv[1][0] : sv[1][0] | (sv[1][1] << 16);
     const uint32_t t0 = __builtin_amdgcn_perm(s1, s0, 0x05010400u), t1 = __builtin_amdgcn_perm(s1, s0, 0x07030602u);
-    uint8_t* d = &lds.scales[buf][4 * b * kGwLd + 2 * p];  // a row's next to that of the row 32 further on
-    *reinterpret_cast<uint16_t*>(d) = (uint16_t)t0;
-    *reinterpret_cast<uint16_t*>(d + kGwLd) = (uint16_t)(t0 >> 16);
-    *reinterpret_cast<uint16_t*>(d + 2 * kGwLd) = (uint16_t)t1;
-    *reinterpret_cast<uint16_t*>(d + 3 * kGwLd) = (uint16_t)(t1 >> 16);
+    // Of each block a row's scale next to that of the row 32 further on.
+    uint8_t* d = &lds.scales[buf][4 * b * kGwScaleLd + 4 * p];
+    *reinterpret_cast<half2_t*>(d) = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(t0, 1.0f, false);
+    *reinterpret_cast<half2_t*>(d + kGwScaleLd) = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(t0, 1.0f, true);
+    *reinterpret_cast<half2_t*>(d + 2 * kGwScaleLd) = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(t1, 1.0f, false);
+    *reinterpret_cast<half2_t*>(d + 3 * kGwScaleLd) = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(t1, 1.0f, true);
   };
 
   f32x16_t acc[RT][2];
@@ -624,7 +645,7 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
   // written the next one, whose first fragments the last slice reads.
   half8_t A[RT], w[2];
   u32x2_t cx, cy;  // codes of two slices, rows n and n + 32
-  u32x4_t sw;
+  u32x4_t sw[2];       // their scales
   uint32_t col[2];
   half2_t sc[4];
   auto afrag = [&](int i, int buf, int sl) {
@@ -634,17 +655,17 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
     const uint8_t* at = &lds.codes[buf][(wave * 32 + r) * kGwLd + 64 * (pair >> 1) + 16 * h + 8 * (pair & 1)];
     cx = *reinterpret_cast<const u32x2_t*>(at);
     cy = *reinterpret_cast<const u32x2_t*>(at + 32);
-    sw = *reinterpret_cast<const u32x4_t*>(&lds.scales[buf][r * kGwLd + 64 * (pair >> 1) + 32 * h + 16 * (pair & 1)]);
+    const uint8_t* st = &lds.scales[buf][r * kGwScaleLd + 128 * (pair >> 1) + 64 * h + 32 * (pair & 1)];
+    sw[0] = *reinterpret_cast<const u32x4_t*>(st);
+    sw[1] = *reinterpret_cast<const u32x4_t*>(st + 16);
   };
   auto prepare = [&](auto jc) {  // columns and scales of a slice
     constexpr int j = decltype(jc)::value;
     const uint32_t x = cx[j], y = cy[j];
     col[0] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
     col[1] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
-    sc[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw[2 * j], 1.0f, false);
-    sc[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw[2 * j], 1.0f, true);
-    sc[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw[2 * j + 1], 1.0f, false);
-    sc[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sw[2 * j + 1], 1.0f, true);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sc[k] = __builtin_bit_cast(half2_t, (uint32_t)sw[j][k]);
   };
   auto convert = [&](auto mc, auto kc) {
     constexpr int m = decltype(mc)::value, k = decltype(kc)::value;
@@ -748,9 +769,9 @@ __global__ __launch_bounds__(kGwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
 }
 
 // dx: the splits' sums, divided by the softmax's, and the loss's own tokens.
-// SHARE: a workgroup's wavefronts share 512 columns, each a quarter of the
-// splits and tokens, joined in a fixed order; otherwise each has 512 of its
-// own.
+// SHARE: a workgroup's 16 wavefronts share 512 columns, each a part of the
+// splits and tokens, joined in a fixed order; otherwise each of four has 512
+// of its own.
 struct DxArgs {
   HeadArgs h;
   const float* part;
@@ -758,11 +779,14 @@ struct DxArgs {
   GradTiles tiles;  // if it has any
 };
 
-constexpr int kDxWaves = 4;
-constexpr int64_t kDxManyWgs = 4096;  // from this many workgroups of 512 columns on, each wavefront has its own
-constexpr int kDxThreads = 64 * kDxWaves;
 template <bool SHARE>
-__global__ __launch_bounds__(kDxThreads) void head_dx_kernel(DxArgs a) {
+constexpr int dx_waves() {
+  return SHARE ? 16 : 4;
+}
+constexpr int64_t kDxManyWgs = 4096;  // from this many workgroups of 512 columns on, each wavefront has its own
+template <bool SHARE>
+__global__ __launch_bounds__(64 * dx_waves<SHARE>()) void head_dx_kernel(DxArgs a) {
+  constexpr int kDxWaves = dx_waves<SHARE>();
   __shared__ float joined[SHARE ? kDxWaves : 1][SHARE ? 64 : 1][9];
   const HeadArgs& h = a.h;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -919,10 +943,13 @@ template <Out M>
 static hipError_t launch_logits(const ExpertArgs& a, bool wide, hipStream_t stream) {
   const Scales sc = scales_of(a);
   if (wide) {
-    const int row_tiles = (a.R + kEtRows - 1) / kEtRows, grid = row_tiles * ((a.N + kEtCols - 1) / kEtCols);
-    if (sc == Scales::k16) head_wide_kernel<M, Scales::k16><<<grid, kEtThreads, 0, stream>>>(a, row_tiles);
-    else if (sc == Scales::k4) head_wide_kernel<M, Scales::k4><<<grid, kEtThreads, 0, stream>>>(a, row_tiles);
-    else head_wide_kernel<M, Scales::kSkewed><<<grid, kEtThreads, 0, stream>>>(a, row_tiles);
+    const int cols = (a.N + kEtCols - 1) / kEtCols;
+    // 64 rows while each compute unit then has one tile at most.
+    const int tile_rows = (a.R + 63) / 64 * cols <= kOneRound ? 64 : kEtRows;
+    const int row_tiles = (a.R + tile_rows - 1) / tile_rows, grid = row_tiles * cols;
+    if (sc == Scales::k16) head_wide_kernel<M, Scales::k16><<<grid, kEtThreads, 0, stream>>>(a, row_tiles, tile_rows);
+    else if (sc == Scales::k4) head_wide_kernel<M, Scales::k4><<<grid, kEtThreads, 0, stream>>>(a, row_tiles, tile_rows);
+    else head_wide_kernel<M, Scales::kSkewed><<<grid, kEtThreads, 0, stream>>>(a, row_tiles, tile_rows);
     return hipGetLastError();
   }
   const int col_tiles = (a.N + kEsRows * kEsWaves - 1) / (kEsRows * kEsWaves);
@@ -939,15 +966,11 @@ static hipError_t launch_logits(const ExpertArgs& a, bool wide, hipStream_t stre
   return hipGetLastError();
 }
 
-static hipError_t launch_tokens(const HeadArgs& h, hipStream_t stream) {
-  const bool dots = h.K <= kTokWaves;
-  if (!dots) {
-    constexpr int per = kTokWaves * kTokPerWave;
-    head_dots_kernel<<<dim3(h.T, (h.K + per - 1) / per), 64 * kTokWaves, 0, stream>>>(h);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  head_tokens_kernel<<<h.T, 64 * kTokWaves, 0, stream>>>(h, dots);
+// The tokens' logits into logq, unless a row's workgroup computes them itself.
+static hipError_t launch_dots(const HeadArgs& h, bool dots, hipStream_t stream) {
+  if (dots) return hipSuccess;
+  constexpr int per = kTokWaves * kTokPerWave;
+  head_dots_kernel<<<dim3(h.T, (h.K + per - 1) / per), 64 * kTokWaves, 0, stream>>>(h);
   return hipGetLastError();
 }
 
@@ -960,6 +983,7 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
   float2* stats = reinterpret_cast<float2*>(ws + p.stats_at);
   a.soft.scale = kLog2e / h.tau;
   a.soft.blocks = (int)p.blocks;
+  const bool dots = h.K <= kTokWaves;
   hipError_t e;
   if (!grad) {
     for (int64_t i = 0; i < p.pieces; ++i) {
@@ -972,12 +996,16 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
     }
     h.stats = stats;
     h.blocks = h.used = (int)p.blocks;
-    return launch_tokens(h, stream);
+    if ((e = launch_dots(h, dots, stream)) != hipSuccess) return e;
+    head_tokens_kernel<<<h.T, 64 * kTokWaves, 0, stream>>>(h, dots);
+    return hipGetLastError();
   }
   float2* state = reinterpret_cast<float2*>(ws + p.state_at);
   float* shrink = reinterpret_cast<float*>(ws + p.shrink_at);
   float* ref = reinterpret_cast<float*>(ws + p.ref_at);
   float* part = reinterpret_cast<float*>(ws + p.part_at);
+  h.lists = reinterpret_cast<TokenList*>(ws + p.lists_at);
+  if ((e = launch_dots(h, dots, stream)) != hipSuccess) return e;
   a.soft.stats = stats;
   a.soft.e = reinterpret_cast<_Float16*>(ws + p.e_at);
   a.soft.ld_e = p.ld_e;
@@ -999,7 +1027,8 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
     n.place_bit = p.wide ? kWidePair : kStreamPair;
     const int segs = !n.rescale ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>((a.N + 2047) / 2048, (1024 + h.T - 1) / h.T));
     n.seg = (int)(((a.N + segs - 1) / segs + 63) / 64 * 64);
-    head_norm_kernel<<<dim3(h.T, segs), kNormThreads, 0, stream>>>(n);
+    if (i + 1 < p.pieces) head_norm_kernel<false><<<dim3(h.T, segs), kNormThreads, 0, stream>>>(n, h, 0);
+    else head_norm_kernel<true><<<dim3(h.T, segs), kNormThreads, 0, stream>>>(n, h, dots);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     GradArgs g{};
     g.e = a.soft.e; g.ld_e = p.ld_e; g.wc = a.wc; g.ws = a.ws; g.T = h.T; g.D = h.D; g.cols = a.N;
@@ -1022,15 +1051,12 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   h.stats = state + ((p.pieces - 1) & 1) * (int64_t)h.T;
-  h.blocks = h.used = 1;
-  h.lists = reinterpret_cast<TokenList*>(ws + p.lists_at);
-  if ((e = launch_tokens(h, stream)) != hipSuccess) return e;
   DxArgs d{h, part, (int)p.splits, p.tiles};
   const int columns = (h.D + 511) / 512;
   if ((int64_t)h.T * columns < kDxManyWgs)
-    head_dx_kernel<true><<<dim3(h.T, columns), kDxThreads, 0, stream>>>(d);
+    head_dx_kernel<true><<<dim3(h.T, columns), 64 * dx_waves<true>(), 0, stream>>>(d);
   else
-    head_dx_kernel<false><<<dim3(h.T, (columns + kDxWaves - 1) / kDxWaves), kDxThreads, 0, stream>>>(d);
+    head_dx_kernel<false><<<dim3(h.T, (columns + dx_waves<false>() - 1) / dx_waves<false>()), 64 * dx_waves<false>(), 0, stream>>>(d);
   return hipGetLastError();
 }
 

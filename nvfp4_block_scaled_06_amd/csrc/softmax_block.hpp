@@ -115,8 +115,17 @@ __device__ __forceinline__ void softmax_block16(const SoftmaxOut& o, const f32x4
 template <bool KEEP, int RT>
 __device__ __forceinline__ void softmax_block32(const SoftmaxOut& o, const f32x16_t (&acc)[RT][2], float scale,
                                                 int row0, int nr, int col0, int N) {
-  if (col0 >= N) return;
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  if (col0 >= N) {
+    // The gradient's product takes the tile's columns past N too: weights of zero.
+    if (KEEP && col0 < o.ld_e) {
+      for (int row = h; row < nr; row += 2) {
+        if (r == 0) o.stats[(int64_t)(row0 + row) * o.blocks + (col0 >> 6)] = make_float2(-__builtin_inff(), 0.0f);
+        *reinterpret_cast<uint32_t*>(o.e + (int64_t)(row0 + row) * o.ld_e + col0 + 2 * r) = 0u;
+      }
+    }
+    return;
+  }
   const float sc = scale * o.scale;
   const bool in0 = col0 + r < N, in1 = col0 + 32 + r < N;
 #pragma unroll
