@@ -864,7 +864,7 @@ __global__ __launch_bounds__(64 * dx_waves<SHARE>()) void head_dx_kernel(DxArgs 
 // ---------------------------------------------------------------------------
 // Dispatch.
 // ---------------------------------------------------------------------------
-constexpr int64_t kWideItems = 96;  // wide tiles from this many of them on
+constexpr int64_t kWideItems = 48;  // wide tiles from this many of 64 rows on
 constexpr int64_t kMaxRange = (int64_t(1) << 31) - 65536;  // bytes a 32-bit buffer offset reaches
 
 // Everything that follows from the sizes. `wide`: the logits' tiles.
@@ -884,12 +884,12 @@ struct HeadPlan {
 
 static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   HeadPlan p{};
-  const int64_t wide_items = ((T + kEtRows - 1) / kEtRows) * ((N + kEtCols - 1) / kEtCols);
-  p.wide = T > 32 && wide_items >= kWideItems;
+  T = std::max(T, int64_t(1));
+  p.wide = T > 32 && ((T + 63) / 64) * ((N + kEtCols - 1) / kEtCols) >= kWideItems;
   p.block_shift = p.wide ? 6 : 5;
   int64_t piece = kMaxRange / (D / 2) / 512 * 512;  // a piece's codes lie within a buffer's range
   // A piece's softmax weights take 512 MB at most, but 4096 columns at least.
-  if (grad) piece = std::min(piece, std::max((int64_t(1) << 28) / std::max(T, int64_t(1)) / 512 * 512, int64_t(4096)));
+  if (grad) piece = std::min(piece, std::max((int64_t(1) << 28) / T / 512 * 512, int64_t(4096)));
   piece = std::max(piece, int64_t(512));
   p.pieces = (N + piece - 1) / piece;
   p.piece = ((N + p.pieces - 1) / p.pieces + 511) / 512 * 512;  // equal pieces
