@@ -160,9 +160,13 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
   const int nr = rt.nr, F = a.N >> 1;
   const int64_t rowc = a.D / 2, rows = a.D / 16, we = (int64_t)rt.g * a.N;
   // This wavefront's first output (GLU) or weight row, and its two 16-row tiles.
-  const int o0 = (tile.ct * kEsWaves + wave % kEsWaves) * (GLU ? 16 : 32);
-  const bool live0 = o0 < (GLU ? F : a.N), live1 = GLU ? live0 : o0 + 16 < a.N;
-  auto wrow = [&](int m) { return GLU ? (m ? F + o0 : o0) : o0 + 16 * m; };
+  // (For a softmax the second tile lies 32 rows after the first: softmax_block16.)
+  constexpr bool SOFT = M == Out::kSums || M == Out::kWeights;
+  constexpr int GAP = SOFT ? 32 : 16;
+  const int slot = tile.ct * kEsWaves + wave % kEsWaves;
+  const int o0 = SOFT ? 64 * (slot >> 1) + 16 * (slot & 1) : slot * (GLU ? 16 : 32);
+  const bool live0 = o0 < (GLU ? F : a.N), live1 = GLU ? live0 : o0 + GAP < a.N;
+  auto wrow = [&](int m) { return GLU ? (m ? F + o0 : o0) : o0 + GAP * m; };
 
   const __amdgpu_buffer_rsrc_t wcr = make_rsrc(a.wc + we * rowc, a.N * rowc);
   const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.ws + we * rows, GLU || M == Out::kProducts ? a.N * rows : scale_range(a.N * rows));

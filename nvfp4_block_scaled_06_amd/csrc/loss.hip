@@ -310,54 +310,41 @@ __global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a,
 // ---------------------------------------------------------------------------
 struct NormArgs {
   const float2* stats;  // [T, blocks]: those of this piece come first in each row
-  int blocks, used, block_shift;  // columns per block: 1 << block_shift
+  int blocks, used;
   const float2* before;     // NULL or [T]: (m, s) of the pieces before
   float2* after;            // [T]
   float* shrink;            // [T]: factor of the sums so far
   float* ref;               // [T]: m for the next piece
   _Float16* e;
   int64_t ld_e;
-  int T, K, n0, cols, seg;  // seg: columns per workgroup, a multiple of 64
-  int rescale;              // 0: the product takes the blocks' m into account
-  int place_bit;            // of weight_place
+  int T, K, n0, cols;
   const int32_t* tokens;
 };
 
-// LAST: the sums are complete, and the first workgroup of a row goes on to
-// its loss.
+// One workgroup per row. LAST: the sums are complete, and it goes on to the
+// row's loss.
 constexpr int kNormThreads = 64 * kTokWaves;
 template <bool LAST>
 __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, HeadArgs ha, int dots) {
   __shared__ TokLds lds;
   const int64_t t = blockIdx.x;
   const float2* st = a.stats + t * a.blocks;
-  if (LAST && dots && blockIdx.y == 0) row_dots(ha, t, lds);
+  if (LAST && dots) row_dots(ha, t, lds);
   float2 v = row_join(st, a.used, lds);
   const float2 old = a.before ? a.before[t] : make_float2(-__builtin_inff(), 0.0f);
   v = soft_join(v, old);
-  if (blockIdx.y == 0 && threadIdx.x == 0) {
+  if (threadIdx.x == 0) {
     a.after[t] = v;
     a.shrink[t] = a.before ? __builtin_amdgcn_exp2f(old.x - v.x) : 0.0f;
     a.ref[t] = v.x;
   }
-  // Weights of blocks whose m is lower than the row's.
-  const int c0 = blockIdx.y * a.seg, c1 = min(c0 + a.seg, (a.cols + 31) & ~31);
+  // The named tokens' own weights.
   _Float16* e = a.e + t * a.ld_e;
-  for (int c = c0 + 8 * threadIdx.x; a.rescale && c < c1; c += 8 * kNormThreads) {
-    const float m = st[c >> a.block_shift].x;
-    if (m == v.x) continue;
-    const float f = __builtin_amdgcn_exp2f(m - v.x);
-    half8_t h = *reinterpret_cast<const half8_t*>(e + c);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = (_Float16)((float)h[i] * f);
-    *reinterpret_cast<half8_t*>(e + c) = h;
-  }
-  __syncthreads();
   for (int j = threadIdx.x; j < a.K; j += kNormThreads) {
     const int64_t c = (int64_t)a.tokens[t * a.K + j] - a.n0;
-    if (c >= c0 && c < min(c1, a.cols)) e[weight_place(c, a.place_bit)] = (_Float16)0.0f;
+    if (c >= 0 && c < a.cols) e[weight_place(c)] = (_Float16)0.0f;
   }
-  if (LAST && blockIdx.y == 0) row_loss(ha, t, v, dots, lds);
+  if (LAST) row_loss(ha, t, v, dots, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -367,111 +354,8 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, Hea
 // of two rows (weight_place's neighbours) are put together so that each byte
 // holds one column's codes of both: a conversion of a byte then gives what MFMA
 // wants, one column's values of two n.
-// ---------------------------------------------------------------------------
-struct GradArgs {
-  const _Float16* e;
-  int64_t ld_e;
-  const uint8_t* wc;  // of the piece
-  const uint8_t* ws;
-  int T, D, cols, splits, steps;  // steps of 32 rows per split
-  float* part;                    // [splits, T, D]
-  const float* shrink;            // NULL: the first piece
-};
-
-// Few rows: a stream of the weights. Lane (r, q) takes columns 16 r .. 16 r +
-// 15 of its wavefront's 256, one for each of 16 tiles, and rows 8 q .. 8 q + 7
-// of 32, straight from memory in MFMA layout: a load takes 8 bytes for each
-// lane, whole 128-byte lines of 4 rows.
-constexpr int kGsWaves = 4;
-constexpr int kGsCols = 256;  // per wavefront
-
-template <int NT>
-__global__ __launch_bounds__(64 * kGsWaves) void head_grad_kernel(GradArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
-  const int d0 = (blockIdx.x * kGsWaves + wave) * kGsCols, dl = d0 + 16 * r;
-  const int split = blockIdx.y, row0 = blockIdx.z * (16 * NT);
-  const int64_t rowc = a.D / 2, rows = a.D / 16;
-  const int n0 = split * a.steps * 32, n1 = min(n0 + a.steps * 32, a.cols);
-  if (d0 >= a.D) return;
-  const int64_t nrows = max(n1 - n0, 0);
-  const __amdgpu_buffer_rsrc_t wcr = make_rsrc(a.wc + n0 * rowc, nrows * rowc);
-  const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.ws + n0 * rows, nrows * rows);
-  const uint32_t oc = dl < a.D ? (uint32_t)(8 * q * rowc + dl / 2) : kMmaOob;
-  const uint32_t os = dl < a.D ? (uint32_t)(8 * q * rows + dl / 16) : kMmaOob;
-  const _Float16* ep[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) ep[t] = a.e + (int64_t)min(row0 + 16 * t + r, a.T - 1) * a.ld_e + n0 + 8 * q;
-  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-  u32x2_t wv[8];
-  uint32_t sv[8];
-  half8_t ev[NT];
-  auto load = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      wv[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(wcr, oc + (uint32_t)((32 * s + i) * rowc), 0, 0));
-      sv[i] = __builtin_amdgcn_raw_buffer_load_b8(wsr, os + (uint32_t)((32 * s + i) * rows), 0, 0);
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) ev[t] = *reinterpret_cast<const half8_t*>(ep[t] + 32 * s);
-  };
-  f32x4_t acc[NT][16];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[t][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const int nsteps = (int)((nrows + 31) / 32);
-  if (nsteps > 0) load(0);
-  for (int s = 0; s < nsteps; ++s) {
-    uint32_t c[2][2][4];  // word, even / odd columns, pair of rows
-    half2_t sc[4];
-    half8_t A[NT];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        const uint32_t x = wv[p][w], y = wv[p + 4][w];
-        c[w][0][p] = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
-        c[w][1][p] = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
-      }
-      sc[p] = e4m3x2_f16(sv[p] | (sv[p + 4] << 8));
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) A[t] = ev[t];
-    if (s + 1 < nsteps) load(s + 1);
-    static_for<0, 16>([&](auto ic) {
-      constexpr int i = decltype(ic)::value, w = i >> 3, odd = i & 1, b = (i & 7) >> 1;
-      half8_t B;
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const half2_t h = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c[w][odd][p], 1.0f, b) * sc[p];
-        B[2 * p] = h[0];
-        B[2 * p + 1] = h[1];
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) acc[t][i] = mfma16(A[t], B, acc[t][i]);
-    });
-  }
-  // Lane (r, q), value v of tile i: row 4 q + v, column 16 r + i.
-  if (dl >= a.D) return;
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int row = row0 + 16 * t + 4 * q + v;
-      if (row >= a.T) continue;
-      float* out = a.part + ((int64_t)split * a.T + row) * a.D + dl;
-      const float f = a.shrink ? a.shrink[row] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f32x4_t y = {acc[t][4 * i][v], acc[t][4 * i + 1][v], acc[t][4 * i + 2][v], acc[t][4 * i + 3][v]};
-        f32x4_t* o = reinterpret_cast<f32x4_t*>(out) + i;
-        if (a.shrink) y += *o * f;
-        *o = y;
-      }
-    }
-}
-
-// Many rows: tiles of 128 rows times 512 columns, 8 wavefronts, two per SIMD,
+//
+// Tiles of up to 128 rows times 512 columns, 8 wavefronts, two per SIMD,
 // 32x32x16 MFMAs, 128 weight rows per step.
 //  * Weights: loaded in whole lines by the workgroup (8 rows x 8 bytes per
 //    thread), bytes transposed in registers, and kept in LDS as [byte
@@ -484,6 +368,7 @@ __global__ __launch_bounds__(64 * kGsWaves) void head_grad_kernel(GradArgs a) {
 //    32 further on to MFMA j.
 // All double-buffered in LDS, one barrier per step; a step's loads go out a step
 // before they are written there.
+// ---------------------------------------------------------------------------
 constexpr int kGwThreads = 512;
 constexpr int kGwRows = 128, kGwCols = 512, kGwStep = 128;
 constexpr int kGwLd = 144;       // LDS bytes per byte column: 128 rows and 16 of padding
@@ -508,10 +393,16 @@ struct GradTiles {
   }
 };
 
-struct GradWideArgs {
-  GradArgs g;
-  const float2* stats;  // [T, blocks] of the piece, blocks of 64 columns
-  int blocks;
+struct GradArgs {
+  const _Float16* e;
+  int64_t ld_e;
+  const uint8_t* wc;  // of the piece
+  const uint8_t* ws;
+  int T, D, cols;
+  float* part;          // [splits, T, D]
+  const float* shrink;  // NULL: the first piece
+  const float2* stats;  // [T, blocks] of the piece
+  int blocks, block_shift;
   const float* ref;     // [T]: the row's m
   GradTiles tiles;
 };
@@ -539,52 +430,55 @@ __device__ __forceinline__ void byte_transpose4(const uint32_t (&a)[4], uint32_t
 
 // S4: rows of scales start at multiples of 4 bytes (D a multiple of 64).
 template <int RT, bool S4>
-__device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, int nr, int ct, int split, int steps,
-                                               GradLds& lds) {
+__device__ __forceinline__ void grad_tile(const GradArgs& a, int row0, int nr, int ct, int split, int steps,
+                                          GradLds& lds) {
   typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t rowc = a.g.D / 2, rows = a.g.D / 16;
+  const int64_t rowc = a.D / 2, rows = a.D / 16;
   const int d0 = ct * kGwCols;
-  const int n0 = split * steps * kGwStep, n1 = min(n0 + steps * kGwStep, a.g.cols);
+  const int n0 = split * steps * kGwStep, n1 = min(n0 + steps * kGwStep, a.cols);
   const int64_t nrows = max(n1 - n0, 0);
   const int nsteps = (int)((nrows + kGwStep - 1) / kGwStep);
-  const __amdgpu_buffer_rsrc_t wcr = make_rsrc(a.g.wc + n0 * rowc, nrows * rowc);
-  const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.g.ws + n0 * rows, nrows * rows);
+  const __amdgpu_buffer_rsrc_t wcr = make_rsrc(a.wc + n0 * rowc, nrows * rowc);
+  const __amdgpu_buffer_rsrc_t wsr = make_rsrc(a.ws + n0 * rows, nrows * rows);
   // Codes: rows 8 o .. 8 o + 7 of a step, bytes 8 c .. 8 c + 7 of the tile's 256.
   const int o = tid >> 5, c = tid & 31;
-  const uint32_t oc = d0 + 16 * c < a.g.D ? (uint32_t)(8 * o * rowc + d0 / 2 + 8 * c) : kMmaOob;
+  const uint32_t oc = d0 + 16 * c < a.D ? (uint32_t)(8 * o * rowc + d0 / 2 + 8 * c) : kMmaOob;
   u32x2_t wv[8];
   // Scales: rows pn and pn + 32, blocks 4 b .. 4 b + 3 of the tile's 32.
   const int p = tid >> 3, b = tid & 7, pn = p + (p & 32);
-  const uint32_t os = d0 + 64 * b < a.g.D ? (uint32_t)(pn * rows + d0 / 16 + 4 * b) : kMmaOob;
-  const uint32_t os2 = d0 + 64 * b + 32 < a.g.D ? os + 2 : kMmaOob;
+  const uint32_t os = d0 + 64 * b < a.D ? (uint32_t)(pn * rows + d0 / 16 + 4 * b) : kMmaOob;
+  const uint32_t os2 = d0 + 64 * b + 32 < a.D ? os + 2 : kMmaOob;
   uint32_t sv[2][2];
   // Softmax weights: row ar, 16-byte pieces aq, aq + 4, aq + 8, aq + 12.
   const int ar = tid >> 2, aq = tid & 3;
   const bool arow = ar < nr;
-  const __amdgpu_buffer_rsrc_t er = make_rsrc(a.g.e + (int64_t)row0 * a.g.ld_e, (int64_t)nr * a.g.ld_e * 2);
-  const uint32_t oe = arow ? (uint32_t)(ar * a.g.ld_e * 2 + 2 * (n0 + 8 * aq)) : kMmaOob;
-  const float2* st = a.stats + (int64_t)(row0 + (arow ? ar : 0)) * a.blocks + n0 / 64;
+  const __amdgpu_buffer_rsrc_t er = make_rsrc(a.e + (int64_t)row0 * a.ld_e, (int64_t)nr * a.ld_e * 2);
+  const uint32_t oe = arow ? (uint32_t)(ar * a.ld_e * 2 + 2 * (n0 + 8 * aq)) : kMmaOob;
+  const float2* st = a.stats + (int64_t)(row0 + (arow ? ar : 0)) * a.blocks;
   const float ref = a.ref[row0 + (arow ? ar : 0)];
   u32x4_t ev[4];
-  float mv[2];
+  float mv[4];
   // A step's loads and stores, half the softmax weights or half the codes at a time. Weights' rows past the split's
   // are zeros; softmax weights past its last step are not wanted, and its last step's are read again.
   const int last = nsteps - 1;
   auto load_x = [&](int s, int u) {
-    mv[u] = st[2 * min(s, last) + u].x;
-#pragma unroll
-    for (int i = 2 * u; i < 2 * u + 2; ++i)
-      ev[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(er, oe + 2 * (kGwStep * min(s, last) + 32 * i), 0, 0));
-  };
-  auto store_x = [&](int buf, int u) {
-    // In two factors where one would be below fp16's normal numbers.
-    const float by = mv[u] - ref;
-    const _Float16 f = (_Float16)__builtin_amdgcn_exp2f(fmaxf(by, -14.0f)), g = (_Float16)__builtin_amdgcn_exp2f(fminf(by + 14.0f, 0.0f));
-    const bool low = __ballot(by < -14.0f) != 0;
 #pragma unroll
     for (int i = 2 * u; i < 2 * u + 2; ++i) {
+      mv[i] = st[(n0 + kGwStep * min(s, last) + 32 * i) >> a.block_shift].x;
+      ev[i] = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(er, oe + 2 * (kGwStep * min(s, last) + 32 * i), 0, 0));
+    }
+  };
+  auto store_x = [&](int buf, int u) {
+#pragma unroll
+    for (int i = 2 * u; i < 2 * u + 2; ++i) {
+      // In two factors where one would be below fp16's normal numbers.
+      const float by = mv[i] - ref;
+      const _Float16 f = (_Float16)__builtin_amdgcn_exp2f(fmaxf(by, -14.0f));
+      const _Float16 g = (_Float16)__builtin_amdgcn_exp2f(fminf(by + 14.0f, 0.0f));
+      const bool low = __ballot(by < -14.0f) != 0;
       half8_t v = __builtin_bit_cast(half8_t, ev[i]);
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] *= f;
@@ -598,7 +492,8 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
   auto load_w = [&](int s) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      wv[i] = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(wcr, oc + (uint32_t)((kGwStep * s + i) * rowc), 0, 0));
+      wv[i] = __builtin_bit_cast(
+          u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(wcr, oc + (uint32_t)((kGwStep * s + i) * rowc), 0, 0));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t at = (uint32_t)((kGwStep * s + 32 * i) * rows);
@@ -640,12 +535,12 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
   // while the odd columns' weights of the slice are converted, then the other
   // way round for the next slice; softmax weight fragment i is read right
   // after its last MFMA of the slice before, the codes of two slices during the
-  // last slice before them. The step's one barrier stands before
-  // its last slice: by then every wavefront has read this buffer to the end and
-  // written the next one, whose first fragments the last slice reads.
+  // last slice before them. The step's one barrier stands before its last
+  // slice: by then every wavefront has read this buffer to the end and written
+  // the next one, whose first fragments the last slice reads.
   half8_t A[RT], w[2];
   u32x2_t cx, cy;  // codes of two slices, rows n and n + 32
-  u32x4_t sw[2];       // their scales
+  u32x4_t sw[2];   // their scales
   uint32_t col[2];
   half2_t sc[4];
   auto afrag = [&](int i, int buf, int sl) {
@@ -725,17 +620,17 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
 
   // Value v of lane (r, h): row 8 (v / 4) + 4 h + v % 4 of its 32-row tile, columns 16 r + 2 wave and the next.
   const int d = d0 + 16 * r + 2 * wave;
-  if (d >= a.g.D) return;
+  if (d >= a.D) return;
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
       const int row = 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
       if (row >= nr) continue;
-      float2* out = reinterpret_cast<float2*>(a.g.part + ((int64_t)split * a.g.T + row0 + row) * a.g.D + d);
+      float2* out = reinterpret_cast<float2*>(a.part + ((int64_t)split * a.T + row0 + row) * a.D + d);
       float2 y = make_float2(acc[i][0][v], acc[i][1][v]);
-      if (a.g.shrink) {
-        const float f = a.g.shrink[row0 + row];
+      if (a.shrink) {
+        const float f = a.shrink[row0 + row];
         const float2 old = *out;
         y.x = fmaf(old.x, f, y.x);
         y.y = fmaf(old.y, f, y.y);
@@ -745,12 +640,12 @@ __device__ __forceinline__ void grad_wide_tile(const GradWideArgs& a, int row0, 
 }
 
 template <bool S4>
-__global__ __launch_bounds__(kGwThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_grad_wide_kernel(
-    GradWideArgs a) {
+__global__ __launch_bounds__(kGwThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_grad_kernel(
+    GradArgs a) {
   __shared__ GradLds lds;
   const GradTiles& tl = a.tiles;
   const int rest = tl.count() - tl.full;
-  int t = blockIdx.x, split = 0, steps = (a.g.cols + kGwStep - 1) / kGwStep;
+  int t = blockIdx.x, split = 0, steps = (a.cols + kGwStep - 1) / kGwStep;
   if (t < tl.full) {
     t = xcd_order(t, tl.full);
   } else {
@@ -761,11 +656,11 @@ __global__ __launch_bounds__(kGwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
   }
   int rt, ct;
   tl.place(t, rt, ct);
-  const int row0 = rt * kGwRows, nr = min(kGwRows, a.g.T - row0);
-  if (nr > 96) grad_wide_tile<4, S4>(a, row0, nr, ct, split, steps, lds);
-  else if (nr > 64) grad_wide_tile<3, S4>(a, row0, nr, ct, split, steps, lds);
-  else if (nr > 32) grad_wide_tile<2, S4>(a, row0, nr, ct, split, steps, lds);
-  else grad_wide_tile<1, S4>(a, row0, nr, ct, split, steps, lds);
+  const int row0 = rt * kGwRows, nr = min(kGwRows, a.T - row0);
+  if (nr > 96) grad_tile<4, S4>(a, row0, nr, ct, split, steps, lds);
+  else if (nr > 64) grad_tile<3, S4>(a, row0, nr, ct, split, steps, lds);
+  else if (nr > 32) grad_tile<2, S4>(a, row0, nr, ct, split, steps, lds);
+  else grad_tile<1, S4>(a, row0, nr, ct, split, steps, lds);
 }
 
 // dx: the splits' sums, divided by the softmax's, and the loss's own tokens.
@@ -775,8 +670,7 @@ __global__ __launch_bounds__(kGwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
 struct DxArgs {
   HeadArgs h;
   const float* part;
-  int splits;       // of every tile, or:
-  GradTiles tiles;  // if it has any
+  GradTiles tiles;
 };
 
 template <bool SHARE>
@@ -801,7 +695,7 @@ __global__ __launch_bounds__(64 * dx_waves<SHARE>()) void head_dx_kernel(DxArgs 
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = 0.0f;
   if (named >= 0 && d < h.D) {
-    const int splits = a.tiles.col_tiles ? a.tiles.parts((int)(t / kGwRows), d / kGwCols) : a.splits;
+    const int splits = a.tiles.parts((int)(t / kGwRows), d / kGwCols);
     const float* part = a.part + t * h.D + d;
     const int64_t slab = (int64_t)h.T * h.D;
     for (int s0 = first; s0 < splits; s0 += 4 * step) {  // 4 splits' loads in flight
@@ -864,7 +758,6 @@ __global__ __launch_bounds__(64 * dx_waves<SHARE>()) void head_dx_kernel(DxArgs 
 // ---------------------------------------------------------------------------
 // Dispatch.
 // ---------------------------------------------------------------------------
-constexpr int64_t kWideItems = 48;  // wide tiles from this many of 64 rows on
 constexpr int64_t kMaxRange = (int64_t(1) << 31) - 65536;  // bytes a 32-bit buffer offset reaches
 
 // Everything that follows from the sizes. `wide`: the logits' tiles.
@@ -874,10 +767,7 @@ struct HeadPlan {
   int64_t piece;     // columns of a piece, a multiple of 512
   int64_t pieces;
   int64_t blocks;    // statistics blocks per row kept at a time
-  bool wide_grad;    // the second product's tiles
-  GradTiles tiles;
-  int row_tiles16;   // 16-row tiles of a workgroup of its stream
-  int64_t splits;    // of a piece's rows there
+  GradTiles tiles;   // of the second product
   int64_t ld_e;
   size_t stats_at, state_at, shrink_at, ref_at, e_at, part_at, lists_at, bytes;
 };
@@ -885,7 +775,12 @@ struct HeadPlan {
 static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   HeadPlan p{};
   T = std::max(T, int64_t(1));
-  p.wide = T > 32 && ((T + 63) / 64) * ((N + kEtCols - 1) / kEtCols) >= kWideItems;
+  // Time over D of the stream's 32 x 128 tiles (768 at a time) and the wide
+  // kernel's (256 at a time), measured at D = 512 to 7168: 4.8 ns for a round
+  // and 12 ps for a tile; 15.2 ns for a round of 64 rows, 24.5 ns of 128.
+  const int64_t cols512 = (N + kEtCols - 1) / kEtCols, tiles64 = (T + 63) / 64 * cols512;
+  const int64_t rounds128 = ((T + 127) / 128 * cols512 + 255) / 256, tiles32 = (T + 31) / 32 * ((N + 127) / 128);
+  p.wide = T > 32 && (tiles64 <= kOneRound ? 15.2 : 24.5 * (double)rounds128) < std::max(4.8, 0.012 * (double)tiles32);
   p.block_shift = p.wide ? 6 : 5;
   int64_t piece = kMaxRange / (D / 2) / 512 * 512;  // a piece's codes lie within a buffer's range
   // A piece's softmax weights take 512 MB at most, but 4096 columns at least.
@@ -895,29 +790,23 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   p.piece = ((N + p.pieces - 1) / p.pieces + 511) / 512 * 512;  // equal pieces
   p.pieces = (N + p.piece - 1) / p.piece;
   const int64_t cols = grad ? p.piece : N;
-  p.blocks = (cols + (int64_t(1) << p.block_shift) - 1) >> p.block_shift;
-  p.row_tiles16 = T <= 16 ? 1 : T <= 32 ? 2 : 4;
-  p.wide_grad = p.wide;
+  p.blocks = (cols + 63) / 64 << (6 - p.block_shift);
   const int64_t rows = std::min(p.piece, N);
-  if (p.wide_grad) {
-    // Whole rounds of 256 workgroups, one on each compute unit, then the tiles left in the splits that end soonest: a
-    // split of 1 / s takes 1 / s of a round.
-    p.tiles.row_tiles = (int)((T + kGwRows - 1) / kGwRows);
-    p.tiles.col_tiles = (int)((D + kGwCols - 1) / kGwCols);
-    p.tiles.full = p.tiles.count() / 256 * 256;
-    // A step of 128 rows takes a workgroup about 3.5 us; each split's sums are written and read once more (5 TB/s).
-    const int64_t rest = p.tiles.count() - p.tiles.full, most = std::min(int64_t(64), std::max(int64_t(1), rows / 512));
-    const double steps = (double)((rows + kGwStep - 1) / kGwStep), sums = (double)T * (double)D * 8e-6 / 5.0;
-    double best = 1e30;
-    p.splits = 1;
-    for (int64_t s = 1; rest && s <= most; ++s) {
-      const double us = 3.5 * std::ceil(steps / (double)s) * (double)((rest * s + 255) / 256) + sums * (double)s;
-      if (us < best) best = us, p.splits = s;
-    }
-    p.tiles.splits = (int)p.splits;
-  } else {
-    const int64_t wgs = ((D + kGsWaves * kGsCols - 1) / (kGsWaves * kGsCols)) * ((T + 16 * p.row_tiles16 - 1) / (16 * p.row_tiles16));
-    p.splits = std::max(int64_t(1), std::min((512 + wgs - 1) / wgs, (rows + 255) / 256));
+  // Whole rounds of 256 workgroups, one on each compute unit, then the tiles left in the splits that end soonest: a
+  // split of 1 / s takes 1 / s of a round.
+  p.tiles.row_tiles = (int)((T + kGwRows - 1) / kGwRows);
+  p.tiles.col_tiles = (int)((D + kGwCols - 1) / kGwCols);
+  p.tiles.full = p.tiles.count() / 256 * 256;
+  // A step takes a workgroup 1.6 us and 0.65 us for each 32 rows of its tile (T = 1 to 4096 at D = 7168); each split's
+  // sums are written and read once more (5 TB/s).
+  const int64_t rest = p.tiles.count() - p.tiles.full, most = std::min(int64_t(64), std::max(int64_t(1), rows / 256));
+  const double steps = (double)((rows + kGwStep - 1) / kGwStep), sums = (double)T * (double)D * 8e-6 / 5.0;
+  const double step_us = 1.6 + 0.65 * (double)std::min(int64_t(4), (T + 31) / 32);
+  double best = 1e30;
+  p.tiles.splits = 1;
+  for (int64_t s = 1; rest && s <= most; ++s) {
+    const double us = step_us * std::ceil(steps / (double)s) * (double)((rest * s + 255) / 256) + sums * (double)s;
+    if (us < best) best = us, p.tiles.splits = (int)s;
   }
   p.ld_e = p.piece;
   size_t at = kScratchOffset;
@@ -932,7 +821,7 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
     p.shrink_at = take((size_t)T * sizeof(float));
     p.ref_at = take((size_t)T * sizeof(float));
     p.e_at = take((size_t)T * p.ld_e * sizeof(_Float16));
-    p.part_at = take((size_t)p.splits * T * D * sizeof(float));
+    p.part_at = take((size_t)p.tiles.splits * T * D * sizeof(float));
     p.lists_at = take((size_t)T * sizeof(TokenList));
   }
   p.bytes = at;
@@ -992,6 +881,7 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
       a.ws = h.ws + n0 * (h.D / 16);
       a.N = (int)std::min(p.piece, h.N - n0);
       a.soft.stats = stats + (n0 >> p.block_shift);
+      a.soft.used = (int)(p.blocks - (n0 >> p.block_shift));
       if ((e = launch_logits<Out::kSums>(a, p.wide, stream)) != hipSuccess) return e;
     }
     h.stats = stats;
@@ -1007,6 +897,7 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
   h.lists = reinterpret_cast<TokenList*>(ws + p.lists_at);
   if ((e = launch_dots(h, dots, stream)) != hipSuccess) return e;
   a.soft.stats = stats;
+  a.soft.used = (int)p.blocks;
   a.soft.e = reinterpret_cast<_Float16*>(ws + p.e_at);
   a.soft.ld_e = p.ld_e;
   for (int64_t i = 0; i < p.pieces; ++i) {
@@ -1017,41 +908,26 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
     a.soft.ref = i ? ref : nullptr;
     if ((e = launch_logits<Out::kWeights>(a, p.wide, stream)) != hipSuccess) return e;
     NormArgs n{};
-    n.stats = stats; n.blocks = (int)p.blocks; n.block_shift = p.block_shift;
-    n.used = (a.N + (1 << p.block_shift) - 1) >> p.block_shift;
+    n.stats = stats; n.blocks = (int)p.blocks;
+    n.used = (a.N + 63) / 64 << (6 - p.block_shift);
     n.before = i ? state + ((i - 1) & 1) * (int64_t)h.T : nullptr;
     n.after = state + (i & 1) * (int64_t)h.T;
     n.shrink = shrink; n.ref = ref; n.e = a.soft.e; n.ld_e = p.ld_e;
     n.T = h.T; n.K = h.K; n.n0 = (int)n0; n.cols = a.N; n.tokens = h.tokens;
-    n.rescale = !p.wide_grad;
-    n.place_bit = p.wide ? kWidePair : kStreamPair;
-    const int segs = !n.rescale ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>((a.N + 2047) / 2048, (1024 + h.T - 1) / h.T));
-    n.seg = (int)(((a.N + segs - 1) / segs + 63) / 64 * 64);
-    if (i + 1 < p.pieces) head_norm_kernel<false><<<dim3(h.T, segs), kNormThreads, 0, stream>>>(n, h, 0);
-    else head_norm_kernel<true><<<dim3(h.T, segs), kNormThreads, 0, stream>>>(n, h, dots);
+    if (i + 1 < p.pieces) head_norm_kernel<false><<<h.T, kNormThreads, 0, stream>>>(n, h, 0);
+    else head_norm_kernel<true><<<h.T, kNormThreads, 0, stream>>>(n, h, dots);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     GradArgs g{};
     g.e = a.soft.e; g.ld_e = p.ld_e; g.wc = a.wc; g.ws = a.ws; g.T = h.T; g.D = h.D; g.cols = a.N;
-    g.splits = (int)p.splits;
-    g.steps = (int)(((a.N + 31) / 32 + p.splits - 1) / p.splits);
     g.part = part; g.shrink = i ? shrink : nullptr;
-    if (p.wide_grad) {
-      const GradWideArgs w{g, stats, (int)p.blocks, ref, p.tiles};
-      const int grid = p.tiles.full + (p.tiles.count() - p.tiles.full) * p.tiles.splits;
-      if (h.D % 64 == 0) head_grad_wide_kernel<true><<<grid, kGwThreads, 0, stream>>>(w);
-      else head_grad_wide_kernel<false><<<grid, kGwThreads, 0, stream>>>(w);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-      continue;
-    }
-    const dim3 grid((h.D + kGsWaves * kGsCols - 1) / (kGsWaves * kGsCols), (int)p.splits,
-                    (h.T + 16 * p.row_tiles16 - 1) / (16 * p.row_tiles16));
-    if (p.row_tiles16 == 1) head_grad_kernel<1><<<grid, 64 * kGsWaves, 0, stream>>>(g);
-    else if (p.row_tiles16 == 2) head_grad_kernel<2><<<grid, 64 * kGsWaves, 0, stream>>>(g);
-    else head_grad_kernel<4><<<grid, 64 * kGsWaves, 0, stream>>>(g);
+    g.stats = stats; g.blocks = (int)p.blocks; g.block_shift = p.block_shift; g.ref = ref; g.tiles = p.tiles;
+    const int grid = p.tiles.full + (p.tiles.count() - p.tiles.full) * p.tiles.splits;
+    if (h.D % 64 == 0) head_grad_kernel<true><<<grid, kGwThreads, 0, stream>>>(g);
+    else head_grad_kernel<false><<<grid, kGwThreads, 0, stream>>>(g);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   h.stats = state + ((p.pieces - 1) & 1) * (int64_t)h.T;
-  DxArgs d{h, part, (int)p.splits, p.tiles};
+  DxArgs d{h, part, p.tiles};
   const int columns = (h.D + 511) / 512;
   if ((int64_t)h.T * columns < kDxManyWgs)
     head_dx_kernel<true><<<dim3(h.T, columns), 64 * dx_waves<true>(), 0, stream>>>(d);

@@ -19,21 +19,20 @@ struct SoftmaxOut {
   const float* ref;   // NULL or [T]: a lower bound of m
   float2* stats;      // [T, blocks] (m, s)
   int blocks;         // stride of stats
+  int used;           // blocks that have room for (m, s)
   _Float16* e;        // [T, ld_e]
-  int64_t ld_e;
+  int64_t ld_e;       // a multiple of 512
 };
 
 constexpr float kWeightOne = 32768.0f;  // a weight of 1 in fp16
 
-// Where the weight of column n stands in its row of e: n and n + 2^bit are
-// neighbours, as the conversion of the gradient's product takes the weights'
-// rows (loss.hip): n + 4 in a stream's rows (bit 2), n + 32 in a wide tile's
-// (bit 5), where a lane holds both.
-__device__ __forceinline__ int64_t weight_place(int64_t n, int bit) {
-  const int64_t low = (int64_t(1) << bit) - 1;
-  return (n & ~(2 * low + 1)) | ((n & low) << 1) | ((n >> bit) & 1);
+// Where the weight of column n stands in its row of e: in every 64 columns n
+// and n + 32 are neighbours, as the conversion of the gradient's product takes
+// the weights' rows (loss.hip). The blocks of a stream are 32 such places, 16
+// columns and the 16 that lie 32 after them.
+__device__ __forceinline__ int64_t weight_place(int64_t n) {
+  return (n & ~int64_t(63)) | ((n & 31) << 1) | ((n >> 5) & 1);
 }
-constexpr int kStreamPair = 2, kWidePair = 5;
 
 // The larger / the sum of a value and its partner 16 or 32 lanes away.
 __device__ __forceinline__ float max_across16(float v) {
@@ -57,13 +56,14 @@ __device__ __forceinline__ float dpp_f(float v) {
   return __int_as_float(dpp_i<CTRL>(__float_as_int(v)));
 }
 
-// Block of 32 columns from the stream's accumulators: lane (r, q), value v of
-// tile m: row r (+ 16 t), column 16 m + 4 q + v.
+// Block of 32 places from the stream's accumulators: lane (r, q), value v of
+// tile m: row r (+ 16 t), column col0 + 32 m + 4 q + v, so that a lane's eight
+// columns are neighbours in e.
 template <bool KEEP, int NT>
 __device__ __forceinline__ void softmax_block16(const SoftmaxOut& o, const f32x4_t (&acc)[2][NT], float scale,
                                                 int row0, int nr, int col0, int N) {
-  if (col0 >= N) return;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int place = (col0 & ~63) + 2 * (col0 & 63);
   const float sc = scale * o.scale;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -71,41 +71,27 @@ __device__ __forceinline__ void softmax_block16(const SoftmaxOut& o, const f32x4
     float y[8], m = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      y[i] = col0 + 16 * (i >> 2) + 4 * q + (i & 3) < N ? acc[i >> 2][t][i & 3] * sc : -__builtin_inff();
+      y[i] = col0 + 32 * (i & 1) + 4 * q + (i >> 1) < N ? acc[i & 1][t][i >> 1] * sc : -__builtin_inff();
       m = fmaxf(m, y[i]);
     }
     m = max_across32(max_across16(m));
-    if (KEEP && o.ref && row < nr) m = fmaxf(m, o.ref[row0 + row]);
+    // Columns past N have weights of zero and take no part in the sums.
+    const bool none = col0 >= N;
+    if (KEEP && o.ref && row < nr && !none) m = fmaxf(m, o.ref[row0 + row]);
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      y[i] = __builtin_amdgcn_exp2f(y[i] - m);
+      y[i] = none ? 0.0f : __builtin_amdgcn_exp2f(y[i] - m);
       s += y[i];
     }
     s = sum_across32(sum_across16(s));
-    // In weight_place's order: of two lanes q that hold 8 columns the even one
-    // takes both first pairs, the odd one both second pairs.
-    half2_t w[4];
-    if constexpr (KEEP) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const half2_t a = {(_Float16)(y[4 * i] * kWeightOne), (_Float16)(y[4 * i + 1] * kWeightOne)};
-        const half2_t b = {(_Float16)(y[4 * i + 2] * kWeightOne), (_Float16)(y[4 * i + 3] * kWeightOne)};
-        const auto p = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
-                                                        false, false);
-        w[2 * i] = __builtin_bit_cast(half2_t, (uint32_t)p[0]);
-        w[2 * i + 1] = __builtin_bit_cast(half2_t, (uint32_t)p[1]);
-      }
-    }
     if (row >= nr) continue;
-    if (q == 0) o.stats[(int64_t)(row0 + row) * o.blocks + (col0 >> 5)] = make_float2(m, s);
+    if (q == 0 && (place >> 5) < o.used) o.stats[(int64_t)(row0 + row) * o.blocks + (place >> 5)] = make_float2(m, s);
     if constexpr (KEEP) {
+      half8_t h;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
-        *reinterpret_cast<half4_t*>(o.e + (int64_t)(row0 + row) * o.ld_e + col0 + 16 * i + 4 * q) =
-            half4_t{w[2 * i][0], w[2 * i + 1][0], w[2 * i][1], w[2 * i + 1][1]};
-      }
+      for (int i = 0; i < 8; ++i) h[i] = (_Float16)(y[i] * kWeightOne);
+      *reinterpret_cast<half8_t*>(o.e + (int64_t)(row0 + row) * o.ld_e + place + 8 * q) = h;
     }
   }
 }
@@ -117,8 +103,8 @@ __device__ __forceinline__ void softmax_block32(const SoftmaxOut& o, const f32x1
                                                 int row0, int nr, int col0, int N) {
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   if (col0 >= N) {
-    // The gradient's product takes the tile's columns past N too: weights of zero.
-    if (KEEP && col0 < o.ld_e) {
+    // As there: the gradient's product takes the tile's columns past N too.
+    if constexpr (KEEP) {
       for (int row = h; row < nr; row += 2) {
         if (r == 0) o.stats[(int64_t)(row0 + row) * o.blocks + (col0 >> 6)] = make_float2(-__builtin_inff(), 0.0f);
         *reinterpret_cast<uint32_t*>(o.e + (int64_t)(row0 + row) * o.ld_e + col0 + 2 * r) = 0u;
