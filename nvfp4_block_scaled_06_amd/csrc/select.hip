@@ -189,6 +189,16 @@ __device__ __forceinline__ void sel_rounds(const SelectArgs& a, F* vals, int& ch
   }
 }
 
+// The larger of a value and its partner 32 or 16 lanes away.
+__device__ __forceinline__ uint32_t max_turn32(uint32_t v) {
+  const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max((uint32_t)p[0], (uint32_t)p[1]);
+}
+__device__ __forceinline__ uint32_t max_turn16(uint32_t v) {
+  const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return max((uint32_t)p[0], (uint32_t)p[1]);
+}
+
 // Survivors that a row may have: two for each of 16 lanes, one for each of 64.
 template <int LPR>
 constexpr int sel_most() {
@@ -205,10 +215,9 @@ enum : int { kSelDecided = 0, kSelOrder = 1, kSelAll = 2 };  // what 64 bits hav
 
 // Expert e's key in 64 bits; `top` and `total` of the row's softmax.
 __device__ __forceinline__ double sel_wide(const SelectArgs& a, float logit, int e, double top, double total) {
-  const double x = (double)logit;
+  const double x = (double)logit, b = a.bias ? (double)a.bias[e] : 0.0;
   double d = exp(a.softmax ? x - top : -x);
-  d = a.softmax ? d / total : 1.0 / (1.0 + d);
-  if (a.bias) d += (double)a.bias[e];
+  d = (a.softmax ? d / total : 1.0 / (1.0 + d)) + b;
   return x > -(double)__builtin_inff() && d > -(double)__builtin_inff() ? d : -(double)__builtin_inff();
 }
 
@@ -232,10 +241,14 @@ __device__ __forceinline__ int sel_survivors(const SelectArgs& a, const float (&
     const int above = count_above<1>(lm, 0);
     tau = row_min_u32(above < a.k ? lm : 0xFFFFFFFFu);
   } else {
-    tau = a.k <= 4    ? wave_min_of_groups<16>(group_max_u32<16>(lm))
-          : a.k <= 8  ? wave_min_of_groups<8>(group_max_u32<8>(lm))
-          : a.k <= 16 ? wave_min_of_groups<4>(group_max_u32<4>(lm))
-                      : wave_min_of_groups<2>(group_max_u32<2>(lm));
+    // Of the largest keys of the lanes l, l + S, l + 2 S, ..., S >= k, the
+    // smallest. (Lanes in turn rather than neighbours: groups of experts left
+    // out take whole runs of lanes with them.)
+    uint32_t m = max_turn32(lm);
+    if (a.k <= 16) m = max_turn16(m);
+    if (a.k <= 8) m = max(m, dpp_u<0x128>(m));  // row_ror:8
+    if (a.k <= 4) m = max(m, dpp_u<0x124>(m));  // row_ror:4
+    tau = wave_min_u32(m);
   }
   if (err > 0.0f && tau != 0u) {  // and all that may be the k-th
     const float t = key_back(tau);
@@ -318,22 +331,28 @@ __device__ __forceinline__ void sel_order(const SelectArgs& a, int64_t base, dou
   SelScratch<LPR>& sc = *reinterpret_cast<SelScratch<LPR>*>(row_lds);
   const int li = threadIdx.x & (LPR - 1);
   double mine[H];
+  float x[H];
   int e[H], rank[H];
 #pragma unroll
   for (int h = 0; h < H; ++h) {
-    const int u = li + LPR * h;
-    e[h] = u < C ? (int)~(uint32_t)sc.cand[u] : 0;
-    mine[h] = sel_wide(a, sel_logit(a.logits, a.bf16, base + e[h]), e[h], top, total);
+    e[h] = li + LPR * h < C ? (int)~(uint32_t)sc.cand[li + LPR * h] : 0;
+    x[h] = sel_logit(a.logits, a.bf16, base + e[h]);
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    mine[h] = sel_wide(a, x[h], e[h], top, total);
     rank[h] = 0;
-    sc.wide[u] = mine[h];
+    sc.wide[li + LPR * h] = li + LPR * h < C ? mine[h] : -(double)__builtin_inff();
   }
   sel_fence();
-#pragma unroll 4
-  for (int u = 0; u < C; ++u) {
-    const double other = sc.wide[u];
-    const int at = (int)~(uint32_t)sc.cand[u];
+  for (int u0 = 0; u0 < C; u0 += 8) {
 #pragma unroll
-    for (int h = 0; h < H; ++h) rank[h] += other > mine[h] || (other == mine[h] && at < e[h]) ? 1 : 0;
+    for (int u = u0; u < u0 + 8; ++u) {
+      const double other = sc.wide[u];
+      const int at = (int)~(uint32_t)sc.cand[u];
+#pragma unroll
+      for (int h = 0; h < H; ++h) rank[h] += other > mine[h] || (other == mine[h] && at < e[h]) ? 1 : 0;
+    }
   }
 #pragma unroll
   for (int h = 0; h < H; ++h)
@@ -365,8 +384,9 @@ __device__ __forceinline__ void sel_choose(const SelectArgs& a, const float (&l)
   double* wide = reinterpret_cast<double*>(row_lds);
   double total = 0.0;  // of the row's softmax, in 64 bits
   // All keys in 64 bits into `wide`. The logits pass through the upper half of
-  // the same LDS: key i overwrites the logits 2 i - PER LPR and the next,
-  // which this or an earlier turn of the loop has read.
+  // the same LDS: key i overwrites the logits 2 i - PER LPR and the next, which
+  // this or an earlier turn of the loop has read. Four keys of a lane at a time,
+  // for their latency.
   auto widen = [&]() {
     constexpr int ALL = PER * LPR;
     sel_fence();
@@ -374,14 +394,19 @@ __device__ __forceinline__ void sel_choose(const SelectArgs& a, const float (&l)
     for (int j = 0; j < PER; ++j) vals[ALL + sel_expert<LPR, VEC>(li, j)] = l[j];
     sel_fence();
     if (a.softmax && total == 0.0) {
-#pragma unroll 2
+#pragma unroll 4
       for (int i = li; i < a.E; i += LPR) total += exp((double)vals[ALL + i] - (double)top);
       total = row_total<LPR>(total);
     }
-    for (int i = li; i < a.E; i += LPR) {
-      const double d = sel_wide(a, vals[ALL + i], i, (double)top, total);
+    constexpr int U = PER < 4 ? PER : 4;
+    for (int i0 = li; i0 < ALL; i0 += U * LPR) {
+      double d[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        d[u] = sel_wide(a, vals[ALL + i0 + u * LPR], min(i0 + u * LPR, a.E - 1), (double)top, total);
       sel_fence();
-      wide[i] = d;
+#pragma unroll
+      for (int u = 0; u < U; ++u) wide[i0 + u * LPR] = d[u];
       sel_fence();
     }
   };
@@ -626,9 +651,13 @@ static hipError_t launch_select_t(SelectArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// 16-byte loads where they give each of 16 lanes some experts; a wavefront's
-// loads of neighbours are whole lines anyway.
-static hipError_t launch_select(const SelectArgs& a, hipStream_t stream) {
+// 16-byte loads where they give each of 16 lanes some experts of every group; a
+// wavefront's loads of neighbours are whole lines anyway. (With groups of 32 a
+// lane's 4 neighbours are of one group in two, and if the other ones are left
+// out the bound rests on half the lanes: 8192 x 256, 4 of 8 groups, 18.5 us
+// with them, 11.1 without.)
+static hipError_t launch_select(SelectArgs a, hipStream_t stream) {
+  a.vec = a.vec && a.kept == a.groups;
   if (select_many(a.T, a.k, a.groups)) {
     if (a.E <= 64) return launch_select_t<16, 4, false>(a, stream);
     if (a.E <= 128) return a.vec ? launch_select_t<16, 8, true>(a, stream) : launch_select_t<16, 8, false>(a, stream);
