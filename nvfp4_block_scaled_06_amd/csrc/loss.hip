@@ -407,11 +407,13 @@ struct GradArgs {
   GradTiles tiles;
 };
 
+// (And the sums of 64 rows on their way out.)
 struct GradLds {
   alignas(16) _Float16 x[2][kGwRows * kGwStep];
   alignas(16) uint8_t codes[2][(kGwCols / 2) * kGwLd];
   alignas(16) uint8_t scales[2][(kGwCols / 16) * kGwScaleLd];  // fp16
 };
+static_assert(sizeof(GradLds) >= 64 * kGwCols * sizeof(float));
 
 // Halves offset of 16-byte piece c (of 16) of row r of the softmax weights.
 __device__ __forceinline__ int grad_x_at(int r, int c) {
@@ -618,25 +620,43 @@ __device__ __forceinline__ void grad_tile(const GradArgs& a, int row0, int nr, i
     });
   }
 
-  // Value v of lane (r, h): row 8 (v / 4) + 4 h + v % 4 of its 32-row tile, columns 16 r + 2 wave and the next.
-  const int d = d0 + 16 * r + 2 * wave;
-  if (d >= a.D) return;
+  // Value v of lane (r, h): row 8 (v / 4) + 4 h + v % 4 of its 32-row tile,
+  // columns 16 r + 2 wave and the next. To memory through LDS, 64 rows at a
+  // time: stores of 8 bytes 64 apart would be one line each. In LDS every 16
+  // columns are turned round by 2 (r / 4), for the banks.
+  float* sums = reinterpret_cast<float*>(&lds);
+  static_for<0, (RT + 1) / 2>([&](auto pc) {
+    constexpr int i0 = 2 * decltype(pc)::value;
+    __syncthreads();
+    static_for<i0, (i0 + 2 < RT ? i0 + 2 : RT)>([&](auto ic) {
+      constexpr int i = decltype(ic)::value;
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int row = 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
-      if (row >= nr) continue;
-      float2* out = reinterpret_cast<float2*>(a.part + ((int64_t)split * a.T + row0 + row) * a.D + d);
-      float2 y = make_float2(acc[i][0][v], acc[i][1][v]);
-      if (a.shrink) {
-        const float f = a.shrink[row0 + row];
-        const float2 old = *out;
-        y.x = fmaf(old.x, f, y.x);
-        y.y = fmaf(old.y, f, y.y);
+      for (int v = 0; v < 16; ++v) {
+        const int row = 32 * (i - i0) + 8 * (v >> 2) + 4 * h + (v & 3);
+        *reinterpret_cast<float2*>(sums + row * kGwCols + 16 * r + ((2 * wave + 2 * (r >> 2)) & 15)) =
+            make_float2(acc[i][0][v], acc[i][1][v]);
       }
-      *out = y;
+    });
+    __syncthreads();
+    const int q = 4 * (tid & (kGwCols / 4 - 1)), g = q >> 4, turn = 2 * (g >> 2);
+    const int at0 = 16 * g + (((q & 15) + turn) & 15), at1 = 16 * g + (((q & 15) + 2 + turn) & 15);
+    if (d0 + q < a.D) {
+#pragma unroll 4
+      for (int row = tid / (kGwCols / 4); row < min(64, nr - 32 * i0); row += kGwThreads / (kGwCols / 4)) {
+        f32x4_t* out = reinterpret_cast<f32x4_t*>(a.part + ((int64_t)split * a.T + row0 + 32 * i0 + row) * a.D + d0 + q);
+        const float2 lo = *reinterpret_cast<const float2*>(sums + row * kGwCols + at0);
+        const float2 hi = *reinterpret_cast<const float2*>(sums + row * kGwCols + at1);
+        f32x4_t y = {lo.x, lo.y, hi.x, hi.y};
+        if (a.shrink) {
+          const float f = a.shrink[row0 + 32 * i0 + row];
+          const f32x4_t old = *out;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) y[u] = fmaf(old[u], f, y[u]);
+        }
+        *out = y;
+      }
     }
+  });
 }
 
 template <bool S4>
@@ -799,7 +819,7 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   p.tiles.full = p.tiles.count() / 256 * 256;
   // A step takes a workgroup 1.6 us and 0.65 us for each 32 rows of its tile (T = 1 to 4096 at D = 7168); each split's
   // sums are written and read once more (5 TB/s).
-  const int64_t rest = p.tiles.count() - p.tiles.full, most = std::min(int64_t(64), std::max(int64_t(1), rows / 256));
+  const int64_t rest = p.tiles.count() - p.tiles.full, most = std::min(int64_t(256), std::max(int64_t(1), rows / 256));
   const double steps = (double)((rows + kGwStep - 1) / kGwStep), sums = (double)T * (double)D * 8e-6 / 5.0;
   const double step_us = 1.6 + 0.65 * (double)std::min(int64_t(4), (T + 31) / 32);
   double best = 1e30;
