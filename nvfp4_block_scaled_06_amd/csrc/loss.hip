@@ -132,24 +132,33 @@ __device__ __forceinline__ float2 teacher_row(const HeadArgs& a, int64_t t) {
   return make_float2(m, wave_sum(s));
 }
 
-// (m, s) of n blocks, by NT threads of which this is one; 8 loads in flight.
+// (m, s) of n blocks, by NT threads of which this is one; 16 loads in flight.
 template <int NT>
 __device__ __forceinline__ float2 thread_join(const float2* st, int n) {
+  constexpr int Q = 16;
   float2 v = make_float2(-__builtin_inff(), 0.0f);
-  for (int i0 = threadIdx.x; i0 < n; i0 += 8 * NT) {
-    float2 u[8];
+  for (int i0 = threadIdx.x; i0 < n; i0 += Q * NT) {
+    float2 u[Q];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) u[q] = i0 + q * NT < n ? st[i0 + q * NT] : make_float2(-__builtin_inff(), 0.0f);
+    for (int q = 0; q < Q; ++q) u[q] = i0 + q * NT < n ? st[i0 + q * NT] : make_float2(-__builtin_inff(), 0.0f);
+    float m = v.x;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v = soft_join(v, u[q]);
+    for (int q = 0; q < Q; ++q) m = fmaxf(m, u[q].x);
+    if (!(m > -__builtin_inff())) continue;  // nothing yet
+    float s = v.y * __builtin_amdgcn_exp2f(v.x - m);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) s += u[q].y * __builtin_amdgcn_exp2f(u[q].x - m);
+    v = make_float2(m, s);
   }
   return v;
 }
 
-// Logits of up to U tokens against row t of x, by a wavefront; exact block
-// products, fp32 sums in a fixed order. A token outside [0, N) gives anything.
+// Logits of up to U tokens against row t of x, by a wavefront, 4 / U chunks of
+// 32 values per lane in flight; exact block products, fp32 sums in a fixed
+// order. A token outside [0, N) gives anything.
 template <int U>
 __device__ __forceinline__ void token_dots(const HeadArgs& a, int64_t t, const int (&n)[U], float (&z)[U]) {
+  constexpr int C = 4 / U;
   const int lane = threadIdx.x & 63, nch = a.D >> 5;
   const int64_t rowc = a.D / 2, rows = a.D / 16;
   const uint8_t *xc = a.xc + t * rowc, *xs = a.xs + t * rows;
@@ -159,27 +168,35 @@ __device__ __forceinline__ void token_dots(const HeadArgs& a, int64_t t, const i
     row[u] = n[u] >= 0 && n[u] < a.N ? n[u] : 0;
     z[u] = 0.0f;
   }
-  for (int c = lane; c < nch; c += 64) {
-    u32x4_t wv[U];
-    uint32_t wb[U];
-    const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(xc + 16 * c);
-    const uint32_t xb = *reinterpret_cast<const uint16_t*>(xs + 2 * c);
+  for (int c0 = lane; c0 < nch; c0 += 64 * C) {
+    u32x4_t xv[C], wv[C][U];
+    uint32_t xb[C], wb[C][U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      wv[u] = *reinterpret_cast<const u32x4_t*>(a.wc + row[u] * rowc + 16 * c);
-      wb[u] = *reinterpret_cast<const uint16_t*>(a.ws + row[u] * rows + 2 * c);
+    for (int i = 0; i < C; ++i) {
+      const int c = min(c0 + 64 * i, nch - 1);
+      xv[i] = *reinterpret_cast<const u32x4_t*>(xc + 16 * c);
+      xb[i] = *reinterpret_cast<const uint16_t*>(xs + 2 * c);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        wv[i][u] = *reinterpret_cast<const u32x4_t*>(a.wc + row[u] * rowc + 16 * c);
+        wb[i][u] = *reinterpret_cast<const uint16_t*>(a.ws + row[u] * rows + 2 * c);
+      }
     }
-    const half2_t xsc = e4m3x2_f16(xb);
-    half8_t x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = fp4x8_scaled(xv[i], xsc, i >> 1);
+    for (int i = 0; i < C; ++i) {
+      if (c0 + 64 * i >= nch) break;
+      const half2_t xsc = e4m3x2_f16(xb[i]);
+      half8_t x[4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const half2_t wsc = e4m3x2_f16(wb[u]);
+      for (int q = 0; q < 4; ++q) x[q] = fp4x8_scaled(xv[i][q], xsc, q >> 1);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        z[u] += dot8(x[2 * i + 1], fp4x8_scaled(wv[u][2 * i + 1], wsc, i),
-                     dot8(x[2 * i], fp4x8_scaled(wv[u][2 * i], wsc, i), 0.0f));
+      for (int u = 0; u < U; ++u) {
+        const half2_t wsc = e4m3x2_f16(wb[i][u]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          z[u] += dot8(x[2 * q + 1], fp4x8_scaled(wv[i][u][2 * q + 1], wsc, q),
+                       dot8(x[2 * q], fp4x8_scaled(wv[i][u][2 * q], wsc, q), 0.0f));
+      }
     }
   }
 #pragma unroll
@@ -695,7 +712,7 @@ struct DxArgs {
 
 template <bool SHARE>
 constexpr int dx_waves() {
-  return SHARE ? 16 : 4;
+  return SHARE ? 8 : 4;
 }
 constexpr int64_t kDxManyWgs = 4096;  // from this many workgroups of 512 columns on, each wavefront has its own
 template <bool SHARE>
@@ -817,15 +834,16 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   p.tiles.row_tiles = (int)((T + kGwRows - 1) / kGwRows);
   p.tiles.col_tiles = (int)((D + kGwCols - 1) / kGwCols);
   p.tiles.full = p.tiles.count() / 256 * 256;
-  // A step takes a workgroup 1.6 us and 0.65 us for each 32 rows of its tile (T = 1 to 4096 at D = 7168); each split's
-  // sums are written and read once more (5 TB/s).
+  // A tile takes 6 us and for each step 0.25 us and 0.8 for each 32 of its rows, 2.3 at least (the weights'
+  // bandwidth); measured 8 to 16 steps, D = 4096: T = 32 2.3 a step, 64 2.35, 96 2.8, 128 3.45. Each split's sums are
+  // written and read once more (5 TB/s).
   const int64_t rest = p.tiles.count() - p.tiles.full, most = std::min(int64_t(256), std::max(int64_t(1), rows / 256));
   const double steps = (double)((rows + kGwStep - 1) / kGwStep), sums = (double)T * (double)D * 8e-6 / 5.0;
-  const double step_us = 1.6 + 0.65 * (double)std::min(int64_t(4), (T + 31) / 32);
+  const double step_us = std::max(2.3, 0.25 + 0.8 * (double)std::min(int64_t(4), (T + 31) / 32));
   double best = 1e30;
   p.tiles.splits = 1;
   for (int64_t s = 1; rest && s <= most; ++s) {
-    const double us = step_us * std::ceil(steps / (double)s) * (double)((rest * s + 255) / 256) + sums * (double)s;
+    const double us = (6.0 + step_us * std::ceil(steps / (double)s)) * (double)((rest * s + 255) / 256) + sums * (double)s;
     if (us < best) best = us, p.tiles.splits = (int)s;
   }
   p.ld_e = p.piece;
