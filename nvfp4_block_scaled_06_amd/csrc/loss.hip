@@ -701,9 +701,14 @@ __global__ __launch_bounds__(kGwThreads) __attribute__((amdgpu_waves_per_eu(2, 2
 }
 
 // dx: the splits' sums, divided by the softmax's, and the loss's own tokens.
-// SHARE: a workgroup's 16 wavefronts share 512 columns, each a part of the
+// SHARE: a workgroup's 8 wavefronts share 512 columns, each a part of the
 // splits and tokens, joined in a fixed order; otherwise each of four has 512
-// of its own.
+// of its own. Few workgroups of 512 columns share, up to more of them the more
+// tokens there are. us shared and not, one token: 63 workgroups 5.1 and 12.6,
+// 448 6.3 and 6.4, 896 9.1 and 8.5, 2842 18.7 and 12.5; 64 tokens: 896 14.9
+// and 18.4, 2842 34.6 and 27.4; 1024 tokens: 896 91 and 154, 2842 255 and 228.
+// Bound by the sums and the tokens' rows (T = 203, D = 7168, 1024 tokens: 3.7
+// TB/s).
 struct DxArgs {
   HeadArgs h;
   const float* part;
@@ -714,7 +719,7 @@ template <bool SHARE>
 constexpr int dx_waves() {
   return SHARE ? 8 : 4;
 }
-constexpr int64_t kDxManyWgs = 4096;  // from this many workgroups of 512 columns on, each wavefront has its own
+static bool dx_share(int64_t T, int64_t columns, int64_t K) { return T * columns < (K > kTokWaves ? 2048 : 512); }
 template <bool SHARE>
 __global__ __launch_bounds__(64 * dx_waves<SHARE>()) void head_dx_kernel(DxArgs a) {
   constexpr int kDxWaves = dx_waves<SHARE>();
@@ -967,7 +972,7 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
   h.stats = state + ((p.pieces - 1) & 1) * (int64_t)h.T;
   DxArgs d{h, part, p.tiles};
   const int columns = (h.D + 511) / 512;
-  if ((int64_t)h.T * columns < kDxManyWgs)
+  if (dx_share(h.T, columns, h.K))
     head_dx_kernel<true><<<dim3(h.T, columns), 64 * dx_waves<true>(), 0, stream>>>(d);
   else
     head_dx_kernel<false><<<dim3(h.T, (columns + dx_waves<false>() - 1) / dx_waves<false>()), 64 * dx_waves<false>(), 0, stream>>>(d);

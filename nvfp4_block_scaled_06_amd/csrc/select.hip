@@ -46,7 +46,7 @@ struct SelectArgs {
   int bf16, T, E, k;
   int groups, size, kept, top, sh;  // sh: log2 of the lanes per group
   uint32_t inv;                     // 2^20 / size rounded up: e / size = e inv >> 20 for e < 512
-  int softmax, renorm, by_logit, vec;
+  int softmax, renorm, by_logit, vec, many;  // many: 16 lanes to a row
   float scale;
   int lds_row;  // bytes of LDS per row
   int32_t* idx;
@@ -637,10 +637,20 @@ __global__ __launch_bounds__(kSelThreads) void select_grad_kernel(SelectGradArgs
   }
 }
 
-// 16 lanes to a row from this many rows on, where a row's places and groups
-// fit into 16 lanes.
-constexpr int64_t kSelManyRows = 1024;
-static bool select_many(int64_t T, int64_t k, int64_t groups) { return T >= kSelManyRows && k <= 16 && groups <= 16; }
+// Rows from which 16 lanes take a row, where its places and groups fit into 16
+// lanes (us with 16 and 64 lanes, k = 8, 256 experts): by the logits alone
+//   T = 1024 5.2, 4.4; 2048 5.3, 4.7 (384 experts: 5.9, 6.9); 4096 5.4, 6.9;
+//   32768 12.2, 21.0;
+// with keys, which put more on a lane,
+//   T = 1024 8.5, 4.8; 2048 8.4, 5.3; 4096 8.6, 6.1; 6000 11.0, 10.3 (384
+//   experts: 11.9, 13.4); 8192 10.0, 9.5 (four of eight groups: 11.3, 16.6);
+//   32768 18.7, 27.2;
+// the gradient
+//   T = 1024 4.7, 3.9; 4096 5.2, 4.9; 8192 5.8, 6.7; 32768 11.3, 17.3.
+constexpr int64_t kSelManyLogits = 2048, kSelManyKeys = 6144, kSelManyGrads = 8192;
+static bool select_many(int64_t T, int64_t from, int64_t k, int64_t groups) {
+  return T >= from && k <= 16 && groups <= 16;
+}
 
 template <int LPR, int PER, bool VEC>
 static hipError_t launch_select_t(SelectArgs a, hipStream_t stream) {
@@ -658,7 +668,7 @@ static hipError_t launch_select_t(SelectArgs a, hipStream_t stream) {
 // with them, 11.1 without.)
 static hipError_t launch_select(SelectArgs a, hipStream_t stream) {
   a.vec = a.vec && a.kept == a.groups;
-  if (select_many(a.T, a.k, a.groups)) {
+  if (a.many) {
     if (a.E <= 64) return launch_select_t<16, 4, false>(a, stream);
     if (a.E <= 128) return a.vec ? launch_select_t<16, 8, true>(a, stream) : launch_select_t<16, 8, false>(a, stream);
     if (a.E <= 256) return a.vec ? launch_select_t<16, 16, true>(a, stream) : launch_select_t<16, 16, false>(a, stream);
@@ -681,7 +691,7 @@ static hipError_t launch_select_grad_t(SelectGradArgs a, hipStream_t stream) {
 }
 
 static hipError_t launch_select_grad(const SelectGradArgs& a, hipStream_t stream) {
-  if (select_many(a.T, a.k, 1)) {
+  if (select_many(a.T, kSelManyGrads, a.k, 1)) {
     if (a.E <= 64) return launch_select_grad_t<16, 4>(a, stream);
     if (a.E <= 128) return launch_select_grad_t<16, 8>(a, stream);
     if (a.E <= 256) return launch_select_grad_t<16, 16>(a, stream);
@@ -731,11 +741,11 @@ int router_select(const void* logits, int dtype, int64_t T, int64_t E, int64_t l
   a.logits = logits; a.ld = ld; a.bias = bias; a.bf16 = dtype == ROUTER_BF16;
   a.T = (int)T; a.E = (int)E; a.k = (int)k;
   a.groups = (int)groups; a.size = (int)(E / groups); a.kept = (int)topk_groups; a.top = (int)group_top;
-  const int lanes = nvr::select_many(T, k, groups) ? 16 : 64;
-  while ((2 << a.sh) * groups <= lanes) ++a.sh;
   a.inv = (uint32_t)(((1u << 20) + a.size - 1) / a.size);
   a.softmax = scoring == ROUTER_SOFTMAX; a.renorm = renormalize != 0;
   a.by_logit = !bias && (groups == 1 || group_top == 1);
+  a.many = nvr::select_many(T, a.by_logit ? nvr::kSelManyLogits : nvr::kSelManyKeys, k, groups);
+  while ((2 << a.sh) * groups <= (a.many ? 16 : 64)) ++a.sh;
   const size_t piece = dtype == ROUTER_F32 ? 16 : 8;  // four logits
   a.vec = aligned(logits, piece) && (size_t)ld * piece / 4 % piece == 0;
   a.scale = routed_scale;

@@ -128,6 +128,38 @@ def test_hard_rows(dev, T, E, k, kind):
             check_grad(x, got[0].cpu().numpy(), gw, grad, kw, torch.float32)
 
 
+@pytest.mark.parametrize("T,E,k", [(2048, 61, 13), (6150, 256, 8), (6147, 384, 8), (6200, 510, 16), (8193, 96, 6),
+                                   (8200, 130, 12), (8192, 256, 17)])
+def test_many_rows(dev, T, E, k):
+    """Row counts where four rows share a wavefront."""
+    for rule, kw in enumerate(RULES):
+        for bias in (True, False):
+            x, b = make(T, E, torch.float32, T + E + rule, "few" if rule == 2 else "normal", bias)
+            x[5::97] = make(1, E, torch.float32, 3, "masked")[0]
+            log(f"many rows T={T} E={E} k={k} {kw} bias={bias}")
+            xd = up(x, dev)
+            got = rt.select(xd, k, bias=None if b is None else up(b, dev), **kw)
+            torch.cuda.synchronize()
+            check(x, b, k, got, kw)
+            gw = np.random.default_rng(4).standard_normal((T, k)).astype(np.float32)
+            grad = rt.select_backward(xd, got[0], up(gw, dev), **kw)
+            torch.cuda.synchronize()
+            check_grad(x, got[0].cpu().numpy(), gw, grad, kw, torch.float32)
+
+
+@pytest.mark.parametrize("kind", ["normal", "few", "masked", "near"])
+@pytest.mark.parametrize("E,groups,kept,top,k", [(256, 8, 4, 2, 8), (60, 6, 3, 1, 6), (96, 16, 9, 2, 7), (340, 5, 2, 2, 16)])
+def test_groups_many_rows(dev, E, groups, kept, top, k, kind):
+    T = 6150
+    for rule, bias in ((0, True), (3, False)):
+        kw = dict(RULES[rule], groups=groups, topk_groups=kept, group_top=top)
+        x, b = make(T, E, torch.float32, E + rule, kind, bias)
+        log(f"groups T={T} E={E} {kind} {kw} bias={bias}")
+        got = rt.select(up(x, dev), k, bias=None if b is None else up(b, dev), **kw)
+        torch.cuda.synchronize()
+        check(x, b, k, got, kw)
+
+
 def test_bias_special_values(dev):
     x, b = make(4, 64, torch.float32, 3)
     b[5], b[6], b[7] = -np.inf, np.nan, 50.0
