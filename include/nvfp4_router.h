@@ -517,14 +517,15 @@ int lmhead_distill(const uint8_t* x_codes, const uint8_t* x_scales, const float*
  *   bias          NULL or [E] fp32.
  *   scoring       ROUTER_SIGMOID or ROUTER_SOFTMAX.
  *   T, E, k       T >= 0; 1 <= k <= topk_groups * (E / groups); E % groups == 0;
- *                 1 <= topk_groups <= groups (ROUTER_EINVAL otherwise); E > 512,
- *                 k > 32 and groups > ROUTER_MAX_GROUPS give
- *                 ROUTER_EUNSUPPORTED.
+ *                 1 <= topk_groups <= groups (ROUTER_EINVAL otherwise); T >
+ *                 ROUTER_MAX_SELECT_ROWS, E > 512, k > 32 and groups >
+ *                 ROUTER_MAX_GROUPS give ROUTER_EUNSUPPORTED.
  * Pointers are aligned to their element. One launch, no workspace.
  */
 #define ROUTER_SIGMOID 0
 #define ROUTER_SOFTMAX 1
 #define ROUTER_MAX_GROUPS 64
+#define ROUTER_MAX_SELECT_ROWS (1 << 25)
 int router_select(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int scoring,
                   int64_t groups, int64_t topk_groups, int64_t group_top, int renormalize, float routed_scale,
                   int64_t k, int32_t* topk_idx, float* topk_w, void* stream);

@@ -827,6 +827,8 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   int64_t piece = kMaxRange / (D / 2) / 512 * 512;  // a piece's codes lie within a buffer's range
   // A piece's softmax weights take 512 MB at most, but 4096 columns at least.
   if (grad) piece = std::min(piece, std::max((int64_t(1) << 28) / T / 512 * 512, int64_t(4096)));
+  // A launch has fewer than 2^32 threads: 512 for a tile of 128 x 512, or of 64 x 512 where those are few.
+  piece = std::min(piece, (int64_t(1) << 37) / T / 512 * 512);
   piece = std::max(piece, int64_t(512));
   p.pieces = (N + piece - 1) / piece;
   p.piece = ((N + p.pieces - 1) / p.pieces + 511) / 512 * 512;  // equal pieces

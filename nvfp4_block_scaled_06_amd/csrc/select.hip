@@ -712,7 +712,7 @@ int check_select(int dtype, int scoring, int64_t T, int64_t E, int64_t k, int64_
   if ((dtype != ROUTER_F32 && dtype != ROUTER_BF16) || (scoring != ROUTER_SIGMOID && scoring != ROUTER_SOFTMAX) ||
       T < 0 || E < 1 || k < 1 || k > E || ld < E)
     return ROUTER_EINVAL;
-  if (E > ROUTER_MAX_EXPERTS || k > ROUTER_MAX_TOPK || T >= (int64_t(1) << 31) || ld >= (int64_t(1) << 31))
+  if (E > ROUTER_MAX_EXPERTS || k > ROUTER_MAX_TOPK || T > ROUTER_MAX_SELECT_ROWS || ld >= (int64_t(1) << 31))
     return ROUTER_EUNSUPPORTED;
   return ROUTER_OK;
 }

@@ -51,6 +51,16 @@ def test_select_refusals(lib):
     assert c(T=0, logits=None, bias=None, idx=None, w=None) == 0
 
 
+def test_select_most_rows(lib):
+    """More rows than a launch takes are refused, by both calls."""
+    a = dict(logits=P, dtype=0, T=(1 << 25) + 1, E=64, ld=64, bias=P, scoring=0, groups=8, kept=4, top=2, renorm=1,
+             scale=1.0, k=8, idx=P, w=P, s=None)
+    assert lib.router_select(*a.values()) == EUNSUPPORTED
+    b = dict(logits=P, dtype=0, T=(1 << 25) + 1, E=64, ld=64, idx=P, gw=P, scoring=1, renorm=0, scale=1.0, k=8,
+             out=off(1 << 20), ldo=64, s=None)
+    assert lib.router_select_backward(*b.values()) == EUNSUPPORTED
+
+
 def test_select_backward_refusals(lib):
     c = Call(lib.router_select_backward, logits=P, dtype=0, T=4, E=64, ld=64, idx=P, gw=P, scoring=1, renorm=0,
              scale=1.0, k=8, out=off(1 << 20), ldo=64, s=None)

@@ -487,3 +487,34 @@ def test_codes_beyond_32_bits(dev, T):
         w = wide(wq, slice(None), a, a + 1024)
         bound = 2.0 ** -8 * torch.mm(p, w).abs() + (3 * 2.0 ** -11 + 4 * tol) * torch.mm(p.abs(), w.abs())
         assert ((dx[:, a:a + 1024].double() - torch.mm(p, w)).abs() <= bound).all(), a
+
+
+def test_most_rows(dev):
+    """The most rows of a call, and a vocabulary that takes more than one launch with them; a few rows against float64."""
+    T, D, N = 1 << 18, 32, (1 << 20) + 700
+    g = torch.Generator(device=dev).manual_seed(2)
+    byte = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device=dev, dtype=torch.uint8)
+    wq = rt.NVFP4Tensor(byte(0, 256, N, D // 2), byte(0x18, 0x30, N, D // 16), torch.tensor([0.5], device=dev))
+    xq = rt.NVFP4Tensor(byte(0, 256, T, D // 2), byte(0x18, 0x30, T, D // 16), torch.tensor([0.5], device=dev))
+    y = torch.randint(0, N, (T,), generator=g, device=dev, dtype=torch.int32)
+    rows = torch.tensor([0, 1, 127, 131072, T - 129, T - 1], device=dev)
+    y[-1] = N - 1
+    log(f"most rows T={T} D={D} N={N}")
+    loss, lse, _ = rt.lmhead_loss(xq, wq, y, workspace(T, D, N, False, dev))
+    torch.cuda.synchronize()
+    lut = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64, device=dev)
+
+    def wide(q, at):
+        c = q.codes[at]
+        v = torch.stack((lut[(c & 15).long()], lut[(c >> 4).long()]), -1).flatten(1)
+        return v * q.scales[at].view(torch.float8_e4m3fn).double().repeat_interleave(16, 1) * q.gscale.double()
+
+    u, v = wide(xq, rows), wide(wq, slice(None))
+    z = torch.mm(u, v.t().contiguous())
+    # D products in fp32, and sums of exponentials in a tree of fp32 over N (a block's 64 in 6 steps, then 64 and more
+    # blocks in a thread, each exponential off by a few steps): 2^-24 (D |x||w| + 128) bounds the logarithm.
+    tol = 2.0 ** -24 * (D * float(torch.mm(u.abs(), v.abs().t().contiguous()).max()) + 128 + 8 * float(z.abs().max()))
+    ref = torch.logsumexp(z, 1)
+    assert (lse[rows].double() - ref).abs().max() <= tol
+    want = ref - z.gather(1, y[rows].long()[:, None])[:, 0]
+    assert (loss[rows].double() - want).abs().max() <= 2 * tol

@@ -289,6 +289,28 @@ def test_graph_streams_and_repeatability(dev, T):
         assert torch.equal(c[0], e[0]) and torch.equal(c[1], e[1]) and torch.equal(gc, ge), i
 
 
+@pytest.mark.parametrize("E,k", [(4, 2), (20, 17)])
+def test_most_rows(dev, E, k):
+    """The most rows of a call: its first and last rows are those of calls of their own."""
+    T = 1 << 25
+    g = torch.Generator(device=dev).manual_seed(E)
+    x = torch.randn((T, E), generator=g, device=dev)
+    gw = torch.randn((T, k), generator=g, device=dev)
+    log(f"most rows E={E} k={k}")
+    idx, w = rt.select(x, k)
+    grad = rt.select_backward(x, idx, gw)
+    torch.cuda.synchronize()
+    # Sums of k terms in two orders, up to 6 steps each, and a quotient: weights 2 (6 + 2) 2^-24 apart; a gradient's
+    # products with grad_w, whose sum it leaves out, 2 (8 + 7 + 2) 2^-24 max|grad_w|.
+    atol = 40 * 2.0 ** -24 * float(gw.abs().max())
+    for rows in (slice(0, 3000), slice(T - 3001, T)):
+        i, v = rt.select(x[rows], k)
+        assert torch.equal(i, idx[rows]) and torch.allclose(v, w[rows], rtol=2.0 ** -20, atol=0.0)
+        assert torch.allclose(rt.select_backward(x[rows], i, gw[rows]), grad[rows], rtol=0.0, atol=atol)
+    with pytest.raises(rt.RouterError):
+        rt.select(torch.empty((T + 1, 1), device=dev), 1)
+
+
 def test_binding_refusals(dev):
     x = torch.zeros((4, 64), device=dev)
     idx, w = rt.select(x, 4)
