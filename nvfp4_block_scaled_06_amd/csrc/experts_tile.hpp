@@ -145,8 +145,9 @@ __device__ __forceinline__ int stream_x_at(int r, int c) {
   return ((c * (MR / 16) + (r >> 4)) * 16 + ((r ^ (c >> 2)) & 15)) * 8;
 }
 
-// One tile.
-template <Out M, int MR, int KB, int KG, Scales S>
+// One tile. AUX: of the weights' loads, kNtAux where no other tile reads the
+// lines.
+template <Out M, int MR, int KB, int KG, Scales S, int AUX = kNtAux>
 __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTile& tile, StreamLds<MR, KB, KG>& lds) {
   constexpr bool GLU = M == Out::kGlu;
   constexpr int NT = MR / 16, NTHREADS = KG * kEsThreads;
@@ -179,7 +180,7 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
   auto load_w = [&](int slot, int step) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      wv[slot][i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wcr, wo[i] + 128 * step, 0, kNtAux));
+      wv[slot][i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wcr, wo[i] + 128 * step, 0, AUX));
   };
   // Scale window: SP pieces of SW bytes per row, 64 / SP rows in each of SL loads; and a load of the rows' last pieces.
   constexpr bool SKEW = S == Scales::kSkewed;

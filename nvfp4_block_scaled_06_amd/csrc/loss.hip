@@ -34,13 +34,13 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // ---------------------------------------------------------------------------
 // Logits of a piece: the experts' tiles, one matrix.
 // ---------------------------------------------------------------------------
-template <Out M, int MR, int KB, Scales S>
-__global__ __launch_bounds__(kEsThreads) void head_stream_kernel(ExpertArgs a, int row_tiles) {
-  __shared__ StreamLds<MR, KB, 1> lds;
+template <Out M, int MR, int KB, int KG, Scales S, int AUX>
+__global__ __launch_bounds__(KG * kEsThreads) void head_stream_kernel(ExpertArgs a, int row_tiles) {
+  __shared__ StreamLds<MR, KB, KG> lds;
   // The row tiles of one column tile side by side on one XCD: they read the same weights.
   const int n = xcd_order(blockIdx.x, gridDim.x), ct = n / row_tiles, row0 = (n - ct * row_tiles) * MR;
   const ExpertTile tile{{0, row0, min(MR, a.R - row0)}, ct};
-  stream_tile<M, MR, KB, 1, S>(a, tile, lds);
+  stream_tile<M, MR, KB, KG, S, AUX>(a, tile, lds);
 }
 
 template <Out M, Scales S>
@@ -817,12 +817,19 @@ struct HeadPlan {
 static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   HeadPlan p{};
   T = std::max(T, int64_t(1));
-  // Time over D of the stream's 32 x 128 tiles (768 at a time) and the wide
-  // kernel's (256 at a time), measured at D = 512 to 7168: 4.8 ns for a round
-  // and 12 ps for a tile; 15.2 ns for a round of 64 rows, 24.5 ns of 128.
+  // Time over D, in ns, of the stream's 32 x 128 tiles and of the wide kernel, whose 512-column tiles take 64 rows while
+  // each compute unit has one at most, else 128 (measured at D = 1056 to 7168, T = 33 to 256, N = 32003 and 129280). The
+  // stream: 0.0117 a tile, 0.013 where rows are no multiple of 128 bytes. The wide kernel: a round 13 and 0.046 for 1000
+  // weight rows (T = 64, N = 129280: 19), 14 and 0.13 then, as its tiles read lines twice; 4.5 for each 32 rows past 64;
+  // 26 for each of several rounds.
+  const bool whole = D % 256 == 0;
   const int64_t cols512 = (N + kEtCols - 1) / kEtCols, tiles64 = (T + 63) / 64 * cols512;
-  const int64_t rounds128 = ((T + 127) / 128 * cols512 + 255) / 256, tiles32 = (T + 31) / 32 * ((N + 127) / 128);
-  p.wide = T > 32 && (tiles64 <= kOneRound ? 15.2 : 24.5 * (double)rounds128) < std::max(4.8, 0.012 * (double)tiles32);
+  const int64_t tiles128 = (T + 127) / 128 * cols512, tiles32 = (T + 31) / 32 * ((N + 127) / 128);
+  double wide_ns = 26.0 * (double)((tiles128 + 255) / 256);
+  if (tiles64 <= kOneRound || tiles128 <= kOneRound)
+    wide_ns = (whole ? 13.0 + 4.6e-5 * (double)N : 14.0 + 1.3e-4 * (double)N) +
+              (tiles64 <= kOneRound ? 0.0 : 4.5 * (double)((std::min(T, int64_t(128)) + 31) / 32 - 2));
+  p.wide = T > 32 && wide_ns < std::max(4.8, (whole ? 0.0117 : 0.013) * (double)tiles32);
   p.block_shift = p.wide ? 6 : 5;
   int64_t piece = kMaxRange / (D / 2) / 512 * 512;  // a piece's codes lie within a buffer's range
   // A piece's softmax weights take 512 MB at most, but 4096 columns at least.
@@ -873,6 +880,28 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   return p;
 }
 
+// The weights' loads pass the caches where their lines are read once: D = 7168,
+// N = 129280, T = 1 83 us (94 through them), T = 32 97 (111). Not with more
+// row tiles (T = 74, D = 5120: 123 us, 118 through the caches), nor for a D
+// that is no multiple of 256, whose steps end inside a line (T = 8, D = 5664:
+// 74 and 58; T = 1, D = 5280, N = 126034: 101 and 91; T = 74, D = 5184: 165 and
+// 133).
+template <Out M, int MR, int KB, int KG>
+static hipError_t launch_stream(const ExpertArgs& a, Scales sc, int col_tiles, hipStream_t stream) {
+  const int row_tiles = (a.R + MR - 1) / MR, grid = row_tiles * col_tiles;
+  constexpr int NT = KG * kEsThreads;
+  if (sc == Scales::k4) head_stream_kernel<M, MR, KB, KG, Scales::k4, 0><<<grid, NT, 0, stream>>>(a, row_tiles);
+  else if (sc == Scales::kSkewed) head_stream_kernel<M, MR, KB, KG, Scales::kSkewed, 0><<<grid, NT, 0, stream>>>(a, row_tiles);
+  else if (row_tiles > 1) head_stream_kernel<M, MR, KB, KG, Scales::k16, 0><<<grid, NT, 0, stream>>>(a, row_tiles);
+  else head_stream_kernel<M, MR, KB, KG, Scales::k16, kNtAux><<<grid, NT, 0, stream>>>(a, row_tiles);
+  return hipGetLastError();
+}
+
+// Up to this many 16-row tiles, one to a compute unit, two K groups share each:
+// T = 16, D = 7168, N = 32000 27.7 -> 23.0 us; T = 28, D = 5344, N = 3501 24.8 ->
+// 19.8; D = 2048 11.9 -> 10.8; level at 1024, 4.8 -> 5.8 at 512.
+constexpr int kHeadFewTiles = 256;
+
 template <Out M>
 static hipError_t launch_logits(const ExpertArgs& a, bool wide, hipStream_t stream) {
   const Scales sc = scales_of(a);
@@ -887,17 +916,10 @@ static hipError_t launch_logits(const ExpertArgs& a, bool wide, hipStream_t stre
     return hipGetLastError();
   }
   const int col_tiles = (a.N + kEsRows * kEsWaves - 1) / (kEsRows * kEsWaves);
-  if (a.R <= 16) {
-    if (sc == Scales::k16) head_stream_kernel<M, 16, 512, Scales::k16><<<col_tiles, kEsThreads, 0, stream>>>(a, 1);
-    else if (sc == Scales::k4) head_stream_kernel<M, 16, 512, Scales::k4><<<col_tiles, kEsThreads, 0, stream>>>(a, 1);
-    else head_stream_kernel<M, 16, 512, Scales::kSkewed><<<col_tiles, kEsThreads, 0, stream>>>(a, 1);
-    return hipGetLastError();
-  }
-  const int row_tiles = (a.R + 31) / 32, grid = row_tiles * col_tiles;
-  if (sc == Scales::k16) head_stream_kernel<M, 32, 256, Scales::k16><<<grid, kEsThreads, 0, stream>>>(a, row_tiles);
-  else if (sc == Scales::k4) head_stream_kernel<M, 32, 256, Scales::k4><<<grid, kEsThreads, 0, stream>>>(a, row_tiles);
-  else head_stream_kernel<M, 32, 256, Scales::kSkewed><<<grid, kEsThreads, 0, stream>>>(a, row_tiles);
-  return hipGetLastError();
+  const int tiles16 = (a.R + 15) / 16 * col_tiles;
+  if (tiles16 <= kHeadFewTiles && a.D > 1024) return launch_stream<M, 16, 1024, 2>(a, sc, col_tiles, stream);
+  if (a.R <= 16) return launch_stream<M, 16, 512, 1>(a, sc, col_tiles, stream);
+  return launch_stream<M, 32, 256, 1>(a, sc, col_tiles, stream);
 }
 
 // The tokens' logits into logq, unless a row's workgroup computes them itself.
