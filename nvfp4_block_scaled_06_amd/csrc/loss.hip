@@ -32,7 +32,12 @@ constexpr int kHeadTokens = 1024;  // ROUTER_MAX_TEACHER
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------------------
-// Logits of a piece: the experts' tiles, one matrix.
+// Logits of a piece: the experts' tiles, one matrix, with softmax_block.hpp's
+// epilogue. D = 7168, N = 129280 (521 MB of weights), the kernel alone:
+//   stream  T = 1 83 us, T = 32 97: HBM, 6.3 and 5.4 TB/s of reads;
+//   wide    T = 1024 1.45 ms, T = 4096 5.7 (1.31 and 1.33 PFLOP/s), keeping the
+//           weights 1.51 and 6.2: the matrix cores, 62 % busy at the clock that
+//           their power leaves.
 // ---------------------------------------------------------------------------
 template <Out M, int MR, int KB, int KG, Scales S, int AUX>
 __global__ __launch_bounds__(KG * kEsThreads) void head_stream_kernel(ExpertArgs a, int row_tiles) {
@@ -205,7 +210,9 @@ __device__ __forceinline__ void token_dots(const HeadArgs& a, int64_t t, const i
 
 // More tokens than a row's workgroup has wavefronts: their logits (over tau)
 // go to logq first, 16 tokens of a row per workgroup, each wavefront's four
-// weight rows in flight together.
+// weight rows in flight together. Bound by the gathered rows: T = 1024, K = 64,
+// D = 7168 (264 MB) 45 us, 5.9 TB/s; T = 32 6.9 us. (A row at a time in the row's
+// one workgroup: T = 32 156 us for the whole call, 113 so.)
 constexpr int kTokWaves = 4;
 constexpr int kTokPerWave = 4;
 __global__ __launch_bounds__(64 * kTokWaves) void head_dots_kernel(HeadArgs a) {
@@ -315,6 +322,9 @@ __device__ __forceinline__ void row_loss(const HeadArgs& a, int64_t t, float2 v,
   if (lane == 0) list.count = out == 0 || tr.y == 0.0f ? -1 : out;
 }
 
+// Without a gradient: the end of a row, from its blocks' (m, s). Latency at few
+// rows (5.4 us at T = 1, N = 129280: 4040 blocks, 32 KB); T = 4096 with 2020
+// blocks each: 23 us, 2.9 TB/s.
 __global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a, int dots) {
   __shared__ TokLds lds;
   const int64_t t = blockIdx.x;
@@ -339,7 +349,7 @@ struct NormArgs {
 };
 
 // One workgroup per row. LAST: the sums are complete, and it goes on to the
-// row's loss.
+// row's loss. 5.5 us at T = 203, 8.8 with 37 tokens, 23 at T = 4096: latency.
 constexpr int kNormThreads = 64 * kTokWaves;
 template <bool LAST>
 __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, HeadArgs ha, int dots) {
@@ -385,6 +395,14 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, Hea
 //    32 further on to MFMA j.
 // All double-buffered in LDS, one barrier per step; a step's loads go out a step
 // before they are written there.
+// D = 7168, N = 129280: T = 4096 6.23 ms for the two pieces (1.22 PFLOP/s), T =
+// 1024 1.56, bound by the matrix cores and their power as the logits' tiles;
+// with few rows by the weights (T = 1 to 8: 117 us for 521 MB, 4.5 TB/s), then
+// by splits that leave a workgroup few steps (T = 203, D = 2080, N = 32003: 48
+// us for 27 GFLOP, 11 steps and 39 MB of sums).
+// Fragments read and converted between the MFMAs rather than ahead of them:
+// 14.1 -> 13.7 ms for the whole call at T = 4096; scales kept in fp16: 13.4 ->
+// 12.9; sums through LDS: T = 203 131 -> 113 us.
 // ---------------------------------------------------------------------------
 constexpr int kGwThreads = 512;
 constexpr int kGwRows = 128, kGwCols = 512, kGwStep = 128;
@@ -832,7 +850,8 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   p.wide = T > 32 && wide_ns < std::max(4.8, (whole ? 0.0117 : 0.013) * (double)tiles32);
   p.block_shift = p.wide ? 6 : 5;
   int64_t piece = kMaxRange / (D / 2) / 512 * 512;  // a piece's codes lie within a buffer's range
-  // A piece's softmax weights take 512 MB at most, but 4096 columns at least.
+  // A piece's softmax weights take 512 MB at most, but 4096 columns at least. (T = 2048, D = 7168, N = 129280: 6.44 ms,
+  // with 256 MB 6.59, with 1 GB 6.45.)
   if (grad) piece = std::min(piece, std::max((int64_t(1) << 28) / T / 512 * 512, int64_t(4096)));
   // A launch has fewer than 2^32 threads: 512 for a tile of 128 x 512, or of 64 x 512 where those are few.
   piece = std::min(piece, (int64_t(1) << 37) / T / 512 * 512);

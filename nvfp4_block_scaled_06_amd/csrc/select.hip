@@ -20,6 +20,13 @@
 // which are put together in LDS and ranked against each other. Rows where too
 // many survive (equal logits, for example) take the rounds, as those that 32
 // bits cannot decide do.
+//
+// Measured, k = 8: T = 1, 256 experts with a bias and four of eight groups 4.6
+// us (the call 10, which the launch and the binding make); T = 32768, 384
+// experts, softmax: 14.6 us, 3.6 TB/s of the 52 MB that it has to read and
+// write, part instructions and part memory (as 12.2 for 256 experts); equal
+// logits throughout, every row by the rounds: 256 experts 26. Gradient, 256
+// experts: T = 8192 6.2 us, T = 32768 11.3, 3.2 TB/s with 34 MB of it stored.
 #include "../../include/nvfp4_router.h"
 #include <algorithm>
 

@@ -38,6 +38,9 @@ Parity status per function:
 * ``grouped_ref``: pinned (hand cases with per-group weight scales and a
   shared activation scale set by another group, offsets closed form, exact
   rational brute force on tiny groups, empty groups).
+* ``select_ref``, ``loss_ref``: pinned (hand cases, gradients against differences,
+  planted mistakes that must be caught); parity unpinned by the pages, whose
+  router has one rule and whose lm_head is greedy.
 
 Two conventions are not fixed by the pages and are parity unpinned by them:
 the nibble order of packed codes (even element in the low nibble) and the
