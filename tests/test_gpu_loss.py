@@ -93,6 +93,28 @@ def test_cross_entropy(dev, T, D, N):
     compare(dict(loss=loss, lse=lse), ref)
 
 
+# Each tile of the logits with each way of its scales (D a multiple of 256, of 64, of 32): streams of 16 rows with two K
+# groups, of 32 rows, alone on their weights and not; 64-row wide tiles, one round of 128-row ones, several rounds.
+TILES = [(5, 1280, 700), (16, 1088, 900), (3, 1056, 500), (40, 1280, 1100), (33, 1088, 900), (20, 96, 900), (40, 1536, 13000),
+         (64, 1600, 8300), (36, 1120, 11897),
+         (200, 256, 32003), (250, 64, 32500), (195, 96, 32003),
+         (96, 256, 100000), (128, 256, 99999), (200, 64, 65000), (180, 96, 65000), (260, 320, 40000), (270, 512, 40001),
+         (400, 256, 50000), (500, 64, 40003), (420, 160, 45007)]
+
+
+@pytest.mark.parametrize("T,D,N", TILES)
+def test_every_tile(dev, T, D, N):
+    log(f"every tile T={T} D={D} N={N}")
+    xq, wq = operands(T, D, N, T + D + N, dev)
+    y = make_targets(T, N, T)
+    ref = lr.loss_ref(host(xq), host(wq), y[:, None])
+    loss, lse, dx = rt.lmhead_loss(xq, wq, up(y, dev), workspace(T, D, N, True, dev), want_grad=True)
+    alone = rt.lmhead_loss(xq, wq, up(y, dev), workspace(T, D, N, False, dev))
+    torch.cuda.synchronize()
+    compare(dict(loss=loss, lse=lse, dx=dx), ref)
+    compare(dict(loss=alone[0], lse=alone[1]), ref)
+
+
 def make_teacher(T, K, N, dtype, seed):
     r = np.random.default_rng(seed)
     tok = r.integers(0, N, (T, K)).astype(np.int32)
