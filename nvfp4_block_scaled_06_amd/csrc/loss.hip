@@ -32,36 +32,6 @@ constexpr int kHeadTokens = 1024;  // ROUTER_MAX_TEACHER
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------------------
-// Logits of a piece: the experts' tiles, one matrix, with softmax_block.hpp's
-// epilogue. D = 7168, N = 129280 (521 MB of weights), the kernel alone:
-//   stream  T = 1 83 us, T = 32 97: HBM, 6.3 and 5.4 TB/s of reads;
-//   wide    T = 1024 1.45 ms, T = 4096 5.7 (1.31 and 1.33 PFLOP/s), keeping the
-//           weights 1.51 and 6.2: the matrix cores, 62 % busy at the clock that
-//           their power leaves.
-// ---------------------------------------------------------------------------
-template <Out M, int MR, int KB, int KG, Scales S, int AUX>
-__global__ __launch_bounds__(KG * kEsThreads) void head_stream_kernel(ExpertArgs a, int row_tiles) {
-  __shared__ StreamLds<MR, KB, KG> lds;
-  // The row tiles of one column tile side by side on one XCD: they read the same weights.
-  const int n = xcd_order(blockIdx.x, gridDim.x), ct = n / row_tiles, row0 = (n - ct * row_tiles) * MR;
-  const ExpertTile tile{{0, row0, min(MR, a.R - row0)}, ct};
-  stream_tile<M, MR, KB, KG, S, AUX>(a, tile, lds);
-}
-
-template <Out M, Scales S>
-__global__ __launch_bounds__(kEtThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_wide_kernel(
-    ExpertArgs a, int row_tiles, int tile_rows) {
-  __shared__ TileLds lds;
-  const int n = xcd_order(blockIdx.x, gridDim.x), ct = n / row_tiles, row0 = (n - ct * row_tiles) * tile_rows;
-  const ExpertTile tile{{0, row0, min(tile_rows, a.R - row0)}, ct};
-  const int nr = tile.rt.nr;
-  if (nr > 96) wide_tile<M, 4, S>(a, tile, lds);
-  else if (nr > 64) wide_tile<M, 3, S>(a, tile, lds);
-  else if (nr > 32) wide_tile<M, 2, S>(a, tile, lds);
-  else wide_tile<M, 1, S>(a, tile, lds);
-}
-
-// ---------------------------------------------------------------------------
 // The tokens of the loss.
 // ---------------------------------------------------------------------------
 // A row's tokens that the gradient multiplies by themselves: q - p, for each
@@ -209,35 +179,80 @@ __device__ __forceinline__ void token_dots(const HeadArgs& a, int64_t t, const i
 }
 
 // More tokens than a row's workgroup has wavefronts: their logits (over tau)
-// go to logq first, 16 tokens of a row per workgroup, each wavefront's four
-// weight rows in flight together. Bound by the gathered rows: T = 1024, K = 64,
-// D = 7168 (264 MB) 45 us, 5.9 TB/s; T = 32 6.9 us. (A row at a time in the row's
-// one workgroup: T = 32 156 us for the whole call, 113 so.)
+// go to logq before it runs, 16 tokens of a row per workgroup (of four wavefronts), each
+// wavefront's four weight rows in flight together. Bound by the gathered rows: T = 1024, K = 64,
+// D = 7168 (264 MB) 45 us, 5.9 TB/s. (A row at a time in the row's one workgroup:
+// T = 32 156 us for the whole call, 113 so.)
 constexpr int kTokWaves = 4;
 constexpr int kTokPerWave = 4;
-__global__ __launch_bounds__(64 * kTokWaves) void head_dots_kernel(HeadArgs a) {
+// Workgroup n of those that take row t's tokens.
+__device__ __forceinline__ void token_block(const HeadArgs& a, int64_t t, int n) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = blockIdx.x;
-  const int j0 = (blockIdx.y * kTokWaves + wave) * kTokPerWave;
+  const int j0 = (n * (int)(blockDim.x >> 6) + wave) * kTokPerWave;
   if (j0 >= a.K) return;
   const float scale = load_early(a.gsa) * load_early(a.gsw) / a.tau;
-  int n[kTokPerWave];
+  int tk[kTokPerWave];
   float z[kTokPerWave];
 #pragma unroll
-  for (int u = 0; u < kTokPerWave; ++u) n[u] = a.tokens[t * a.K + min(j0 + u, a.K - 1)];
-  token_dots<kTokPerWave>(a, t, n, z);
+  for (int u = 0; u < kTokPerWave; ++u) tk[u] = a.tokens[t * a.K + min(j0 + u, a.K - 1)];
+  token_dots<kTokPerWave>(a, t, tk, z);
 #pragma unroll
   for (int u = 0; u < kTokPerWave; ++u)
     if (lane == u && j0 + u < a.K) a.logq[t * a.K + j0 + u] = z[u] * scale;
 }
 
+__host__ __device__ constexpr int token_blocks(int K, int threads) {
+  return (K + threads / 64 * kTokPerWave - 1) / (threads / 64 * kTokPerWave);
+}
+
+__global__ __launch_bounds__(64 * kTokWaves) void head_dots_kernel(HeadArgs a) {
+  token_block(a, blockIdx.x, blockIdx.y);
+}
+
+// ---------------------------------------------------------------------------
+// Logits of a piece: the experts' tiles, one matrix, with softmax_block.hpp's
+// epilogue. D = 7168, N = 129280 (521 MB of weights), the kernel alone:
+//   stream  T = 1 83 us, T = 32 97: HBM, 6.3 and 5.4 TB/s of reads;
+//   wide    T = 1024 1.45 ms, T = 4096 5.7 (1.31 and 1.33 PFLOP/s), keeping the
+//           weights 1.51 and 6.2: the matrix cores, 62 % busy at the clock that
+//           their power leaves.
+// ---------------------------------------------------------------------------
+template <Out M, int MR, int KB, int KG, Scales S, int AUX>
+__global__ __launch_bounds__(KG * kEsThreads) void head_stream_kernel(ExpertArgs a, int row_tiles, int tiles, HeadArgs h) {
+  __shared__ StreamLds<MR, KB, KG> lds;
+  if ((int)blockIdx.x >= tiles) {
+    const int b = blockIdx.x - tiles, per_row = token_blocks(h.K, KG * kEsThreads), t = b / per_row;
+    return token_block(h, t, b - t * per_row);
+  }
+  // The row tiles of one column tile side by side on one XCD: they read the same weights.
+  const int n = xcd_order(blockIdx.x, tiles), ct = n / row_tiles, row0 = (n - ct * row_tiles) * MR;
+  const ExpertTile tile{{0, row0, min(MR, a.R - row0)}, ct};
+  stream_tile<M, MR, KB, KG, S, AUX>(a, tile, lds);
+}
+
+template <Out M, Scales S>
+__global__ __launch_bounds__(kEtThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) void head_wide_kernel(
+    ExpertArgs a, int row_tiles, int tile_rows) {
+  __shared__ TileLds lds;
+  const int n = xcd_order(blockIdx.x, gridDim.x), ct = n / row_tiles, row0 = (n - ct * row_tiles) * tile_rows;
+  const ExpertTile tile{{0, row0, min(tile_rows, a.R - row0)}, ct};
+  const int nr = tile.rt.nr;
+  if (nr > 96) wide_tile<M, 4, S>(a, tile, lds);
+  else if (nr > 64) wide_tile<M, 3, S>(a, tile, lds);
+  else if (nr > 32) wide_tile<M, 2, S>(a, tile, lds);
+  else wide_tile<M, 1, S>(a, tile, lds);
+}
+
+// ---------------------------------------------------------------------------
+// The rows' losses.
+// ---------------------------------------------------------------------------
 // A row's loss by its workgroup, from its logits' sum (m, s). Up to as many
 // tokens as wavefronts have their logits computed here (first by row_dots),
 // `dots` says.
 struct TokLds {
   float2 part[kTokWaves];
   float terms[kTokWaves], zs[kTokWaves], lz[kHeadTokens];
-  int tk[kHeadTokens];
+  alignas(16) int tk[kHeadTokens];
 };
 
 __device__ __forceinline__ void row_dots(const HeadArgs& a, int64_t t, TokLds& lds) {
@@ -296,26 +311,39 @@ __device__ __forceinline__ void row_loss(const HeadArgs& a, int64_t t, float2 v,
     a.lse[t] = lse;
   }
   if (!a.lists) return;
-  // The first wavefront lists the places that name a token, in order. A token
-  // named more than once has its q at its first place.
+  // q - p of each place. A token named more than once has its q at its first
+  // place: every place looks at all before it, four at a time. (T = 30, K = 1024,
+  // D = 7168: 367 us for the whole call; by one wavefront, a place at a time, 946.)
+  const int* tk = lds.tk;
+  for (int j = threadIdx.x; j < a.K; j += 64 * kTokWaves) {
+    const int n = tk[j];
+    int again = 0;
+    const int upto = min((j | 63) + 1, a.K);  // of the wavefront
+#pragma unroll 4
+    for (int i = 0; i < upto; i += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(tk + i);
+      again |= (int)(o.x == n && i < j) | (int)(o.y == n && i + 1 < j) | (int)(o.z == n && i + 2 < j) | (int)(o.w == n && i + 3 < j);
+    }
+    if (n >= 0 && n < a.N) {
+      const float z = dots ? zs[j] : lz[j];
+      const float p = a.teacher ? expf(teacher_at(a, t * a.K + j) - tr.x) / tr.y : 1.0f;
+      lz[j] = (again ? 0.0f : expf(z - lse)) - p;
+    }
+  }
+  __syncthreads();
+  // The first wavefront lists the places that name a token, in order.
   if (wave != 0) return;
   TokenList& list = a.lists[t];
-  const int* tk = lds.tk;
   int out = 0;
   for (int j0 = 0; j0 < a.K; j0 += 64) {
     const int j = j0 + lane;
     const int n = j < a.K ? tk[j] : -1;
     const bool valid = n >= 0 && n < a.N;
-    bool first = true;
-#pragma unroll 8
-    for (int i = 0; i < min(j0 + 64, a.K); ++i) first = first && (i >= j || tk[i] != n);
     const uint64_t bal = __ballot(valid);
     if (valid) {
       const int at = out + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(bal >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)bal, 0u));
-      const float z = dots ? zs[j] : lz[j];
-      const float p = a.teacher ? expf(teacher_at(a, t * a.K + j) - tr.x) / tr.y : 1.0f;
       list.token[at] = n;
-      list.coef[at] = (first ? expf(z - lse) : 0.0f) - p;
+      list.coef[at] = lz[j];
     }
     out += (int)__popcll(bal);
   }
@@ -349,7 +377,7 @@ struct NormArgs {
 };
 
 // One workgroup per row. LAST: the sums are complete, and it goes on to the
-// row's loss. 5.5 us at T = 203, 8.8 with 37 tokens, 23 at T = 4096: latency.
+// row's loss. 5.5 us at T = 203, 6.6 with 37 tokens, 23 at T = 4096: latency.
 constexpr int kNormThreads = 64 * kTokWaves;
 template <bool LAST>
 __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, HeadArgs ha, int dots) {
@@ -899,6 +927,19 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   return p;
 }
 
+static hipError_t launch_dots(const HeadArgs& h, hipStream_t stream) {
+  head_dots_kernel<<<dim3(h.T, token_blocks(h.K, 64 * kTokWaves)), 64 * kTokWaves, 0, stream>>>(h);
+  return hipGetLastError();
+}
+
+// The stream's launch takes the tokens along, in up to this many workgroups (a
+// launch's threads are fewer than 2^32), rather than one of their own before
+// it: T = 21, K = 37 of D = 1056 21.1 -> 18.8 us without a gradient; T = 32, K =
+// 64 of 7168 113.7 -> 109.5; T = 1000, K = 64, D = 1024, N = 4000 33.6 -> 31.3; K =
+// 1024, T = 30 153 -> 145. (The wide kernel has one workgroup to a compute unit,
+// too few for gathers.)
+constexpr int64_t kHeadAlong = 1 << 20;
+
 // The weights' loads pass the caches where their lines are read once: D = 7168,
 // N = 129280, T = 1 83 us (94 through them), T = 32 97 (111). Not with more
 // row tiles (T = 74, D = 5120: 123 us, 118 through the caches), nor for a D
@@ -906,13 +947,20 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
 // 74 and 58; T = 1, D = 5280, N = 126034: 101 and 91; T = 74, D = 5184: 165 and
 // 133).
 template <Out M, int MR, int KB, int KG>
-static hipError_t launch_stream(const ExpertArgs& a, Scales sc, int col_tiles, hipStream_t stream) {
-  const int row_tiles = (a.R + MR - 1) / MR, grid = row_tiles * col_tiles;
+static hipError_t launch_stream(const ExpertArgs& a, const HeadArgs& h, bool tokens, Scales sc, int col_tiles,
+                                hipStream_t stream) {
+  const int row_tiles = (a.R + MR - 1) / MR, tiles = row_tiles * col_tiles;
   constexpr int NT = KG * kEsThreads;
-  if (sc == Scales::k4) head_stream_kernel<M, MR, KB, KG, Scales::k4, 0><<<grid, NT, 0, stream>>>(a, row_tiles);
-  else if (sc == Scales::kSkewed) head_stream_kernel<M, MR, KB, KG, Scales::kSkewed, 0><<<grid, NT, 0, stream>>>(a, row_tiles);
-  else if (row_tiles > 1) head_stream_kernel<M, MR, KB, KG, Scales::k16, 0><<<grid, NT, 0, stream>>>(a, row_tiles);
-  else head_stream_kernel<M, MR, KB, KG, Scales::k16, kNtAux><<<grid, NT, 0, stream>>>(a, row_tiles);
+  const bool along = tokens && (int64_t)h.T * token_blocks(h.K, NT) <= kHeadAlong;
+  if (tokens && !along) {
+    const hipError_t e = launch_dots(h, stream);
+    if (e != hipSuccess) return e;
+  }
+  const int grid = tiles + (along ? h.T * token_blocks(h.K, NT) : 0);
+  if (sc == Scales::k4) head_stream_kernel<M, MR, KB, KG, Scales::k4, 0><<<grid, NT, 0, stream>>>(a, row_tiles, tiles, h);
+  else if (sc == Scales::kSkewed) head_stream_kernel<M, MR, KB, KG, Scales::kSkewed, 0><<<grid, NT, 0, stream>>>(a, row_tiles, tiles, h);
+  else if (row_tiles > 1) head_stream_kernel<M, MR, KB, KG, Scales::k16, 0><<<grid, NT, 0, stream>>>(a, row_tiles, tiles, h);
+  else head_stream_kernel<M, MR, KB, KG, Scales::k16, kNtAux><<<grid, NT, 0, stream>>>(a, row_tiles, tiles, h);
   return hipGetLastError();
 }
 
@@ -921,10 +969,14 @@ static hipError_t launch_stream(const ExpertArgs& a, Scales sc, int col_tiles, h
 // 19.8; D = 2048 11.9 -> 10.8; level at 1024, 4.8 -> 5.8 at 512.
 constexpr int kHeadFewTiles = 256;
 
+// A piece's logits; `tokens`: and the tokens' own into logq, which the stream's
+// launch takes along.
 template <Out M>
-static hipError_t launch_logits(const ExpertArgs& a, bool wide, hipStream_t stream) {
+static hipError_t launch_logits(const ExpertArgs& a, const HeadArgs& h, bool wide, bool tokens, hipStream_t stream) {
   const Scales sc = scales_of(a);
   if (wide) {
+    const hipError_t e = tokens ? launch_dots(h, stream) : hipSuccess;
+    if (e != hipSuccess) return e;
     const int cols = (a.N + kEtCols - 1) / kEtCols;
     // 64 rows while each compute unit then has one tile at most.
     const int tile_rows = (a.R + 63) / 64 * cols <= kOneRound ? 64 : kEtRows;
@@ -936,17 +988,9 @@ static hipError_t launch_logits(const ExpertArgs& a, bool wide, hipStream_t stre
   }
   const int col_tiles = (a.N + kEsRows * kEsWaves - 1) / (kEsRows * kEsWaves);
   const int tiles16 = (a.R + 15) / 16 * col_tiles;
-  if (tiles16 <= kHeadFewTiles && a.D > 1024) return launch_stream<M, 16, 1024, 2>(a, sc, col_tiles, stream);
-  if (a.R <= 16) return launch_stream<M, 16, 512, 1>(a, sc, col_tiles, stream);
-  return launch_stream<M, 32, 256, 1>(a, sc, col_tiles, stream);
-}
-
-// The tokens' logits into logq, unless a row's workgroup computes them itself.
-static hipError_t launch_dots(const HeadArgs& h, bool dots, hipStream_t stream) {
-  if (dots) return hipSuccess;
-  constexpr int per = kTokWaves * kTokPerWave;
-  head_dots_kernel<<<dim3(h.T, (h.K + per - 1) / per), 64 * kTokWaves, 0, stream>>>(h);
-  return hipGetLastError();
+  if (tiles16 <= kHeadFewTiles && a.D > 1024) return launch_stream<M, 16, 1024, 2>(a, h, tokens, sc, col_tiles, stream);
+  if (a.R <= 16) return launch_stream<M, 16, 512, 1>(a, h, tokens, sc, col_tiles, stream);
+  return launch_stream<M, 32, 256, 1>(a, h, tokens, sc, col_tiles, stream);
 }
 
 static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream_t stream) {
@@ -958,7 +1002,7 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
   float2* stats = reinterpret_cast<float2*>(ws + p.stats_at);
   a.soft.scale = kLog2e / h.tau;
   a.soft.blocks = (int)p.blocks;
-  const bool dots = h.K <= kTokWaves;
+  const bool dots = h.K <= kTokWaves;  // the row's workgroup computes its tokens' logits
   hipError_t e;
   if (!grad) {
     for (int64_t i = 0; i < p.pieces; ++i) {
@@ -968,11 +1012,10 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
       a.N = (int)std::min(p.piece, h.N - n0);
       a.soft.stats = stats + (n0 >> p.block_shift);
       a.soft.used = (int)(p.blocks - (n0 >> p.block_shift));
-      if ((e = launch_logits<Out::kSums>(a, p.wide, stream)) != hipSuccess) return e;
+      if ((e = launch_logits<Out::kSums>(a, h, p.wide, !dots && i == 0, stream)) != hipSuccess) return e;
     }
     h.stats = stats;
     h.blocks = h.used = (int)p.blocks;
-    if ((e = launch_dots(h, dots, stream)) != hipSuccess) return e;
     head_tokens_kernel<<<h.T, 64 * kTokWaves, 0, stream>>>(h, dots);
     return hipGetLastError();
   }
@@ -981,7 +1024,6 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
   float* ref = reinterpret_cast<float*>(ws + p.ref_at);
   float* part = reinterpret_cast<float*>(ws + p.part_at);
   h.lists = reinterpret_cast<TokenList*>(ws + p.lists_at);
-  if ((e = launch_dots(h, dots, stream)) != hipSuccess) return e;
   a.soft.stats = stats;
   a.soft.used = (int)p.blocks;
   a.soft.e = reinterpret_cast<_Float16*>(ws + p.e_at);
@@ -992,7 +1034,7 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
     a.ws = h.ws + n0 * (h.D / 16);
     a.N = (int)std::min(p.piece, h.N - n0);
     a.soft.ref = i ? ref : nullptr;
-    if ((e = launch_logits<Out::kWeights>(a, p.wide, stream)) != hipSuccess) return e;
+    if ((e = launch_logits<Out::kWeights>(a, h, p.wide, !dots && i == 0, stream)) != hipSuccess) return e;
     NormArgs n{};
     n.stats = stats; n.blocks = (int)p.blocks;
     n.used = (a.N + 63) / 64 << (6 - p.block_shift);
