@@ -978,7 +978,8 @@ static hipError_t launch_logits(const ExpertArgs& a, const HeadArgs& h, bool wid
     const hipError_t e = tokens ? launch_dots(h, stream) : hipSuccess;
     if (e != hipSuccess) return e;
     const int cols = (a.N + kEtCols - 1) / kEtCols;
-    // 64 rows while each compute unit then has one tile at most.
+    // 64 rows while each compute unit then has one tile at most (T = 192, D = 4096, N = 32000: 62 us, with 128 92; more
+    // tiles: T = 256, D = 7168, N = 129280 394 us with 128, 484 with 64).
     const int tile_rows = (a.R + 63) / 64 * cols <= kOneRound ? 64 : kEtRows;
     const int row_tiles = (a.R + tile_rows - 1) / tile_rows, grid = row_tiles * cols;
     if (sc == Scales::k16) head_wide_kernel<M, Scales::k16><<<grid, kEtThreads, 0, stream>>>(a, row_tiles, tile_rows);
