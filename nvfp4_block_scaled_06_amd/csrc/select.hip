@@ -127,7 +127,11 @@ __device__ __forceinline__ int sel_place(int e) {
 }
 
 // Groups that stay, from the row's keys in LDS: bit g << sh. `unsure`: the
-// border is closer than 2 err (a score is a sum of two keys).
+// border is closer than the two scores' errors. A score's goes by the size of
+// its keys, not by its own: keys of +b and -b leave a sum near 1 that is off by
+// steps of b. (Half of err is more than one key's error, and what is left of
+// it more than the sum's rounding; a softmax's error that all its keys share is
+// in a sum of two no more than once, as two scores add up to 1 at most.)
 template <int LPR, class F>
 __device__ __forceinline__ uint64_t sel_groups(const SelectArgs& a, const F* vals, float err, bool& unsure) {
   const F ninf = -(F)__builtin_inff();
@@ -159,9 +163,12 @@ __device__ __forceinline__ uint64_t sel_groups(const SelectArgs& a, const F* val
   }
   const bool keep = g < a.groups && rank < a.kept;
   if (err > 0.0f) {
-    const F lowest = -row_fmax<LPR, F>(keep ? -score : ninf);
-    const F next = row_fmax<LPR, F>(!keep && g < a.groups ? score : ninf);
-    if (lowest > ninf && lowest - next <= (F)(2.0f * err) * (F)fmaxf(1.0f, fabsf((float)lowest))) unsure = true;
+    const float m1 = fmaxf(1.0f, fabsf((float)b1)), m2 = fmaxf(1.0f, fabsf((float)b2));
+    float slack = err * (a.top == 2 && a.size > 1 ? 0.5f * (m1 + m2) : m1);
+    if (!(slack < __builtin_inff())) slack = 0.0f;  // infinite keys are exact
+    const F lowest = -row_fmax<LPR, F>(keep ? (F)slack - score : ninf);
+    const F next = row_fmax<LPR, F>(!keep && g < a.groups ? score + (F)slack : ninf);
+    if (lowest > ninf && lowest <= next) unsure = true;
   }
   return __ballot(keep) >> row;
 }
