@@ -502,12 +502,15 @@ int lmhead_distill(const uint8_t* x_codes, const uint8_t* x_scales, const float*
  *   - the experts form `groups` groups of E / groups neighbours; a group's
  *     score is the sum of its group_top (1 or 2) largest keys, and experts
  *     outside the topk_groups groups with the largest scores (a tie going to
- *     the lower group) are left out;
+ *     the larger logit where a score is one key, then to the lower group) are
+ *     left out;
  *   - topk_idx [T, k] int32: the k largest keys among the rest, in descending
- *     order, a tie going to the lower expert;
+ *     order, a tie going to the larger logit, then to the lower expert;
  *   - topk_w [T, k] fp32: routed_scale * s / (renormalize ? sum of the chosen
  *     s : 1), the bias left out.
- * The order is that of keys computed in 64 bits. An expert whose logit is
+ * The order is that of keys computed in 64 bits; with the ties' rule that is the
+ * logits' own order wherever there is no bias, or the same one for all, also
+ * where scores saturate (sigmoid logits of 40 and 50). An expert whose logit is
  * -infinity or NaN, or whose key is, is never chosen (it counts as -infinity
  * in its group); where fewer than k remain, the places left hold -1 and weight
  * 0, which grouped_plan takes as slots of no expert. Renormalised weights hold

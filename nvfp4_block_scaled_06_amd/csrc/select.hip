@@ -3,12 +3,14 @@
 //
 // Per row: s = sigmoid(l) or softmax(l); key = s + bias; of `groups` groups of
 // neighbouring experts the `kept` with the largest sums of their one or two
-// best keys stay; the k largest keys among them in descending order, ties to
-// the lower expert; w = scale s / (1 or the sum of the chosen s).
+// best keys stay; the k largest keys among them in descending order; w = scale
+// s / (1 or the sum of the chosen s).
 //
 // The order is that of keys computed in 64 bits, so it does not hang on how a
-// logistic function rounds. Nearly every row is decided in 32 bits: without a
-// bias the order of the logits is the order of the keys, and is exact; with
+// logistic function rounds; keys that are equal there (saturated scores, say)
+// go by their logits, then to the lower expert; groups of equal scores likewise
+// where a score is one key, and to the lower group where it is a sum of two. Nearly every row is
+// decided in 32 bits: without a bias that order is the logits' own; with
 // one, keys computed in 32 bits are off by less than kKeyErr, and where two
 // neighbours in the order, or the last group kept and the first one left out,
 // are closer than that, the wavefront does its rows again in 64 bits (about
@@ -132,39 +134,61 @@ __device__ __forceinline__ int sel_place(int e) {
 // steps of b. (Half of err is more than one key's error, and what is left of
 // it more than the sum's rounding; a softmax's error that all its keys share is
 // in a sum of two no more than once, as two scores add up to 1 at most.)
+// In 64 bits (F = double) equal scores of one key go by that expert's logit,
+// which is looked up in the row from logit `base` on; in 32 bits they are
+// unsure, or logits themselves.
 template <int LPR, class F>
-__device__ __forceinline__ uint64_t sel_groups(const SelectArgs& a, const F* vals, float err, bool& unsure) {
+__device__ __forceinline__ uint64_t sel_groups(const SelectArgs& a, const F* vals, int64_t base, float err, bool& unsure) {
+  constexpr bool WIDE = sizeof(F) == 8;
   const F ninf = -(F)__builtin_inff();
   const int lane = threadIdx.x & 63, li = lane & (LPR - 1), row = lane & ~(LPR - 1);
+  const bool two = a.top == 2 && a.size > 1;
   const int g = li >> a.sh, lpg = 1 << a.sh, run = (a.size + lpg - 1) >> a.sh, sub = li & (lpg - 1);
   F b1 = ninf, b2 = ninf;
+  int e1 = 0;                          // WIDE: the expert of b1
+  float l1 = -__builtin_inff();  // and its logit
   if (g < a.groups) {
     const int end = min((sub + 1) * run, a.size);
-#pragma unroll 8
+#pragma clang loop unroll_count(WIDE ? 2 : 8)
     for (int i = sub * run; i < end; ++i) {
       const F x = vals[sel_place<F>(g * a.size + i)];
+      if constexpr (WIDE) {
+        const int e = g * a.size + i;
+        if (x > b1 || (!two && x == b1 && x > ninf && sel_logit(a.logits, a.bf16, base + e) > sel_logit(a.logits, a.bf16, base + e1)))
+          e1 = e;
+      }
       const F lo = x < b1 ? x : b1;
       b2 = lo > b2 ? lo : b2;
       b1 = x > b1 ? x : b1;
     }
+    if (WIDE && !two && b1 > ninf) l1 = sel_logit(a.logits, a.bf16, base + e1);
   }
   for (int o = 1; o < lpg; o <<= 1) {
     const F o1 = __shfl_xor(b1, o), o2 = __shfl_xor(b2, o);
+    if constexpr (WIDE) {
+      const float ol = __shfl_xor(l1, o);
+      l1 = o1 > b1 || (o1 == b1 && ol > l1) ? ol : l1;
+    }
     const F lo = o1 < b1 ? o1 : b1, hi2 = o2 > b2 ? o2 : b2;
     b2 = lo > hi2 ? lo : hi2;
     b1 = o1 > b1 ? o1 : b1;
   }
-  F score = a.top == 2 && a.size > 1 ? b1 + b2 : b1;
+  F score = two ? b1 + b2 : b1;
   if (!(score == score) || g >= a.groups) score = ninf;
   int rank = 0;
   for (int j = 0; j < a.groups; ++j) {
     const F s = __shfl(score, row + (j << a.sh));
-    rank += s > score || (s == score && j < g) ? 1 : 0;
+    bool before = j < g;
+    if constexpr (WIDE) {
+      const float l = __shfl(l1, row + (j << a.sh));
+      before = l > l1 || (l == l1 && before);
+    }
+    rank += s > score || (s == score && before) ? 1 : 0;
   }
   const bool keep = g < a.groups && rank < a.kept;
   if (err > 0.0f) {
     const float m1 = fmaxf(1.0f, fabsf((float)b1)), m2 = fmaxf(1.0f, fabsf((float)b2));
-    float slack = err * (a.top == 2 && a.size > 1 ? 0.5f * (m1 + m2) : m1);
+    float slack = err * (two ? 0.5f * (m1 + m2) : m1);
     if (!(slack < __builtin_inff())) slack = 0.0f;  // infinite keys are exact
     const F lowest = -row_fmax<LPR, F>(keep ? (F)slack - score : ninf);
     const F next = row_fmax<LPR, F>(!keep && g < a.groups ? score + (F)slack : ninf);
@@ -178,9 +202,10 @@ __device__ __forceinline__ bool sel_kept(const SelectArgs& a, uint64_t kept, uin
   return (kept >> (g << a.sh)) & 1ull;
 }
 
-// The choice by k rounds over the row's keys in LDS, which it uses up.
+// The choice by k rounds over the row's keys in LDS, which it uses up. Equal keys
+// in 64 bits go by the logits of the row, which start at `base`.
 template <int LPR, class F>
-__device__ __forceinline__ void sel_rounds(const SelectArgs& a, F* vals, int& chosen) {
+__device__ __forceinline__ void sel_rounds(const SelectArgs& a, F* vals, int64_t base, int& chosen) {
   const F ninf = -(F)__builtin_inff();
   const int li = threadIdx.x & (LPR - 1);
   chosen = -1;
@@ -190,13 +215,22 @@ __device__ __forceinline__ void sel_rounds(const SelectArgs& a, F* vals, int& ch
 #pragma unroll 4
     for (int i = li; i < a.E; i += LPR) {
       const F v = vals[sel_place<F>(i)];
-      if (v > m) {
+      bool first = v > m;
+      if constexpr (sizeof(F) == 8)
+        first = first || (v == m && v > ninf && sel_logit(a.logits, a.bf16, base + i) > sel_logit(a.logits, a.bf16, base + e));
+      if (first) {
         m = v;
         e = (uint32_t)i;
       }
     }
     const F best = row_fmax<LPR, F>(m);
-    const uint32_t at = row_min<LPR>(m == best ? e : 0xFFFFFFFFu);
+    bool mine = m == best && best > ninf;
+    if constexpr (sizeof(F) == 8) {
+      const float l = mine ? sel_logit(a.logits, a.bf16, base + e) : -__builtin_inff();
+      const float top = row_fmax<LPR, float>(l);
+      mine = mine && l == top;
+    }
+    const uint32_t at = row_min<LPR>(mine ? e : 0xFFFFFFFFu);
     if (at == e && at != 0xFFFFFFFFu) vals[sel_place<F>((int)at)] = ninf;
     if (li == r) chosen = (int)at;
     sel_fence();
@@ -221,7 +255,7 @@ constexpr int sel_most() {
 template <int LPR>
 struct SelScratch {
   uint64_t cand[sel_most<LPR>() + 1];  // key << 32 | ~expert; the last one takes what does not survive
-  uint32_t key[sel_most<LPR>()];       // in order
+  uint32_t key[sel_most<LPR>()];       // in order; if 32 bits do not decide, the logits of cand
   int expert[sel_most<LPR>()];
   double wide[sel_most<LPR>()];  // the survivors' keys in 64 bits, if 32 do not decide
 };
@@ -336,8 +370,8 @@ __device__ __forceinline__ int sel_survivors(const SelectArgs& a, const float (&
   return kSelDecided;
 }
 
-// The survivors in the order of their 64-bit keys. The bound left out nothing
-// that may be among the k largest.
+// The survivors in the order of their 64-bit keys, equal ones by their logits.
+// The bound left out nothing that may be among the k largest.
 template <int LPR>
 __device__ __forceinline__ void sel_order(const SelectArgs& a, int64_t base, double top, double total, char* row_lds,
                                           int C, int& chosen) {
@@ -357,6 +391,7 @@ __device__ __forceinline__ void sel_order(const SelectArgs& a, int64_t base, dou
     mine[h] = sel_wide(a, x[h], e[h], top, total);
     rank[h] = 0;
     sc.wide[li + LPR * h] = li + LPR * h < C ? mine[h] : -(double)__builtin_inff();
+    sc.key[li + LPR * h] = __float_as_uint(x[h]);
   }
   sel_fence();
   for (int u0 = 0; u0 < C; u0 += 8) {
@@ -364,8 +399,10 @@ __device__ __forceinline__ void sel_order(const SelectArgs& a, int64_t base, dou
     for (int u = u0; u < u0 + 8; ++u) {
       const double other = sc.wide[u];
       const int at = (int)~(uint32_t)sc.cand[u];
+      const float l = __uint_as_float(sc.key[u]);
 #pragma unroll
-      for (int h = 0; h < H; ++h) rank[h] += other > mine[h] || (other == mine[h] && at < e[h]) ? 1 : 0;
+      for (int h = 0; h < H; ++h)
+        rank[h] += other > mine[h] || (other == mine[h] && (l > x[h] || (l == x[h] && at < e[h]))) ? 1 : 0;
     }
   }
 #pragma unroll
@@ -430,10 +467,10 @@ __device__ __forceinline__ void sel_choose(const SelectArgs& a, const float (&l)
 #pragma unroll
     for (int j = 0; j < PER; ++j) vals[sel_place<float>(sel_expert<LPR, VEC>(li, j))] = v[j];
     sel_fence();
-    kept = sel_groups<LPR, float>(a, vals, err, border);
+    kept = sel_groups<LPR, float>(a, vals, base, err, border);
     if (__ballot(border && live)) {
       widen();
-      kept = sel_groups<LPR, double>(a, wide, 0.0f, border);
+      kept = sel_groups<LPR, double>(a, wide, base, 0.0f, border);
     }
 #pragma unroll
     for (int j = 0; j < PER; ++j)
@@ -449,7 +486,7 @@ __device__ __forceinline__ void sel_choose(const SelectArgs& a, const float (&l)
 #pragma unroll
     for (int j = 0; j < PER; ++j) vals[sel_place<float>(sel_expert<LPR, VEC>(li, j))] = v[j];
     sel_fence();
-    sel_rounds<LPR, float>(a, vals, chosen);
+    sel_rounds<LPR, float>(a, vals, base, chosen);
     return;
   }
   if (!all) {
@@ -468,7 +505,7 @@ __device__ __forceinline__ void sel_choose(const SelectArgs& a, const float (&l)
       if (!sel_kept(a, kept, (uint32_t)i)) wide[i] = -(double)__builtin_inff();
     sel_fence();
   }
-  sel_rounds<LPR, double>(a, wide, chosen);
+  sel_rounds<LPR, double>(a, wide, base, chosen);
 }
 
 // s of a logit, up to a factor common to the row that makes the largest of the

@@ -26,20 +26,23 @@ def scores_ref(row, scoring):
         return x, e / e.sum()
 
 
-def choose_ref(key, k, groups=1, topk_groups=1, group_top=2):
-    """Experts by descending key (ties to the lower one) inside the best groups; keys of -inf are never chosen."""
+def choose_ref(key, x, k, groups=1, topk_groups=1, group_top=2):
+    """Experts by descending key, equal ones by descending logit x, then the lower one, inside the best groups (by score,
+    equal ones by the logit where that is one expert's key, then the lower one); keys of -inf are never chosen."""
     key = np.array(key, dtype=np.float64)
     if topk_groups < groups:
-        g = key.reshape(groups, -1)
-        best = -np.sort(-g, axis=1)[:, :min(group_top, g.shape[1])]
+        g, l = key.reshape(groups, -1), x.reshape(groups, -1)
+        best = np.lexsort((-l, -g), axis=1)[:, :group_top]  # stable: what is left goes to the lower one
         with np.errstate(invalid="ignore"):
-            score = best.sum(axis=1)
+            score = np.take_along_axis(g, best, 1).sum(axis=1)
         score = np.where(np.isnan(score), -np.inf, score)
-        keep = sorted(range(groups), key=lambda i: (-score[i], i))[:topk_groups]
+        one = np.full(groups, -np.inf)
+        if best.shape[1] == 1:
+            one = np.where(score > -np.inf, np.take_along_axis(l, best, 1)[:, 0], -np.inf)
         out = np.ones(groups, dtype=bool)
-        out[keep] = False
+        out[np.lexsort((-one, -score))[:topk_groups]] = False
         key = np.where(np.repeat(out, g.shape[1]), -np.inf, key)
-    order = sorted(range(len(key)), key=lambda i: (-key[i], i))[:k]
+    order = np.lexsort((-x, -key))[:k].tolist()
     return [i if key[i] > -np.inf else -1 for i in order] + [-1] * (k - len(order))
 
 
@@ -63,11 +66,9 @@ def select_ref(logits, k, bias=None, scoring="sigmoid", groups=1, topk_groups=1,
     w, bound = np.zeros((T, k)), np.zeros((T, k))
     for t in range(T):
         x, s = scores_ref(logits[t], scoring)
-        # Without a bias the order of the scores is that of the logits, also where scores saturate.
-        by_logit = bias is None and (topk_groups == groups or group_top == 1)
-        key = x if by_logit else np.where(x > -np.inf, s + (0.0 if bias is None else np.asarray(bias, np.float64)), -np.inf)
+        key = np.where(x > -np.inf, s + (0.0 if bias is None else np.asarray(bias, np.float64)), -np.inf)
         key = np.where(np.isnan(key), -np.inf, key)
-        idx[t] = choose_ref(key, k, groups, topk_groups, group_top)
+        idx[t] = choose_ref(key, x, k, groups, topk_groups, group_top)
         c = idx[t] >= 0
         if not c.any():
             continue

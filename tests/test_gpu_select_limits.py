@@ -37,6 +37,9 @@ def check(x, b, k, got, **kw):
 
 
 # A wavefront to a row, and four rows to one.
+ROWS = [3, 6200]
+
+
 @pytest.mark.parametrize("T", [4000, 6200])
 @pytest.mark.parametrize("big", [64.0, 1e4])
 def test_group_border_of_keys_that_cancel(dev, T, big):
@@ -55,3 +58,56 @@ def test_group_border_of_keys_that_cancel(dev, T, big):
     got = rt.select(up(x, dev), 8, bias=up(b, dev), **kw)
     torch.cuda.synchronize()
     check(x, b, 8, got, **kw)
+
+
+def saturated(T, E, scoring, seed):
+    """Rows of which many scores, or all, are the same number in 64 bits although their logits differ, and some not."""
+    r = np.random.default_rng(seed)
+    x = r.uniform(38.0, 60.0, (T, E)) if scoring == "sigmoid" else r.uniform(-1200.0, -900.0, (T, E))
+    x = np.round(x * 8) / 8  # equal logits too
+    x[:, ::7] = r.uniform(-2.0, 2.0, x[:, ::7].shape)
+    x[T // 2:, 1::3] = -np.inf
+    if scoring == "softmax":
+        x[:, 3] = 1.0
+    return x.astype(np.float32)
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("T,E,k", [(3, 48, 12), (4, 256, 8), (5, 500, 32), (2100, 48, 12), (6200, 256, 8), (6200, 384, 16)])
+def test_saturated_scores(dev, T, E, k, scoring):
+    """Equal keys go to the larger logit, so a bias of zeros chooses what no bias chooses: the order of the logits."""
+    x = saturated(T, E, scoring, T + E)
+    log(f"saturated T={T} E={E} k={k} {scoring}")
+    zeros = torch.zeros(E, device=dev)
+    want = np.argsort(np.where(x > -np.inf, -x, np.inf), axis=1, kind="stable")[:, :k]
+    for groups, kept, top in ((1, 1, 1), (4, 2, 1), (4, 4, 2)):
+        if k > kept * (E // groups):
+            continue
+        kw = dict(scoring=scoring, groups=groups, topk_groups=kept, group_top=top, renormalize=False)
+        a, b = rt.select(up(x, dev), k, **kw), rt.select(up(x, dev), k, bias=zeros, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], b[0])
+        if kept == groups:
+            assert np.array_equal(a[0].cpu().numpy(), want)
+        check(x, None, k, a, **kw)  # each row count has its own order of sums, so the weights are not the same bits
+        check(x, np.zeros(E, np.float32), k, b, **kw)
+    if E % 4 == 0 and k <= E // 2:  # sums of two saturated scores
+        kw = dict(scoring=scoring, groups=4, topk_groups=2, group_top=2)
+        a, b = rt.select(up(x, dev), k, **kw), rt.select(up(x, dev), k, bias=zeros, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], b[0])
+        check(x, None, k, a, **kw)
+
+
+@pytest.mark.parametrize("T", ROWS)
+def test_equal_keys_of_different_biases(dev, T):
+    """A key that is the same number in 64 bits by a larger score and a smaller bias: the larger logit comes first."""
+    x = np.tile(np.array([0.0, 50.0, 50.0, 0.0, 60.0, -np.inf], np.float32), (T, 4))
+    b = np.tile(np.array([1.0, 0.5, 0.5, 1.0, 0.5, 3.0], np.float32), 4)
+    log(f"equal keys T={T}")
+    for kw in (dict(), dict(groups=4, topk_groups=2, group_top=1), dict(groups=2, topk_groups=1, group_top=2)):
+        got = rt.select(up(x, dev), 7, bias=up(b, dev), **kw)
+        torch.cuda.synchronize()
+        check(x, b, 7, got, **kw)
+        if not kw:
+            assert got[0].cpu().numpy().tolist() == [[4, 10, 16, 22, 1, 2, 7]] * T
