@@ -514,8 +514,10 @@ int lmhead_distill(const uint8_t* x_codes, const uint8_t* x_scales, const float*
  * -infinity or NaN, or whose key is, is never chosen (it counts as -infinity
  * in its group); where fewer than k remain, the places left hold -1 and weight
  * 0, which grouped_plan takes as slots of no expert. Renormalised weights hold
- * for any finite logits, however small their s. A logit of +infinity makes
- * softmax weights NaN.
+ * for any finite logits, however small their s. A bias of +infinity puts its
+ * experts before all others. A logit of +infinity makes its row's softmax
+ * scores NaN: weights of NaN where the logits decide alone, and nothing chosen
+ * where the order needs keys (with a bias, or groups by two keys).
  *   logits        [T, E] of `dtype`, ld >= E elements between rows.
  *   bias          NULL or [E] fp32.
  *   scoring       ROUTER_SIGMOID or ROUTER_SOFTMAX.

@@ -300,7 +300,7 @@ __device__ __forceinline__ int sel_survivors(const SelectArgs& a, const float (&
   }
   if (err > 0.0f && tau != 0u) {  // and all that may be the k-th
     const float t = key_back(tau);
-    tau = score_key(t - err * fmaxf(1.0f, fabsf(t)));
+    if (t < __builtin_inff()) tau = score_key(t - err * fmaxf(1.0f, fabsf(t)));  // (infinite: of a bias, exact)
   }
   tau = max(tau, 1u);
   int C = 0;
@@ -365,7 +365,7 @@ __device__ __forceinline__ int sel_survivors(const SelectArgs& a, const float (&
   count = C;
   if (err > 0.0f && li < a.k && li + 1 < C) {
     const float p = key_back(sc.key[li]);
-    if (p - key_back(sc.key[li + 1]) <= err * fmaxf(1.0f, fabsf(p))) return kSelOrder;
+    if (!(p - key_back(sc.key[li + 1]) > err * fmaxf(1.0f, fabsf(p)))) return kSelOrder;  // (two infinite ones too)
   }
   return kSelDecided;
 }

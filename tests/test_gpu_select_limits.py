@@ -111,3 +111,42 @@ def test_equal_keys_of_different_biases(dev, T):
         check(x, b, 7, got, **kw)
         if not kw:
             assert got[0].cpu().numpy().tolist() == [[4, 10, 16, 22, 1, 2, 7]] * T
+
+
+@pytest.mark.parametrize("k", [1, 4, 9])
+@pytest.mark.parametrize("T", ROWS)
+def test_infinite_biases(dev, T, k):
+    """Experts forced by a bias of +infinity, as many as are chosen, fewer and more; banned and masked ones beside them."""
+    E = 128
+    x = np.random.default_rng(k).standard_normal((T, E)).astype(np.float32)
+    for forced in (1, 4, 9, 40, 128):
+        log(f"infinite biases T={T} k={k} forced={forced}")
+        b = np.zeros(E, np.float32)
+        b[np.random.default_rng(forced).permutation(E)[:forced]] = np.inf
+        b[5] = -np.inf
+        x[:, 11] = -np.inf
+        for kw in (dict(), dict(scoring="softmax"), dict(groups=8, topk_groups=3, group_top=2),
+                   dict(groups=8, topk_groups=3, group_top=1)):
+            got = rt.select(up(x, dev), k, bias=up(b, dev), **kw)
+            torch.cuda.synchronize()
+            check(x, b, k, got, **kw)
+
+
+@pytest.mark.parametrize("T", ROWS)
+def test_infinite_logits(dev, T):
+    """+infinity is the largest logit; softmax scores of its row are NaN, and other rows do not feel it."""
+    E, k = 64, 4
+    x = np.random.default_rng(1).standard_normal((T, E)).astype(np.float32)
+    x[1, 20] = np.inf
+    rest = [t for t in range(T) if t != 1]
+    for bias in (None, torch.zeros(E, device=dev)):
+        got = rt.select(up(x, dev), k, bias=bias)
+        torch.cuda.synchronize()
+        check(x, None, k, got)
+        idx, w = rt.select(up(x, dev), k, bias=bias, scoring="softmax")
+        torch.cuda.synchronize()
+        if bias is None:
+            assert idx[1].tolist() == got[0][1].tolist() and torch.isnan(w[1]).all()
+        else:
+            assert (idx[1] == -1).all() and not w[1].any()
+        check(x[rest], None, k, (idx[rest], w[rest]), scoring="softmax")
