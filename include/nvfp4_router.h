@@ -455,6 +455,10 @@ int lmhead_penalize(const void* logits, int dtype, int64_t T, int64_t N, int64_t
  * named more than once. Teacher logits of NaN or +infinity make their row's
  * loss and gradient NaN.
  *
+ * A row with a logit of NaN or +infinity anywhere in the vocabulary has lse
+ * NaN, and with it its loss and gradient, but for the zeros of ignored targets
+ * and of rows without any place.
+ *
  * dx is the gradient of sum_t weight[t] * loss[t] with respect to the
  * dequantized x (the quantization of x passes it through); the 4-bit weights
  * have none.

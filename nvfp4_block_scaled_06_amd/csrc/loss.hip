@@ -70,10 +70,16 @@ __device__ __forceinline__ float teacher_at(const HeadArgs& a, int64_t i) {
                          : static_cast<const float*>(a.teacher)[i]) / a.tau;
 }
 
+// A sum s at a scale brought to another, 2^by. "Nothing yet" is s = 0 and not m
+// = -infinity: maxima leave NaN out, so logits of NaN alone have (-infinity, NaN),
+// and that NaN has to reach the row's sum.
+__device__ __forceinline__ float soft_scaled(float s, float by) {
+  return s == 0.0f ? 0.0f : s * __builtin_amdgcn_exp2f(by);
+}
+
 __device__ __forceinline__ float2 soft_join(float2 a, float2 b) {
   const float m = fmaxf(a.x, b.x);
-  if (!(m > -__builtin_inff())) return a;  // nothing yet
-  return make_float2(m, a.y * __builtin_amdgcn_exp2f(a.x - m) + b.y * __builtin_amdgcn_exp2f(b.x - m));
+  return make_float2(m, soft_scaled(a.y, a.x - m) + soft_scaled(b.y, b.x - m));
 }
 
 __device__ __forceinline__ float2 wave_join(float2 v) {
@@ -119,10 +125,9 @@ __device__ __forceinline__ float2 thread_join(const float2* st, int n) {
     float m = v.x;
 #pragma unroll
     for (int q = 0; q < Q; ++q) m = fmaxf(m, u[q].x);
-    if (!(m > -__builtin_inff())) continue;  // nothing yet
-    float s = v.y * __builtin_amdgcn_exp2f(v.x - m);
+    float s = soft_scaled(v.y, v.x - m);
 #pragma unroll
-    for (int q = 0; q < Q; ++q) s += u[q].y * __builtin_amdgcn_exp2f(u[q].x - m);
+    for (int q = 0; q < Q; ++q) s += soft_scaled(u[q].y, u[q].x - m);
     v = make_float2(m, s);
   }
   return v;

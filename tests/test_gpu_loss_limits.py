@@ -1,0 +1,110 @@
+"""GPU tests of the lm_head's losses where they lose something most easily: NaN, near-certain tokens, cold temperatures,
+roundings, workspaces made for more rows."""
+
+import numpy as np
+import pytest
+import torch
+
+from nvfp4_block_scaled_06_amd import router as rt
+from nvfp4_block_scaled_06_amd import workloads as wl
+from oracle import loss_ref as lr
+
+pytestmark = pytest.mark.gpu
+
+NAN8 = 0x7F  # an E4M3 scale that is NaN
+
+
+def log(msg):
+    print(f"[gpu-loss-limits] {msg}", flush=True)
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    rt.load_library()
+    d = torch.device("cuda:0")
+    torch.cuda.set_device(d)
+    return d
+
+
+def up(a, dev):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(dev)
+
+
+def quantized(a, dev):
+    ws = rt.Workspace(rt.workspace_bytes(a.shape[0], a.shape[1], 1, 1), dev)
+    return rt.quantize(up(wl.bf16_bits(a.astype(np.float32)).view(np.int16), dev), ws)
+
+
+def operands(T, D, N, seed, dev, scale=1.0):
+    r = np.random.default_rng(seed)
+    return quantized(scale * r.standard_normal((T, D)), dev), quantized(1.5 * D ** -0.5 * r.standard_normal((N, D)), dev)
+
+
+def workspace(T, D, N, grad, dev):
+    return rt.Workspace(rt.lmhead_loss_workspace_bytes(T, D, N, grad), dev)
+
+
+def host(q):
+    return q.codes.cpu().numpy(), q.scales.cpu().numpy(), q.gscale.cpu().numpy()[0]
+
+
+def copy(q):
+    return rt.NVFP4Tensor(q.codes.clone(), q.scales.clone(), q.gscale.clone())
+
+
+# Streams of 16 rows, of 32 rows, and wide tiles.
+NAN_SIZES = [(4, 96, 2000), (20, 256, 1500), (70, 128, 13000)]
+
+
+@pytest.mark.parametrize("T,D,N", NAN_SIZES)
+def test_rows_of_nan(dev, T, D, N):
+    """A row of x with NaN has NaN for everything but an ignored target's loss and gradient; the others keep their bits."""
+    xq, wq = operands(T, D, N, 1, dev)
+    y = np.random.default_rng(2).integers(0, N, T).astype(np.int32)
+    y[2] = -100
+    bad = [1, 2, T - 1]
+    xn = copy(xq)
+    xn.scales[bad] = NAN8
+    log(f"rows of NaN T={T} D={D} N={N}")
+    for grad in (False, True):
+        ws = workspace(T, D, N, grad, dev)
+        want = rt.lmhead_loss(xq, wq, up(y, dev), ws, want_grad=grad)
+        got = rt.lmhead_loss(xn, wq, up(y, dev), ws, want_grad=grad)
+        torch.cuda.synchronize()
+        rest = [t for t in range(T) if t not in bad]
+        for u, v in zip(got, want):
+            assert u is v is None or torch.equal(u[rest], v[rest])
+        assert torch.isnan(got[1][bad]).all()
+        assert torch.isnan(got[0][[1, T - 1]]).all() and got[0][2] == 0
+        if grad:
+            assert torch.isnan(got[2][[1, T - 1]].float()).all() and not got[2][2].any()
+
+
+@pytest.mark.parametrize("T,D,N", NAN_SIZES)
+def test_columns_of_nan(dev, T, D, N):
+    """Weight rows of NaN, wherever they lie and whatever they fill, make every row's sum NaN."""
+    xq, wq = operands(T, D, N, 3, dev)
+    y = up(np.random.default_rng(4).integers(0, 5, T).astype(np.int32), dev)
+    for a, b in ((7, 8), (64, 96), (64, 80), (96, 112), (128, 192), (512, 1024), (N - 3, N), (N - N % 64, N), (0, N)):
+        wn = copy(wq)
+        wn.scales[a:b] = NAN8
+        log(f"columns of NaN T={T} D={D} N={N} {a}:{b}")
+        for grad in (False, True):
+            loss, lse, dx = rt.lmhead_loss(xq, wn, y, workspace(T, D, N, grad, dev), want_grad=grad)
+            torch.cuda.synchronize()
+            assert torch.isnan(lse).all() and torch.isnan(loss).all(), (a, b, grad)
+            assert not grad or torch.isnan(dx.float()).all(), (a, b)
+
+
+@pytest.mark.parametrize("T,D,N", NAN_SIZES)
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+def test_global_scales_that_are_not_finite(dev, T, D, N, value):
+    xq, wq = operands(T, D, N, 5, dev)
+    y = torch.full((T,), -100, dtype=torch.int32, device=dev)
+    for which in (0, 1):
+        q = [copy(xq), copy(wq)]
+        q[which].gscale.fill_(value)
+        loss, lse, _ = rt.lmhead_loss(*q, y, workspace(T, D, N, False, dev))
+        torch.cuda.synchronize()
+        assert torch.isnan(lse).all() and not loss.any()
