@@ -94,16 +94,17 @@ __device__ __forceinline__ float2 wave_join(float2 v) {
 __device__ __forceinline__ float2 teacher_row(const HeadArgs& a, int64_t t) {
   const int lane = threadIdx.x & 63;
   float m = -__builtin_inff();
+  bool nan = false;  // one of a token that counts; a maximum leaves it out
   for (int j = lane; j < a.K; j += 64) {
     const int n = a.tokens[t * a.K + j];
     if (n >= 0 && n < a.N) {
       const float v = teacher_at(a, t * a.K + j);
-      m = v != v ? v : fmaxf(m, v);  // a NaN of a token that counts stays one
+      nan = nan || v != v;
+      m = fmaxf(m, v);
     }
   }
-  const bool nan = __ballot(m != m) != 0;
   m = wave_max(m);
-  if (nan) return make_float2(__builtin_nanf(""), __builtin_nanf(""));
+  if (__ballot(nan)) return make_float2(__builtin_nanf(""), __builtin_nanf(""));
   if (!(m > -__builtin_inff())) return make_float2(0.0f, 0.0f);
   float s = 0.0f;
   for (int j = lane; j < a.K; j += 64) {

@@ -108,3 +108,35 @@ def test_global_scales_that_are_not_finite(dev, T, D, N, value):
         loss, lse, _ = rt.lmhead_loss(*q, y, workspace(T, D, N, False, dev))
         torch.cuda.synchronize()
         assert torch.isnan(lse).all() and not loss.any()
+
+
+def test_teacher_nan_is_kept(dev):
+    """A NaN of a token that counts makes its row NaN, wherever it stands and whatever else the row holds; lse and logq,
+    which do not depend on the teacher, are those of a row without it."""
+    T, D, N, K = 12, 64, 300, 200
+    xq, wq = operands(T, D, N, 6, dev)
+    r = np.random.default_rng(7)
+    tok = r.integers(0, N, (T, K)).astype(np.int32)
+    tok[:, 5] = 17  # named by every row
+    clean = r.standard_normal((T, K)).astype(np.float32)
+    clean[1::2] = -np.inf  # nothing else in the row counts
+    clean[1::2, 150] = 1.0
+    te = clean.copy()
+    at = [0, 1, 5, 5, 63, 64, 69, 69, 128, 191, 199, 199]
+    for t in range(T):
+        te[t] = np.where(np.isinf(te[t]) | (t % 2 == 1), -np.inf, te[t])
+        te[t, at[t]] = np.nan
+        tok[t, at[t]] = 100 + t
+    ws = workspace(T, D, N, True, dev)
+    want = rt.lmhead_distill(xq, wq, up(tok, dev), up(clean, dev), ws, want_grad=True)
+    got = rt.lmhead_distill(xq, wq, up(tok, dev), up(te, dev), ws, want_grad=True)
+    torch.cuda.synchronize()
+    assert torch.isnan(got[0]).all() and torch.isnan(got[3].float()).all()
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    assert torch.isfinite(want[0]).all() and torch.isfinite(got[1]).all() and torch.isfinite(got[2]).all()
+    tok[:, 5] = -1
+    for t in range(T):
+        tok[t, at[t]] = -1  # left out: whatever its teacher's logit is
+    got = rt.lmhead_distill(xq, wq, up(tok, dev), up(te, dev), ws, want_grad=True)
+    torch.cuda.synchronize()
+    assert torch.isfinite(got[0]).all() and torch.isfinite(got[3].float()).all()
