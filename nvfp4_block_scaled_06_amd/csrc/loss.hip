@@ -70,11 +70,12 @@ __device__ __forceinline__ float teacher_at(const HeadArgs& a, int64_t i) {
                          : static_cast<const float*>(a.teacher)[i]) / a.tau;
 }
 
-// A sum s at a scale brought to another, 2^by. "Nothing yet" is s = 0 and not m
-// = -infinity: maxima leave NaN out, so logits of NaN alone have (-infinity, NaN),
-// and that NaN has to reach the row's sum.
+// s 2^by for whole by <= 0, exact but where it ends below fp32's numbers. "Nothing
+// yet" is s = 0 and not m = -infinity: maxima leave NaN out, so logits of NaN
+// alone have (-infinity, NaN), and that NaN has to reach the row's sum. (by is
+// NaN where both m are -infinity.)
 __device__ __forceinline__ float soft_scaled(float s, float by) {
-  return s == 0.0f ? 0.0f : s * __builtin_amdgcn_exp2f(by);
+  return ldexpf(s, (int)fmaxf(by, -1000.0f));
 }
 
 __device__ __forceinline__ float2 soft_join(float2 a, float2 b) {
@@ -396,7 +397,7 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, Hea
   v = soft_join(v, old);
   if (threadIdx.x == 0) {
     a.after[t] = v;
-    a.shrink[t] = a.before ? __builtin_amdgcn_exp2f(old.x - v.x) : 0.0f;
+    a.shrink[t] = a.before ? soft_scaled(1.0f, old.x - v.x) : 0.0f;
     a.ref[t] = v.x;
   }
   // The named tokens' own weights.
@@ -424,7 +425,7 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, Hea
 //    once. Wavefront w takes the columns 16 r + 2 w and 16 r + 2 w + 1 of lane
 //    r, all in the scale block r. Scales likewise, as [block][n].
 //  * Softmax weights: on their way into LDS they are brought to the row's m
-//    from their block's, a second rounding to fp16 where those differ.
+//    from their block's, by a power of two.
 //  * K order: in every 64 rows lane (r, h) supplies [16 h + 4 j, +4) and those
 //    32 further on to MFMA j.
 // All double-buffered in LDS, one barrier per step; a step's loads go out a step
@@ -545,7 +546,7 @@ __device__ __forceinline__ void grad_tile(const GradArgs& a, int row0, int nr, i
   auto store_x = [&](int buf, int u) {
 #pragma unroll
     for (int i = 2 * u; i < 2 * u + 2; ++i) {
-      // In two factors where one would be below fp16's normal numbers.
+      // A power of two, in two factors where one would be below fp16's normal numbers.
       const float by = mv[i] - ref;
       const _Float16 f = (_Float16)__builtin_amdgcn_exp2f(fmaxf(by, -14.0f));
       const _Float16 g = (_Float16)__builtin_amdgcn_exp2f(fminf(by + 14.0f, 0.0f));

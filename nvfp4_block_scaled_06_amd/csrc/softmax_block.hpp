@@ -4,8 +4,10 @@
 // In base 2, with y = z log2(e) / temperature, each row of a block gives
 // (m, s) with m >= its largest y and s = sum 2^(y - m); joined over the blocks
 // of a row they give log sum e^z. kWeights also keeps 2^(y - m) itself, as
-// fp16 times 2^15: relative error 2^-11 down to 2^-29 of the row's largest,
-// absolute 2^-40 below (bf16 would keep 2^-8 of each). `ref` lets m start at
+// fp16 times 2^15: relative error 2^-11 down to 2^-28 of the row's largest,
+// absolute 2^-39 of it below (bf16 would keep 2^-8 of each). m is a whole
+// number, the next one up, so that a block's weights and sums are brought to
+// another m by powers of two and are rounded this once. `ref` lets m start at
 // what earlier columns have reached, so that few blocks have a scale of their
 // own.
 #pragma once
@@ -56,6 +58,12 @@ __device__ __forceinline__ float dpp_f(float v) {
   return __int_as_float(dpp_i<CTRL>(__float_as_int(v)));
 }
 
+// A whole number at least as large as the exact product that y is rounded from
+// (by a half step, relative 2^-24), and less than 2 above it; -infinity for none.
+__device__ __forceinline__ float whole_above(float y) {
+  return y > -__builtin_inff() ? ceilf(fmaf(fabsf(y), 0x1p-22f, y)) : y;
+}
+
 // Block of 32 places from the stream's accumulators: lane (r, q), value v of
 // tile m: row r (+ 16 t), column col0 + 32 m + 4 q + v, so that a lane's eight
 // columns are neighbours in e.
@@ -74,7 +82,7 @@ __device__ __forceinline__ void softmax_block16(const SoftmaxOut& o, const f32x4
       y[i] = col0 + 32 * (i & 1) + 4 * q + (i >> 1) < N ? acc[i & 1][t][i >> 1] * sc : -__builtin_inff();
       m = fmaxf(m, y[i]);
     }
-    m = max_across32(max_across16(m));
+    m = whole_above(max_across32(max_across16(m)));
     // Columns past N have weights of zero and take no part in the sums.
     const bool none = col0 >= N;
     if (KEEP && o.ref && row < nr && !none) m = fmaxf(m, o.ref[row0 + row]);
@@ -125,7 +133,7 @@ __device__ __forceinline__ void softmax_block32(const SoftmaxOut& o, const f32x1
       m = fmaxf(m, dpp_f<kDppXor2>(m));
       m = fmaxf(m, dpp_f<kDppHalfMirror>(m));
       m = fmaxf(m, dpp_f<kDppMirror>(m));
-      m = max_across16(m);
+      m = whole_above(max_across16(m));
       if (KEEP && o.ref && row < nr) m = fmaxf(m, o.ref[row0 + row]);
       const float e0 = __builtin_amdgcn_exp2f(y0 - m), e1 = __builtin_amdgcn_exp2f(y1 - m);
       float s = e0 + e1;

@@ -4,8 +4,10 @@ TEST INFRASTRUCTURE (CPU oracle); see the package docstring.
 
 ``loss_ref`` returns each output with a bound on how far an evaluation may be
 from it that sums exact products in fp32 (half a step U32 = 2^-24 each),
-keeps the columns' softmax weights as fp16 (U16 = 2^-11, three roundings at
-most, and 2^-25 / 2^15 below fp16's range) and rounds dx to bf16 (2^-8).
+keeps the columns' softmax weights as fp16 times 2^15, rounded once (UF16 =
+2^-11, and 2^-25 / 2^15 below fp16's range, at the block's scale and at the
+row's, which is less than twice the largest weight: 3 2^-40 of that in all)
+and rounds dx to bf16 (2^-8).
 """
 
 import numpy as np
@@ -69,7 +71,7 @@ def loss_ref(xq, wq, tokens, teacher=None, tau=1.0, weight=None):
         named[np.arange(T)[valid[:, j]], at[:, j][valid[:, j]]] = True
     c = q.copy()
     np.add.at(c, (np.broadcast_to(rows, (T, K)), at), np.where(valid, -p, 0.0))
-    eq = q * (3 * UF16 + 2 * elog[:, None] + ez + (mag[:, None] + 64) * U32) + 2.0 ** -40 * q.max(axis=1, keepdims=True) * 3
+    eq = q * (UF16 + 2 * elog[:, None] + ez + (mag[:, None] + 64) * U32) + 2.0 ** -40 * q.max(axis=1, keepdims=True) * 3
     ec = np.where(named, q * (2 * else_[:, None] + ez + 8 * U32), eq)
     np.add.at(ec, (np.broadcast_to(rows, (T, K)), at), np.where(valid, p * (ep + 4 * U32), 0.0))
     aw = np.abs(w)

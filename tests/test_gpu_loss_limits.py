@@ -140,3 +140,35 @@ def test_teacher_nan_is_kept(dev):
     got = rt.lmhead_distill(xq, wq, up(tok, dev), up(te, dev), ws, want_grad=True)
     torch.cuda.synchronize()
     assert torch.isfinite(got[0]).all() and torch.isfinite(got[3].float()).all()
+
+
+@pytest.mark.parametrize("T,N", [(1, 192), (20, 192), (64, 30016)])
+def test_softmax_weights_are_rounded_once(dev, T, N):
+    """Three levels of logits, 7, 2.1 and 1.1667 in base 2, of which the lowest shares its block with the second and 57 of its
+    columns cancel one of the highest in dx: what is left shows how often the weights 2^-5.83 were rounded to 11 bits. (Once
+    with the block's own scale, once as that is brought to the row's and once as both are multiplied: 2.5 half steps.)"""
+    D = 64
+    wc, ws8 = np.zeros((N, D // 2), np.uint8), np.full((N, D // 16), 0x38, np.uint8)
+    wc[:64, 0], ws8[:64, 0] = 7, 0x3A          # 6 * 1.25
+    wc[64:128, 0], ws8[64:128, 0] = 2, 0x3A    # 1 * 1.25
+    wc[[64, 80], 0], ws8[[64, 80], 0] = 7, 0x2C  # 6 * 0.375, in each block of 32 of these 64
+    low = [n for n in range(64, 128) if n not in (64, 80)][:57]
+    wc[5, 16:24], wc[low, 16:24] = 0x77, 0xFF  # +6 and -6 where x is 0
+    xc, xs = np.zeros((T, D // 2), np.uint8), np.full((T, D // 16), 0x38, np.uint8)
+    xc[:, 0] = 7
+    gsa = np.float32(7.0 / (np.log2(np.e) * 6 * 7.5))
+    q = lambda c, s, g: rt.NVFP4Tensor(up(c, dev), up(s, dev), torch.tensor([g], device=dev))
+    xq, wq = q(xc, xs, gsa), q(wc, ws8, 1.0)
+    y = np.full((T, 1), 130, np.int32)
+    log(f"one rounding T={T} N={N}")
+    _, _, dx = rt.lmhead_loss(xq, wq, up(y[:, 0], dev), workspace(T, D, N, True, dev), want_grad=True)
+    torch.cuda.synchronize()
+    want = lr.loss_ref(host(xq), host(wq), y)["dx"][0][:, 32:48]
+    z = lr.dequant_ref(*host(xq))[:1] @ lr.dequant_ref(*host(wq)).T
+    p = np.exp(z - lr._lse(z)[:, None])[0]
+    share = 6 * p[low].sum()
+    # One half step of 11 bits, 2^-11; 2^-17 for the exponential of arguments up to 7 and the sums in fp32; bf16 at the end.
+    bound = share * (2.0 ** -11 + 2.0 ** -17) + 2.0 ** -8 * np.abs(want)
+    assert np.abs(want).max() < 0.01 * share
+    err = np.abs(dx[:, 32:48].double().cpu().numpy() - want)
+    assert (err <= bound).all(), (err.max() / share * 2048, bound.max() / share * 2048)
