@@ -483,8 +483,12 @@ int lmhead_penalize(const void* logits, int dtype, int64_t T, int64_t N, int64_t
  *                            state prefix (see router_workspace_bytes) is not
  *                            touched. 0 for sizes that the calls refuse.
  * Products are exact with fp32 sums in a fixed order, so results repeat bit for
- * bit. In dx the columns' softmax weights are rounded to 11 bits, those of the
- * named tokens to 24, and dx to bf16 at the end.
+ * bit. A named token's logit is the one that the sum over the vocabulary has in
+ * it: no probability is above 1, no logq above 0 and no cross entropy below 0,
+ * at any temperature. z / tau is rounded to 24 bits, an absolute error of
+ * |z / tau| 2^-24 in each exponent beside that of the sum over D. In dx the
+ * columns' softmax weights are rounded to 11 bits, those of the named tokens to
+ * 24, and dx to bf16 at the end.
  */
 #define ROUTER_MAX_LOSS_ROWS (1 << 18)
 #define ROUTER_MAX_TEACHER 1024

@@ -255,6 +255,8 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
 
   const int nsteps = (a.D + 255) / 256;
   load_x(0);
+  [[maybe_unused]] uint32_t hits = 0u;
+  if constexpr (SOFT) hits = named_hits<true>(a.soft, rt.row0, nr, o0, 0);
   store_x(0, 0);
   __syncthreads();
   f32x4_t acc[2][NT];
@@ -337,7 +339,9 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
   // Lane (r, q), value v of tile m: row r (+ 16 t), weight row 4 q + v of the tile.
   const float scale = gsa * gsw;
   if constexpr (M == Out::kSums || M == Out::kWeights) {
-    softmax_block16<M == Out::kWeights, NT>(a.soft, acc, scale, rt.row0, nr, o0, a.N);
+    static_assert(sizeof(lds.codes[0]) >= MR * 32 * sizeof(float));
+    softmax_block16<M == Out::kWeights, NT>(a.soft, acc, scale, rt.row0, nr, o0, a.N, hits,
+                                                 reinterpret_cast<float*>(my_codes));
   } else if constexpr (GLU) {
     if (!live0) return;
     const int f = o0 + 4 * q;
@@ -516,6 +520,8 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
 
   const int nbatch = (a.D + 255) / 256;
   load_x(0, 0);
+  [[maybe_unused]] uint32_t hits = 0u;
+  if constexpr (M == Out::kSums || M == Out::kWeights) hits = named_hits<false>(a.soft, rt.row0, nr, o0, 0);
 #pragma unroll
   for (int j = 0; j < 4; ++j) store_x(0, 0, j);
   store_w();
@@ -601,7 +607,9 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
   // Value v of lane (r, h): row 8 (v / 4) + 4 h + v % 4 of its 32-row tile, column r of its 32 weight rows.
   const float scale = gsa * gsw;
   if constexpr (M == Out::kSums || M == Out::kWeights) {
-    softmax_block32<M == Out::kWeights, RT>(a.soft, acc, scale, rt.row0, nr, o0, a.N);
+    static_assert(sizeof(lds.codes[0]) >= 32 * 64 * sizeof(float));
+    softmax_block32<M == Out::kWeights, RT>(a.soft, acc, scale, rt.row0, nr, o0, a.N, hits,
+                                                 reinterpret_cast<float*>(codes));
   } else if constexpr (GLU) {
     const int f = o0 + r;
     if (f >= F) return;

@@ -20,6 +20,11 @@
 // The K tokens of the loss do not take part in that second product: their
 // weights are set to zero there, and q_j - p_j, in fp32, multiplies their rows
 // at the end. Where q is near p nothing is lost to fp16.
+//
+// Their logits are those of the first product, left by the tiles that hold them,
+// and everything of them is taken as a difference from the row's m. So q <= 1 and
+// loss >= 0 hold at any temperature; what the temperature magnifies is the
+// rounding of the logits alone, 2^-24 of |z / tau| and their sums' over D.
 #include "../../include/nvfp4_router.h"
 #include "experts_tile.hpp"
 
@@ -56,6 +61,7 @@ struct HeadArgs {
   int teacher_bf16;
   float tau;
   const float* weight;  // NULL (1) or [T]
+  const float* named;   // [T, K]: y of the tokens
   const float2* stats;  // [T, blocks] (m, s), the first `used` of each row
   int blocks, used;
   float* loss;
@@ -66,8 +72,12 @@ struct HeadArgs {
 };
 
 __device__ __forceinline__ float teacher_at(const HeadArgs& a, int64_t i) {
-  return (a.teacher_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.teacher)[i] << 16)
-                         : static_cast<const float*>(a.teacher)[i]) / a.tau;
+  return a.teacher_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.teacher)[i] << 16)
+                        : static_cast<const float*>(a.teacher)[i];
+}
+// teacher_at over tau, from its row's largest: no quotient overflows.
+__device__ __forceinline__ float teacher_below(const HeadArgs& a, int64_t i, float top) {
+  return (teacher_at(a, i) - top) / a.tau;
 }
 
 // s 2^by for whole by <= 0, exact but where it ends below fp32's numbers. "Nothing
@@ -110,7 +120,7 @@ __device__ __forceinline__ float2 teacher_row(const HeadArgs& a, int64_t t) {
   float s = 0.0f;
   for (int j = lane; j < a.K; j += 64) {
     const int n = a.tokens[t * a.K + j];
-    if (n >= 0 && n < a.N) s += expf(teacher_at(a, t * a.K + j) - m);
+    if (n >= 0 && n < a.N) s += expf(teacher_below(a, t * a.K + j, m));
   }
   return make_float2(m, wave_sum(s));
 }
@@ -135,87 +145,6 @@ __device__ __forceinline__ float2 thread_join(const float2* st, int n) {
   return v;
 }
 
-// Logits of up to U tokens against row t of x, by a wavefront, 4 / U chunks of
-// 32 values per lane in flight; exact block products, fp32 sums in a fixed
-// order. A token outside [0, N) gives anything.
-template <int U>
-__device__ __forceinline__ void token_dots(const HeadArgs& a, int64_t t, const int (&n)[U], float (&z)[U]) {
-  constexpr int C = 4 / U;
-  const int lane = threadIdx.x & 63, nch = a.D >> 5;
-  const int64_t rowc = a.D / 2, rows = a.D / 16;
-  const uint8_t *xc = a.xc + t * rowc, *xs = a.xs + t * rows;
-  int64_t row[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    row[u] = n[u] >= 0 && n[u] < a.N ? n[u] : 0;
-    z[u] = 0.0f;
-  }
-  for (int c0 = lane; c0 < nch; c0 += 64 * C) {
-    u32x4_t xv[C], wv[C][U];
-    uint32_t xb[C], wb[C][U];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c = min(c0 + 64 * i, nch - 1);
-      xv[i] = *reinterpret_cast<const u32x4_t*>(xc + 16 * c);
-      xb[i] = *reinterpret_cast<const uint16_t*>(xs + 2 * c);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        wv[i][u] = *reinterpret_cast<const u32x4_t*>(a.wc + row[u] * rowc + 16 * c);
-        wb[i][u] = *reinterpret_cast<const uint16_t*>(a.ws + row[u] * rows + 2 * c);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      if (c0 + 64 * i >= nch) break;
-      const half2_t xsc = e4m3x2_f16(xb[i]);
-      half8_t x[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) x[q] = fp4x8_scaled(xv[i][q], xsc, q >> 1);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const half2_t wsc = e4m3x2_f16(wb[i][u]);
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          z[u] += dot8(x[2 * q + 1], fp4x8_scaled(wv[i][u][2 * q + 1], wsc, q),
-                       dot8(x[2 * q], fp4x8_scaled(wv[i][u][2 * q], wsc, q), 0.0f));
-      }
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) z[u] = wave_sum(z[u]);
-}
-
-// More tokens than a row's workgroup has wavefronts: their logits (over tau)
-// go to logq before it runs, 16 tokens of a row per workgroup (of four wavefronts), each
-// wavefront's four weight rows in flight together. Bound by the gathered rows: T = 1024, K = 64,
-// D = 7168 (264 MB) 45 us, 5.9 TB/s. (A row at a time in the row's one workgroup:
-// T = 32 156 us for the whole call, 113 so.)
-constexpr int kTokWaves = 4;
-constexpr int kTokPerWave = 4;
-// Workgroup n of those that take row t's tokens.
-__device__ __forceinline__ void token_block(const HeadArgs& a, int64_t t, int n) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int j0 = (n * (int)(blockDim.x >> 6) + wave) * kTokPerWave;
-  if (j0 >= a.K) return;
-  const float scale = load_early(a.gsa) * load_early(a.gsw) / a.tau;
-  int tk[kTokPerWave];
-  float z[kTokPerWave];
-#pragma unroll
-  for (int u = 0; u < kTokPerWave; ++u) tk[u] = a.tokens[t * a.K + min(j0 + u, a.K - 1)];
-  token_dots<kTokPerWave>(a, t, tk, z);
-#pragma unroll
-  for (int u = 0; u < kTokPerWave; ++u)
-    if (lane == u && j0 + u < a.K) a.logq[t * a.K + j0 + u] = z[u] * scale;
-}
-
-__host__ __device__ constexpr int token_blocks(int K, int threads) {
-  return (K + threads / 64 * kTokPerWave - 1) / (threads / 64 * kTokPerWave);
-}
-
-__global__ __launch_bounds__(64 * kTokWaves) void head_dots_kernel(HeadArgs a) {
-  token_block(a, blockIdx.x, blockIdx.y);
-}
-
 // ---------------------------------------------------------------------------
 // Logits of a piece: the experts' tiles, one matrix, with softmax_block.hpp's
 // epilogue. D = 7168, N = 129280 (521 MB of weights), the kernel alone:
@@ -225,14 +154,10 @@ __global__ __launch_bounds__(64 * kTokWaves) void head_dots_kernel(HeadArgs a) {
 //           their power leaves.
 // ---------------------------------------------------------------------------
 template <Out M, int MR, int KB, int KG, Scales S, int AUX>
-__global__ __launch_bounds__(KG * kEsThreads) void head_stream_kernel(ExpertArgs a, int row_tiles, int tiles, HeadArgs h) {
+__global__ __launch_bounds__(KG * kEsThreads) void head_stream_kernel(ExpertArgs a, int row_tiles) {
   __shared__ StreamLds<MR, KB, KG> lds;
-  if ((int)blockIdx.x >= tiles) {
-    const int b = blockIdx.x - tiles, per_row = token_blocks(h.K, KG * kEsThreads), t = b / per_row;
-    return token_block(h, t, b - t * per_row);
-  }
   // The row tiles of one column tile side by side on one XCD: they read the same weights.
-  const int n = xcd_order(blockIdx.x, tiles), ct = n / row_tiles, row0 = (n - ct * row_tiles) * MR;
+  const int n = xcd_order(blockIdx.x, gridDim.x), ct = n / row_tiles, row0 = (n - ct * row_tiles) * MR;
   const ExpertTile tile{{0, row0, min(MR, a.R - row0)}, ct};
   stream_tile<M, MR, KB, KG, S, AUX>(a, tile, lds);
 }
@@ -253,23 +178,13 @@ __global__ __launch_bounds__(kEtThreads) __attribute__((amdgpu_waves_per_eu(2, 2
 // ---------------------------------------------------------------------------
 // The rows' losses.
 // ---------------------------------------------------------------------------
-// A row's loss by its workgroup, from its logits' sum (m, s). Up to as many
-// tokens as wavefronts have their logits computed here (first by row_dots),
-// `dots` says.
+// A row's loss by its workgroup, from its logits' sum (m, s).
+constexpr int kTokWaves = 4;
 struct TokLds {
   float2 part[kTokWaves];
-  float terms[kTokWaves], zs[kTokWaves], lz[kHeadTokens];
+  float terms[kTokWaves], lz[kHeadTokens];
   alignas(16) int tk[kHeadTokens];
 };
-
-__device__ __forceinline__ void row_dots(const HeadArgs& a, int64_t t, TokLds& lds) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (wave >= a.K) return;
-  const int n[1] = {a.tokens[t * a.K + wave]};
-  float z[1];
-  token_dots<1>(a, t, n, z);
-  if (lane == 0) lds.zs[wave] = z[0] * (load_early(a.gsa) * load_early(a.gsw) / a.tau);
-}
 
 // (m, s) of a row's blocks, by a workgroup of kTokWaves wavefronts.
 __device__ __forceinline__ float2 row_join(const float2* st, int n, TokLds& lds) {
@@ -282,10 +197,10 @@ __device__ __forceinline__ float2 row_join(const float2* st, int n, TokLds& lds)
   return v;
 }
 
-__device__ __forceinline__ void row_loss(const HeadArgs& a, int64_t t, float2 v, int dots, TokLds& lds) {
-  float (&terms)[kTokWaves] = lds.terms, (&zs)[kTokWaves] = lds.zs, (&lz)[kHeadTokens] = lds.lz;
+__device__ __forceinline__ void row_loss(const HeadArgs& a, int64_t t, float2 v, TokLds& lds) {
+  float (&terms)[kTokWaves] = lds.terms, (&lz)[kHeadTokens] = lds.lz;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const float lse = v.x * kLn2 + logf(v.y);
+  const float lsum = logf(v.y);  // log sum, from m on
   float2 tr = make_float2(0.0f, 1.0f);  // log p = 0 for cross entropy
   if (a.teacher) tr = teacher_row(a, t);
   const float logs = a.teacher ? logf(tr.y) : 0.0f;
@@ -295,14 +210,15 @@ __device__ __forceinline__ void row_loss(const HeadArgs& a, int64_t t, float2 v,
     lds.tk[j] = n;
     float logq = 0.0f;
     if (n >= 0 && n < a.N) {
-      const float z = dots ? zs[j] : a.logq[t * a.K + j];
-      lz[j] = z;
-      logq = z - lse;
+      const float y = a.named[t * a.K + j] - v.x;  // (logq itself is where they stand, if there is one)
+      lz[j] = y;
+      logq = y * kLn2 - lsum;
+      if (logq > 0.0f) logq = 0.0f;  // by the roundings of these two
       if (a.teacher) {
-        const float lp = teacher_at(a, t * a.K + j) - tr.x - logs, p = expf(lp);
+        const float lp = teacher_below(a, t * a.K + j, tr.x) - logs, p = expf(lp);
         if (p != 0.0f) sum += p * (lp - logq);  // p log p is 0 at 0
       } else {
-        sum = -logq;
+        sum = 0.0f - logq;
       }
     }
     if (a.logq) a.logq[t * a.K + j] = logq;
@@ -315,7 +231,7 @@ __device__ __forceinline__ void row_loss(const HeadArgs& a, int64_t t, float2 v,
 #pragma unroll
     for (int w = 1; w < kTokWaves; ++w) l += terms[w];
     a.loss[t] = tr.y == 0.0f ? 0.0f : l * a.tau * a.tau;
-    a.lse[t] = lse;
+    a.lse[t] = v.x * kLn2 + lsum;
   }
   if (!a.lists) return;
   // q - p of each place. A token named more than once has its q at its first
@@ -332,9 +248,9 @@ __device__ __forceinline__ void row_loss(const HeadArgs& a, int64_t t, float2 v,
       again |= (int)(o.x == n && i < j) | (int)(o.y == n && i + 1 < j) | (int)(o.z == n && i + 2 < j) | (int)(o.w == n && i + 3 < j);
     }
     if (n >= 0 && n < a.N) {
-      const float z = dots ? zs[j] : lz[j];
-      const float p = a.teacher ? expf(teacher_at(a, t * a.K + j) - tr.x) / tr.y : 1.0f;
-      lz[j] = (again ? 0.0f : expf(z - lse)) - p;
+      const float p = a.teacher ? expf(teacher_below(a, t * a.K + j, tr.x)) / tr.y : 1.0f;
+      // 2^y as in the sum, which holds it: the quotient is 1 at most.
+      lz[j] = (again ? 0.0f : __builtin_amdgcn_exp2f(lz[j]) / v.y) - p;
     }
   }
   __syncthreads();
@@ -360,11 +276,10 @@ __device__ __forceinline__ void row_loss(const HeadArgs& a, int64_t t, float2 v,
 // Without a gradient: the end of a row, from its blocks' (m, s). Latency at few
 // rows (5.4 us at T = 1, N = 129280: 4040 blocks, 32 KB); T = 4096 with 2020
 // blocks each: 23 us, 2.9 TB/s.
-__global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a, int dots) {
+__global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a) {
   __shared__ TokLds lds;
   const int64_t t = blockIdx.x;
-  if (dots) row_dots(a, t, lds);
-  row_loss(a, t, row_join(a.stats + t * a.blocks, a.used, lds), dots, lds);
+  row_loss(a, t, row_join(a.stats + t * a.blocks, a.used, lds), lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -387,11 +302,10 @@ struct NormArgs {
 // row's loss. 5.5 us at T = 203, 6.6 with 37 tokens, 23 at T = 4096: latency.
 constexpr int kNormThreads = 64 * kTokWaves;
 template <bool LAST>
-__global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, HeadArgs ha, int dots) {
+__global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, HeadArgs ha) {
   __shared__ TokLds lds;
   const int64_t t = blockIdx.x;
   const float2* st = a.stats + t * a.blocks;
-  if (LAST && dots) row_dots(ha, t, lds);
   float2 v = row_join(st, a.used, lds);
   const float2 old = a.before ? a.before[t] : make_float2(-__builtin_inff(), 0.0f);
   v = soft_join(v, old);
@@ -406,7 +320,7 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, Hea
     const int64_t c = (int64_t)a.tokens[t * a.K + j] - a.n0;
     if (c >= 0 && c < a.cols) e[weight_place(c)] = (_Float16)0.0f;
   }
-  if (LAST) row_loss(ha, t, v, dots, lds);
+  if (LAST) row_loss(ha, t, v, lds);
 }
 
 // ---------------------------------------------------------------------------
@@ -864,7 +778,7 @@ struct HeadPlan {
   int64_t blocks;    // statistics blocks per row kept at a time
   GradTiles tiles;   // of the second product
   int64_t ld_e;
-  size_t stats_at, state_at, shrink_at, ref_at, e_at, part_at, lists_at, bytes;
+  size_t named_at, stats_at, state_at, shrink_at, ref_at, e_at, part_at, lists_at, bytes;
 };
 
 static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
@@ -921,6 +835,7 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
     at = (at + bytes + 255) / 256 * 256;
     return here;
   };
+  p.named_at = take((size_t)T * sizeof(float));
   p.stats_at = take((size_t)T * p.blocks * sizeof(float2));
   if (grad) {
     p.state_at = take((size_t)T * 2 * sizeof(float2));
@@ -934,19 +849,6 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   return p;
 }
 
-static hipError_t launch_dots(const HeadArgs& h, hipStream_t stream) {
-  head_dots_kernel<<<dim3(h.T, token_blocks(h.K, 64 * kTokWaves)), 64 * kTokWaves, 0, stream>>>(h);
-  return hipGetLastError();
-}
-
-// The stream's launch takes the tokens along, in up to this many workgroups (a
-// launch's threads are fewer than 2^32), rather than one of their own before
-// it: T = 21, K = 37 of D = 1056 21.1 -> 18.8 us without a gradient; T = 32, K =
-// 64 of 7168 113.7 -> 109.5; T = 1000, K = 64, D = 1024, N = 4000 33.6 -> 31.3; K =
-// 1024, T = 30 153 -> 145. (The wide kernel has one workgroup to a compute unit,
-// too few for gathers.)
-constexpr int64_t kHeadAlong = 1 << 20;
-
 // The weights' loads pass the caches where their lines are read once: D = 7168,
 // N = 129280, T = 1 83 us (94 through them), T = 32 97 (111). Not with more
 // row tiles (T = 74, D = 5120: 123 us, 118 through the caches), nor for a D
@@ -954,20 +856,13 @@ constexpr int64_t kHeadAlong = 1 << 20;
 // 74 and 58; T = 1, D = 5280, N = 126034: 101 and 91; T = 74, D = 5184: 165 and
 // 133).
 template <Out M, int MR, int KB, int KG>
-static hipError_t launch_stream(const ExpertArgs& a, const HeadArgs& h, bool tokens, Scales sc, int col_tiles,
-                                hipStream_t stream) {
-  const int row_tiles = (a.R + MR - 1) / MR, tiles = row_tiles * col_tiles;
+static hipError_t launch_stream(const ExpertArgs& a, Scales sc, int col_tiles, hipStream_t stream) {
+  const int row_tiles = (a.R + MR - 1) / MR, grid = row_tiles * col_tiles;
   constexpr int NT = KG * kEsThreads;
-  const bool along = tokens && (int64_t)h.T * token_blocks(h.K, NT) <= kHeadAlong;
-  if (tokens && !along) {
-    const hipError_t e = launch_dots(h, stream);
-    if (e != hipSuccess) return e;
-  }
-  const int grid = tiles + (along ? h.T * token_blocks(h.K, NT) : 0);
-  if (sc == Scales::k4) head_stream_kernel<M, MR, KB, KG, Scales::k4, 0><<<grid, NT, 0, stream>>>(a, row_tiles, tiles, h);
-  else if (sc == Scales::kSkewed) head_stream_kernel<M, MR, KB, KG, Scales::kSkewed, 0><<<grid, NT, 0, stream>>>(a, row_tiles, tiles, h);
-  else if (row_tiles > 1) head_stream_kernel<M, MR, KB, KG, Scales::k16, 0><<<grid, NT, 0, stream>>>(a, row_tiles, tiles, h);
-  else head_stream_kernel<M, MR, KB, KG, Scales::k16, kNtAux><<<grid, NT, 0, stream>>>(a, row_tiles, tiles, h);
+  if (sc == Scales::k4) head_stream_kernel<M, MR, KB, KG, Scales::k4, 0><<<grid, NT, 0, stream>>>(a, row_tiles);
+  else if (sc == Scales::kSkewed) head_stream_kernel<M, MR, KB, KG, Scales::kSkewed, 0><<<grid, NT, 0, stream>>>(a, row_tiles);
+  else if (row_tiles > 1) head_stream_kernel<M, MR, KB, KG, Scales::k16, 0><<<grid, NT, 0, stream>>>(a, row_tiles);
+  else head_stream_kernel<M, MR, KB, KG, Scales::k16, kNtAux><<<grid, NT, 0, stream>>>(a, row_tiles);
   return hipGetLastError();
 }
 
@@ -976,14 +871,10 @@ static hipError_t launch_stream(const ExpertArgs& a, const HeadArgs& h, bool tok
 // 19.8; D = 2048 11.9 -> 10.8; level at 1024, 4.8 -> 5.8 at 512.
 constexpr int kHeadFewTiles = 256;
 
-// A piece's logits; `tokens`: and the tokens' own into logq, which the stream's
-// launch takes along.
 template <Out M>
-static hipError_t launch_logits(const ExpertArgs& a, const HeadArgs& h, bool wide, bool tokens, hipStream_t stream) {
+static hipError_t launch_logits(const ExpertArgs& a, bool wide, hipStream_t stream) {
   const Scales sc = scales_of(a);
   if (wide) {
-    const hipError_t e = tokens ? launch_dots(h, stream) : hipSuccess;
-    if (e != hipSuccess) return e;
     const int cols = (a.N + kEtCols - 1) / kEtCols;
     // 64 rows while each compute unit then has one tile at most (T = 192, D = 4096, N = 32000: 62 us, with 128 92; more
     // tiles: T = 256, D = 7168, N = 129280 394 us with 128, 484 with 64).
@@ -996,9 +887,9 @@ static hipError_t launch_logits(const ExpertArgs& a, const HeadArgs& h, bool wid
   }
   const int col_tiles = (a.N + kEsRows * kEsWaves - 1) / (kEsRows * kEsWaves);
   const int tiles16 = (a.R + 15) / 16 * col_tiles;
-  if (tiles16 <= kHeadFewTiles && a.D > 1024) return launch_stream<M, 16, 1024, 2>(a, h, tokens, sc, col_tiles, stream);
-  if (a.R <= 16) return launch_stream<M, 16, 512, 1>(a, h, tokens, sc, col_tiles, stream);
-  return launch_stream<M, 32, 256, 1>(a, h, tokens, sc, col_tiles, stream);
+  if (tiles16 <= kHeadFewTiles && a.D > 1024) return launch_stream<M, 16, 1024, 2>(a, sc, col_tiles, stream);
+  if (a.R <= 16) return launch_stream<M, 16, 512, 1>(a, sc, col_tiles, stream);
+  return launch_stream<M, 32, 256, 1>(a, sc, col_tiles, stream);
 }
 
 static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream_t stream) {
@@ -1010,7 +901,10 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
   float2* stats = reinterpret_cast<float2*>(ws + p.stats_at);
   a.soft.scale = kLog2e / h.tau;
   a.soft.blocks = (int)p.blocks;
-  const bool dots = h.K <= kTokWaves;  // the row's workgroup computes its tokens' logits
+  a.soft.tokens = h.tokens;
+  a.soft.K = h.K;
+  a.soft.named = h.logq ? h.logq : reinterpret_cast<float*>(ws + p.named_at);
+  h.named = a.soft.named;
   hipError_t e;
   if (!grad) {
     for (int64_t i = 0; i < p.pieces; ++i) {
@@ -1018,13 +912,14 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
       a.wc = h.wc + n0 * (h.D / 2);
       a.ws = h.ws + n0 * (h.D / 16);
       a.N = (int)std::min(p.piece, h.N - n0);
+      a.soft.n0 = (int)n0;
       a.soft.stats = stats + (n0 >> p.block_shift);
       a.soft.used = (int)(p.blocks - (n0 >> p.block_shift));
-      if ((e = launch_logits<Out::kSums>(a, h, p.wide, !dots && i == 0, stream)) != hipSuccess) return e;
+      if ((e = launch_logits<Out::kSums>(a, p.wide, stream)) != hipSuccess) return e;
     }
     h.stats = stats;
     h.blocks = h.used = (int)p.blocks;
-    head_tokens_kernel<<<h.T, 64 * kTokWaves, 0, stream>>>(h, dots);
+    head_tokens_kernel<<<h.T, 64 * kTokWaves, 0, stream>>>(h);
     return hipGetLastError();
   }
   float2* state = reinterpret_cast<float2*>(ws + p.state_at);
@@ -1041,8 +936,9 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
     a.wc = h.wc + n0 * (h.D / 2);
     a.ws = h.ws + n0 * (h.D / 16);
     a.N = (int)std::min(p.piece, h.N - n0);
+    a.soft.n0 = (int)n0;
     a.soft.ref = i ? ref : nullptr;
-    if ((e = launch_logits<Out::kWeights>(a, h, p.wide, !dots && i == 0, stream)) != hipSuccess) return e;
+    if ((e = launch_logits<Out::kWeights>(a, p.wide, stream)) != hipSuccess) return e;
     NormArgs n{};
     n.stats = stats; n.blocks = (int)p.blocks;
     n.used = (a.N + 63) / 64 << (6 - p.block_shift);
@@ -1050,8 +946,8 @@ static hipError_t launch_head(const HeadArgs& in, bool grad, char* ws, hipStream
     n.after = state + (i & 1) * (int64_t)h.T;
     n.shrink = shrink; n.ref = ref; n.e = a.soft.e; n.ld_e = p.ld_e;
     n.T = h.T; n.K = h.K; n.n0 = (int)n0; n.cols = a.N; n.tokens = h.tokens;
-    if (i + 1 < p.pieces) head_norm_kernel<false><<<h.T, kNormThreads, 0, stream>>>(n, h, 0);
-    else head_norm_kernel<true><<<h.T, kNormThreads, 0, stream>>>(n, h, dots);
+    if (i + 1 < p.pieces) head_norm_kernel<false><<<h.T, kNormThreads, 0, stream>>>(n, h);
+    else head_norm_kernel<true><<<h.T, kNormThreads, 0, stream>>>(n, h);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     GradArgs g{};
     g.e = a.soft.e; g.ld_e = p.ld_e; g.wc = a.wc; g.ws = a.ws; g.T = h.T; g.D = h.D; g.cols = a.N;

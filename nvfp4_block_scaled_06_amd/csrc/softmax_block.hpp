@@ -5,8 +5,9 @@
 // (m, s) with m >= its largest y and s = sum 2^(y - m); joined over the blocks
 // of a row they give log sum e^z. kWeights also keeps 2^(y - m) itself, as
 // fp16 times 2^15: relative error 2^-11 down to 2^-28 of the row's largest,
-// absolute 2^-39 of it below (bf16 would keep 2^-8 of each). m is a whole
-// number, the next one up, so that a block's weights and sums are brought to
+// absolute 2^-39 of it below (bf16 would keep 2^-8 of each). y is rounded
+// before m is taken off it, so that no difference is above 0 and equal logits
+// give equal weights wherever they stand. m is the next whole number, so that a block's weights and sums are brought to
 // another m by powers of two and are rounded this once. `ref` lets m start at
 // what earlier columns have reached, so that few blocks have a scale of their
 // own.
@@ -24,9 +25,20 @@ struct SoftmaxOut {
   int used;           // blocks that have room for (m, s)
   _Float16* e;        // [T, ld_e]
   int64_t ld_e;       // a multiple of 512
+  const int32_t* tokens;  // [T, K]: columns that rows name; others than [0, all columns) are none
+  int K;
+  int n0;                 // the piece's first column
+  float* named;           // [T, K] their y
 };
 
 constexpr float kWeightOne = 32768.0f;  // a weight of 1 in fp16
+
+// Between writes and reads of LDS that is the wavefront's own.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // Where the weight of column n stands in its row of e: in every 64 columns n
 // and n + 32 are neighbours, as the conversion of the gradient's product takes
@@ -58,21 +70,94 @@ __device__ __forceinline__ float dpp_f(float v) {
   return __int_as_float(dpp_i<CTRL>(__float_as_int(v)));
 }
 
-// A whole number at least as large as the exact product that y is rounded from
-// (by a half step, relative 2^-24), and less than 2 above it; -infinity for none.
-__device__ __forceinline__ float whole_above(float y) {
-  return y > -__builtin_inff() ? ceilf(fmaf(fabsf(y), 0x1p-22f, y)) : y;
+// Logits of the tokens that a block's rows name, from the block's own sums: the
+// rows' losses (loss.hip) then hold them against a sum of which they are a part,
+// and no probability comes out above 1, however large the logits are. Every
+// wavefront looks through the tokens of its tile's rows for those in its columns
+// (STREAM: 16 columns from col0 and the 16 that lie 32 after them, else 64) and
+// stores their y; few have any.
+//
+// Which of 64 x 32 tokens, from p0 on, may be such: bit 31 - u for token p0 + 64 u
+// + lane, by its column alone (places past the n-th read as token 0). The tile
+// asks for the first of them before its loop, where the loads' latency is not
+// felt (after it: T = 4096 0.6 % more).
+constexpr int kNamedLoads = 32;
+template <bool STREAM, int U>
+__device__ __forceinline__ uint32_t named_bits(const int32_t* tokens, int n, uint32_t base, int p0) {
+  const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(tokens, (int64_t)n * 4);
+  uint32_t c[U], hits = 0u;
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    c[u] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, 4 * (p0 + (int)(threadIdx.x & 63)) + 256 * u, 0, 0);
+#pragma unroll
+  for (int u = 0; u < U; ++u) hits = hits + hits + ((STREAM ? (c[u] - base) & ~47u : (c[u] - base) >> 6) == 0u ? 1u : 0u);
+  return hits << (32 - U);
+}
+template <bool STREAM>
+__device__ __forceinline__ uint32_t named_hits(const SoftmaxOut& o, int row0, int nr, int col0, int p0) {
+  const int n = nr * o.K;
+  const int32_t* tokens = o.tokens + (int64_t)row0 * o.K;
+  const uint32_t base = (uint32_t)(o.n0 + col0);
+  uint32_t hits;
+  if (n - p0 <= 128) hits = named_bits<STREAM, 2>(tokens, n, base, p0);
+  else if (n - p0 <= 1024) hits = named_bits<STREAM, 16>(tokens, n, base, p0);
+  else hits = named_bits<STREAM, kNamedLoads>(tokens, n, base, p0);
+  asm volatile("" : "+v"(hits));  // here, not where it is used: that would hold the tokens until then
+  return hits;
+}
+
+// `hits`: named_hits from 0 on. `stage` puts row tile i's y into the wavefront's
+// LDS, [32 rows][columns].
+template <int RT, bool STREAM, class Stage>
+__device__ __forceinline__ void named_logits(const SoftmaxOut& o, int row0, int nr, int col0, int N, uint32_t hits,
+                                             const float* lds, Stage stage) {
+  const int n = nr * o.K;
+  const int32_t* tokens = o.tokens + (int64_t)row0 * o.K;
+  float* named = o.named + (int64_t)row0 * o.K;
+  int staged = -1;
+  for (int p0 = 0;;) {
+    while (__ballot(hits != 0u)) {
+      const int u = (int)__builtin_clz(hits | 1u), p = p0 + (int)(threadIdx.x & 63) + 64 * u;
+      const bool in = hits != 0u && p < n;
+      hits &= ~(0x80000000u >> u);
+      const uint32_t col = in ? (uint32_t)(tokens[p] - o.n0 - col0) : 0u;
+      const int row = in ? p / o.K : 0;
+      const uint32_t at = STREAM ? 32 * row + ((col >> 5) << 4) + (col & 15u) : 64 * (row & 31) + col;
+      static_for<0, RT>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        const bool here = in && (row >> 5) == i && col0 + (int)col < N;
+        if (!__ballot(here)) return;
+        if (staged != i) stage(ic);
+        staged = i;
+        if (here) named[p] = lds[at];
+      });
+    }
+    p0 += 64 * kNamedLoads;
+    if (p0 >= n) return;
+    hits = named_hits<STREAM>(o, row0, nr, col0, p0);
+  }
 }
 
 // Block of 32 places from the stream's accumulators: lane (r, q), value v of
 // tile m: row r (+ 16 t), column col0 + 32 m + 4 q + v, so that a lane's eight
 // columns are neighbours in e.
+// `hits`: named_hits from 0 on; `lds`: 16 NT rows of 32 floats of the wavefront's own.
 template <bool KEEP, int NT>
 __device__ __forceinline__ void softmax_block16(const SoftmaxOut& o, const f32x4_t (&acc)[2][NT], float scale,
-                                                int row0, int nr, int col0, int N) {
+                                                int row0, int nr, int col0, int N, uint32_t hits, float* lds) {
+#pragma clang fp contract(off)
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int place = (col0 & ~63) + 2 * (col0 & 63);
   const float sc = scale * o.scale;
+  named_logits<1, true>(o, row0, nr, col0, N, hits, lds, [&](auto) {
+    wave_lds_fence();
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        *reinterpret_cast<f32x4_t*>(lds + 32 * (16 * t + r) + 16 * m + 4 * q) = acc[m][t] * sc;
+    wave_lds_fence();
+  });
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int row = 16 * t + r;
@@ -82,7 +167,7 @@ __device__ __forceinline__ void softmax_block16(const SoftmaxOut& o, const f32x4
       y[i] = col0 + 32 * (i & 1) + 4 * q + (i >> 1) < N ? acc[i & 1][t][i >> 1] * sc : -__builtin_inff();
       m = fmaxf(m, y[i]);
     }
-    m = whole_above(max_across32(max_across16(m)));
+    m = ceilf(max_across32(max_across16(m)));
     // Columns past N have weights of zero and take no part in the sums.
     const bool none = col0 >= N;
     if (KEEP && o.ref && row < nr && !none) m = fmaxf(m, o.ref[row0 + row]);
@@ -106,9 +191,11 @@ __device__ __forceinline__ void softmax_block16(const SoftmaxOut& o, const f32x4
 
 // Block of 64 columns from a wide tile's accumulators: lane (r, h), value v of
 // row tile i: row 32 i + 8 (v / 4) + 4 h + v % 4, columns r and 32 + r.
+// `hits`: named_hits from 0 on; `lds`: 32 rows of 64 floats of the wavefront's own.
 template <bool KEEP, int RT>
 __device__ __forceinline__ void softmax_block32(const SoftmaxOut& o, const f32x16_t (&acc)[RT][2], float scale,
-                                                int row0, int nr, int col0, int N) {
+                                                int row0, int nr, int col0, int N, uint32_t hits, float* lds) {
+#pragma clang fp contract(off)
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   if (col0 >= N) {
     // As there: the gradient's product takes the tile's columns past N too.
@@ -121,6 +208,15 @@ __device__ __forceinline__ void softmax_block32(const SoftmaxOut& o, const f32x1
     return;
   }
   const float sc = scale * o.scale;
+  named_logits<RT, false>(o, row0, nr, col0, N, hits, lds, [&](auto ic) {
+    constexpr int i = decltype(ic)::value;
+    wave_lds_fence();
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) lds[64 * (8 * (v >> 2) + 4 * h + (v & 3)) + 32 * m + r] = acc[i][m][v] * sc;
+    wave_lds_fence();
+  });
   const bool in0 = col0 + r < N, in1 = col0 + 32 + r < N;
 #pragma unroll
   for (int i = 0; i < RT; ++i)
@@ -133,7 +229,7 @@ __device__ __forceinline__ void softmax_block32(const SoftmaxOut& o, const f32x1
       m = fmaxf(m, dpp_f<kDppXor2>(m));
       m = fmaxf(m, dpp_f<kDppHalfMirror>(m));
       m = fmaxf(m, dpp_f<kDppMirror>(m));
-      m = whole_above(max_across16(m));
+      m = ceilf(max_across16(m));
       if (KEEP && o.ref && row < nr) m = fmaxf(m, o.ref[row0 + row]);
       const float e0 = __builtin_amdgcn_exp2f(y0 - m), e1 = __builtin_amdgcn_exp2f(y1 - m);
       float s = e0 + e1;

@@ -172,3 +172,85 @@ def test_softmax_weights_are_rounded_once(dev, T, N):
     assert np.abs(want).max() < 0.01 * share
     err = np.abs(dx[:, 32:48].double().cpu().numpy() - want)
     assert (err <= bound).all(), (err.max() / share * 2048, bound.max() / share * 2048)
+
+
+CONF_SIZES = [(4, 256, 900), (16, 1280, 700), (20, 96, 5000), (40, 1056, 1100), (70, 128, 13000), (130, 288, 9000)]
+
+
+@pytest.mark.parametrize("T,D,N", CONF_SIZES)
+@pytest.mark.parametrize("scale", [1.0, 60.0])
+def test_no_probability_exceeds_one(dev, T, D, N, scale):
+    """The row's own best token: its loss is a logarithm of 1 and more, so not below 0, at any temperature; where the
+    second best is far behind both are 0 but for a few steps of 1, however large the logits over the temperature are."""
+    xq, wq = operands(T, D, N, 11, dev, scale)
+    z = lr.dequant_ref(*host(xq)) @ lr.dequant_ref(*host(wq)).T
+    top = np.sort(z, axis=1)[:, -2:]
+    err = (D + 8) * 2.0 ** -24 * (np.abs(lr.dequant_ref(*host(xq))) @ np.abs(lr.dequant_ref(*host(wq))).T).max(axis=1)
+    best = z.argmax(axis=1).astype(np.int32)
+    ws = workspace(T, D, N, True, dev)
+    wmax = np.abs(lr.dequant_ref(*host(wq))).sum(axis=0)
+    log(f"confident T={T} D={D} N={N} scale={scale}")
+    loss, lse, dx = rt.lmhead_loss(xq, wq, up(best, dev), ws, want_grad=True)
+    torch.cuda.synchronize()
+    assert (loss >= 0).all()
+    for K in (1, 3, 9):
+        tok = np.tile(best[:, None], (1, K))
+        tok[:, 1:] = np.random.default_rng(K).integers(0, N, (T, K - 1))
+        te = np.full((T, K), -np.inf, np.float32)
+        te[:, 0] = 3.0
+        for tau in (2.0 ** -6, 2.0 ** -10, 2.0 ** -15, 2.0 ** -20):
+            loss, lse, logq, dx = rt.lmhead_distill(xq, wq, up(tok, dev), up(te, dev), ws, temperature=tau, want_grad=True)
+            torch.cuda.synchronize()
+            loss, logq, dx = loss.double().cpu().numpy(), logq.double().cpu().numpy(), dx.double().cpu().numpy()
+            assert (logq <= 0).all() and (loss >= 0).all(), (K, tau, logq.max(), loss.min())
+            sure = (top[:, 1] - top[:, 0] - 2 * err) / tau > 40.0  # N e^-40 is below 2^-24
+            # The sum's roundings: at most 2^-24 for each of the 64 and more steps of its tree.
+            assert (-logq[sure, 0] <= 2.0 ** -18).all() and (loss[sure] <= tau * tau * 2.0 ** -18).all()
+            assert (np.abs(dx[sure]) <= tau * 2.0 ** -18 * wmax + 2.0 ** -133).all()
+            if tau <= 2.0 ** -10 and scale > 1:
+                assert sure.any()
+
+
+@pytest.mark.parametrize("tau", [2.0 ** -4, 2.0 ** -8])
+def test_cold_temperatures(dev, tau):
+    """Against float64 on the logits that the device itself sums, whose roundings the temperature magnifies for any
+    evaluation: they are taken from lmhead_argmax and counted; the quotients by the temperature are not."""
+    T, D, N, K = 4, 1024, 5003, 6
+    xq, wq = operands(T, D, N, 12, dev, 2.0)
+    ws = rt.Workspace(max(rt.lmhead_workspace_bytes(T, D, N), rt.lmhead_loss_workspace_bytes(T, D, N, True)), dev)
+    _, _, logits = rt.lmhead_argmax(xq, wq, ws, want_logits=True)
+    torch.cuda.synchronize()
+    z = logits.double().cpu().numpy()
+    order = np.argsort(-z, axis=1)
+    tok = order[:, :K].astype(np.int32)
+    te = np.take_along_axis(z, tok, 1).astype(np.float32) + np.random.default_rng(1).uniform(-tau, tau, (T, K)).astype(np.float32)
+    loss, lse, logq, _ = rt.lmhead_distill(xq, wq, up(tok, dev), up(te, dev), ws, temperature=tau, want_grad=True)
+    torch.cuda.synchronize()
+    # Two sums of D products in fp32 with random signs: partial sums stay below 6 times the products' norm, and at most D
+    # roundings of half a step of those, with random signs too, add up to sqrt(D) of them.
+    norm = np.sqrt((lr.dequant_ref(*host(xq)) ** 2) @ (lr.dequant_ref(*host(wq)) ** 2).T).max()
+    err = 2 * D ** 0.5 * 2.0 ** -24 * 6 * norm / tau
+    zt = z / tau
+    ref = lr._lse(zt)
+    want = np.take_along_axis(zt, tok, 1) - ref[:, None]
+    got = logq.double().cpu().numpy()
+    bound = 2 * err + 2.0 ** -18 + 2.0 ** -21 * np.abs(want)
+    assert (np.abs(got - want) <= bound).all(), (np.abs(got - want) / bound).max()
+    t = te.astype(np.float64) / tau
+    p = np.exp(t - lr._lse(t)[:, None])
+    kl = (p * (t - lr._lse(t)[:, None] - want)).sum(axis=1)
+    assert (np.abs(loss.double().cpu().numpy() - tau * tau * kl) <= tau * tau * (bound.max() + 2.0 ** -18)).all()
+
+
+def test_largest_teacher_logits(dev):
+    """Finite teacher logits give finite losses, also where their quotients by the temperature would not be."""
+    T, D, N, K = 3, 64, 200, 4
+    xq, wq = operands(T, D, N, 13, dev)
+    big = np.finfo(np.float32).max
+    te = np.tile(np.array([[big, 0.0, -big, big]], np.float32), (T, 1))
+    tok = np.tile(np.array([[3, 4, 5, 6]], np.int32), (T, 1))
+    loss, _, logq, dx = rt.lmhead_distill(xq, wq, up(tok, dev), up(te, dev), workspace(T, D, N, True, dev), temperature=0.5,
+                                          want_grad=True)
+    torch.cuda.synchronize()
+    want = 0.25 * (-np.log(2.0) - logq.double().cpu().numpy()[:, [0, 3]].mean(axis=1))
+    assert np.abs(loss.double().cpu().numpy() - want).max() <= 1e-5 and torch.isfinite(dx.float()).all()
