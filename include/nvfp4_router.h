@@ -481,7 +481,10 @@ int lmhead_penalize(const void* logits, int dtype, int64_t T, int64_t N, int64_t
  *   workspace                lmhead_loss_workspace_bytes(T, D, N, dx != NULL)
  *                            bytes, 256-byte aligned, for either call; its
  *                            state prefix (see router_workspace_bytes) is not
- *                            touched. 0 for sizes that the calls refuse.
+ *                            touched. 0 for sizes that the calls refuse. A
+ *                            workspace made for T rows takes every call with
+ *                            fewer, one made for the gradient also those
+ *                            without it.
  * Products are exact with fp32 sums in a fixed order, so results repeat bit for
  * bit. A named token's logit is the one that the sum over the vocabulary has in
  * it: no probability is above 1, no logq above 0 and no cross entropy below 0,

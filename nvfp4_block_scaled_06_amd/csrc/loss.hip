@@ -824,7 +824,7 @@ static HeadPlan head_plan(int64_t T, int64_t D, int64_t N, bool grad) {
   const double step_us = std::max(2.3, 0.25 + 0.8 * (double)std::min(int64_t(4), (T + 31) / 32));
   double best = 1e30;
   p.tiles.splits = 1;
-  for (int64_t s = 1; rest && s <= most; ++s) {
+  for (int64_t s = 1; grad && rest && s <= most && sums * (double)s < best; ++s) {
     const double us = (6.0 + step_us * std::ceil(steps / (double)s)) * (double)((rest * s + 255) / 256) + sums * (double)s;
     if (us < best) best = us, p.tiles.splits = (int)s;
   }
@@ -994,7 +994,7 @@ int head_call(nvr::HeadArgs& h, int64_t T, int64_t D, int64_t N, int64_t K, void
       !aligned(h.teacher, h.teacher_bf16 ? 2 : 4))
     return ROUTER_EINVAL;
   if (T == 0) return ROUTER_OK;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < lmhead_loss_workspace_bytes(T, D, N, h.dx != nullptr))
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < nvr::head_plan(T, D, N, h.dx != nullptr).bytes)
     return ROUTER_EINVAL;
   h.T = (int)T; h.D = (int)D; h.N = (int)N; h.K = (int)K;
   const hipError_t e = nvr::launch_head(h, h.dx != nullptr, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
@@ -1007,7 +1007,14 @@ extern "C" {
 
 size_t lmhead_loss_workspace_bytes(int64_t T, int64_t D, int64_t N, int grad) {
   if (check_head_sizes(T, D, N) != ROUTER_OK) return 0;
-  return nvr::head_plan(T, D, N, grad != 0).bytes;
+  // What a call needs falls in places as T grows (other tiles, splits and pieces), so this is the most of all row counts
+  // up to T, and with a gradient of the calls without one too: 3 ms at T = 4096.
+  size_t bytes = 0;
+  for (int64_t t = std::min(T, int64_t(1)); t <= T; ++t) {
+    bytes = std::max(bytes, nvr::head_plan(t, D, N, false).bytes);
+    if (grad) bytes = std::max(bytes, nvr::head_plan(t, D, N, true).bytes);
+  }
+  return bytes;
 }
 
 int lmhead_loss(const uint8_t* x_codes, const uint8_t* x_scales, const float* gsa, const uint8_t* w_codes,

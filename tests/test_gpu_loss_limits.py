@@ -254,3 +254,23 @@ def test_largest_teacher_logits(dev):
     torch.cuda.synchronize()
     want = 0.25 * (-np.log(2.0) - logq.double().cpu().numpy()[:, [0, 3]].mean(axis=1))
     assert np.abs(loss.double().cpu().numpy() - want).max() <= 1e-5 and torch.isfinite(dx.float()).all()
+
+
+@pytest.mark.parametrize("D,N,most", [(96, 13000, 130), (256, 6000, 300), (1024, 2000, 140)])
+def test_a_workspace_for_more_rows(dev, D, N, most):
+    """A workspace made for the most rows, with the gradient, takes every call with fewer, with the gradient and without."""
+    _, wq = operands(1, D, N, 20, dev)
+    xq = quantized(np.random.default_rng(21).standard_normal((most, D)), dev)
+    y = up(np.random.default_rng(22).integers(0, N, most).astype(np.int32), dev)
+    ws = workspace(most, D, N, True, dev)
+    for T in (0, 1, 16, 17, 32, 33, 64, 65, 96, 128, 129, most):
+        if T > most:
+            continue
+        log(f"workspace for {most} rows, T={T} D={D} N={N}")
+        part = rt.NVFP4Tensor(xq.codes[:T], xq.scales[:T], xq.gscale)
+        got = rt.lmhead_loss(part, wq, y[:T], ws, want_grad=True)
+        alone = rt.lmhead_loss(part, wq, y[:T], ws)
+        want = rt.lmhead_loss(part, wq, y[:T], workspace(T, D, N, True, dev), want_grad=True)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert alone[2] is None and torch.allclose(alone[0], got[0], rtol=1e-5, atol=1e-5)
