@@ -394,15 +394,28 @@ __device__ __forceinline__ void sel_order(const SelectArgs& a, int64_t base, dou
     sc.key[li + LPR * h] = __float_as_uint(x[h]);
   }
   sel_fence();
+  int same[H] = {};  // keys equal to the lane's, its own among them
   for (int u0 = 0; u0 < C; u0 += 8) {
 #pragma unroll
     for (int u = u0; u < u0 + 8; ++u) {
       const double other = sc.wide[u];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        rank[h] += other > mine[h] ? 1 : 0;
+        same[h] += other == mine[h] ? 1 : 0;
+      }
+    }
+  }
+  bool tie = false;
+#pragma unroll
+  for (int h = 0; h < H; ++h) tie = tie || (li + LPR * h < C && same[h] > 1);
+  if (__ballot(tie)) {
+    for (int u = 0; u < C; ++u) {
+      const double other = sc.wide[u];
       const int at = (int)~(uint32_t)sc.cand[u];
       const float l = __uint_as_float(sc.key[u]);
 #pragma unroll
-      for (int h = 0; h < H; ++h)
-        rank[h] += other > mine[h] || (other == mine[h] && (l > x[h] || (l == x[h] && at < e[h]))) ? 1 : 0;
+      for (int h = 0; h < H; ++h) rank[h] += other == mine[h] && (l > x[h] || (l == x[h] && at < e[h])) ? 1 : 0;
     }
   }
 #pragma unroll
