@@ -193,6 +193,7 @@ __device__ __forceinline__ uint64_t sel_groups(const SelectArgs& a, const F* val
     const F lowest = -row_fmax<LPR, F>(keep ? (F)slack - score : ninf);
     const F next = row_fmax<LPR, F>(!keep && g < a.groups ? score + (F)slack : ninf);
     if (lowest > ninf && lowest <= next) unsure = true;
+    if (b2 > ninf && b1 < -ninf && !(score > ninf && score < -ninf)) unsure = true;  // a sum beyond 32 bits
   }
   return __ballot(keep) >> row;
 }

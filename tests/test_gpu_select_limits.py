@@ -150,3 +150,22 @@ def test_infinite_logits(dev, T):
         else:
             assert (idx[1] == -1).all() and not w[1].any()
         check(x[rest], None, k, (idx[rest], w[rest]), scoring="softmax")
+
+
+@pytest.mark.parametrize("T", ROWS)
+def test_biases_of_the_lowest_value(dev, T):
+    """Experts banned by the type's lowest value and by less: sums of two such keys, beyond 32 bits, still have an order, and
+    come before groups of masked experts."""
+    G, E = 8, 32
+    low = np.finfo(np.float32).min
+    x = np.random.default_rng(T).standard_normal((T, E)).astype(np.float32)
+    b = np.full(E, low, np.float32)
+    b[20:22] = low / 2   # group 5: the largest of the sums
+    b[26] = low / 3      # group 6: the second
+    x[:, 0:4] = -np.inf  # group 0: nothing to choose
+    log(f"lowest biases T={T}")
+    for kept, top in ((1, 2), (2, 2), (7, 2), (2, 1)):
+        kw = dict(groups=G, topk_groups=kept, group_top=top)
+        got = rt.select(up(x, dev), 4, bias=up(b, dev), **kw)
+        torch.cuda.synchronize()
+        check(x, b, 4, got, **kw)
