@@ -149,23 +149,29 @@ __device__ __forceinline__ uint64_t sel_groups(const SelectArgs& a, const F* val
   float l1 = -__builtin_inff();  // and its logit
   if (g < a.groups) {
     const int end = min((sub + 1) * run, a.size);
-#pragma clang loop unroll_count(WIDE ? 2 : 8)
-    for (int i = sub * run; i < end; ++i) {
-      const F x = vals[sel_place<F>(g * a.size + i)];
-      if constexpr (WIDE) {
+    if (WIDE && !two) {
+      for (int i = sub * run; i < end; ++i) {
         const int e = g * a.size + i;
-        if (x > b1 || (!two && x == b1 && x > ninf && sel_logit(a.logits, a.bf16, base + e) > sel_logit(a.logits, a.bf16, base + e1)))
+        const F x = vals[sel_place<F>(e)];
+        if (x > b1 || (x == b1 && x > ninf && sel_logit(a.logits, a.bf16, base + e) > sel_logit(a.logits, a.bf16, base + e1))) {
+          b1 = x;
           e1 = e;
+        }
       }
-      const F lo = x < b1 ? x : b1;
-      b2 = lo > b2 ? lo : b2;
-      b1 = x > b1 ? x : b1;
+      if (b1 > ninf) l1 = sel_logit(a.logits, a.bf16, base + e1);
+    } else {
+#pragma unroll 8
+      for (int i = sub * run; i < end; ++i) {
+        const F x = vals[sel_place<F>(g * a.size + i)];
+        const F lo = x < b1 ? x : b1;
+        b2 = lo > b2 ? lo : b2;
+        b1 = x > b1 ? x : b1;
+      }
     }
-    if (WIDE && !two && b1 > ninf) l1 = sel_logit(a.logits, a.bf16, base + e1);
   }
   for (int o = 1; o < lpg; o <<= 1) {
     const F o1 = __shfl_xor(b1, o), o2 = __shfl_xor(b2, o);
-    if constexpr (WIDE) {
+    if (WIDE && !two) {
       const float ol = __shfl_xor(l1, o);
       l1 = o1 > b1 || (o1 == b1 && ol > l1) ? ol : l1;
     }
@@ -179,7 +185,7 @@ __device__ __forceinline__ uint64_t sel_groups(const SelectArgs& a, const F* val
   for (int j = 0; j < a.groups; ++j) {
     const F s = __shfl(score, row + (j << a.sh));
     bool before = j < g;
-    if constexpr (WIDE) {
+    if (WIDE && !two) {
       const float l = __shfl(l1, row + (j << a.sh));
       before = l > l1 || (l == l1 && before);
     }
