@@ -432,9 +432,13 @@ int lmhead_penalize(const void* logits, int dtype, int64_t T, int64_t N, int64_t
                     float* out_logit, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * Losses of the lm_head over its whole vocabulary, with the gradient of x, and
- * without T x N logits in memory: z[t, n] = gsa * gsw * sum_d xhat[t, d] *
- * what[n, d], lmhead_argmax's logits, are taken in pieces of the vocabulary.
+ * Losses of the lm_head over its whole vocabulary, with the gradient of x: z[t,
+ * n] = gsa * gsw * sum_d xhat[t, d] * what[n, d], lmhead_argmax's logits. A loss
+ * alone keeps T x N / 8 to / 4 bytes of sums and no logits. The gradient keeps its
+ * softmax weights, fp16 [T, piece], for a piece of the vocabulary at a time:
+ * 512 MB of them or 4096 columns, whichever is more, so up to T = 2^28 / N rows
+ * that is all of T x N; beside them sums of [T, D] in fp32, for up to 256 splits
+ * of a piece where tiles are few, and 8.2 KB for each row's named tokens.
  *
  * lmhead_loss, the cross entropy (the negative log-probability of a token):
  *   lse[t] = log sum_n e^z[t, n];  loss[t] = lse[t] - z[t, targets[t]]
@@ -465,7 +469,9 @@ int lmhead_penalize(const void* logits, int dtype, int64_t T, int64_t N, int64_t
  *   x_codes, x_scales, gsa   router_quantize outputs for x [T, D] (16- and
  *                            2-byte aligned).
  *   w_codes, w_scales, gsw   the weights in the same format: [N, D/2],
- *                            [N, D/16] (16- and 4-byte aligned).
+ *                            [N, D/16] (16- and 4-byte aligned). Where N and
+ *                            D/32 are odd the word that holds the last two
+ *                            scales is read whole, 2 bytes past them.
  *   targets                  [T] int32.
  *   tokens, teacher          [T, K] int32 and [T, K] of `dtype`.
  *   temperature              2^-20 to 2^20.

@@ -1,5 +1,5 @@
 // Losses of the NVFP4 lm_head over its whole vocabulary, with their gradients
-// (gfx950), without T x N logits in memory.
+// (gfx950).
 //
 //   z[t, n] = gsa gsw sum_d xhat[t, d] what[n, d],   xhat, what = q S
 //   lmhead_loss:    lse = log sum_n e^z;  loss = lse - z[t, target]
@@ -11,8 +11,8 @@
 // The vocabulary is taken in pieces. A piece's products stay in registers and
 // give each row a maximum and a sum for every block of columns
 // (softmax_block.hpp); with a gradient they also leave the columns' weights
-// e = 2^(y - m), fp16, and a second product sum_n e[t, n] what[n] is added to
-// what the pieces before gave. The weights of a piece are those of the
+// e = 2^(y - m), fp16 (of a piece: 512 MB, T x N where that is less), and a second
+// product sum_n e[t, n] what[n] is added to what the pieces before gave. The weights of a piece are those of the
 // softmax up to a factor per row, which the pieces after may change: as a row's
 // maximum rises, its sums so far shrink. So the gradient needs two products,
 // not the three of computing the logits again once their sum is known.
@@ -148,10 +148,11 @@ __device__ __forceinline__ float2 thread_join(const float2* st, int n) {
 // ---------------------------------------------------------------------------
 // Logits of a piece: the experts' tiles, one matrix, with softmax_block.hpp's
 // epilogue. D = 7168, N = 129280 (521 MB of weights), the kernel alone:
-//   stream  T = 1 83 us, T = 32 97: HBM, 6.3 and 5.4 TB/s of reads;
-//   wide    T = 1024 1.45 ms, T = 4096 5.7 (1.31 and 1.33 PFLOP/s), keeping the
-//           weights 1.51 and 6.2: the matrix cores, 62 % busy at the clock that
-//           their power leaves.
+//   stream  T = 1 84 us, T = 32 with 64 tokens a row 102: HBM, 6.2 and 5.1 TB/s of
+//           reads (1.2 us for the search for the tokens, by its instructions);
+//   wide    T = 1024 1.54 ms, T = 4096 6.0 (1.24 and 1.26 PFLOP/s), keeping the
+//           weights 1.64 and 6.4: the matrix cores, 64 to 68 % busy at the 1.9
+//           GHz that their power leaves. (Boxes differ by 6 %.)
 // ---------------------------------------------------------------------------
 template <Out M, int MR, int KB, int KG, Scales S, int AUX>
 __global__ __launch_bounds__(KG * kEsThreads) void head_stream_kernel(ExpertArgs a, int row_tiles) {
@@ -274,8 +275,8 @@ __device__ __forceinline__ void row_loss(const HeadArgs& a, int64_t t, float2 v,
 }
 
 // Without a gradient: the end of a row, from its blocks' (m, s). Latency at few
-// rows (5.4 us at T = 1, N = 129280: 4040 blocks, 32 KB); T = 4096 with 2020
-// blocks each: 23 us, 2.9 TB/s.
+// rows (4.9 us at T = 1, N = 129280: 4040 blocks, 32 KB); T = 4096 with 2020
+// blocks each: 15 us, 4.5 TB/s.
 __global__ __launch_bounds__(64 * kTokWaves) void head_tokens_kernel(HeadArgs a) {
   __shared__ TokLds lds;
   const int64_t t = blockIdx.x;
@@ -299,7 +300,7 @@ struct NormArgs {
 };
 
 // One workgroup per row. LAST: the sums are complete, and it goes on to the
-// row's loss. 5.5 us at T = 203, 6.6 with 37 tokens, 23 at T = 4096: latency.
+// row's loss. 5.0 us at T = 203, 6.4 with 37 tokens, 16 at T = 4096: latency.
 constexpr int kNormThreads = 64 * kTokWaves;
 template <bool LAST>
 __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, HeadArgs ha) {
@@ -344,8 +345,9 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, Hea
 //    32 further on to MFMA j.
 // All double-buffered in LDS, one barrier per step; a step's loads go out a step
 // before they are written there.
-// D = 7168, N = 129280: T = 4096 6.23 ms for the two pieces (1.22 PFLOP/s), T =
-// 1024 1.56, bound by the matrix cores and their power as the logits' tiles;
+// D = 7168, N = 129280: T = 4096 6.4 ms for the two pieces (1.18 PFLOP/s), T =
+// 1024 1.65, bound by the matrix cores (68 % busy) and their power as the logits'
+// tiles (boxes differ by 6 %);
 // with few rows by the weights (T = 1 to 8: 117 us for 521 MB, 4.5 TB/s), then
 // by splits that leave a workgroup few steps (T = 203, D = 2080, N = 32003: 48
 // us for 27 GFLOP, 11 steps and 39 MB of sums).

@@ -609,7 +609,7 @@ def lmhead_loss(xq, wq, targets, workspace, weight=None, want_grad=False, out=No
     """lmhead_loss: cross entropy of the NVFP4 lm_head wq [N, D] on xq [T, D] for targets [T] int32 (outside [0, N):
     ignored), without the logits in memory. Returns ``(loss [T] fp32, lse [T] fp32, dx)``; with want_grad dx [T, D] bf16
     is the gradient of sum(weight * loss) with respect to the dequantized x (weight [T] fp32, None for ones), else
-    None."""
+    None; its workspace holds a piece of the softmax weights (512 MB)."""
     dev, T, D, N, out = _check_head(xq, wq, weight, workspace, want_grad, out)
     _tensor(targets, "targets", torch.int32, (T,), dev)
     loss = torch.empty(T, dtype=torch.float32, device=dev)
