@@ -341,7 +341,7 @@ __device__ __forceinline__ void stream_tile(const ExpertArgs& a, const ExpertTil
   if constexpr (M == Out::kSums || M == Out::kWeights) {
     static_assert(sizeof(lds.codes[0]) >= MR * 32 * sizeof(float));
     softmax_block16<M == Out::kWeights, NT>(a.soft, acc, scale, rt.row0, nr, o0, a.N, hits,
-                                                 reinterpret_cast<float*>(my_codes));
+                                            reinterpret_cast<float*>(my_codes));
   } else if constexpr (GLU) {
     if (!live0) return;
     const int f = o0 + 4 * q;
@@ -609,7 +609,7 @@ __device__ __forceinline__ void wide_tile(const ExpertArgs& a, const ExpertTile&
   if constexpr (M == Out::kSums || M == Out::kWeights) {
     static_assert(sizeof(lds.codes[0]) >= 32 * 64 * sizeof(float));
     softmax_block32<M == Out::kWeights, RT>(a.soft, acc, scale, rt.row0, nr, o0, a.N, hits,
-                                                 reinterpret_cast<float*>(codes));
+                                            reinterpret_cast<float*>(codes));
   } else if constexpr (GLU) {
     const int f = o0 + r;
     if (f >= F) return;

@@ -12,10 +12,11 @@
 // give each row a maximum and a sum for every block of columns
 // (softmax_block.hpp); with a gradient they also leave the columns' weights
 // e = 2^(y - m), fp16 (of a piece: 512 MB, T x N where that is less), and a second
-// product sum_n e[t, n] what[n] is added to what the pieces before gave. The weights of a piece are those of the
-// softmax up to a factor per row, which the pieces after may change: as a row's
-// maximum rises, its sums so far shrink. So the gradient needs two products,
-// not the three of computing the logits again once their sum is known.
+// product sum_n e[t, n] what[n] is added to what the pieces before gave. The
+// weights of a piece are those of the softmax up to a factor per row, which the
+// pieces after may change: as a row's maximum rises, its sums so far shrink. So
+// the gradient needs two products, not the three of computing the logits again
+// once their sum is known.
 //
 // The K tokens of the loss do not take part in that second product: their
 // weights are set to zero there, and q_j - p_j, in fp32, multiplies their rows

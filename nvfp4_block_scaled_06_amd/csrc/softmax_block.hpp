@@ -7,10 +7,10 @@
 // fp16 times 2^15: relative error 2^-11 down to 2^-28 of the row's largest,
 // absolute 2^-39 of it below (bf16 would keep 2^-8 of each). y is rounded
 // before m is taken off it, so that no difference is above 0 and equal logits
-// give equal weights wherever they stand. m is the next whole number, so that a block's weights and sums are brought to
-// another m by powers of two and are rounded this once. `ref` lets m start at
-// what earlier columns have reached, so that few blocks have a scale of their
-// own.
+// give equal weights wherever they stand. m is the next whole number, so that a
+// block's weights and sums are brought to another m by powers of two and are
+// rounded this once. `ref` lets m start at what earlier columns have reached, so
+// that few blocks have a scale of their own.
 #pragma once
 
 #include "mma_tile.hpp"
@@ -18,17 +18,17 @@
 namespace nvr {
 
 struct SoftmaxOut {
-  float scale;        // log2(e) / temperature
-  const float* ref;   // NULL or [T]: a lower bound of m
-  float2* stats;      // [T, blocks] (m, s)
-  int blocks;         // stride of stats
-  int used;           // blocks that have room for (m, s)
-  _Float16* e;        // [T, ld_e]
-  int64_t ld_e;       // a multiple of 512
-  const int32_t* tokens;  // [T, K]: columns that rows name; others than [0, all columns) are none
+  float scale;            // log2(e) / temperature
+  const float* ref;       // NULL or [T]: a lower bound of m
+  float2* stats;          // [T, blocks] (m, s)
+  int blocks;             // stride of stats
+  int used;               // blocks that have room for (m, s)
+  _Float16* e;            // [T, ld_e]
+  int64_t ld_e;           // a multiple of 512
+  const int32_t* tokens;  // [T, K]: columns that rows name; any other number is none
   int K;
   int n0;                 // the piece's first column
-  float* named;           // [T, K] their y
+  float* named;           // [T, K]: their y
 };
 
 constexpr float kWeightOne = 32768.0f;  // a weight of 1 in fp16
