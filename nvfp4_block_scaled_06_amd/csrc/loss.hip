@@ -150,7 +150,7 @@ __device__ __forceinline__ float2 thread_join(const float2* st, int n) {
 // Logits of a piece: the experts' tiles, one matrix, with softmax_block.hpp's
 // epilogue. D = 7168, N = 129280 (521 MB of weights), the kernel alone:
 //   stream  T = 1 84 us, T = 32 with 64 tokens a row 102: HBM, 6.2 and 5.1 TB/s of
-//           reads (1.2 us for the search for the tokens, by its instructions);
+//           reads (1 us for the search for the tokens);
 //   wide    T = 1024 1.54 ms, T = 4096 6.0 (1.24 and 1.26 PFLOP/s), keeping the
 //           weights 1.64 and 6.4: the matrix cores, 64 to 68 % busy at the 1.9
 //           GHz that their power leaves. (Boxes differ by 6 %.)

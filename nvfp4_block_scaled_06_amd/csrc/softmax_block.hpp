@@ -86,18 +86,22 @@ template <bool STREAM, int U>
 __device__ __forceinline__ uint32_t named_bits(const int32_t* tokens, int n, uint32_t base, int p0) {
   const __amdgpu_buffer_rsrc_t rsrc = make_rsrc(tokens, (int64_t)n * 4);
   uint32_t c[U], hits = 0u;
+  // (The last first where they are many: the compiler would take the loads that two of named_hits' cases begin with out of
+  // both, and wait for them before the others.)
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+  for (int i = 0; i < U; ++i) {
+    const int u = U == kNamedLoads ? U - 1 - i : i;
     c[u] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, 4 * (p0 + (int)(threadIdx.x & 63)) + 256 * u, 0, 0);
+  }
 #pragma unroll
-  for (int u = 0; u < U; ++u) hits = hits + hits + ((STREAM ? (c[u] - base) & ~47u : (c[u] - base) >> 6) == 0u ? 1u : 0u);
+  for (int u = 0; u < U; ++u) hits = hits + hits + ((c[u] & (STREAM ? ~47u : ~63u)) == base ? 1u : 0u);
   return hits << (32 - U);
 }
 template <bool STREAM>
 __device__ __forceinline__ uint32_t named_hits(const SoftmaxOut& o, int row0, int nr, int col0, int p0) {
   const int n = nr * o.K;
   const int32_t* tokens = o.tokens + (int64_t)row0 * o.K;
-  const uint32_t base = (uint32_t)(o.n0 + col0);
+  const uint32_t base = (uint32_t)(o.n0 + col0);  // none of the bits that its columns differ in
   uint32_t hits;
   if (n - p0 <= 128) hits = named_bits<STREAM, 2>(tokens, n, base, p0);
   else if (n - p0 <= 1024) hits = named_bits<STREAM, 16>(tokens, n, base, p0);
