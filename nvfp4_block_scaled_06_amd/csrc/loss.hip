@@ -153,7 +153,7 @@ __device__ __forceinline__ float2 thread_join(const float2* st, int n) {
 //           reads (1 us for the search for the tokens);
 //   wide    T = 1024 1.54 ms, T = 4096 6.0 (1.24 and 1.26 PFLOP/s), keeping the
 //           weights 1.64 and 6.4: the matrix cores, 64 to 68 % busy at the 1.9
-//           GHz that their power leaves. (Boxes differ by 6 %.)
+//           GHz that their power leaves. (Cards differ by 6 %.)
 // ---------------------------------------------------------------------------
 template <Out M, int MR, int KB, int KG, Scales S, int AUX>
 __global__ __launch_bounds__(KG * kEsThreads) void head_stream_kernel(ExpertArgs a, int row_tiles) {
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(NormArgs a, Hea
 // before they are written there.
 // D = 7168, N = 129280: T = 4096 6.4 ms for the two pieces (1.18 PFLOP/s), T =
 // 1024 1.65, bound by the matrix cores (68 % busy) and their power as the logits'
-// tiles (boxes differ by 6 %);
+// tiles (cards differ by 6 %);
 // with few rows by the weights (T = 1 to 8: 117 us for 521 MB, 4.5 TB/s), then
 // by splits that leave a workgroup few steps (T = 203, D = 2080, N = 32003: 48
 // us for 27 GFLOP, 11 steps and 39 MB of sums).
